@@ -1,5 +1,6 @@
 """Thin ctypes binding of libmoewarp.so — the same entry points as the C ABI
-in include/moe_warp.h, taking torch CUDA tensors for the device pointers.
+in include/moe_warp.h and include/moe_batch.h, taking torch CUDA tensors for
+the device pointers.
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels. If the library has not been built, or no CUDA device is present,
@@ -25,7 +26,13 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_build_union", "moe_verify_p
             "moe_verify_dedup", "moe_combine", "moe_last_device_error", "moe_status_str",
             "moe_last_cuda_error_string", "moe_verify_dedup_noalloc", "moe_noalloc_scratch_limit",
             "moe_diag_bounded_wait", "moe_route_biased", "moe_route_union", "moe_verify_pass",
-            "moe_verify_pass_fused", "moe_gate")
+            "moe_verify_pass_fused", "moe_gate", "moe_plan_batch", "moe_kv_append",
+            "moe_attend_workspace_bytes", "moe_attend", "moe_route_grouped")
+
+MOE_F32, MOE_BF16, MOE_F16 = range(3)
+MOE_MAX_REQUESTS, MOE_MAX_GROUPS, MOE_MAX_HEAD_GROUP = 1024, 32, 128
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 
 
 class MoeError(RuntimeError):
@@ -49,6 +56,33 @@ class LayerWeightsC(ctypes.Structure):
 class UnionC(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in
                 ("union_ids", "union_count", "offsets", "pair_tok", "pair_slot", "bytes")]
+
+
+class BatchC(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in
+                 ("n_requests", "max_blocks", "page_size", "free_capacity")] +
+                [(name, ctypes.c_void_p) for name in
+                 ("q_len", "cached", "held", "free_pages", "free_range", "block_table",
+                  "q_start", "kv_len", "held_out", "free_head")])
+
+
+class KvCacheC(ctypes.Structure):
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64)] +
+                [(name, ctypes.c_int32) for name in
+                 ("page_size", "n_kv_heads", "head_dim", "dtype")] +
+                [(name, ctypes.c_int64) for name in
+                 ("page_stride", "token_stride", "head_stride")])
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class RouterDesc(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in
+                 ("n_experts", "top_k", "n_groups", "top_groups", "group_top", "score",
+                  "renorm")] + [("scale", ctypes.c_float)])
 
 
 _lib = None
@@ -89,6 +123,16 @@ def load(path: str = LIB_PATH):
     lib.moe_status_str.restype = ctypes.c_char_p
     lib.moe_last_cuda_error_string.argtypes = []
     lib.moe_last_cuda_error_string.restype = ctypes.c_char_p
+    I64 = ctypes.c_int64
+    C, A = ctypes.POINTER(KvCacheC), ctypes.POINTER(AttnDesc)
+    lib.moe_plan_batch.argtypes = [ctypes.POINTER(BatchC), I32, P, P, P]
+    lib.moe_kv_append.argtypes = [C, P, P, I32, I64, I64, I32, P, P]
+    lib.moe_attend_workspace_bytes.argtypes = [C, A]
+    lib.moe_attend_workspace_bytes.restype = SZ
+    lib.moe_attend.argtypes = [C, A, P, I64, I64, I32, P, P, P, I32, I32, P, SZ, P, I64, I64, P]
+    lib.moe_route_grouped.argtypes = [ctypes.POINTER(RouterDesc), P, I32, I64, P, I32, P, P, P]
+    for f in ("moe_plan_batch", "moe_kv_append", "moe_attend", "moe_route_grouped"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_route", "moe_build_union", "moe_verify_perslot", "moe_verify_dedup",
               "moe_combine", "moe_last_device_error", "moe_verify_dedup_noalloc",
               "moe_diag_bounded_wait", "moe_route_biased", "moe_route_union", "moe_verify_pass",
@@ -238,3 +282,73 @@ def moe_diag_bounded_wait(limit_us: int, stream=None):
 
 def moe_last_device_error(stream=None) -> int:
     return int(load().moe_last_device_error(_stream(stream)))
+
+
+# ---- include/moe_batch.h -----------------------------------------------------
+def _raw(t: Optional[torch.Tensor]):
+    """The device pointer of a tensor whose strides the call takes."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor, got one on %s" % t.device)
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _stride(t: torch.Tensor, i: int) -> int:
+    """The stride of dimension i, or of one contiguous row where the dimension
+    has one entry (torch leaves any value there)."""
+    return t.stride(i) if t.shape[i] > 1 else t.shape[-1]
+
+
+def make_cache(k: torch.Tensor, v: torch.Tensor) -> KvCacheC:
+    """From page pools [n_pages][page_size][n_kv_heads][head_dim], the last
+    dimension contiguous, both with the same strides."""
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or any(
+            _stride(k, i) != _stride(v, i) for i in range(4)):
+        raise ValueError("k and v must be [pages][rows][heads][dim] of one type, shape and strides")
+    if k.dtype not in DTYPES or k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("cache pages must be float32, bfloat16 or float16 with contiguous rows")
+    return KvCacheC(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], k.shape[3],
+                    DTYPES[k.dtype], _stride(k, 0), _stride(k, 1), _stride(k, 2))
+
+
+def moe_plan_batch(batch: BatchC, n_tokens, slots, positions, stream=None):
+    _check(load().moe_plan_batch(ctypes.byref(batch), n_tokens, _ptr(slots), _ptr(positions),
+                                 _stream(stream)), "moe_plan_batch")
+
+
+def moe_kv_append(cache: KvCacheC, k, v, slots, stream=None):
+    """k, v: [n_tokens][n_kv_heads][head_dim], last dimension contiguous."""
+    if k.shape != v.shape or k.dtype != v.dtype or k.stride(2) != 1 or v.stride(2) != 1 or any(
+            _stride(k, i) != _stride(v, i) for i in range(2)):
+        raise ValueError("k and v must share type, shape and strides, their rows contiguous")
+    _check(load().moe_kv_append(ctypes.byref(cache), _raw(k), _raw(v), DTYPES[k.dtype],
+                                _stride(k, 0), _stride(k, 1), k.shape[0], _ptr(slots),
+                                _stream(stream)), "moe_kv_append")
+
+
+def moe_attend_workspace_bytes(cache: KvCacheC, attn: AttnDesc) -> int:
+    return int(load().moe_attend_workspace_bytes(ctypes.byref(cache), ctypes.byref(attn)))
+
+
+def moe_attend(cache: KvCacheC, attn: AttnDesc, q, q_start, kv_len, block_table, workspace, out,
+               stream=None):
+    """q, out: [n_tokens][n_heads][head_dim], last dimension contiguous."""
+    if q.stride(2) != 1 or out.stride(2) != 1 or q.shape != out.shape:
+        raise ValueError("q and out must have one shape and contiguous rows")
+    _check(load().moe_attend(ctypes.byref(cache), ctypes.byref(attn), _raw(q), _stride(q, 0),
+                             _stride(q, 1), q.shape[0], _ptr(q_start), _ptr(kv_len),
+                             _ptr(block_table), block_table.shape[1], kv_len.shape[0],
+                             _ptr(workspace), workspace.numel() * workspace.element_size(),
+                             _raw(out), _stride(out, 0), _stride(out, 1), _stream(stream)),
+           "moe_attend")
+
+
+def moe_route_grouped(router: RouterDesc, logits, bias, topk_idx, topk_w, stream=None):
+    """logits: [n][E] float32, bfloat16 or float16, last dimension contiguous."""
+    if logits.stride(1) != 1:
+        raise ValueError("the rows of logits must be contiguous")
+    _check(load().moe_route_grouped(ctypes.byref(router), _raw(logits), DTYPES[logits.dtype],
+                                    _stride(logits, 0), _ptr(bias),
+                                    logits.shape[0], _ptr(topk_idx), _ptr(topk_w),
+                                    _stream(stream)), "moe_route_grouped")

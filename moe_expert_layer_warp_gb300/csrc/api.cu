@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "moe_warp.h"
+#include "batch_launch.h"
 #include "launch.h"
 
 namespace {
@@ -199,6 +200,25 @@ moe_status check_weights(const moe_layer_desc* d, const moe_layer_weights* w) {
   } while (0)
 
 }  // namespace
+
+namespace moe {
+
+moe_status call_device(int* num_sms, unsigned int** err) {
+  DeviceInfo* di;
+  MOE_TRY(device_info(&di));
+  *num_sms = di->num_sms;
+  *err = di->err;
+  return MOE_OK;
+}
+
+moe_status fail_cuda(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+
+moe_status refuse(moe_status st, const char* where, const char* why) {
+  snprintf(g_last_cuda_err, sizeof g_last_cuda_err, "%s: %s", where, why);
+  return st;
+}
+
+}  // namespace moe
 
 extern "C" {
 
