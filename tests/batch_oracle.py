@@ -1,5 +1,5 @@
-"""The operators of include/moe_batch.h from their definitions, in 64 bits on
-the CPU, with the error bounds their tests use. Shares no code with the
+"""The operators of include/moe_batch.h from their definitions, in 64 bits, with
+the error bounds their tests use. Shares no code with the
 package."""
 from __future__ import annotations
 
@@ -35,8 +35,8 @@ def plan(q_len, cached, held, free, head, end, table, page, n_tokens):
 
 
 def attend(q, k, v, q_start, kv_len, table, scale, window, sinks):
-    """(out, bound) for q [T][Hq][D] and page pools k, v [pages][rows][heads][D]
-    (CPU tensors), both float64 [T][Hq][D].
+    """(out, bound) for q [T][Hq][D] and page pools k, v [pages][rows][heads][D],
+    both float64 [T][Hq][D], on q's device.
 
     bound: what a kernel may be off by that rounds its softmax weights and its
     result to the type of q (half a step each, of Σ p|v| and of |out|), sums
@@ -48,31 +48,41 @@ def attend(q, k, v, q_start, kv_len, table, scale, window, sinks):
     per = Hq // H
     eps = torch.finfo(q.dtype).eps / 2
     tiny = 2.0 ** -25 if q.dtype == torch.float16 else 0.0
-    out = torch.zeros((T, Hq, D), dtype=torch.float64)
-    bound = torch.zeros((T, Hq, D), dtype=torch.float64)
+    out = torch.zeros((T, Hq, D), dtype=torch.float64, device=q.device)
+    bound = torch.zeros((T, Hq, D), dtype=torch.float64, device=q.device)
     for b in range(len(kv_len)):
-        n = q_start[b + 1] - q_start[b]
-        for i in range(n):
-            p = kv_len[b] - n + i
-            j = [x for x in range(p + 1) if not window or p - x < window or x < sinks]
-            if not j:
+        first, n = q_start[b], q_start[b + 1] - q_start[b]
+        for t0 in range(0, n, 256):                       # a block of tokens at a time
+            pos = torch.arange(t0, min(n, t0 + 256), device=q.device) + kv_len[b] - n
+            j = torch.arange(max(0, int(pos[-1]) + 1), device=q.device)
+            back = pos[:, None] - j[None, :]
+            see = back >= 0
+            if window:
+                see &= (back < window) | (j[None, :] < sinks)
+            j, see = j[see.any(0)], see[:, see.any(0)]
+            if not j.numel():
                 continue
-            jt = torch.tensor(j)
-            pages = table[b].long()[jt // page]
-            kk = k[pages, jt % page].double()            # [keys][H][D]
-            vv = v[pages, jt % page].double()
-            x = q[q_start[b] + i].double().view(H, per, D)
-            s = torch.einsum("hgd,mhd->hgm", x, kk) * scale
-            mag = torch.einsum("hgd,mhd->hgm", x.abs(), kk.abs()) * scale
-            w = torch.softmax(s, dim=2)
-            y = torch.einsum("hgm,mhd->hgd", w, vv)
-            a = torch.einsum("hgm,mhd->hgd", w, vv.abs())
-            ds = (D + 8) * 2.0 ** -24 * mag.amax(2, keepdim=True)
-            row = q_start[b] + i
-            out[row] = y.reshape(Hq, D)
-            lost = tiny * vv.abs().sum(0)[:, None, :].expand(H, per, D)
-            bound[row] = ((eps * y.abs() + (eps + 2 * ds + 2.0 ** -20) * a + lost) * 1.01 +
-                          tiny).reshape(Hq, D)
+            rows = slice(first + t0, first + t0 + pos.numel())
+            pages = table[b].long()[j // page]
+            kk, vv = k[pages, j % page].double(), v[pages, j % page].double()   # [keys][H][D]
+            for h in range(H):
+                x = q[rows, h * per:(h + 1) * per].double()                      # [rows][per][D]
+                s = torch.einsum("rgd,md->rgm", x, kk[:, h]) * scale
+                s = s.masked_fill(~see[:, None, :], -math.inf)
+                top = s.amax(2, keepdim=True)
+                w = torch.where(see[:, None, :], (s - top.clamp_min(-1e300)).exp(), 0.0)
+                total = w.sum(2, keepdim=True)
+                w = w / torch.where(total > 0, total, 1.0)
+                mag = torch.einsum("rgd,md->rgm", x.abs(), kk[:, h].abs()) * scale
+                mag = torch.where(see[:, None, :], mag, 0.0)
+                ds = (D + 8) * 2.0 ** -24 * mag.amax(2, keepdim=True)
+                y = torch.einsum("rgm,md->rgd", w, vv[:, h])
+                a = torch.einsum("rgm,md->rgd", w, vv[:, h].abs())
+                lost = tiny * (see.double() @ vv[:, h].abs())[:, None, :]
+                cut = slice(h * per, (h + 1) * per)
+                out[rows, cut] = y
+                bound[rows, cut] = (eps * y.abs() + (eps + 2 * ds + 2.0 ** -20) * a +
+                                    lost) * 1.01 + tiny
     return out, bound
 
 

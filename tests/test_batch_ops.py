@@ -192,15 +192,15 @@ class Attend:
             at += blocks[b]
             first = m - q_len[b]
             lo = max(0, first - window + 1) if window else 0
-            for blk in range(blocks[b]):
-                rows = [r for r in range(page) if blk * page + r < m and
-                        (blk * page + r >= lo or blk * page + r < sinks)]
-                if not rows or q_len[b] == 0:
-                    table[b, blk] = -1 if window or q_len[b] == 0 else table[b, blk]
-                    continue
-                pg = int(table[b, blk])
-                for pool in (kc, vc):
-                    pool[pg, rows] = torch.randn((len(rows), H, D), generator=g).to(dtype)
+            j = torch.arange(m)
+            seen = (j >= lo) | (j < sinks) if q_len[b] else j < 0
+            for pool in (kc, vc):
+                pool[table[b].long()[j // page][seen], (j % page)[seen]] = torch.randn(
+                    (int(seen.sum()), H, D), generator=g).to(dtype)
+            # pages without a key that a new token sees are not to be read
+            used = torch.zeros(M, dtype=torch.bool)
+            used[(j // page)[seen]] = True
+            table[b][~used] = -1
         k.copy_(kc)
         v.copy_(vc)
         self.k, self.v, self.kc, self.vc, self.table = k, v, kc, vc, table
@@ -219,11 +219,11 @@ class Attend:
         return self.q.cuda(), i32(self.q_start), i32(self.kv_len), self.table.cuda()
 
     def check(self, got):
-        kc = torch.nan_to_num(self.kc.double(), nan=0.0)     # unseen places, never read below
-        vc = torch.nan_to_num(self.vc.double(), nan=0.0)
-        want, bound = oracle.attend(self.q, kc, vc, self.q_start, self.kv_len, self.table,
-                                    self.scale, self.window, self.sinks)
-        got = got.cpu().double()
+        kc = torch.nan_to_num(self.kc.cuda(), nan=0.0)     # unseen places, not used below
+        vc = torch.nan_to_num(self.vc.cuda(), nan=0.0)
+        want, bound = oracle.attend(self.q.cuda(), kc, vc, self.q_start, self.kv_len,
+                                    self.table.cuda(), self.scale, self.window, self.sinks)
+        got = got.double()
         assert torch.isfinite(got).all()
         over = (got - want).abs() - bound
         assert (over <= 0).all(), "off by %.3g beyond %.3g at %s" % (
@@ -260,6 +260,20 @@ ATTENDS = {
     "peaked scores": Attend([9, 150], [800, 400], 4, 2, 128, B16, 64, spread=12.0),
     "peaked scores in fp16": Attend([9, 150], [800, 400], 4, 2, 128, F16, 64, spread=12.0),
     "large scale": Attend([4], [300], 4, 2, 64, B16, 16, scale=3.0),
+    # several tiles and several items per CTA
+    "many passes": Attend([1 + i % 9 for i in range(40)], [100 + 97 * i for i in range(40)], 16, 4,
+                          128, B16, 64),
+    "many passes, small pages": Attend([1 + i % 5 for i in range(60)], [3000 - 49 * i for i in
+                                       range(60)], 12, 4, 64, F16, 16, heads_first=True),
+    "long chunks": Attend([900, 1100], [2600, 1100], 8, 2, 128, B16, 64),
+    "long chunks, odd groups": Attend([700, 333, 40], [3000, 333, 2000], 15, 3, 64, F16, 32),
+    "mixed batch": Attend([500, 3, 9, 0, 260, 1] + [4] * 30, [1500, 0, 2500, 9, 2000, 1] +
+                          [600 + 31 * i for i in range(30)], 28, 4, 128, F16, 16),
+    "many windows": Attend([1 + i % 9 for i in range(40)], [200 + 190 * i for i in range(40)], 16,
+                           4, 64, B16, 16, window=700, sinks=5),
+    "long windows over chunks": Attend([1500, 800], [2500, 4000], 8, 4, 128, B16, 128, window=900,
+                                       sinks=200),
+    "peaked long chunks": Attend([900, 1100], [2600, 1500], 8, 2, 128, F16, 64, spread=10.0),
     "tiny scale": Attend([4], [300], 4, 2, 64, F16, 16, scale=1e-20),
 }
 
