@@ -30,11 +30,14 @@
 // from them by itself.
 //
 // Warps (one CTA per SM):
-//   0-3   softmax of stream 0, one thread per row; queries in, results out
-//   4-7   the same for stream 1
-//   8     TMA: key and value tiles into a ring, a box per page and 64 columns
-//   9     MMA issue; clears value rows that no row of the item sees
+//   0-3    softmax of stream 0, one thread per row, and its results out
+//   4-7    the same for stream 1
+//   8      TMA: key and value tiles into a ring, a box per page and 64 columns
+//   9      MMA issue; clears value rows that no row of the item sees
+//   10-11  query tiles into two slots, the next as soon as one is free
+#include <limits.h>
 #include <math.h>
+#include <string.h>
 
 #include "batch_launch.h"
 #include "common.cuh"
@@ -45,14 +48,19 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128;        // rows of a query tile, keys of a key tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 constexpr int kPlanThreads = 256;
 constexpr int kPerThread = MOE_MAX_REQUESTS / kPlanThreads;
+// What an item costs beside its tiles, in tiles, when the work is cut.
+constexpr int kItemCost = 2;
 // The reference m follows the row's maximum only when that has grown by more
 // than this (in powers of two): until then weights are up to 2^8 instead of
 // 1, which fp32 sums and both 16-bit types hold, and O needs no rescaling.
 constexpr float kGrow = 8.f;
+// Registers per thread: launched with 168, the softmax warps take 216 and the
+// others leave 72 (2·216 + 72 = 3·168).
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 
 template <int kDim>
 struct Sizes {
@@ -60,8 +68,8 @@ struct Sizes {
   static constexpr int kStages = kDim == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
-  static constexpr int kMiscBytes = 1536;  // Misc, then the streams' row statistics
-  static constexpr int kSmem = kOffMisc + kMiscBytes + 1024;  // slack to align the base to 1024
+  static constexpr int kMiscBytes = 512 + 2048;  // Misc, then the streams' row statistics
+  static constexpr int kSmem = kOffMisc + kMiscBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // one slot of the workspace: O as [kDim/4][256 rows] float4, then m and Σ
   static constexpr size_t kSlotFloats = size_t(2 * kTile) * (kDim + 2);
@@ -129,40 +137,70 @@ MOE_DEV Item make_item(const AttendArgs& a, const Request& r, int block, int fix
   return it;
 }
 
-// Where a CTA is in its range of tiles; every role walks it by itself.
+// Where a CTA is in its range; every role walks it by itself. Units are key
+// tiles, with kItemCost more at the head of every item.
 struct Walk {
-  int b, h, block, t0, left;
+  int b, h, block, u0, left;
 };
 
-// The walk's present item; skips requests without new tokens.
-MOE_DEV Item walk_item(const Params& p, Walk& w, Request& r) {
-  bool bad;
-  r = request(p.a, p.page_shift, w.b, &bad);
-  while (r.q == 0 && w.b + 1 < p.a.n_requests) r = request(p.a, p.page_shift, ++w.b, &bad);
-  return make_item(p.a, r, w.block, 2 * p.tpt);
-}
+// The CTA's part of an item: tiles [t0, t1).
+struct Part {
+  Item it;
+  int t0, t1;
+  bool two;  // the block's tokens fill more than one query tile
+};
 
-MOE_DEV void walk_next(const Params& p, Walk& w, const Request& r, int done) {
-  w.left -= done;
-  w.t0 = 0;
-  if (++w.block * 2 * p.tpt >= r.q) {
-    w.block = 0;
-    if (++w.h == p.a.cache.n_kv_heads) {
-      w.h = 0;
-      ++w.b;
-    }
+// The next part of the walk with tiles in it, which is then behind the walk;
+// false when there is none. w keeps the part's request and key head in b, h
+// until the next call moves on.
+struct Walker {
+  const Params& p;
+  Walk w;
+  Request r;
+  int b, h;  // of the present part
+
+  MOE_DEV Walker(const Params& prm, const Walk& start) : p(prm), w(start), b(start.b), h(start.h) {
+    bool bad;
+    r = request(p.a, p.page_shift, min(w.b, p.a.n_requests - 1), &bad);
   }
-}
+
+  MOE_DEV bool next(Part* out) {
+    const int fixed = 2 * p.tpt;
+    while (w.left > 0) {
+      const Item it = make_item(p.a, r, w.block, fixed);
+      const int u1 = min(w.u0 + w.left, it.n + kItemCost);
+      out->it = it;
+      out->t0 = max(0, w.u0 - kItemCost);
+      out->t1 = max(0, u1 - kItemCost);
+      out->two = it.ntok > p.tpt;
+      b = w.b;
+      h = w.h;
+      w.left -= u1 - w.u0;
+      w.u0 = 0;
+      if (w.left > 0 && ++w.block * fixed >= r.q) {
+        w.block = 0;
+        if (++w.h == p.a.cache.n_kv_heads) {
+          w.h = 0;
+          bool bad;
+          do {
+            r = request(p.a, p.page_shift, ++w.b, &bad);
+          } while (r.q == 0 && w.b + 1 < p.a.n_requests);
+        }
+      }
+      if (out->t1 > out->t0) return true;
+    }
+    return false;
+  }
+};
 
 struct Start {
   Walk w;
-  int first;  // 1: the range begins inside an item
   int has_rec;
   JoinRec rec;
 };
 
-// The CTA's range of tiles: prefix sums over the requests' tile counts, then
-// the place of its first tile. Threads 0..kPlanThreads-1 call it.
+// The CTA's range: prefix sums over the requests' units, then the place of
+// its first one. Threads 0..kPlanThreads-1 call it.
 MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   const AttendArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -177,7 +215,7 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
       bool bad;
       const Request r = request(a, p.page_shift, b, &bad);
       any_bad |= bad;
-      for (int q = 0; q * fixed < r.q; ++q) n += make_item(a, r, q, fixed).n;
+      for (int q = 0; q * fixed < r.q; ++q) n += make_item(a, r, q, fixed).n + kItemCost;
     }
     count[i] = n;
     sum += n;
@@ -200,10 +238,11 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   const int H = a.cache.n_kv_heads;
   total *= H;
   before *= H;
-  // no more CTAs than tiles, so that no range among them is empty
+  // no more CTAs than units, so that no range among them is empty
   const long long C = min((long long)gridDim.x, total), c = blockIdx.x;
   const long long w0 = c < C ? c * total / C : 0, w1 = c < C ? (c + 1) * total / C : 0;
   if (tid == 0) {
+    out->w.b = 0;
     out->w.left = (int)(w1 - w0);
     out->has_rec = 0;
   }
@@ -222,15 +261,16 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
       const Request r = request(a, p.page_shift, b, &bad);
       int q = 0;
       Item it = make_item(a, r, 0, fixed);
-      while (rem >= it.n) {
-        rem -= it.n;
+      while (rem >= it.n + kItemCost) {
+        rem -= it.n + kItemCost;
         it = make_item(a, r, ++q, fixed);
       }
       out->w.block = q;
-      out->w.t0 = (int)rem;
-      // the item ends here and began in an earlier range: this CTA's record
-      if (rem > 0 && it.n - rem <= w1 - w0) {
-        const long long s = w0 - rem;
+      out->w.u0 = (int)rem;
+      // the item's last tile is here and its first in an earlier range: this
+      // CTA's record
+      if (rem > kItemCost && it.n + kItemCost - rem <= w1 - w0) {
+        const long long s = w0 - rem + kItemCost;  // unit of the item's first tile
         long long c0 = s * C / total;
         while (c0 + 1 < C && (c0 + 1) * total / C <= s) ++c0;
         out->has_rec = 1;
@@ -266,6 +306,33 @@ MOE_DEV float exp2_approx(float x) {
   return y;
 }
 
+MOE_DEV float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+MOE_DEV uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+MOE_DEV uint64_t pair_f(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+MOE_DEV void split(uint64_t v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+MOE_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <bool kF16>
 MOE_DEV uint32_t narrow(float lo, float hi) {
   if constexpr (kF16) {
@@ -279,7 +346,7 @@ MOE_DEV uint32_t narrow(float lo, float hi) {
 // Barriers and words behind the ring.
 struct Misc {
   uint64_t full[10], empty[10];
-  uint64_t q_ready, q_free;
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;
   Start start;
@@ -288,7 +355,7 @@ struct Misc {
   int abort_flag;
 };
 static_assert(sizeof(Misc) <= 512, "misc words");
-constexpr int kOffStat = 512;  // then [2][128] floats: row statistics the streams exchange
+constexpr int kOffStat = 512;  // then [2 streams][m, Σ][128 rows] floats
 
 template <int kDim, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Params p) {
@@ -298,22 +365,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   constexpr int kHalfBytes = kTile * 128;
   constexpr uint32_t kCols = 512;              // S0 S1 O0 O1, 128 columns each
   const AttendArgs& a = p.a;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_addr(smem) & 1023u) {               // the tiles' swizzle needs it
+    if (threadIdx.x == 0) report_error(a.err, ERR_CHECK, 0xA23);
+    return;
+  }
   unsigned char* ring = smem + Z::kOffRing;
   Misc& m = *reinterpret_cast<Misc*>(smem + Z::kOffMisc);
   volatile int* abort_flag = &m.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same value in every lane, and known to be
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 1);
     }
-    mbar_init(&m.q_ready, 8);
-    mbar_init(&m.q_free, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&m.q_full[s], 2);
+      mbar_init(&m.q_empty[s], 1);
       mbar_init(&m.s_full[s], 1);
       mbar_init(&m.p_full[s], 4);
       mbar_init(&m.o_full[s], 1);
@@ -333,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  const uint32_t tmem = m.tmem;
-  Walk w = m.start.w;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
   if (threadIdx.x == 0) {
     JoinRec& rec = p.rec[blockIdx.x];
     if (m.start.has_rec) {
@@ -343,50 +413,53 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       rec.valid = 0;
     }
   }
+  bool ok = true;  // no wait of this role has been lost
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int site) {
+    ok = __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, abort_flag, a.err, site));
+  };
+  Part pt;
 
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  }
   if (warp == 8) {
     // ------------------------------------------------------------- loader --
+    Walker walk(p, m.start.w);
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
     const uint64_t policy = l2_evict_normal_policy();
     int stage = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    while (w.left > 0) {
-      Request r;
-      const Item it = walk_item(p, w, r);
-      const int n = min(w.left, it.n - w.t0);
-      const int lead = it.ntok > p.tpt ? 1 : 2;  // key tiles ahead of the value tiles
-      const int32_t* table = a.block_table + (size_t)w.b * a.max_blocks;
-      // keys 0..lead-1, then values j, keys j + lead, for j = 0..n-1
-      for (int step = 0; step < 2 * n + 2 * lead; ++step) {
-        const bool is_v = step >= lead && ((step - lead) & 1) == 0;
-        const int j = step < lead ? step : is_v ? (step - lead) >> 1 : ((step - lead) >> 1) + lead;
-        if (j >= n) continue;
-        const int key0 = tile_of(it, w.t0 + j) * kTile;
-        // this lane's page of the tile, if any row of it is seen
-        const int r0 = key0 + lane * rows;
-        bool want = lane < n_pages && r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk);
-        int pg = -1;
-        if (want) pg = table[r0 >> p.page_shift];
-        if (want && (pg < 0 || pg >= a.cache.n_pages)) {
-          report_error(a.err, ERR_CHECK, 0xA21);
-          pg = (int)a.cache.n_pages;             // out of the map: the box reads zeros
-        }
-        const uint32_t wanted = __ballot_sync(0xffffffffu, want);
-        ok = ok && wait_or_abort(&m.empty[stage], phase ^ 1u, abort_flag, a.err, 0xA30);
-        ok = __all_sync(0xffffffffu, ok);
+    while (walk.next(&pt)) {
+      const Item& it = pt.it;
+      const int n = pt.t1 - pt.t0;
+      const int lead = pt.two ? 1 : 2;          // key tiles ahead of the value tiles
+      const int32_t* table = a.block_table + (size_t)walk.b * a.max_blocks;
+      // this lane's page of tile j (−1: it has none, or no row of it is seen)
+      auto page_of = [&](int j) {
+        if (j >= n) return -1;
+        const int r0 = tile_of(it, pt.t0 + j) * kTile + lane * rows;
+        const bool want = lane < n_pages && r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk);
+        if (!want) return -1;
+        const int pg = table[r0 >> p.page_shift];
+        if (pg >= 0 && pg < a.cache.n_pages) return pg;
+        report_error(a.err, ERR_CHECK, 0xA21);
+        return (int)a.cache.n_pages;            // out of the map: the box reads zeros
+      };
+      auto load = [&](const CUtensorMap* map, int j, int pg) {
+        const uint32_t wanted = __ballot_sync(0xffffffffu, pg >= 0);
+        wait(&m.empty[stage], phase ^ 1u, 0xA30);
         if (ok) {
           unsigned char* dst = ring + stage * Z::kTileBytes;
           if (lane == 0)
             mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim * 2);
           __syncwarp();
-          if (want) {
-            const CUtensorMap* map = is_v ? &p.vmap : &p.kmap;
+          if (pg >= 0) {
+            const int r0 = tile_of(it, pt.t0 + j) * kTile + lane * rows;
 #pragma unroll
             for (int half = 0; half < kHalves; ++half)
-              tma_load_4d(dst + half * kHalfBytes + lane * rows * 128, map, half * 64, w.h,
+              tma_load_4d(dst + half * kHalfBytes + lane * rows * 128, map, half * 64, walk.h,
                           r0 & (page - 1), pg, &m.full[stage], policy);
           }
         }
@@ -394,8 +467,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           stage = 0;
           phase ^= 1u;
         }
+      };
+      // keys 0..lead-1, then values j, keys j + lead, for j = 0..n-1; the
+      // pages of a tile are fetched one tile ahead
+      int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
+      load(&p.kmap, 0, pg0);
+      if (lead == 2 && n > 1) load(&p.kmap, 1, pg1);
+      for (int j = 0; j < n; ++j) {
+        const int pg3 = page_of(j + 3);
+        load(&p.vmap, j, pg0);
+        if (j + lead < n) load(&p.kmap, j + lead, lead == 1 ? pg1 : pg2);
+        pg0 = pg1;
+        pg1 = pg2;
+        pg2 = pg3;
       }
-      walk_next(p, w, r, n);
     }
     // After a lost wait the tiles still in flight must land before the CTA
     // ends; without one, every tile has been waited for by the MMA warp.
@@ -405,90 +490,89 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMA --
+    Walker walk(p, m.start.w);
     const uint32_t id_s = umma::idesc_f16(kTile, kTile, kF16, false);
     const uint32_t id_o = umma::idesc_f16(kTile, kDim, kF16, true);
-    const uint32_t q_addr = smem_addr(smem), ring_addr = smem_addr(ring);
-    int stage = 0;
+    const uint32_t q_lo = umma::desc_lo(smem_addr(smem), 0);
+    const uint32_t k_lo = umma::desc_lo(smem_addr(ring), 0);
+    const uint32_t v_lo = umma::desc_lo(smem_addr(ring), kHalfBytes);
+    int stage = 0, q_slot = 0;
     uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
-    bool ok = true;
     auto next_tile = [&]() {
       const int s = stage;
-      ok = ok && wait_or_abort(&m.full[s], phase, abort_flag, a.err, 0xA40);
-      ok = __all_sync(0xffffffffu, ok);
+      wait(&m.full[s], phase, 0xA40);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;
       }
       return s;
     };
-    auto scores = [&](int s, int q_tile, int st) {  // S_s = Q · Kᵀ
-      if (ok && lane == 0) {
-        umma::fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < kDim / 16; ++k) {
-          const uint32_t off = (k >> 2) * kHalfBytes + (k & 3) * 32;
-          umma::mma_bf16(tmem + s * 128, umma::desc_sw128(q_addr + q_tile * Z::kTileBytes + off),
-                         umma::desc_sw128(ring_addr + st * Z::kTileBytes + off), id_s, k != 0);
-        }
-        umma::commit(&m.s_full[s]);
-      }
+    auto scores = [&](int s, int slot, int st) {  // S_s = Q · Kᵀ
+      if (!ok) return;
+      umma::fence_after_sync();
+      const uint32_t q = q_lo + slot * (Z::kTileBytes >> 4), k = k_lo + st * (Z::kTileBytes >> 4);
+      umma::mma4_ss(tmem + s * 128, q, k, id_s, 0u);
+      if (kHalves == 2)
+        umma::mma4_ss(tmem + s * 128, q + (kHalfBytes >> 4), k + (kHalfBytes >> 4), id_s, 1u);
+      umma::commit_elect(&m.s_full[s]);
     };
     auto values = [&](int s, int st, bool first) {  // O_s (+)= P_s · V
-      ok = ok && wait_or_abort(&m.p_full[s], p_phase[s], abort_flag, a.err, 0xA41);
-      ok = __all_sync(0xffffffffu, ok);
+      wait(&m.p_full[s], p_phase[s], 0xA41);
       p_phase[s] ^= 1u;
-      if (ok && lane == 0) {
-        umma::fence_after_sync();
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          umma::mma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8,
-                           umma::desc_sw128_mn(ring_addr + st * Z::kTileBytes + k * 2048,
-                                               kHalfBytes),
-                           id_o, !first || k != 0);
-      }
+      if (!ok) return;
+      umma::fence_after_sync();
+      const uint32_t v = v_lo + st * (Z::kTileBytes >> 4);
+      umma::mma4_ts(tmem + 256 + s * 128, tmem + s * 128, v, id_o, first ? 0u : 1u);
+      umma::mma4_ts(tmem + 256 + s * 128, tmem + s * 128 + 32, v + (4 * 2048 >> 4), id_o, 1u);
     };
-    auto release = [&](int st) {
-      if (ok && lane == 0) umma::commit(&m.empty[st]);
+    auto commit = [&](uint64_t* bar) {
+      if (ok) umma::commit_elect(bar);
     };
-    while (w.left > 0) {
-      Request r;
-      const Item it = walk_item(p, w, r);
-      const int n = min(w.left, it.n - w.t0);
-      const bool two = it.ntok > p.tpt;
-      // stream s's rows see something of a tile
-      auto active = [&](int s, int j) {
-        const int key0 = tile_of(it, w.t0 + j) * kTile;
-        const int t_first = two ? s * p.tpt : 0;
-        const int t_last = two ? min(it.ntok, (s + 1) * p.tpt) : it.ntok;
-        const int hi = it.pos0 + t_last, lo = it.pos0 + t_first - a.window + 1;
-        return key0 < hi && (a.window == 0 || key0 + kTile > lo || key0 < a.sinks);
-      };
-      ok = ok && wait_or_abort(&m.q_ready, q_phase, abort_flag, a.err, 0xA42);
-      ok = __all_sync(0xffffffffu, ok);
-      q_phase ^= 1u;
-      bool first[2] = {true, true};
+    while (walk.next(&pt)) {
+      const Item& it = pt.it;
+      const int n = pt.t1 - pt.t0;
+      const bool two = pt.two;
+      // query slots of the streams: two tiles take both, one tile the next
+      const int slot0 = q_slot, slot1 = two ? q_slot ^ 1 : q_slot;
+      // a stream sees something of a tile that begins at key0
+      const int tok1 = two ? p.tpt : it.ntok;      // end of stream 0's tokens
+      const int hi0 = it.pos0 + tok1, hi1 = it.pos0 + it.ntok;
+      const int low = a.window > 0 ? it.pos0 - a.window + 1 - (kTile - 1) : INT_MIN;
+      const int lo1 = a.window > 0 ? low + (two ? p.tpt : 0) : INT_MIN;
+      auto sees0 = [&](int key0) { return key0 < hi0 && (key0 >= low || key0 < a.sinks); };
+      auto sees1 = [&](int key0) { return key0 < hi1 && (key0 >= lo1 || key0 < a.sinks); };
+      bool first0 = true, first1 = true;
       const int lead = two ? 1 : 2;
-      for (int j = 0; j < min(lead, n); ++j) {
-        const int st = next_tile();
-        if (two) {
-          if (active(0, 0)) scores(0, 0, st);
-          if (active(1, 0)) scores(1, 1, st);
-        } else if (active(0, j)) {
-          scores(j, 0, st);
-        }
-        release(st);
+      wait(&m.q_full[slot0], q_phase, 0xA42);
+      if (q_slot == 1) q_phase ^= 1u;
+      if (two) wait(&m.q_full[slot1], q_phase, 0xA44);
+      if (two && q_slot == 0) q_phase ^= 1u;
+      {
+        const int st = next_tile(), key0 = tile_of(it, pt.t0) * kTile;
+        if (sees0(key0)) scores(0, slot0, st);
+        if (two && sees1(key0)) scores(1, slot1, st);
+        commit(&m.empty[st]);
       }
-      if (n <= lead && ok && lane == 0) umma::commit(&m.q_free);
+      if (!two && n > 1) {
+        const int st = next_tile();
+        scores(1, slot0, st);
+        commit(&m.empty[st]);
+      }
+      if (n <= lead) {
+        commit(&m.q_empty[slot0]);
+        if (two) commit(&m.q_empty[slot1]);
+      }
       for (int j = 0; j < n; ++j) {
+        const int key0 = tile_of(it, pt.t0 + j) * kTile;
         const int vt = next_tile();
-        const int kt = j + lead < n ? next_tile() : -1;
+        const bool more = j + lead < n;
+        const int kt = more ? next_tile() : 0;
         // rows of V that no row of the item sees may hold anything: their
         // weights are 0, and 0 · NaN is not
-        const int key0 = tile_of(it, w.t0 + j) * kTile;
         if (ok && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
           unsigned char* v = ring + vt * Z::kTileBytes;
           for (int i = lane; i < kTile * kHalves * 8; i += 32) {
-            const int row = (i >> 3) & (kTile - 1), key = key0 + row;
+            const int key = key0 + ((i >> 3) & (kTile - 1));
             if (key >= it.hi || (key < it.lo && key >= it.sk))
               *reinterpret_cast<uint4*>(v + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -496,102 +580,121 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           __syncwarp();
         }
         if (two) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (active(s, j)) {
-              values(s, vt, first[s]);
-              first[s] = false;
-            }
-            if (s == 1) release(vt);
-            if (kt >= 0 && active(s, j + 1)) scores(s, s, kt);
+          const int key1 = tile_of(it, pt.t0 + j + 1) * kTile;
+          if (sees0(key0)) {
+            values(0, vt, first0);
+            first0 = false;
           }
+          if (more && sees0(key1)) scores(0, slot0, kt);
+          if (sees1(key0)) {
+            values(1, vt, first1);
+            first1 = false;
+          }
+          commit(&m.empty[vt]);
+          if (more && sees1(key1)) scores(1, slot1, kt);
+        } else if (j & 1) {
+          values(1, vt, first1);
+          first1 = false;
+          commit(&m.empty[vt]);
+          if (more) scores(1, slot0, kt);
         } else {
-          const int s = j & 1;
-          if (active(0, j)) {
-            values(s, vt, first[s]);
-            first[s] = false;
+          if (sees0(key0)) {
+            values(0, vt, first0);
+            first0 = false;
           }
-          release(vt);
-          if (kt >= 0 && active(0, j + lead)) scores(s, 0, kt);
+          commit(&m.empty[vt]);
+          if (more) scores(0, slot0, kt);
         }
-        if (kt >= 0) release(kt);
-        if (j + lead + 1 == n && ok && lane == 0) umma::commit(&m.q_free);
+        if (more) commit(&m.empty[kt]);
+        if (j + lead + 1 == n) {                   // the last scores are issued
+          commit(&m.q_empty[slot0]);
+          if (two) commit(&m.q_empty[slot1]);
+        }
       }
-      if (ok && lane == 0) {
-        if (!first[0]) umma::commit(&m.o_full[0]);
-        if (!first[1]) umma::commit(&m.o_full[1]);
-      }
-      walk_next(p, w, r, n);
+      if (!first0) commit(&m.o_full[0]);
+      if (!first1) commit(&m.o_full[1]);
+      if (!two) q_slot ^= 1;
     }
     // Every MMA, and every arrival that hangs on one, is done before tensor
     // memory is released.
-    if (lane == 0) {
-      umma::commit(&m.drain);
-      mbar_wait(&m.drain, 0, a.err, 0xA43);
-    }
+    umma::commit_elect(&m.drain);
+    mbar_wait(&m.drain, 0, a.err, 0xA43);
     __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ queries --
+    // 16-byte pieces by cp.async, a row's pieces in neighbouring lanes
+    Walker walk(p, m.start.w);
+    constexpr int kChunks = kDim / 8;
+    constexpr int kRowStep = 64 / kChunks;        // rows the two warps copy at a time
+    const int t = threadIdx.x - 320, c = t & (kChunks - 1), G = a.group;
+    int slot = 0;
+    uint32_t phase = 0;
+    while (walk.next(&pt)) {
+      for (int q = 0; q < (pt.two ? 2 : 1); ++q) {
+        const int tok0 = q * p.tpt;
+        const int rows = min(p.tpt, pt.it.ntok - tok0) * G;
+        wait(&m.q_empty[slot], phase ^ 1u, 0xA60);
+        if (ok) {
+          int rr = t / kChunks, tok = rr / G, g = rr - tok * G;
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                                (int64_t)(pt.it.row0 + tok0) * a.q_token_stride +
+                                (int64_t)walk.h * G * a.q_head_stride + c * 8;
+          const uint32_t dst = smem_addr(smem) + slot * Z::kTileBytes + (c >> 3) * kHalfBytes;
+          for (; rr < rows; rr += kRowStep) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
+                         "l"(src + tok * a.q_token_stride + g * a.q_head_stride)
+                         : "memory");
+            g += kRowStep;
+            while (g >= G) {
+              g -= G;
+              ++tok;
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m.q_full[slot]);
+        }
+        if (slot) phase ^= 1u;
+        slot ^= 1;
+      }
+    }
   } else {
     // ------------------------------------------------------------ softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    Walker walk(p, m.start.w);
     const int s = warp >> 2;               // stream
     const int row = threadIdx.x & 127;     // row of the tile, TMEM lane
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32·(warp % 4) in the upper half
     const uint32_t s_addr = tmem + lane_base + s * 128;
     const uint32_t o_addr = tmem + lane_base + 256 + s * 128;
     const float to_log2 = a.scale * 1.4426950408889634f;
+    const uint64_t to_log2_2 = pair_f(to_log2, to_log2);
     // fp16 weights are held 2^4 larger, so that small ones keep their bits
     const float offset = kF16 ? 4.f : 0.f;
-    const int G = a.group;
+    const int t_in = row / a.group, g_in = row - t_in * a.group;
     float* stat = reinterpret_cast<float*>(smem + Z::kOffMisc + kOffStat);
-    uint32_t s_phase = 0, o_phase = 0, qf_phase = 0;
-    bool ok = true, first_item = true;
-    while (w.left > 0) {
-      Request r;
-      const Item it = walk_item(p, w, r);
-      const int n = min(w.left, it.n - w.t0);
-      const bool two = it.ntok > p.tpt;
-      // ---- queries in: stream s its own tile, or both streams half a tile
-      if (!first_item) {
-        ok = ok && wait_or_abort(&m.q_free, qf_phase, abort_flag, a.err, 0xA50);
-        qf_phase ^= 1u;
-      }
-      first_item = false;
-      {
-        constexpr int kChunks = kDim / 8;          // 16-byte pieces of a row
-        const int toks = two ? min(it.ntok - s * p.tpt, p.tpt) : it.ntok;
-        const int rows = toks * G;
-        const int r_first = two ? 0 : s * 64, r_end = two ? rows : min(rows, r_first + 64);
-        unsigned char* q_tile = smem + (two ? s : 0) * Z::kTileBytes;
-        const int row0 = it.row0 + (two ? s * p.tpt : 0);
-        for (int i = row; i < (r_end - r_first) * kChunks; i += 128) {
-          const int rr = r_first + i / kChunks, c = i & (kChunks - 1);
-          const int tok = rr / G, g = rr - tok * G;
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-              static_cast<const uint16_t*>(a.q) + (row0 + tok) * a.q_token_stride +
-              (w.h * G + g) * a.q_head_stride + c * 8));
-          *reinterpret_cast<uint4*>(q_tile + (c >> 3) * kHalfBytes + rr * 128 +
-                                    (((c & 7) ^ (rr & 7)) << 4)) = v;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m.q_ready);
-      }
-      // ---- this thread's row
-      const int t_in = row / G, tok = (two ? s * p.tpt : 0) + t_in;
-      const bool valid = t_in < p.tpt && tok < it.ntok;
+    uint32_t s_phase = 0, o_phase = 0;
+    while (walk.next(&pt)) {
+      const Item& it = pt.it;
+      const int n = pt.t1 - pt.t0;
+      const bool two = pt.two;
+      const int t_first = two ? s * p.tpt : 0, t_last = two && s == 0 ? p.tpt : it.ntok;
+      const int tok = t_first + t_in;
+      const bool valid = t_in < p.tpt && tok < t_last;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const int pos = it.pos0 + tok;
       const int hi = valid ? max(0, pos + 1) : 0;
       const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-      const int t_first = two ? s * p.tpt : 0;
-      const int t_last = two ? min(it.ntok, (s + 1) * p.tpt) : it.ntok;
-      const int s_hi = it.pos0 + t_last, s_lo = it.pos0 + t_first - a.window + 1;
+      const int s_hi = it.pos0 + t_last;
+      const int s_lo = a.window > 0 ? it.pos0 + t_first - a.window + 1 - (kTile - 1) : INT_MIN;
       float ref = -INFINITY, sum = 0.f;
       bool began = false;
       for (int j = two ? 0 : s; j < n; j += two ? 1 : 2) {
-        const int key0 = tile_of(it, w.t0 + j) * kTile;
-        if (!(key0 < s_hi && (a.window == 0 || key0 + kTile > s_lo || key0 < a.sinks))) continue;
-        ok = ok && wait_or_abort(&m.s_full[s], s_phase, abort_flag, a.err, 0xA51);
-        ok = __all_sync(0xffffffffu, ok);
+        const int key0 = tile_of(it, pt.t0 + j) * kTile;
+        if (!(key0 < s_hi && (key0 >= s_lo || key0 < a.sinks))) continue;
+        wait(&m.s_full[s], s_phase, 0xA51);
         s_phase ^= 1u;
         if (ok && warp_valid) {
           umma::fence_after_sync();
@@ -607,11 +710,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             for (int c = 0; c < kTile; ++c)
               if (!(c < e_hi && (c >= e_lo || c < e_sk))) x[c] = 0xff800000u;  // −inf
           }
-          float top = __uint_as_float(x[0]);
+          float t4[4];
 #pragma unroll
-          for (int c = 1; c < kTile; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-          top *= to_log2;
-          const bool grown = top > ref + kGrow || (ref == -INFINITY && top > -INFINITY);
+          for (int i = 0; i < 4; ++i) t4[i] = __uint_as_float(x[i]);
+#pragma unroll
+          for (int c = 4; c + 8 <= kTile; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              t4[i] = max3(t4[i], __uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(x[kTile - 4 + i]));
+          const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]) * to_log2;
+          const bool grown = top > ref + kGrow;
           if (__any_sync(0xffffffffu, grown)) {
             const float keep = grown ? exp2_approx(ref - top) : 1.f;
             if (grown) ref = top;
@@ -629,18 +739,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
           }
           const float shift = ref == -INFINITY ? 0.f : offset - ref;
-          float s0 = 0.f, s1 = 0.f;
+          const uint64_t shift_2 = pair_f(shift, shift);
+          uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int c = 0; c < kTile; c += 2) {
-            const float p0 = exp2_approx(fmaf(__uint_as_float(x[c]), to_log2, shift));
-            const float p1 = exp2_approx(fmaf(__uint_as_float(x[c + 1]), to_log2, shift));
-            s0 += p0;
-            s1 += p1;
+            float p0, p1;
+            split(fma2(pair(x[c], x[c + 1]), to_log2_2, shift_2), &p0, &p1);
+            p0 = exp2_approx(p0);
+            p1 = exp2_approx(p1);
+            sums[(c >> 1) & 3] = add2(sums[(c >> 1) & 3], pair_f(p0, p1));
             x[c >> 1] = narrow<kF16>(p0, p1);
+            if (c == kTile / 2 - 2) umma::st_x32(s_addr, x);
           }
-          sum += s0 + s1;
-          umma::st_x32(s_addr, x);
           umma::st_x32(s_addr + 32, x + 32);
+          float s0, s1;
+          split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), &s0, &s1);
+          sum += s0 + s1;
           umma::wait_st();
         }
         began = true;
@@ -649,80 +763,75 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&m.p_full[s]);
       }
       // ---- results out
+      if (!two) {
+        stat[s * 256 + row] = ref;
+        stat[s * 256 + 128 + row] = sum;
+      }
       if (began) {
-        ok = ok && wait_or_abort(&m.o_full[s], o_phase, abort_flag, a.err, 0xA52);
+        wait(&m.o_full[s], o_phase, 0xA52);
         o_phase ^= 1u;
       }
-      ok = __all_sync(0xffffffffu, ok);
-      umma::fence_after_sync();
-      const bool ends = w.t0 + n == it.n, whole_item = ends && w.t0 == 0;
-      float* slot = p.part + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * Z::kSlotFloats;
-      // factors of the two streams' O for this thread's columns
+      const bool ends = pt.t1 == it.n, whole_item = ends && pt.t0 == 0;
+      // factors of the two streams' O, and this thread's columns
       float f0 = 1.f, f1 = 0.f;
       int c_first = 0, c_end = kDim;
       if (!two) {
         // both streams hold sums of the same rows: each joins half the columns
-        stat[s * 128 + row] = ref;
         asm volatile("bar.sync 2, 256;" ::: "memory");
-        const float other = stat[(s ^ 1) * 128 + row];
-        const float top = fmaxf(ref, other);
-        const float mine = ref == -INFINITY ? 0.f : exp2_approx(ref - top);
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        stat[s * 128 + row] = sum * mine;
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        umma::fence_after_sync();
-        sum = sum * mine + stat[(s ^ 1) * 128 + row];
-        const float theirs = other == -INFINITY ? 0.f : exp2_approx(other - top);
-        f0 = s == 0 ? mine : theirs;
-        f1 = s == 0 ? theirs : mine;
-        ref = top;
+        const float ref0 = stat[row], ref1 = stat[256 + row];
+        ref = fmaxf(ref0, ref1);
+        f0 = ref0 == -INFINITY ? 0.f : exp2_approx(ref0 - ref);
+        f1 = ref1 == -INFINITY ? 0.f : exp2_approx(ref1 - ref);
+        sum = stat[128 + row] * f0 + stat[256 + 128 + row] * f1;
         c_first = s * (kDim / 2);
         c_end = c_first + kDim / 2;
       }
+      umma::fence_after_sync();
       if (ok && warp_valid) {
-        const float inv = whole_item ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        f0 *= inv;
-        f1 *= inv;
-        const int o0 = two ? s : 0;
-        const int head = w.h * G + (row - t_in * G);
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
-                        head * a.out_head_stride;
+        if (whole_item) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          f0 *= inv;
+          f1 *= inv;
+        }
+        // a stream that saw no key never wrote its O: what is there is not a
+        // number to be scaled
+        const bool any0 = f0 > 0.f && sum > 0.f, any1 = f1 > 0.f;
+        const bool warp_any1 = __any_sync(0xffffffffu, any1);
+        const uint32_t from = tmem + lane_base + 256 + (two ? s * 128 : 0);
+        uint16_t* dst = static_cast<uint16_t*>(a.out) +
+                        (int64_t)(it.row0 + tok) * a.out_token_stride +
+                        (int64_t)(walk.h * a.group + g_in) * a.out_head_stride;
+        float* slot = p.part + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * Z::kSlotFloats;
         const int prow = (two ? s * kTile : 0) + row;
+#pragma unroll 1
         for (int c = c_first; c < c_end; c += 32) {
-          uint32_t o[32];
-          umma::ld_x32(tmem + lane_base + 256 + o0 * 128 + c, o);
+          uint32_t o[32], o1[32];
+          umma::ld_x32(from + c, o);
+          if (warp_any1) umma::ld_x32(from + 128 + c, o1);
           umma::wait_ld();
-          // a stream that saw no key never wrote its O: what is there is not
-          // a number to be scaled
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            o[i] = f0 > 0.f && sum > 0.f ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
-          if (!two && __any_sync(0xffffffffu, f1 > 0.f)) {
-            uint32_t o1[32];
-            umma::ld_x32(tmem + lane_base + 384 + c, o1);
-            umma::wait_ld();
+          for (int i = 0; i < 32; ++i) o[i] = any0 ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
+          if (warp_any1) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (f1 > 0.f)
+              if (any1)
                 o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
           }
-          if (valid) {
-            if (whole_item) {
+          if (valid && whole_item) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint4 v;
-                v.x = narrow<kF16>(__uint_as_float(o[i]), __uint_as_float(o[i + 1]));
-                v.y = narrow<kF16>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-                v.z = narrow<kF16>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5]));
-                v.w = narrow<kF16>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
-                *reinterpret_cast<uint4*>(dst + c + i) = v;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                reinterpret_cast<uint4*>(slot)[((c + i) >> 2) * (2 * kTile) + prow] =
-                    make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 32; i += 8) {
+              uint4 v;
+              v.x = narrow<kF16>(__uint_as_float(o[i]), __uint_as_float(o[i + 1]));
+              v.y = narrow<kF16>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+              v.z = narrow<kF16>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5]));
+              v.w = narrow<kF16>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
+              *reinterpret_cast<uint4*>(dst + c + i) = v;
             }
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              reinterpret_cast<uint4*>(slot)[((c + i) >> 2) * (2 * kTile) + prow] =
+                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
         if (valid && !whole_item && (two || s == 0)) {
@@ -731,11 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           st[2 * kTile + prow] = sum;
         }
       }
-      // this item's O and statistics have been read before the next item's
-      // are written (of both streams, where they were joined)
+      // joined O and statistics have been read before either stream goes on
       umma::fence_before_sync();
       if (!two) asm volatile("bar.sync 2, 256;" ::: "memory");
-      walk_next(p, w, r, n);
     }
   }
   umma::fence_before_sync();

@@ -45,18 +45,15 @@ MOE_DEV uint32_t idesc_f16(int M, int N, bool f16, bool b_mn) {
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Shared-memory descriptor of a 128-byte-swizzled tile whose rows run along
-// K: row k holds 64 elements of N (128 bytes), 8-row groups are 1024 bytes
-// apart, and the next 64 elements of N are n_stride bytes on. A K-step of 16
-// advances the start address by 2048 bytes.
-MOE_DEV uint64_t desc_sw128_mn(uint32_t smem_byte_addr, uint32_t n_stride) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_byte_addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((n_stride >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// The same descriptor in two words: the high one is the same for every
+// 128-byte-swizzled tile with 8-row groups 1024 bytes apart, and the low one
+// moves with the address (16-byte units; it never carries, shared memory ends
+// below 2^18). A tile whose rows run along K (row k holds 64 elements of N,
+// 128 bytes) gives the distance of the next 64 elements of N as n_stride; its
+// K-step of 16 advances the address by 2048 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+MOE_DEV uint32_t desc_lo(uint32_t smem_byte_addr, uint32_t n_stride) {
+  return ((smem_byte_addr >> 4) & 0x3FFFu) | ((n_stride ? n_stride >> 4 : 1u) << 16);
 }
 
 // D[tmem] (+)= A[smem] · B[smem]ᵀ; accumulate when `acc` != 0. One thread.
@@ -70,15 +67,57 @@ MOE_DEV void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t 
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] · B[smem]: A's row r is TMEM lane r, two 16-bit elements
-// per column along K. One thread.
-MOE_DEV void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                        uint32_t acc) {
+// Four K-steps (64 elements of K) in one go, issued by one elected lane of a
+// converged warp; `alo`, `blo` are the low words of the operands' descriptors
+// at the first step. With the whole sequence in one block and the operands
+// equal in every lane, issuing an MMA costs less than the MMA takes; from a
+// divergent branch with a 64-bit descriptor each it cost 75 cycles apiece.
+// mma4_ss: A and B both K-major tiles in shared memory.
+MOE_DEV void mma4_ss(uint32_t tmem_d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(acc)
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n\t"
+      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n\t"
+      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, 1;\n\t}"
+      ::"r"(tmem_d), "r"(alo), "r"(blo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+
+// mma4_ts: A from tensor memory (row r is lane r, two 16-bit elements per
+// column along K), B a tile whose rows run along K (desc_lo with n_stride).
+MOE_DEV void mma4_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t blo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b32 a, %1;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, a, 8;\n\tadd.s64 b, b, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, 1;\n\t"
+      "add.s32 a, a, 8;\n\tadd.s64 b, b, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, 1;\n\t"
+      "add.s32 a, a, 8;\n\tadd.s64 b, b, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, 1;\n\t}"
+      ::"r"(tmem_d), "r"(tmem_a), "r"(blo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+
+// commit (below) by the lane that mma4_ss and mma4_ts elect.
+MOE_DEV void commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_addr(bar))
       : "memory");
 }
 
