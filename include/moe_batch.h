@@ -135,7 +135,7 @@ size_t moe_attend_workspace_bytes(const moe_kv_cache* cache, const moe_attn_desc
  * shorter than the pass) gets zeros. The keys and values of the new tokens
  * themselves are read from the cache: append them first.
  *   q         [n_tokens][n_heads][head_dim] of the cache's type, strides
- *             multiples of 8, 16-byte aligned.
+ *             positive multiples of 8, 16-byte aligned.
  *   q_start   [n_requests+1], kv_len [n_requests], block_table
  *             [n_requests][max_blocks]: as moe_plan_batch writes them.
  *   out       same shape and type, with its own strides (multiples of 8,

@@ -33,8 +33,11 @@
 //   0-3    softmax of stream 0, one thread per row, and its results out
 //   4-7    the same for stream 1
 //   8      TMA: key and value tiles into a ring, a box per page and 64 columns
-//   9      MMA issue; clears value rows that no row of the item sees
-//   10-11  query tiles into two slots, the next as soon as one is free
+//   10     TMA: query tiles into two slots, the next as soon as one is free
+//   9, 11  MMA issue of stream 0 and of stream 1 (one warp for both could not
+//          keep up: the waits, issues and commits of a key tile took it 3900
+//          cycles, the products themselves take 2048); they also clear value
+//          rows that no row of the item sees
 #include <limits.h>
 #include <math.h>
 #include <string.h>
@@ -82,7 +85,7 @@ struct JoinRec {
 };
 
 struct Params {
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap, vmap, qmap;
   AttendArgs a;
   int page_shift;
   int tpt;       // tokens per query tile, 128 / group
@@ -199,32 +202,59 @@ struct Start {
   JoinRec rec;
 };
 
+MOE_DEV long long divide(long long a, long long b) {  // of non-negative numbers
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The units of one request for one key head; every lane of the warp has the
+// same request.
+MOE_DEV long long warp_units(const AttendArgs& a, const Request& r, int fixed) {
+  long long n = 0;
+  for (int q = threadIdx.x & 31; q * fixed < r.q; q += 32)
+    n += make_item(a, r, q, fixed).n + kItemCost;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
 // The CTA's range: prefix sums over the requests' units, then the place of
-// its first one. Threads 0..kPlanThreads-1 call it.
+// its first one. The first kPlanThreads threads call it, warps converged.
 MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   const AttendArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int fixed = 2 * p.tpt;
+  const int fixed = 2 * p.tpt, H = a.cache.n_kv_heads;
+  constexpr uint32_t kAll = 0xffffffffu;
+  Request req[kPerThread];
   long long count[kPerThread], sum = 0;
   bool any_bad = false;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int b = tid * kPerThread + i;
-    long long n = 0;
-    if (b < a.n_requests) {
-      bool bad;
-      const Request r = request(a, p.page_shift, b, &bad);
-      any_bad |= bad;
-      for (int q = 0; q * fixed < r.q; ++q) n += make_item(a, r, q, fixed).n + kItemCost;
+    bool bad = false;
+    req[i] = Request{0, 0, 0};
+    if (b < a.n_requests) req[i] = request(a, p.page_shift, b, &bad);
+    any_bad |= bad;
+  }
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    // a request of one block by its own thread, longer ones by the warp
+    count[i] = req[i].q > 0 ? make_item(a, req[i], 0, fixed).n + kItemCost : 0;
+    uint32_t longer = __ballot_sync(kAll, req[i].q > fixed);
+    while (longer) {
+      const int from = __ffs(longer) - 1;
+      longer &= longer - 1;
+      const Request r = {__shfl_sync(kAll, req[i].first, from), __shfl_sync(kAll, req[i].q, from),
+                         __shfl_sync(kAll, req[i].len, from)};
+      const long long n = warp_units(a, r, fixed);
+      if (lane == from) count[i] = n;
     }
-    count[i] = n;
-    sum += n;
+    sum += count[i];
   }
   if (any_bad && blockIdx.x == 0) report_error(a.err, ERR_CHECK, 0xA20);
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    const long long t = __shfl_up_sync(kAll, incl, o);
     if (lane >= o) incl += t;
   }
   if (lane == 31) part[warp] = incl;
@@ -235,12 +265,13 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
     if (w < warp) before += part[w];
     total += part[w];
   }
-  const int H = a.cache.n_kv_heads;
   total *= H;
   before *= H;
-  // no more CTAs than units, so that no range among them is empty
+  // no more CTAs than units, so that no range among them is empty: the first
+  // `more` ranges are one unit longer than the others
   const long long C = min((long long)gridDim.x, total), c = blockIdx.x;
-  const long long w0 = c < C ? c * total / C : 0, w1 = c < C ? (c + 1) * total / C : 0;
+  const long long each = C > 0 ? divide(total, C) : 0, more = total - each * C;
+  const long long w0 = c * each + min(c, more), w1 = c < C ? w0 + each + (c < more ? 1 : 0) : w0;
   if (tid == 0) {
     out->w.b = 0;
     out->w.left = (int)(w1 - w0);
@@ -248,36 +279,62 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   }
   asm volatile("bar.sync 1, 256;" ::: "memory");
   if (w1 == w0) return;
+  // the request whose units hold w0, then the warp looks through its blocks
+  Request r = {0, 0, 0};
+  int b = -1, h = 0;
+  long long rem = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const long long n = count[i] * H;
     if (w0 >= before && w0 < before + n) {
-      const int b = tid * kPerThread + i;
-      long long rem = w0 - before;
-      out->w.b = b;
-      out->w.h = (int)(rem / count[i]);
-      rem -= out->w.h * count[i];
-      bool bad;
-      const Request r = request(a, p.page_shift, b, &bad);
-      int q = 0;
-      Item it = make_item(a, r, 0, fixed);
-      while (rem >= it.n + kItemCost) {
-        rem -= it.n + kItemCost;
-        it = make_item(a, r, ++q, fixed);
-      }
-      out->w.block = q;
-      out->w.u0 = (int)rem;
-      // the item's last tile is here and its first in an earlier range: this
-      // CTA's record
-      if (rem > kItemCost && it.n + kItemCost - rem <= w1 - w0) {
-        const long long s = w0 - rem + kItemCost;  // unit of the item's first tile
-        long long c0 = s * C / total;
-        while (c0 + 1 < C && (c0 + 1) * total / C <= s) ++c0;
-        out->has_rec = 1;
-        out->rec = JoinRec{1, it.row0, it.ntok, out->w.h * a.group, (int)c0, {0, 0, 0}};
-      }
+      b = tid * kPerThread + i;
+      r = req[i];
+      h = (int)divide(w0 - before, count[i]);
+      rem = w0 - before - h * count[i];
     }
     before += n;
+  }
+  const uint32_t here = __ballot_sync(kAll, b >= 0);
+  if (here == 0) return;
+  const int from = __ffs(here) - 1;
+  r = Request{__shfl_sync(kAll, r.first, from), __shfl_sync(kAll, r.q, from),
+              __shfl_sync(kAll, r.len, from)};
+  b = __shfl_sync(kAll, b, from);
+  h = __shfl_sync(kAll, h, from);
+  rem = __shfl_sync(kAll, rem, from);
+  for (int q0 = 0; q0 * fixed < r.q; q0 += 32) {
+    const int q = q0 + lane;
+    Item it;
+    long long n = 0, upto;
+    if (q * fixed < r.q) {
+      it = make_item(a, r, q, fixed);
+      n = it.n + kItemCost;
+    }
+    upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(kAll, upto, o);
+      if (lane >= o) upto += t;
+    }
+    if (rem < upto && rem >= upto - n) {
+      const long long u0 = rem - (upto - n);
+      out->w.b = b;
+      out->w.h = h;
+      out->w.block = q;
+      out->w.u0 = (int)u0;
+      // the item's last tile is here and its first in an earlier range: this
+      // CTA's record
+      if (u0 > kItemCost && n - u0 <= w1 - w0) {
+        const long long s = w0 - u0 + kItemCost;  // unit of the item's first tile
+        const long long head = more * (each + 1);
+        const long long c0 = s < head ? divide(s, each + 1) : more + divide(s - head, each);
+        out->has_rec = 1;
+        out->rec = JoinRec{1, it.row0, it.ntok, h * a.group, (int)c0, {0, 0, 0}};
+      }
+    }
+    const long long block_sum = __shfl_sync(kAll, upto, 31);
+    if (rem < block_sum) return;
+    rem -= block_sum;
   }
 }
 
@@ -343,12 +400,35 @@ MOE_DEV uint32_t narrow(float lo, float hi) {
   }
 }
 
+// v[i] of lane 4q + j  <->  v[j] of lane 4q + i.
+MOE_DEV uint4 shfl_xor4(uint4 v, int mask) {
+  return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask),
+                    __shfl_xor_sync(0xffffffffu, v.z, mask), __shfl_xor_sync(0xffffffffu, v.w, mask));
+}
+MOE_DEV void quad_transpose(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+      // the lane without the bit sends v[i | bit], the lane with it v[i]
+      const uint4 got = shfl_xor4(up ? v[i] : v[i | bit], bit);
+      if (up) {
+        v[i] = got;
+      } else {
+        v[i | bit] = got;
+      }
+    }
+  }
+}
+
 // Barriers and words behind the ring.
 struct Misc {
   uint64_t full[10], empty[10];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t drain;
+  uint64_t turn[2], drain[2];
   Start start;
   long long part[8];
   uint32_t tmem;
@@ -380,16 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&m.full[i], 1);
-      mbar_init(&m.empty[i], 1);
+      mbar_init(&m.empty[i], 2);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&m.q_full[s], 2);
-      mbar_init(&m.q_empty[s], 1);
+      mbar_init(&m.q_full[s], 1);
+      mbar_init(&m.q_empty[s], 2);
       mbar_init(&m.s_full[s], 1);
       mbar_init(&m.p_full[s], 4);
       mbar_init(&m.o_full[s], 1);
+      mbar_init(&m.turn[s], 1);
+      mbar_init(&m.drain[s], 1);
     }
-    mbar_init(&m.drain, 1);
     m.abort_flag = 0;
     fence_mbar_init();
   }
@@ -488,88 +569,121 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       for (int i = 0; i < kStages; ++i)
         for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_for(&m.full[i], ph, a.err, 0xA31, 1000000ull);
     }
-  } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMA --
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ queries --
+    // a box is the 128 / group tokens of a tile, times the group's heads, in
+    // the order of the tile's rows
     Walker walk(p, m.start.w);
+    const uint64_t policy = l2_evict_normal_policy();
+    int slot = 0;
+    uint32_t phase = 0;
+    while (walk.next(&pt)) {
+      for (int q = 0; q < (pt.two ? 2 : 1); ++q) {
+        wait(&m.q_empty[slot], phase ^ 1u, 0xA60);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&m.q_full[slot], p.tpt * a.group * kDim * 2);
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half)
+            tma_load_3d(smem + slot * Z::kTileBytes + half * kHalfBytes, &p.qmap, half * 64,
+                        walk.h * a.group, pt.it.row0 + q * p.tpt, &m.q_full[slot], policy);
+        }
+        __syncwarp();
+        if (slot) phase ^= 1u;
+        slot ^= 1;
+      }
+    }
+    if (!ok && lane == 0) {
+      for (int i = 0; i < 2; ++i)
+        for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_for(&m.q_full[i], ph, a.err, 0xA61, 1000000ull);
+    }
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- MMA --
+    // Both warps follow every tile of the ring and of the query slots, in
+    // order: a barrier tells only the parity of its phase, so a warp that
+    // passed over a tile could take an older phase for the one it wants. A
+    // tile that is the other stream's alone is released as soon as it is there.
+    Walker walk(p, m.start.w);
+    const int s = (warp - 9) >> 1;                     // stream
     const uint32_t id_s = umma::idesc_f16(kTile, kTile, kF16, false);
     const uint32_t id_o = umma::idesc_f16(kTile, kDim, kF16, true);
     const uint32_t q_lo = umma::desc_lo(smem_addr(smem), 0);
     const uint32_t k_lo = umma::desc_lo(smem_addr(ring), 0);
     const uint32_t v_lo = umma::desc_lo(smem_addr(ring), kHalfBytes);
-    int stage = 0, q_slot = 0;
-    uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
-    auto next_tile = [&]() {
-      const int s = stage;
-      wait(&m.full[s], phase, 0xA40);
+    const uint32_t d_s = tmem + s * 128, d_o = tmem + 256 + s * 128;
+    int stage = 0;
+    uint32_t phase = 0, n_q = 0, p_phase = 0, turn = s ^ 1u;
+    auto next_tile = [&]() {                           // waits for the ring's next tile
+      const int st = stage;
+      wait(&m.full[st], phase, 0xA40);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;
       }
-      return s;
+      return st;
     };
-    auto scores = [&](int s, int slot, int st) {  // S_s = Q · Kᵀ
-      if (!ok) return;
-      umma::fence_after_sync();
-      const uint32_t q = q_lo + slot * (Z::kTileBytes >> 4), k = k_lo + st * (Z::kTileBytes >> 4);
-      umma::mma4_ss(tmem + s * 128, q, k, id_s, 0u);
-      if (kHalves == 2)
-        umma::mma4_ss(tmem + s * 128, q + (kHalfBytes >> 4), k + (kHalfBytes >> 4), id_s, 1u);
-      umma::commit_elect(&m.s_full[s]);
-    };
-    auto values = [&](int s, int st, bool first) {  // O_s (+)= P_s · V
-      wait(&m.p_full[s], p_phase[s], 0xA41);
-      p_phase[s] ^= 1u;
-      if (!ok) return;
-      umma::fence_after_sync();
-      const uint32_t v = v_lo + st * (Z::kTileBytes >> 4);
-      umma::mma4_ts(tmem + 256 + s * 128, tmem + s * 128, v, id_o, first ? 0u : 1u);
-      umma::mma4_ts(tmem + 256 + s * 128, tmem + s * 128 + 32, v + (4 * 2048 >> 4), id_o, 1u);
-    };
-    auto commit = [&](uint64_t* bar) {
+    auto commit = [&](uint64_t* bar) {                 // arrives when the MMAs so far are done
       if (ok) umma::commit_elect(bar);
+    };
+    auto pass = [&](uint64_t* bar) {                   // arrives now
+      if (ok && lane == 0) mbar_arrive(bar);
+      __syncwarp();
+    };
+    auto scores = [&](uint32_t slot, int st) {         // S = Q · Kᵀ
+      if (!ok) return;
+      const uint32_t q = q_lo + slot * (Z::kTileBytes >> 4), k = k_lo + st * (Z::kTileBytes >> 4);
+      umma::mma4_ss(d_s, q, k, id_s, 0u);
+      if (kHalves == 2) umma::mma4_ss(d_s, q + (kHalfBytes >> 4), k + (kHalfBytes >> 4), id_s, 1u);
+      umma::commit_elect(&m.s_full[s]);
     };
     while (walk.next(&pt)) {
       const Item& it = pt.it;
       const int n = pt.t1 - pt.t0;
       const bool two = pt.two;
-      // query slots of the streams: two tiles take both, one tile the next
-      const int slot0 = q_slot, slot1 = two ? q_slot ^ 1 : q_slot;
-      // a stream sees something of a tile that begins at key0
-      const int tok1 = two ? p.tpt : it.ntok;      // end of stream 0's tokens
-      const int hi0 = it.pos0 + tok1, hi1 = it.pos0 + it.ntok;
-      const int low = a.window > 0 ? it.pos0 - a.window + 1 - (kTile - 1) : INT_MIN;
-      const int lo1 = a.window > 0 ? low + (two ? p.tpt : 0) : INT_MIN;
-      auto sees0 = [&](int key0) { return key0 < hi0 && (key0 >= low || key0 < a.sinks); };
-      auto sees1 = [&](int key0) { return key0 < hi1 && (key0 >= lo1 || key0 < a.sinks); };
-      bool first0 = true, first1 = true;
-      const int lead = two ? 1 : 2;
-      wait(&m.q_full[slot0], q_phase, 0xA42);
-      if (q_slot == 1) q_phase ^= 1u;
-      if (two) wait(&m.q_full[slot1], q_phase, 0xA44);
-      if (two && q_slot == 0) q_phase ^= 1u;
-      {
-        const int st = next_tile(), key0 = tile_of(it, pt.t0) * kTile;
-        if (sees0(key0)) scores(0, slot0, st);
-        if (two && sees1(key0)) scores(1, slot1, st);
-        commit(&m.empty[st]);
-      }
-      if (!two && n > 1) {
-        const int st = next_tile();
-        scores(1, slot0, st);
-        commit(&m.empty[st]);
-      }
-      if (n <= lead) {
-        commit(&m.q_empty[slot0]);
-        if (two) commit(&m.q_empty[slot1]);
-      }
-      for (int j = 0; j < n; ++j) {
+      // the stream sees something of a tile that begins at key0
+      const int t_first = two ? s * p.tpt : 0, t_last = two && s == 0 ? p.tpt : it.ntok;
+      const int hi = it.pos0 + t_last;
+      const int lo = a.window > 0 ? it.pos0 + t_first - a.window + 1 - (kTile - 1) : INT_MIN;
+      auto sees = [&](int j) {
         const int key0 = tile_of(it, pt.t0 + j) * kTile;
+        return (two || (j & 1) == s) && key0 < hi && (key0 >= lo || key0 < a.sinks);
+      };
+      // the query tiles: the stream's own, and the other one's
+      uint32_t slot = 0;
+      for (int q = 0; q < (two ? 2 : 1); ++q, ++n_q) {
+        wait(&m.q_full[n_q & 1u], n_q >> 1 & 1u, 0xA42);
+        if (!two || q == s) {
+          slot = n_q & 1u;
+        } else {
+          pass(&m.q_empty[n_q & 1u]);
+        }
+      }
+      const int lead = two ? 1 : 2;                    // the next key tile of the stream
+      const int last = two ? n - 1 : ((n - 1 - s) & ~1) + s;  // its last tile (< s: it has none)
+      bool first = true;
+      for (int j = 0; j < min(lead, n); ++j) {
+        const int st = next_tile();
+        if (!two && j != s) {
+          pass(&m.empty[st]);
+        } else {
+          if (sees(j)) scores(slot, st);
+          commit(&m.empty[st]);
+        }
+      }
+      if (last < lead) commit(&m.q_empty[slot]);
+      for (int j = 0; j < n; ++j) {
+        const bool more = j + lead < n, mine = two || (j & 1) == s;
         const int vt = next_tile();
-        const bool more = j + lead < n;
         const int kt = more ? next_tile() : 0;
+        if (!mine) {
+          pass(&m.empty[vt]);
+          if (more) pass(&m.empty[kt]);
+          continue;
+        }
         // rows of V that no row of the item sees may hold anything: their
         // weights are 0, and 0 · NaN is not
-        if (ok && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
+        const int key0 = tile_of(it, pt.t0 + j) * kTile;
+        const bool now = sees(j);
+        if (ok && now && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
           unsigned char* v = ring + vt * Z::kTileBytes;
           for (int i = lane; i < kTile * kHalves * 8; i += 32) {
             const int key = key0 + ((i >> 3) & (kTile - 1));
@@ -579,87 +693,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           fence_proxy_async_smem();
           __syncwarp();
         }
+        if (now) wait(&m.p_full[s], p_phase, 0xA41);
+        // Two query tiles take turns: a stream's P·V and its next scores are
+        // issued in one piece. Were they mixed with the other's, both scores
+        // would be ready late and together, both softmaxes would run at the
+        // same time, and the tensor cores would wait for them.
         if (two) {
-          const int key1 = tile_of(it, pt.t0 + j + 1) * kTile;
-          if (sees0(key0)) {
-            values(0, vt, first0);
-            first0 = false;
-          }
-          if (more && sees0(key1)) scores(0, slot0, kt);
-          if (sees1(key0)) {
-            values(1, vt, first1);
-            first1 = false;
-          }
-          commit(&m.empty[vt]);
-          if (more && sees1(key1)) scores(1, slot1, kt);
-        } else if (j & 1) {
-          values(1, vt, first1);
-          first1 = false;
-          commit(&m.empty[vt]);
-          if (more) scores(1, slot0, kt);
-        } else {
-          if (sees0(key0)) {
-            values(0, vt, first0);
-            first0 = false;
-          }
-          commit(&m.empty[vt]);
-          if (more) scores(0, slot0, kt);
+          wait(&m.turn[s], turn, 0xA44);
+          turn ^= 1u;
         }
+        if (now) {                                     // O (+)= P · V
+          p_phase ^= 1u;
+          umma::fence_after_sync();
+          if (ok) {
+            const uint32_t v = v_lo + vt * (Z::kTileBytes >> 4);
+            umma::mma4_ts(d_o, d_s, v, id_o, first ? 0u : 1u);
+            umma::mma4_ts(d_o, d_s + 32, v + (4 * 2048 >> 4), id_o, 1u);
+          }
+          first = false;
+        }
+        if (more && sees(j + lead)) scores(slot, kt);  // into S, behind the product that reads P
+        if (two) pass(&m.turn[s ^ 1]);
+        if (j == last && !first) commit(&m.o_full[s]);
+        commit(&m.empty[vt]);
         if (more) commit(&m.empty[kt]);
-        if (j + lead + 1 == n) {                   // the last scores are issued
-          commit(&m.q_empty[slot0]);
-          if (two) commit(&m.q_empty[slot1]);
-        }
+        if (more && j + lead == last) commit(&m.q_empty[slot]);  // the last scores are issued
       }
-      if (!first0) commit(&m.o_full[0]);
-      if (!first1) commit(&m.o_full[1]);
-      if (!two) q_slot ^= 1;
     }
     // Every MMA, and every arrival that hangs on one, is done before tensor
     // memory is released.
-    umma::commit_elect(&m.drain);
-    mbar_wait(&m.drain, 0, a.err, 0xA43);
+    umma::commit_elect(&m.drain[s]);
+    mbar_wait(&m.drain[s], 0, a.err, 0xA43);
     __syncwarp();
-  } else if (warp >= 10) {
-    // ------------------------------------------------------------ queries --
-    // 16-byte pieces by cp.async, a row's pieces in neighbouring lanes
-    Walker walk(p, m.start.w);
-    constexpr int kChunks = kDim / 8;
-    constexpr int kRowStep = 64 / kChunks;        // rows the two warps copy at a time
-    const int t = threadIdx.x - 320, c = t & (kChunks - 1), G = a.group;
-    int slot = 0;
-    uint32_t phase = 0;
-    while (walk.next(&pt)) {
-      for (int q = 0; q < (pt.two ? 2 : 1); ++q) {
-        const int tok0 = q * p.tpt;
-        const int rows = min(p.tpt, pt.it.ntok - tok0) * G;
-        wait(&m.q_empty[slot], phase ^ 1u, 0xA60);
-        if (ok) {
-          int rr = t / kChunks, tok = rr / G, g = rr - tok * G;
-          const uint16_t* src = static_cast<const uint16_t*>(a.q) +
-                                (int64_t)(pt.it.row0 + tok0) * a.q_token_stride +
-                                (int64_t)walk.h * G * a.q_head_stride + c * 8;
-          const uint32_t dst = smem_addr(smem) + slot * Z::kTileBytes + (c >> 3) * kHalfBytes;
-          for (; rr < rows; rr += kRowStep) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                             dst + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)),
-                         "l"(src + tok * a.q_token_stride + g * a.q_head_stride)
-                         : "memory");
-            g += kRowStep;
-            while (g >= G) {
-              g -= G;
-              ++tok;
-            }
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&m.q_full[slot]);
-        }
-        if (slot) phase ^= 1u;
-        slot ^= 1;
-      }
-    }
   } else {
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -798,9 +863,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const bool any0 = f0 > 0.f && sum > 0.f, any1 = f1 > 0.f;
         const bool warp_any1 = __any_sync(0xffffffffu, any1);
         const uint32_t from = tmem + lane_base + 256 + (two ? s * 128 : 0);
-        uint16_t* dst = static_cast<uint16_t*>(a.out) +
-                        (int64_t)(it.row0 + tok) * a.out_token_stride +
-                        (int64_t)(walk.h * a.group + g_in) * a.out_head_stride;
+        // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
+        const uint64_t dst = reinterpret_cast<uint64_t>(
+            static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
+            (int64_t)(walk.h * a.group + g_in) * a.out_head_stride);
+        const uint32_t quad_valid = __ballot_sync(0xffffffffu, valid) >> (lane & ~3) & 15u;
+        uint16_t* quad_dst[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          quad_dst[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, dst, (lane & ~3) + i));
         float* slot = p.part + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * Z::kSlotFloats;
         const int prow = (two ? s * kTile : 0) + row;
 #pragma unroll 1
@@ -817,16 +888,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               if (any1)
                 o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
           }
-          if (valid && whole_item) {
+          if (whole_item) {
+            uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint4 v;
-              v.x = narrow<kF16>(__uint_as_float(o[i]), __uint_as_float(o[i + 1]));
-              v.y = narrow<kF16>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-              v.z = narrow<kF16>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5]));
-              v.w = narrow<kF16>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7]));
-              *reinterpret_cast<uint4*>(dst + c + i) = v;
+            for (int i = 0; i < 4; ++i) {
+              v[i].x = narrow<kF16>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]));
+              v[i].y = narrow<kF16>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
+              v[i].z = narrow<kF16>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
+              v[i].w = narrow<kF16>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
             }
+            // four lanes turn their 4 rows × 4 pieces, so that a store covers
+            // 64 bytes of 8 rows instead of 16 bytes of 32
+            quad_transpose(v, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (quad_valid >> i & 1u)
+                *reinterpret_cast<uint4*>(quad_dst[i] + c + (lane & 3) * 8) = v[i];
           } else if (valid) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -946,6 +1023,17 @@ cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream)
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
+  // queries as [token][head][dim]: a box is the rows of a query tile
+  const cuuint64_t q_dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)a.n_heads,
+                                (cuuint64_t)a.n_tokens};
+  const cuuint64_t q_strides[2] = {(cuuint64_t)a.q_head_stride * 2,
+                                   (cuuint64_t)a.q_token_stride * 2};
+  const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)p.tpt};
+  if (encode(&p.qmap, type, 3, const_cast<void*>(a.q), q_dims, q_strides, q_box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
   const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   const bool f16 = c.dtype == MOE_F16;
   if (c.head_dim == 128)

@@ -11,6 +11,9 @@ namespace {
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// A tensor map's strides are below 2^40 bytes; no GPU holds an array near it.
+constexpr int64_t kMaxStride = int64_t(1) << 38;
+
 bool page_size_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128 || p == 256; }
 
 // The cache descriptor's reason for a refusal, or null.
@@ -26,10 +29,8 @@ const char* cache_fault(const moe_kv_cache* c, moe_status* st) {
   if (c->page_stride < 1 || c->token_stride < 1 || c->head_stride < 1 || c->page_stride % 8 != 0 ||
       c->token_stride % 8 != 0 || c->head_stride % 8 != 0)
     return "cache strides must be positive multiples of 8 elements";
-  // one stride of 2^39 elements is the most a tensor map's 40-bit byte stride
-  // takes; no GPU holds a pool near it
-  if (c->page_stride >= (int64_t(1) << 38) || c->token_stride >= (int64_t(1) << 38) ||
-      c->head_stride >= (int64_t(1) << 38))
+  if (c->page_stride >= kMaxStride || c->token_stride >= kMaxStride ||
+      c->head_stride >= kMaxStride)
     return "cache stride out of range";
   *st = MOE_EUNSUPPORTED;
   if (c->dtype == MOE_F32) return "the cache holds bf16 or fp16";
@@ -137,8 +138,9 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_attn_desc* attn, cons
   auto bad = [&](const char* why) { return moe::refuse(MOE_EINVAL, fn, why); };
   if (n_requests < 1 || n_requests > MOE_MAX_REQUESTS) return bad("n_requests out of range");
   if (n_tokens < 0 || max_blocks < 1) return bad("n_tokens or max_blocks out of range");
-  if (q_token_stride < 0 || q_head_stride < 0 || q_token_stride % 8 != 0 || q_head_stride % 8 != 0)
-    return bad("q strides must be multiples of 8 elements");
+  if (q_token_stride < 1 || q_head_stride < 1 || q_token_stride % 8 != 0 ||
+      q_head_stride % 8 != 0 || q_token_stride >= kMaxStride || q_head_stride >= kMaxStride)
+    return bad("q strides must be positive multiples of 8 elements");
   // rows of out must not overlap: either order of tokens and heads
   const int64_t D = cache->head_dim, H = attn->n_heads;
   const bool heads_in = out_head_stride >= D && (n_tokens < 2 || out_token_stride >= H * out_head_stride);
