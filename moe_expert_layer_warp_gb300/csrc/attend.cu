@@ -30,14 +30,15 @@
 // from them by itself.
 //
 // Warps (one CTA per SM):
-//   0-3    softmax of stream 0, one thread per row, and its results out
-//   4-7    the same for stream 1
-//   8      TMA: key and value tiles into a ring, a box per page and 64 columns
-//   10     TMA: query tiles into two slots, the next as soon as one is free
-//   9, 11  MMA issue of stream 0 and of stream 1 (one warp for both could not
-//          keep up: the waits, issues and commits of a key tile took it 3900
-//          cycles, the products themselves take 2048); they also clear value
-//          rows that no row of the item sees
+//   0-3    softmax of stream 0 over the first 64 keys of a tile, one thread per
+//          row, and a share of its results out
+//   4-7    the same over the last 64 keys; the two halves agree on a row's
+//          maximum through shared memory
+//   8-15   the same for stream 1
+//   16     TMA: key and value tiles into a ring, a box per page and 64 columns
+//   18     TMA: query tiles into two slots, the next as soon as one is free
+//   17, 19 MMA issue of stream 0 and of stream 1; they also clear value rows
+//          that no row of the item sees
 #include <limits.h>
 #include <math.h>
 #include <string.h>
@@ -51,7 +52,8 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 128;        // rows of a query tile, keys of a key tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kHalf = kTile / 2;  // keys of one softmax thread
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 constexpr int kPlanThreads = 256;
 constexpr int kPerThread = MOE_MAX_REQUESTS / kPlanThreads;
@@ -61,9 +63,9 @@ constexpr int kItemCost = 2;
 // than this (in powers of two): until then weights are up to 2^8 instead of
 // 1, which fp32 sums and both 16-bit types hold, and O needs no rescaling.
 constexpr float kGrow = 8.f;
-// Registers per thread: launched with 168, the softmax warps take 216 and the
-// others leave 72 (2·216 + 72 = 3·168).
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+// Registers per thread: launched with 96, the 16 softmax warps take 104 and
+// the 4 others leave 64 (4·104 + 64 = 5·96).
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 
 template <int kDim>
 struct Sizes {
@@ -435,7 +437,7 @@ struct Misc {
   int abort_flag;
 };
 static_assert(sizeof(Misc) <= 512, "misc words");
-constexpr int kOffStat = 512;  // then [2 streams][m, Σ][128 rows] floats
+constexpr int kOffStat = 512;  // then [2 streams][2][128 rows] floats
 
 template <int kDim, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Params p) {
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(&m.q_full[s], 1);
       mbar_init(&m.q_empty[s], 2);
       mbar_init(&m.s_full[s], 1);
-      mbar_init(&m.p_full[s], 4);
+      mbar_init(&m.p_full[s], 8);
       mbar_init(&m.o_full[s], 1);
       mbar_init(&m.turn[s], 1);
       mbar_init(&m.drain[s], 1);
@@ -474,8 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     m.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) umma::tmem_alloc(&m.tmem, kCols);
-  if (threadIdx.x == 8 * 32) {
+  if (warp == 17) umma::tmem_alloc(&m.tmem, kCols);
+  if (threadIdx.x == 16 * 32) {
     prefetch_tmap(&p.kmap);
     prefetch_tmap(&p.vmap);
   }
@@ -500,10 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   };
   Part pt;
 
-  if (warp >= 8) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------- loader --
     Walker walk(p, m.start.w);
     const int page = 1 << p.page_shift;
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       for (int i = 0; i < kStages; ++i)
         for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_for(&m.full[i], ph, a.err, 0xA31, 1000000ull);
     }
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ------------------------------------------------------------ queries --
     // a box is the 128 / group tokens of a tile, times the group's heads, in
     // the order of the tile's rows
@@ -596,14 +598,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       for (int i = 0; i < 2; ++i)
         for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_for(&m.q_full[i], ph, a.err, 0xA61, 1000000ull);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     // ---------------------------------------------------------------- MMA --
     // Both warps follow every tile of the ring and of the query slots, in
     // order: a barrier tells only the parity of its phase, so a warp that
     // passed over a tile could take an older phase for the one it wants. A
     // tile that is the other stream's alone is released as soon as it is there.
     Walker walk(p, m.start.w);
-    const int s = (warp - 9) >> 1;                     // stream
+    const int s = (warp - 17) >> 1;                    // stream
     const uint32_t id_s = umma::idesc_f16(kTile, kTile, kF16, false);
     const uint32_t id_o = umma::idesc_f16(kTile, kDim, kF16, true);
     const uint32_t q_lo = umma::desc_lo(smem_addr(smem), 0);
@@ -729,17 +731,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     Walker walk(p, m.start.w);
-    const int s = warp >> 2;               // stream
-    const int row = threadIdx.x & 127;     // row of the tile, TMEM lane
-    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // 32·(warp % 4) in the upper half
-    const uint32_t s_addr = tmem + lane_base + s * 128;
-    const uint32_t o_addr = tmem + lane_base + 256 + s * 128;
+    const int s = warp >> 3, half = warp >> 2 & 1;  // stream, and half of a tile's keys
+    const int row = threadIdx.x & 127;               // row of the tile, TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32·(warp % 4) in the upper half
+    const uint32_t s_addr = lanes + s * 128 + half * kHalf;
+    const uint32_t p_addr = lanes + s * 128 + half * (kHalf / 2);
+    const uint32_t o_addr = lanes + 256 + s * 128;
     const float to_log2 = a.scale * 1.4426950408889634f;
     const uint64_t to_log2_2 = pair_f(to_log2, to_log2);
     // fp16 weights are held 2^4 larger, so that small ones keep their bits
     const float offset = kF16 ? 4.f : 0.f;
     const int t_in = row / a.group, g_in = row - t_in * a.group;
     float* stat = reinterpret_cast<float*>(smem + Z::kOffMisc + kOffStat);
+    float* mine = stat + (2 * s + half) * kTile + row;
+    const float* theirs = stat + (2 * s + (half ^ 1)) * kTile + row;
+    // the two warps of the same rows
+    auto pair_sync = [&]() {
+      asm volatile("bar.sync %0, 64;" ::"r"(3 + 4 * s + (warp & 3)) : "memory");
+    };
     uint32_t s_phase = 0, o_phase = 0;
     while (walk.next(&pt)) {
       const Item& it = pt.it;
@@ -757,43 +766,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       float ref = -INFINITY, sum = 0.f;
       bool began = false;
       for (int j = two ? 0 : s; j < n; j += two ? 1 : 2) {
-        const int key0 = tile_of(it, pt.t0 + j) * kTile;
+        int key0 = tile_of(it, pt.t0 + j) * kTile;
         if (!(key0 < s_hi && (key0 >= s_lo || key0 < a.sinks))) continue;
+        key0 += half * kHalf;                        // this thread's keys
         wait(&m.s_full[s], s_phase, 0xA51);
         s_phase ^= 1u;
-        if (ok && warp_valid) {
+        // (a lost wait leaves the sums wrong, and the barriers in step)
+        if (warp_valid) {
           umma::fence_after_sync();
-          uint32_t x[kTile];
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) umma::ld_x32(s_addr + c, x + c);
+          uint32_t x[kHalf];
+          umma::ld_x32(s_addr, x);
+          umma::ld_x32(s_addr + 32, x + 32);
           umma::wait_ld();
           const bool whole =
-              !valid || (key0 + kTile <= hi && (key0 >= lo || key0 + kTile <= a.sinks));
+              !valid || (key0 + kHalf <= hi && (key0 >= lo || key0 + kHalf <= a.sinks));
           if (!__all_sync(0xffffffffu, whole)) {
             const int e_hi = hi - key0, e_lo = lo - key0, e_sk = a.sinks - key0;
 #pragma unroll
-            for (int c = 0; c < kTile; ++c)
+            for (int c = 0; c < kHalf; ++c)
               if (!(c < e_hi && (c >= e_lo || c < e_sk))) x[c] = 0xff800000u;  // −inf
           }
           float t4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) t4[i] = __uint_as_float(x[i]);
 #pragma unroll
-          for (int c = 4; c + 8 <= kTile; c += 8)
+          for (int c = 4; c + 8 <= kHalf; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               t4[i] = max3(t4[i], __uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1]));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(x[kTile - 4 + i]));
-          const float top = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]) * to_log2;
+          for (int i = 0; i < 4; ++i) t4[i] = fmaxf(t4[i], __uint_as_float(x[kHalf - 4 + i]));
+          const float own = fmaxf(max3(t4[0], t4[1], t4[2]), t4[3]);
+          *mine = own;
+          // behind this, the other half's maximum is there, and both halves
+          // have read the scores that the weights replace
+          pair_sync();
+          const float top = fmaxf(own, *theirs) * to_log2;
           const bool grown = top > ref + kGrow;
-          if (__any_sync(0xffffffffu, grown)) {
+          if (__any_sync(0xffffffffu, grown)) {      // the same in both warps
             const float keep = grown ? exp2_approx(ref - top) : 1.f;
             if (grown) ref = top;
             sum *= keep;
             if (began) {
 #pragma unroll 1
-              for (int c = 0; c < kDim; c += 32) {
+              for (int c = half * (kDim / 2); c < (half + 1) * (kDim / 2); c += 32) {
                 uint32_t o[32];
                 umma::ld_x32(o_addr + c, o);
                 umma::wait_ld();
@@ -807,16 +823,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const uint64_t shift_2 = pair_f(shift, shift);
           uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int c = 0; c < kTile; c += 2) {
+          for (int c = 0; c < kHalf; c += 2) {
             float p0, p1;
             split(fma2(pair(x[c], x[c + 1]), to_log2_2, shift_2), &p0, &p1);
             p0 = exp2_approx(p0);
             p1 = exp2_approx(p1);
             sums[(c >> 1) & 3] = add2(sums[(c >> 1) & 3], pair_f(p0, p1));
             x[c >> 1] = narrow<kF16>(p0, p1);
-            if (c == kTile / 2 - 2) umma::st_x32(s_addr, x);
           }
-          umma::st_x32(s_addr + 32, x + 32);
+          umma::st_x32(p_addr, x);
           float s0, s1;
           split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), &s0, &s1);
           sum += s0 + s1;
@@ -828,28 +843,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&m.p_full[s]);
       }
       // ---- results out
-      if (!two) {
-        stat[s * 256 + row] = ref;
-        stat[s * 256 + 128 + row] = sum;
-      }
       if (began) {
         wait(&m.o_full[s], o_phase, 0xA52);
         o_phase ^= 1u;
       }
+      // the halves' sums, then (one query tile) both streams' statistics; the
+      // other half has read the last maximum: O is complete, its weights are in
+      *mine = sum;
+      pair_sync();
+      sum += *theirs;
+      pair_sync();
+      if (!two) *mine = half == 0 ? ref : sum;
       const bool ends = pt.t1 == it.n, whole_item = ends && pt.t0 == 0;
       // factors of the two streams' O, and this thread's columns
       float f0 = 1.f, f1 = 0.f;
-      int c_first = 0, c_end = kDim;
+      int c_first = half * (kDim / 2), c_end = c_first + kDim / 2;
       if (!two) {
-        // both streams hold sums of the same rows: each joins half the columns
-        asm volatile("bar.sync 2, 256;" ::: "memory");
-        const float ref0 = stat[row], ref1 = stat[256 + row];
+        // both streams hold sums of the same rows: every warp of a row joins
+        // its share of the columns, 32 at least
+        asm volatile("bar.sync 2, 512;" ::: "memory");
+        const float ref0 = stat[row], ref1 = stat[2 * kTile + row];
         ref = fmaxf(ref0, ref1);
         f0 = ref0 == -INFINITY ? 0.f : exp2_approx(ref0 - ref);
         f1 = ref1 == -INFINITY ? 0.f : exp2_approx(ref1 - ref);
-        sum = stat[128 + row] * f0 + stat[256 + 128 + row] * f1;
-        c_first = s * (kDim / 2);
-        c_end = c_first + kDim / 2;
+        sum = stat[kTile + row] * f0 + stat[3 * kTile + row] * f1;
+        c_first = kDim == 128 ? 64 * half + 32 * s : 32 * s;
+        c_end = kDim == 128 || half == 0 ? c_first + 32 : c_first;
       }
       umma::fence_after_sync();
       if (ok && warp_valid) {
@@ -862,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // number to be scaled
         const bool any0 = f0 > 0.f && sum > 0.f, any1 = f1 > 0.f;
         const bool warp_any1 = __any_sync(0xffffffffu, any1);
-        const uint32_t from = tmem + lane_base + 256 + (two ? s * 128 : 0);
+        const uint32_t from = lanes + 256 + (two ? s * 128 : 0);
         // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
         const uint64_t dst = reinterpret_cast<uint64_t>(
             static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
@@ -876,13 +895,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const int prow = (two ? s * kTile : 0) + row;
 #pragma unroll 1
         for (int c = c_first; c < c_end; c += 32) {
-          uint32_t o[32], o1[32];
+          uint32_t o[32];
           umma::ld_x32(from + c, o);
-          if (warp_any1) umma::ld_x32(from + 128 + c, o1);
           umma::wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = any0 ? __float_as_uint(__uint_as_float(o[i]) * f0) : 0u;
           if (warp_any1) {
+            uint32_t o1[32];
+            umma::ld_x32(from + 128 + c, o1);
+            umma::wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (any1)
@@ -911,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                   make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (valid && !whole_item && (two || s == 0)) {
+        if (valid && !whole_item && half == 0 && (two || s == 0)) {
           float* st = slot + (size_t)2 * kTile * kDim;
           st[prow] = ref;
           st[2 * kTile + prow] = sum;
@@ -919,12 +940,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       // joined O and statistics have been read before either stream goes on
       umma::fence_before_sync();
-      if (!two) asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (two) {
+        pair_sync();
+      } else {
+        asm volatile("bar.sync 2, 512;" ::: "memory");
+      }
     }
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == 9) umma::tmem_dealloc(tmem, kCols);
+  if (warp == 17) umma::tmem_dealloc(tmem, kCols);
 }
 
 // ------------------------------------------------------------------ join --
