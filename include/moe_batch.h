@@ -179,8 +179,9 @@ typedef struct {
  * score 0, choice −inf; it is kept, with weight 0, only when a token has
  * fewer than k others in its groups. If every kept score is 0 the weights
  * are 0. +inf and NaN logits are not supported (the indices stay in range).
- * The selection is that of exact arithmetic: where two choices lie closer
- * than fp32 resolves, they are compared in fp64.
+ * The selection is that of exact arithmetic: without a bias experts compare
+ * by their logits, and where two choices or group sums lie closer than fp32
+ * resolves, they are compared in fp64.
  *   logits    [n][E] of `dtype` (MOE_F32, MOE_BF16, MOE_F16), rows row_stride
  *             apart (row_stride ≥ E), aligned to their type.
  *   bias      [E] fp32 finite, or NULL.

@@ -116,7 +116,11 @@ def route(logits, bias, topk, groups, top_groups, group_top, score, renorm, scal
                 for g in range(groups)]
         kept = sorted(range(groups), key=lambda g: (-best[g], g))[:top_groups]
         pool = [e for g in kept for e in range(g * size, (g + 1) * size)]
-        chosen = sorted(pool, key=lambda e: (-c[e], e))[:topk]
+        # without a bias the order of the choices is that of the logits, which
+        # no exponential's underflow can hide
+        order = (lambda e: (-c[e], e)) if bias is not None else (
+            lambda e: (off[t, e], -x[t, e] if not off[t, e] else 0.0, e))
+        chosen = sorted(pool, key=order)[:topk]
         w = np.array([s[e] for e in chosen])
         if renorm:
             w = w / w.sum() if w.sum() > 0 else 0 * w
