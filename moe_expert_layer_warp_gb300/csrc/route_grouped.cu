@@ -8,11 +8,13 @@
 // comparisons of c (and of sums of two c), and what is asked for is the
 // selection of exact arithmetic. fp32 decides almost every comparison: a
 // value computed here is off by at most a bound that is known, so a
-// difference larger than the two bounds has the right sign. Only a token
-// with a closer one is done again in fp64 (a few in ten thousand, with
-// trained routers' spreads); doing all of them there took 848 us for 20011
-// tokens of 256 experts, fp64 being 1/64 of fp32's rate. Without a bias, c is
-// monotone in the logit, and experts are compared by their logits, exactly.
+// difference larger than the two bounds has the right sign. Closer ones (a
+// few tokens in ten thousand, with trained routers' spreads) are decided in
+// fp64, whose rate is 1/64 of fp32's: by the choices of the few experts in
+// question, one in a lane, and only where that does not settle it by all of
+// the token's. (Everything in fp64 took 848 us for 20011 tokens of 256
+// experts; close tokens whole in fp64, 81 us.) Without a bias, c is monotone
+// in the logit, and experts are compared by their logits, exactly.
 #include <math.h>
 
 #include "batch_launch.h"
@@ -190,6 +192,36 @@ __device__ __noinline__ void route_exact(const moe_router_desc& r, const T* row,
   *weight = (float)(w * r.scale);
 }
 
+// Order-preserving integer key of a double.
+MOE_DEV unsigned long long order_key64(double f) {
+  const long long u = __double_as_longlong(f == 0.0 ? 0.0 : f);
+  return u < 0 ? ~(unsigned long long)u : (unsigned long long)u | 0x8000000000000000ull;
+}
+
+// What fp64 needs of a row for a softmax: its maximum and sum.
+struct RowSum {
+  double top, sum;
+};
+template <typename T>
+__device__ __noinline__ RowSum row_sum64(const T* row, int E) {
+  const int lane = threadIdx.x & 31;
+  RowSum q{-INFINITY, 0.0};
+  for (int e = lane; e < E; e += 32) q.top = fmax(q.top, (double)load_logit(row + e));
+  q.top = warp_max(q.top);
+  for (int e = lane; e < E; e += 32) {
+    const double l = load_logit(row + e);
+    if (l != -INFINITY) q.sum += exp(l - q.top);
+  }
+  q.sum = warp_add(q.sum);
+  return q;
+}
+
+// The choice of one expert in fp64 (−inf for a masked one).
+__device__ __noinline__ double choice64(float x, float bias, bool sigmoid, RowSum q) {
+  if (x == -INFINITY) return -INFINITY;
+  return (sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - q.top) / q.sum) + (double)bias;
+}
+
 // exp of a non-positive or moderate argument by the hardware's base-2
 // exponential: x·log2(e) is rounded (|x|·2^-24·1.45 of an exponent step at
 // most) and the exponential itself is good to 2^-22, so the result is off by
@@ -315,20 +347,64 @@ __global__ void __launch_bounds__(kWarps * 32)
       const float other = __shfl_sync(kAll, mine, o * share);
       if (other > mine || (other == mine && o < g)) ++before;
     }
-    const bool keep = g < G && before < r.top_groups;
+    bool keep = g < G && before < r.top_groups;
     // Group sums compare only by a margin. A score is off by less than
-    // 2^-19.4: s·|x| ≤ 0.37 for a softmax's x = l − top, s·(1 − s)·|x| ≤ 0.23
+    // 2^-19.4: s·|x| ≤ 0.37 for a softmax's x = l − top, s·(1 − s)·|x| ≤ 0.28
     // for a sigmoid, and the rest is relative to s ≤ 1; four scores make
     // 2^-17.4. Roundings of c and of the sums go by the largest |a| + |b|.
     if (!by_logit || r.group_top == 2) {
       const float size_ab = (a == -INFINITY ? 0.f : fabsf(a)) + (b == -INFINITY ? 0.f : fabsf(b));
       const float largest =
           __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(g < G ? size_ab : 0.f)));
-      const float worst_kept = key_value(__reduce_min_sync(kAll, keep ? order_key(mine) : 0xff800000u));
+      const float worst_kept =
+          key_value(__reduce_min_sync(kAll, keep ? order_key(mine) : 0xff800000u));
       const float best_left =
           key_value(__reduce_max_sync(kAll, g < G && !keep ? order_key(mine) : 0x007fffffu));
       const float margin = 0x1p-17f + largest * 0x1p-21f;
-      if (worst_kept != -INFINITY && !(worst_kept - best_left > margin)) unsure = true;
+      if (worst_kept != -INFINITY && !(worst_kept - best_left > margin)) {
+        // the groups' sums in fp64, a group in a lane: its two best choices,
+        // if they are its two best for certain
+        float c1 = -INFINITY, c2 = -INFINITY, c3 = -INFINITY;
+        int e1 = 0, e2 = 0;
+        if (lane < G) {
+          for (int i = 0; i < size; ++i) {
+            const int e = lane * size + i;
+            const float c = choice[warp][e + (e >> 5)];
+            if (c > c1) {
+              c3 = c2;
+              c2 = c1;
+              e2 = e1;
+              c1 = c;
+              e1 = e;
+            } else if (c > c2) {
+              c3 = c2;
+              c2 = c;
+              e2 = e;
+            } else {
+              c3 = fmaxf(c3, c);
+            }
+          }
+        }
+        const float next = r.group_top == 2 ? c3 : c2, last = r.group_top == 2 ? c2 : c1;
+        unsure |= __any_sync(kAll, next != -INFINITY && !(last - next > margin));
+        const RowSum q = sigmoid ? RowSum{0.0, 0.0} : row_sum64(row, E);
+        double sum = -INFINITY;
+        if (c1 != -INFINITY) {
+          sum = choice64(load_logit(row + e1), bias ? bias[e1] : 0.f, sigmoid, q);
+          if (r.group_top == 2)
+            sum = c2 == -INFINITY ? -INFINITY
+                                  : sum + choice64(load_logit(row + e2), bias ? bias[e2] : 0.f,
+                                                   sigmoid, q);
+        }
+        const unsigned long long mine64 = order_key64(sum);
+        int rank = 0;
+        for (int o = 0; o < G; ++o) {
+          const unsigned long long other = __shfl_sync(kAll, mine64, o);
+          if (other > mine64 || (other == mine64 && o < lane)) ++rank;
+        }
+        const uint32_t kept64 = __ballot_sync(kAll, lane < G && rank < r.top_groups);
+        keep = g < G && ((kept64 >> g) & 1u);
+      }
     }
     const uint32_t kept = __ballot_sync(kAll, keep && sub == 0);
 #pragma unroll
@@ -338,11 +414,11 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
 
-  // k + 1 rounds: the largest key left, of equal ones the lowest expert's;
-  // round j's expert ends in lane j (the last is only for the comparison)
+  // rounds: the largest key left, of equal ones the lowest expert's; round
+  // j's expert ends in lane j
   uint32_t my_key = 0u;
   int my_e = 0;
-  for (int j = 0; j <= k; ++j) {
+  auto round = [&](int j) {
     uint32_t best = key[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
@@ -362,24 +438,67 @@ __global__ void __launch_bounds__(kWarps * 32)
       my_key = most;
       my_e = most ? e : 0;
     }
-  }
+  };
+  for (int j = 0; j < k; ++j) round(j);
+  if (!by_logit) round(k);                 // the best one left out, for the comparison
   // the chosen experts' scores, accurately
-  const bool mine = lane <= k && my_key != 0u;
-  const float x = mine ? load_logit(row + my_e) : -INFINITY;
-  const float s = x == -INFINITY ? 0.f : sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) * inv;
+  auto score_of = [&](float x) {
+    return x == -INFINITY ? 0.f : sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) * inv;
+  };
+  float x = my_key != 0u ? load_logit(row + my_e) : -INFINITY;
+  float s = score_of(x);
   if (!by_logit) {
-    // neighbours in the order must differ by more than their bounds, or be
-    // equal in logit and bias: then the index decides, here as exactly
-    const float b = mine ? __ldg(bias + my_e) : 0.f;
+    // Neighbours in the order must differ by more than their bounds — for a
+    // sigmoid s·((1 − s)·(|x|·2^-23.4 + 2^-22) + 2^-23), (1 − s)·|x| ≤ 0.28
+    // for x > 0 and s·|x| ≤ 0.28 for x < 0; for a softmax
+    // s·(|x|·2^-23.4 + 2^-19.4) — or be equal in logit and bias: then the
+    // index decides, here as exactly.
+    auto bound = [&](float v_s, float v_x, float v_c) {
+      return (sigmoid ? v_s * 0x1p-21f + fmaxf(-v_x, 0.f) * v_s * 0x1p-23f
+                      : v_s * (fabsf(v_x - top) * 0x1p-23f + 0x1p-19f)) +
+             fabsf(v_c) * 0x1p-23f;
+    };
+    float b = my_key != 0u ? __ldg(bias + my_e) : 0.f;
     const float c = key_value(my_key);
-    const float off =
-        s * (fabsf(sigmoid ? x : x - top) + 16.f) * 0x1p-22f + fabsf(c) * 0x1p-23f;
+    const float off = my_key != 0u && x != -INFINITY ? bound(s, x, c) : 0.f;
     const float x2 = __shfl_down_sync(kAll, x, 1), b2 = __shfl_down_sync(kAll, b, 1);
     const float c2 = __shfl_down_sync(kAll, c, 1), off2 = __shfl_down_sync(kAll, off, 1);
-    const uint32_t key2 = __shfl_down_sync(kAll, my_key, 1);
-    const bool close = lane < k && key2 != 0u && x2 != -INFINITY && !(c - c2 > off + off2) &&
+    const bool close = lane < k && x2 != -INFINITY && !(c - c2 > off + off2) &&
                        !(x == x2 && b == b2);
-    unsure |= __any_sync(kAll, close);
+    if (__any_sync(kAll, close)) {
+      // Every expert that may belong to the k, one in a lane: those whose
+      // choice is not certainly below the k-th. Then by fp64.
+      const float c_k = __shfl_sync(kAll, c, k - 1), off_k = __shfl_sync(kAll, off, k - 1);
+      const float off_max = (sigmoid ? 0x1p-20f : 0x1p-18f) + fabsf(c_k) * 0x1p-22f;
+      int count = k + 1;
+      for (; count < 32; ++count) {
+        const uint32_t last = __shfl_sync(kAll, my_key, count - 1);
+        if (last == 0u || c_k - key_value(last) > off_k + off_max) break;
+        round(count);
+      }
+      if (count == 32) unsure = true;      // too many to tell here
+      x = my_key != 0u ? load_logit(row + my_e) : -INFINITY;
+      b = my_key != 0u ? __ldg(bias + my_e) : 0.f;
+      const RowSum q = sigmoid ? RowSum{0.0, 0.0} : row_sum64(row, E);
+      const unsigned long long mine64 =
+          my_key != 0u ? order_key64(choice64(x, b, sigmoid, q)) : 0ull;
+      int rank = 0;
+      for (int o = 0; o < 32; ++o) {
+        const unsigned long long other = __shfl_sync(kAll, mine64, o);
+        const int e_o = __shfl_sync(kAll, my_e, o);
+        if (other > mine64 || (other == mine64 && other != 0ull && e_o < my_e)) ++rank;
+      }
+      // rank j's expert to lane j
+      int e_new = 0;
+      for (int o = 0; o < 32; ++o) {
+        const int r_o = __shfl_sync(kAll, rank, o), e_o = __shfl_sync(kAll, my_e, o);
+        const uint32_t key_o = __shfl_sync(kAll, my_key, o);
+        if (r_o == lane && key_o != 0u) e_new = e_o;
+      }
+      my_e = e_new;
+      x = lane < k ? load_logit(row + my_e) : -INFINITY;
+      s = score_of(x);
+    }
   }
   // sigmoids that fp32 cannot hold, of which quotients are wanted
   if (sigmoid && r.renorm && lane < k && x != -INFINITY && s < 0x1p-100f) unsure = true;
