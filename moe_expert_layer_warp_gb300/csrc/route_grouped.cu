@@ -15,6 +15,7 @@
 // the token's. (Everything in fp64 took 848 us for 20011 tokens of 256
 // experts; close tokens whole in fp64, 81 us.) Without a bias, c is monotone
 // in the logit, and experts are compared by their logits, exactly.
+#include <limits.h>
 #include <math.h>
 
 #include "batch_launch.h"
@@ -51,16 +52,14 @@ MOE_DEV float load_logit(const T* p) {
   return v <= lowest<T>() ? -INFINITY : v;
 }
 
-// Order-preserving integer keys of floats (−0 and +0 have one key; 0 is below
-// every float's key).
-MOE_DEV uint32_t order_key(float f) {
-  uint32_t u = __float_as_uint(f);
-  if ((u << 1) == 0u) u = 0u;
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+// Order-preserving integer keys of floats (−0 and +0 have one key); kNone is
+// below every float's key.
+constexpr int kNone = INT_MIN;
+MOE_DEV int order_key(float f) {
+  const int u = __float_as_int(f + 0.f);
+  return u ^ ((u >> 31) & 0x7fffffff);
 }
-MOE_DEV float key_value(uint32_t key) {
-  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
-}
+MOE_DEV float key_value(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7fffffff)); }
 
 MOE_DEV double warp_max(double v) {
 #pragma unroll
@@ -232,17 +231,34 @@ MOE_DEV float exp_fast(float x) {
   return y;
 }
 
-// One warp per token; lane holds kPer consecutive experts, so that a lower
-// lane is a lower expert.
+MOE_DEV float reciprocal_fast(float x) {  // good to 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The descriptor, and what follows from it.
+struct Router {
+  moe_router_desc d;
+  int size;         // experts of a group
+  int to_group;     // e / size = e·to_group >> 16, for e < 256
+  int share_shift;  // log2 of the lanes that look through one group
+  int wide;         // rows are whole, aligned 16-byte pieces
+};
+
+// One warp per token; lane holds kPer consecutive experts.
 template <typename T, int kPer>
 __global__ void __launch_bounds__(kWarps * 32)
-    route_grouped_kernel(const __grid_constant__ moe_router_desc r, const T* __restrict__ logits,
-                         int64_t row_stride, const float* __restrict__ bias, int n, int wide,
+    route_grouped_kernel(const __grid_constant__ Router p, const T* __restrict__ logits,
+                         int64_t row_stride, const float* __restrict__ bias, int n,
                          int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
   // choices of the warp's token, one float of padding after every 32
   __shared__ float choice[kWarps][32 * kPer + kPer];
+  // the experts that may be among the k, with their keys; then by rank
+  __shared__ int2 cand[kWarps][32];
   pdl_wait();
   pdl_trigger();
+  const moe_router_desc& r = p.d;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kWarps + warp;
   if (t >= n) return;
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const bool grouped = r.top_groups < r.n_groups;
 
   float l[kPer];
-  if (wide) {                              // rows of whole, aligned 16-byte pieces
+  if (p.wide) {
     constexpr int kVec = 16 / sizeof(T) < kPer ? 16 / sizeof(T) : kPer;
 #pragma unroll
     for (int v = 0; v < kPer; v += kVec) {
@@ -294,23 +310,22 @@ __global__ void __launch_bounds__(kWarps * 32)
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
 
-  // what experts are compared by, as keys; 0: not to be chosen
-  uint32_t key[kPer];
+  // what experts are compared by, as keys
+  int key[kPer];
   bool unsure = false;
   if (by_logit) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = lane * kPer + i < E ? order_key(l[i]) : 0u;
+    for (int i = 0; i < kPer; ++i) key[i] = lane * kPer + i < E ? order_key(l[i]) : kNone;
   }
   if (!by_logit || (grouped && r.group_top == 2)) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = lane * kPer + i;
-      // off by at most s·(|x| + 16)·2^-22, x = l or l − top (for a softmax the
-      // sum adds its own errors, 13 roundings and 2^-22 of each term)
-      const float s = sigmoid ? __frcp_rn(1.f + exp_fast(-l[i])) : exp_fast(l[i] - top) * inv;
+      const float s =
+          sigmoid ? reciprocal_fast(1.f + exp_fast(-l[i])) : exp_fast(l[i] - top) * inv;
       float c = -INFINITY;
       if (e < E && l[i] != -INFINITY) c = by_logit ? s : s + __ldg(bias + e);
-      if (!by_logit) key[i] = e < E ? order_key(c) : 0u;
+      if (!by_logit) key[i] = e < E ? order_key(c) : kNone;
       if (grouped) choice[warp][e + (e >> 5)] = c;
     }
   } else if (grouped) {                    // groups by their largest logit
@@ -323,10 +338,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   if (grouped) {
     __syncwarp();
-    // `share` lanes per group, a power of two
-    const int G = r.n_groups, size = E / G;
-    const int share = 1 << (31 - __clz(32 / G));
-    const int g = lane / share, sub = lane & (share - 1);
+    const int G = r.n_groups, size = p.size, share = 1 << p.share_shift;
+    const int g = lane >> p.share_shift, sub = lane & (share - 1);
     float a = -INFINITY, b = -INFINITY;    // best and second best
     if (g < G) {
       for (int i = sub; i < size; i += share) {
@@ -344,8 +357,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     const float mine = g < G ? (r.group_top == 2 ? a + b : a) : -INFINITY;
     int before = 0;
     for (int o = 0; o < G; ++o) {
-      const float other = __shfl_sync(kAll, mine, o * share);
-      if (other > mine || (other == mine && o < g)) ++before;
+      const float other = __shfl_sync(kAll, mine, o << p.share_shift);
+      before += other > mine || (other == mine && o < g);
     }
     bool keep = g < G && before < r.top_groups;
     // Group sums compare only by a margin. A score is off by less than
@@ -357,9 +370,9 @@ __global__ void __launch_bounds__(kWarps * 32)
       const float largest =
           __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(g < G ? size_ab : 0.f)));
       const float worst_kept =
-          key_value(__reduce_min_sync(kAll, keep ? order_key(mine) : 0xff800000u));
+          key_value(__reduce_min_sync(kAll, keep ? order_key(mine) : order_key(INFINITY)));
       const float best_left =
-          key_value(__reduce_max_sync(kAll, g < G && !keep ? order_key(mine) : 0x007fffffu));
+          key_value(__reduce_max_sync(kAll, order_key(g < G && !keep ? mine : -INFINITY)));
       const float margin = 0x1p-17f + largest * 0x1p-21f;
       if (worst_kept != -INFINITY && !(worst_kept - best_left > margin)) {
         // the groups' sums in fp64, a group in a lane: its two best choices,
@@ -410,93 +423,115 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = lane * kPer + i;
-      if (e < E && !((kept >> (e / size * share)) & 1u)) key[i] = 0u;
+      if (!((kept >> ((e * p.to_group >> 16) << p.share_shift)) & 1u)) key[i] = kNone;
     }
   }
 
-  // rounds: the largest key left, of equal ones the lowest expert's; round
-  // j's expert ends in lane j
-  uint32_t my_key = 0u;
-  int my_e = 0;
-  auto round = [&](int j) {
-    uint32_t best = key[0];
+  // At least k + 1 experts are no worse than the (k + 1)-th best of the lanes'
+  // best ones, and few more: they go one to a lane and are ranked against
+  // each other. Beside a bias, those that lie below it by no more than the
+  // choices may be off come along.
+  auto best_below = [&](int limit) {       // this lane's largest key under `limit`
+    int m = kNone;
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) best = max(best, key[i]);
-    const uint32_t most = __reduce_max_sync(kAll, best);
-    const int from = __ffs(__ballot_sync(kAll, best == most)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int i = kPer - 1; i >= 0; --i)
-      if (key[i] == most) at = i;
-    if (lane == from) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == at) key[i] = 0u;
-    }
-    const int e = __shfl_sync(kAll, lane * kPer + at, from);
-    if (lane == j) {
-      my_key = most;
-      my_e = most ? e : 0;
-    }
+    for (int i = 0; i < kPer; ++i) m = max(m, key[i] < limit ? key[i] : kNone);
+    return m;
   };
-  for (int j = 0; j < k; ++j) round(j);
-  if (!by_logit) round(k);                 // the best one left out, for the comparison
+  int best = best_below(INT_MAX);
+  // (with experts left in k lanes or fewer, a lane's next best takes its turn)
+  const bool few = __popc(__ballot_sync(kAll, best != kNone)) <= k;
+  int least = kNone;
+  for (int j = 0; j <= k; ++j) {
+    least = __reduce_max_sync(kAll, best);
+    if (best == least) best = few ? best_below(least) : kNone;
+  }
+  // what a choice near `least` may be off by: see bound() below
+  const float off_max = (sigmoid ? 0x1p-20f : 0x1p-18f) + fabsf(key_value(least)) * 0x1p-22f;
+  if (!by_logit && least > order_key(-INFINITY)) least = order_key(key_value(least) - 2.f * off_max);
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool in = key[i] != kNone && key[i] >= least;
+    const uint32_t who = __ballot_sync(kAll, in);
+    const int at = count + __popc(who & ((1u << lane) - 1u));
+    if (in && at < 32) cand[warp][at] = make_int2(key[i], lane * kPer + i);
+    count += __popc(who);
+  }
+  const bool crowd = count > 32;
+  __syncwarp();
+  if (!crowd) {
+    const int2 my = lane < count ? cand[warp][lane] : make_int2(kNone, 0);
+    int rank = 0;
+    for (int o = 0; o < count; ++o) {
+      const int2 other = cand[warp][o];
+      rank += other.x > my.x || (other.x == my.x && other.y < my.y);
+    }
+    __syncwarp();
+    if (lane < count) cand[warp][rank] = my;
+  } else {
+    // many equal ones: the largest key left k + 1 times, of equal ones the
+    // lowest expert's, which is in the lowest lane
+    count = k + 1;
+    for (int j = 0; j <= k; ++j) {
+      const int mine = best_below(INT_MAX), most = __reduce_max_sync(kAll, mine);
+      const int from = __ffs(__ballot_sync(kAll, mine == most)) - 1;
+      if (lane == from) {
+        int at = 0;
+#pragma unroll
+        for (int i = kPer - 1; i >= 0; --i)
+          if (key[i] == most) at = i;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (i == at) key[i] = kNone;
+        cand[warp][j] = make_int2(most, lane * kPer + at);
+      }
+    }
+  }
+  __syncwarp();
+  const int2 my = lane < count ? cand[warp][lane] : make_int2(kNone, 0);
+  int my_e = my.y;                         // rank j's expert in lane j
+
   // the chosen experts' scores, accurately
   auto score_of = [&](float x) {
     return x == -INFINITY ? 0.f : sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) * inv;
   };
-  float x = my_key != 0u ? load_logit(row + my_e) : -INFINITY;
+  float x = lane < count ? load_logit(row + my_e) : -INFINITY;
   float s = score_of(x);
   if (!by_logit) {
     // Neighbours in the order must differ by more than their bounds — for a
-    // sigmoid s·((1 − s)·(|x|·2^-23.4 + 2^-22) + 2^-23), (1 − s)·|x| ≤ 0.28
-    // for x > 0 and s·|x| ≤ 0.28 for x < 0; for a softmax
-    // s·(|x|·2^-23.4 + 2^-19.4) — or be equal in logit and bias: then the
-    // index decides, here as exactly.
+    // sigmoid s·((1 − s)·(|x|·2^-23.4 + 2^-22) + 2^-22), (1 − s)·|x| ≤ 0.28
+    // for x > 0; for a softmax s·(|x|·2^-23.4 + 2^-19.4) — or be equal in
+    // logit and bias: then the index decides, here as exactly.
     auto bound = [&](float v_s, float v_x, float v_c) {
-      return (sigmoid ? v_s * 0x1p-21f + fmaxf(-v_x, 0.f) * v_s * 0x1p-23f
+      return (sigmoid ? v_s * 0x1.6ap-21f + fmaxf(-v_x, 0.f) * v_s * 0x1p-23f
                       : v_s * (fabsf(v_x - top) * 0x1p-23f + 0x1p-19f)) +
              fabsf(v_c) * 0x1p-23f;
     };
-    float b = my_key != 0u ? __ldg(bias + my_e) : 0.f;
-    const float c = key_value(my_key);
-    const float off = my_key != 0u && x != -INFINITY ? bound(s, x, c) : 0.f;
+    const float b = lane < count ? __ldg(bias + my_e) : 0.f;
+    const float c = key_value(my.x);
+    const float off = lane < count && x != -INFINITY ? bound(s, x, c) : 0.f;
     const float x2 = __shfl_down_sync(kAll, x, 1), b2 = __shfl_down_sync(kAll, b, 1);
     const float c2 = __shfl_down_sync(kAll, c, 1), off2 = __shfl_down_sync(kAll, off, 1);
-    const bool close = lane < k && x2 != -INFINITY && !(c - c2 > off + off2) &&
+    const bool close = lane < k && lane + 1 < count && x2 != -INFINITY && !(c - c2 > off + off2) &&
                        !(x == x2 && b == b2);
-    if (__any_sync(kAll, close)) {
-      // Every expert that may belong to the k, one in a lane: those whose
-      // choice is not certainly below the k-th. Then by fp64.
-      const float c_k = __shfl_sync(kAll, c, k - 1), off_k = __shfl_sync(kAll, off, k - 1);
-      const float off_max = (sigmoid ? 0x1p-20f : 0x1p-18f) + fabsf(c_k) * 0x1p-22f;
-      int count = k + 1;
-      for (; count < 32; ++count) {
-        const uint32_t last = __shfl_sync(kAll, my_key, count - 1);
-        if (last == 0u || c_k - key_value(last) > off_k + off_max) break;
-        round(count);
-      }
-      if (count == 32) unsure = true;      // too many to tell here
-      x = my_key != 0u ? load_logit(row + my_e) : -INFINITY;
-      b = my_key != 0u ? __ldg(bias + my_e) : 0.f;
+    if (!__any_sync(kAll, close)) {
+    } else if (crowd) {
+      unsure = true;                       // others may be as close
+    } else {                               // all candidates by fp64
       const RowSum q = sigmoid ? RowSum{0.0, 0.0} : row_sum64(row, E);
       const unsigned long long mine64 =
-          my_key != 0u ? order_key64(choice64(x, b, sigmoid, q)) : 0ull;
+          lane < count ? order_key64(choice64(x, b, sigmoid, q)) : 0ull;
       int rank = 0;
-      for (int o = 0; o < 32; ++o) {
+      for (int o = 0; o < count; ++o) {
         const unsigned long long other = __shfl_sync(kAll, mine64, o);
         const int e_o = __shfl_sync(kAll, my_e, o);
-        if (other > mine64 || (other == mine64 && other != 0ull && e_o < my_e)) ++rank;
+        rank += other > mine64 || (other == mine64 && e_o < my_e);
       }
-      // rank j's expert to lane j
-      int e_new = 0;
-      for (int o = 0; o < 32; ++o) {
-        const int r_o = __shfl_sync(kAll, rank, o), e_o = __shfl_sync(kAll, my_e, o);
-        const uint32_t key_o = __shfl_sync(kAll, my_key, o);
-        if (r_o == lane && key_o != 0u) e_new = e_o;
-      }
-      my_e = e_new;
-      x = lane < k ? load_logit(row + my_e) : -INFINITY;
+      __syncwarp();
+      if (lane < count) cand[warp][rank].y = my_e;
+      __syncwarp();
+      my_e = cand[warp][lane < count ? lane : 0].y;
+      x = lane < count ? load_logit(row + my_e) : -INFINITY;
       s = score_of(x);
     }
   }
@@ -523,11 +558,17 @@ template <typename T, int kPer>
 cudaError_t launch_t(const moe_router_desc& r, const T* logits, int64_t row_stride,
                      const float* bias, int n, int32_t* topk_idx, float* topk_w,
                      cudaStream_t stream) {
+  Router p;
+  p.d = r;
+  p.size = r.n_experts / r.n_groups;
+  p.to_group = (65536 + p.size - 1) / p.size;
+  p.share_shift = 0;
+  while ((2 << p.share_shift) * r.n_groups <= 32) ++p.share_shift;
   // rows in whole pieces: every lane's experts exist or none does
-  const int wide = r.n_experts % kPer == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 &&
-                   row_stride * sizeof(T) % 16 == 0 && kPer * sizeof(T) % 16 == 0;
+  p.wide = r.n_experts % kPer == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 &&
+           row_stride * sizeof(T) % 16 == 0 && kPer * sizeof(T) % 16 == 0;
   return launch_pdl(route_grouped_kernel<T, kPer>, dim3((n - 1) / kWarps + 1), dim3(kWarps * 32), 0,
-                    stream, r, logits, row_stride, bias, n, wide, topk_idx, topk_w);
+                    stream, p, logits, row_stride, bias, n, topk_idx, topk_w);
 }
 
 template <typename T>

@@ -410,6 +410,8 @@ ROUTERS = {
     "groups by maxima": dict(E=160, k=6, G=8, tg=3, top=1, renorm=False, scale=16.0),
     "groups of one": dict(E=32, k=5, G=32, tg=9, score="sigmoid", bias=True),
     "uneven lanes": dict(E=120, k=12, G=24, tg=11, top=2, score="softmax", bias=True),
+    "one group of many": dict(E=256, k=12, G=8, tg=1, top=2, score="sigmoid", bias=True),
+    "two groups, few lanes": dict(E=256, k=16, G=8, tg=2, top=2, score="softmax", bias=True),
     "every group": dict(E=64, k=3, G=8, tg=8, top=2, score="sigmoid"),
 }
 
@@ -456,6 +458,23 @@ def test_route(lib, name, kind, dtype):
             bias = torch.randn(E, generator=g) * 2.0 ** -24
     _route(lib, x.to(dtype), p["k"], p["G"], p["tg"], p["top"], p["score"], bias, p["renorm"],
            p["scale"])
+
+
+@pytest.mark.parametrize("name", ROUTERS)
+def test_route_equal_logits(lib, name):
+    """Rows of one value (padding) and rows with many equal best ones."""
+    p = dict(dict(G=1, tg=1, top=1, score="softmax", bias=False, renorm=True, scale=1.0),
+             **ROUTERS[name])
+    x = torch.zeros(6, p["E"])
+    x[1] = -3.5
+    x[2:, ::2] = 0.25
+    x[4:, 1::3] = 7.0
+    bias = torch.zeros(p["E"]) if p["bias"] else None
+    _route(lib, x, p["k"], p["G"], p["tg"], p["top"], p["score"], bias, p["renorm"], p["scale"])
+    if p["bias"]:
+        bias[::5] = 0.5
+        _route(lib, x, p["k"], p["G"], p["tg"], p["top"], p["score"], bias, p["renorm"],
+               p["scale"])
 
 
 @pytest.mark.parametrize("n", [1, 2, 1000])
