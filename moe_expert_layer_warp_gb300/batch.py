@@ -29,14 +29,23 @@ import torch
 from . import api
 
 
-def _need(t, name, dtype, shape, device):
+# A call here takes a few microseconds of the GPU at its smallest, so what it
+# does on the host is kept short: checks read each attribute once, C structs
+# and views of the buffers are kept, and the stream is fetched as a handle.
+def _need(t, name, dtype, shape, index):
     """The device pointer of `t`, a contiguous tensor of the given kind."""
-    if (t.dtype != dtype or t.device != device or not t.is_contiguous() or
-            tuple(t.shape) != tuple(shape)):
-        raise ValueError("%s must be a contiguous %s %s tensor on %s, got %s %s on %s"
-                         % (name, str(dtype)[6:], list(shape), device, str(t.dtype)[6:],
-                            list(t.shape), t.device))
-    return t.data_ptr()
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        return t.data_ptr()
+    raise ValueError("%s must be a contiguous %s %s tensor on cuda:%d, got %s %s on %s"
+                     % (name, str(dtype)[6:], list(shape), index, str(t.dtype)[6:],
+                        list(t.shape), t.device))
+
+
+def _handle(stream, index):
+    """The handle of `stream`, or of torch's current stream on the device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return api._stream(stream)
 
 
 def _cuda(device) -> torch.device:
@@ -74,6 +83,13 @@ class BatchPlanner:
         self._positions = torch.empty(max_tokens, **i32)
         self._slots = torch.empty(max_tokens, dtype=torch.int64, device=self.device)
         self._lib = api.load()
+        self._index = self.device.index
+        self._c = api.BatchC(page_size=page_size, q_start=self._q_start.data_ptr(),
+                             kv_len=self._kv_len.data_ptr(), held_out=self._held.data_ptr(),
+                             free_head=self._free_head.data_ptr())
+        self._cref = ctypes.byref(self._c)
+        self._slots_ptr, self._pos_ptr = self._slots.data_ptr(), self._positions.data_ptr()
+        self._size, self._plan = None, None
 
     def plan(self, q_len, cached, held, free_pages, free_range, block_table, n_tokens: int,
              stream=None) -> BatchPlan:
@@ -82,26 +98,30 @@ class BatchPlanner:
         from entry held[b] on. The returned buffers are the planner's own: to
         feed `held` or `free_head` to the next plan, copy them into the
         caller's first."""
-        B, dev, i32 = q_len.shape[0], self.device, torch.int32
-        if not 1 <= B <= self.max_requests or not 0 <= n_tokens <= self.max_tokens:
-            raise ValueError("a plan holds 1..%d requests and 0..%d tokens, got %d and %d"
-                             % (self.max_requests, self.max_tokens, B, n_tokens))
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be [requests][blocks]")
-        F, M = free_pages.numel(), block_table.shape[1]
-        b = api.BatchC(B, M, self.page_size, F, _need(q_len, "q_len", i32, [B], dev),
-                       _need(cached, "cached", i32, [B], dev), _need(held, "held", i32, [B], dev),
-                       _need(free_pages, "free_pages", i32, [F], dev),
-                       _need(free_range, "free_range", i32, [2], dev),
-                       _need(block_table, "block_table", i32, [B, M], dev),
-                       self._q_start.data_ptr(), self._kv_len.data_ptr(), self._held.data_ptr(),
-                       self._free_head.data_ptr())
-        slots, positions = self._slots[:n_tokens], self._positions[:n_tokens]
-        api._check(self._lib.moe_plan_batch(ctypes.byref(b), n_tokens, slots.data_ptr(),
-                                            positions.data_ptr(), api._stream(stream)),
-                   "moe_plan_batch")
-        return BatchPlan(self._q_start[:B + 1], self._kv_len[:B], self._held[:B], self._free_head,
-                         slots, positions)
+        c, at, i32 = self._c, self._index, torch.int32
+        if block_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("block_table must be [requests][blocks], free_pages [pages]")
+        (B, M), F = block_table.shape, free_pages.shape[0]
+        if (B, n_tokens) != self._size:
+            if not 1 <= B <= self.max_requests or not 0 <= n_tokens <= self.max_tokens:
+                raise ValueError("a plan holds 1..%d requests and 0..%d tokens, got %d and %d"
+                                 % (self.max_requests, self.max_tokens, B, n_tokens))
+            self._plan = BatchPlan(self._q_start[:B + 1], self._kv_len[:B], self._held[:B],
+                                   self._free_head, self._slots[:n_tokens],
+                                   self._positions[:n_tokens])
+            self._size = (B, n_tokens)
+        c.n_requests, c.max_blocks, c.free_capacity = B, M, F
+        c.q_len = _need(q_len, "q_len", i32, (B,), at)
+        c.cached = _need(cached, "cached", i32, (B,), at)
+        c.held = _need(held, "held", i32, (B,), at)
+        c.free_pages = _need(free_pages, "free_pages", i32, (F,), at)
+        c.free_range = _need(free_range, "free_range", i32, (2,), at)
+        c.block_table = _need(block_table, "block_table", i32, (B, M), at)
+        st = self._lib.moe_plan_batch(self._cref, n_tokens, self._slots_ptr, self._pos_ptr,
+                                      _handle(stream, at))
+        if st:
+            api._check(st, "moe_plan_batch")
+        return self._plan
 
 
 class PagedCache:
@@ -117,6 +137,8 @@ class PagedCache:
         self.page_size, self.n_kv_heads, self.head_dim = k.shape[1:]
         self.dtype = k.dtype
         self._lib = api.load()
+        self._index, self._cref = self.device.index, ctypes.byref(self.c)
+        self._row = (self.n_kv_heads, self.head_dim)
 
     @classmethod
     def allocate(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
@@ -132,21 +154,22 @@ class PagedCache:
         """New keys and values [n][n_kv_heads][head_dim] (of the cache's type
         or float32, rounded once) to their slots (moe_kv_append). Rows must be
         contiguous; token and head strides may be any multiple of 16 bytes."""
-        n = k.shape[0]
-        if (k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or
-                any(api._stride(k, i) != api._stride(v, i) for i in range(2)) or
-                tuple(k.shape[1:]) != (self.n_kv_heads, self.head_dim) or k.stride(2) != 1 or
-                v.stride(2) != 1 or
-                k.dtype not in (self.dtype, torch.float32) or
-                k.device != self.device or v.device != self.device):
+        n, dt, at = k.shape[0], k.dtype, self._index
+        sk, sv = k.stride(), v.stride()
+        if (k.shape != (n, *self._row) or v.shape != k.shape or v.dtype is not dt or
+                (dt is not self.dtype and dt is not torch.float32) or k.get_device() != at or
+                v.get_device() != at or sk[2] != 1 or sv[2] != 1 or (n > 1 and sk[0] != sv[0]) or
+                (self.n_kv_heads > 1 and sk[1] != sv[1])):
             raise ValueError("k and v must be [n][%d][%d] %s or float32 tensors on %s with "
                              "contiguous rows and equal strides"
-                             % (self.n_kv_heads, self.head_dim, str(self.dtype)[6:], self.device))
-        sp = _need(slots, "slots", torch.int64, [n], self.device)
-        api._check(self._lib.moe_kv_append(ctypes.byref(self.c), k.data_ptr(), v.data_ptr(),
-                                           api.DTYPES[k.dtype], api._stride(k, 0),
-                                           api._stride(k, 1), n, sp, api._stream(stream)),
-                   "moe_kv_append")
+                             % (*self._row, str(self.dtype)[6:], self.device))
+        D = self.head_dim                      # for the stride of a dimension of one entry
+        st = self._lib.moe_kv_append(self._cref, k.data_ptr(), v.data_ptr(), api.DTYPES[dt],
+                                     sk[0] if n > 1 else D, sk[1] if self.n_kv_heads > 1 else D, n,
+                                     _need(slots, "slots", torch.int64, (n,), at),
+                                     _handle(stream, at))
+        if st:
+            api._check(st, "moe_kv_append")
 
 
 class PagedAttention:
@@ -170,6 +193,19 @@ class PagedAttention:
         self._out = torch.empty((max_tokens, n_heads, cache.head_dim), dtype=cache.dtype,
                                 device=cache.device)
         self._lib = api.load()
+        self._dref, self._ws_ptr, self._ws_bytes = (ctypes.byref(self.desc),
+                                                    self.workspace.data_ptr(), nbytes)
+        self._n, self._view = None, None
+
+    def _check(self, name, t, n):
+        """The token and head strides of q or out."""
+        c, H = self.cache, self.n_heads
+        s = t.stride()
+        if (t.shape != (n, H, c.head_dim) or t.dtype is not c.dtype or
+                t.get_device() != c._index or s[2] != 1):
+            raise ValueError("%s must be a %s %s tensor on %s with contiguous rows"
+                             % (name, str(c.dtype)[6:], [n, H, c.head_dim], c.device))
+        return s[0] if n > 1 else c.head_dim, s[1] if H > 1 else c.head_dim
 
     def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
                block_table: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -178,29 +214,26 @@ class PagedAttention:
         [B] and block_table [B][M] int32 as BatchPlanner.plan leaves them.
         Returns `out` (same shape and type, rows contiguous), or the object's
         own buffer. Rows of no request keep what `out` held."""
-        c, n = self.cache, q.shape[0]
-        shape = (n, self.n_heads, c.head_dim)
+        c, n, i32 = self.cache, q.shape[0], torch.int32
+        at = c._index
         if out is None:
-            if n > self.max_tokens:
-                raise ValueError("%d tokens, more than max_tokens %d" % (n, self.max_tokens))
-            out = self._out[:n]
-        for name, t in (("q", q), ("out", out)):
-            if (tuple(t.shape) != shape or t.dtype != c.dtype or t.device != c.device or
-                    t.stride(2) != 1):
-                raise ValueError("%s must be a %s %s tensor on %s with contiguous rows"
-                                 % (name, str(c.dtype)[6:], list(shape), c.device))
+            if n != self._n:
+                if n > self.max_tokens:
+                    raise ValueError("%d tokens, more than max_tokens %d" % (n, self.max_tokens))
+                self._n, self._view = n, self._out[:n]
+            out = self._view
+        q_token, q_head = self._check("q", q, n)
+        out_token, out_head = self._check("out", out, n)
         if block_table.dim() != 2:
             raise ValueError("block_table must be [requests][blocks]")
         B, M = block_table.shape
-        i32 = torch.int32
-        api._check(self._lib.moe_attend(
-            ctypes.byref(c.c), ctypes.byref(self.desc), q.data_ptr(), api._stride(q, 0),
-            api._stride(q, 1), n,
-            _need(q_start, "q_start", i32, [B + 1], c.device),
-            _need(kv_len, "kv_len", i32, [B], c.device),
-            _need(block_table, "block_table", i32, [B, M], c.device), M, B,
-            self.workspace.data_ptr(), self.workspace.numel(), out.data_ptr(),
-            api._stride(out, 0), api._stride(out, 1), api._stream(stream)), "moe_attend")
+        st = self._lib.moe_attend(
+            c._cref, self._dref, q.data_ptr(), q_token, q_head, n,
+            _need(q_start, "q_start", i32, (B + 1,), at), _need(kv_len, "kv_len", i32, (B,), at),
+            _need(block_table, "block_table", i32, (B, M), at), M, B, self._ws_ptr,
+            self._ws_bytes, out.data_ptr(), out_token, out_head, _handle(stream, at))
+        if st:
+            api._check(st, "moe_attend")
         return out
 
 
@@ -216,16 +249,19 @@ class GroupedRouter:
         if score not in ("softmax", "sigmoid"):
             raise ValueError("score must be 'softmax' or 'sigmoid'")
         self.device = _cuda(device if bias is None else bias.device)
-        if bias is not None:
-            _need(bias, "bias", torch.float32, [n_experts], self.device)
+        self._index = self.device.index
+        self._bias_ptr = None if bias is None else _need(bias, "bias", torch.float32,
+                                                         (n_experts,), self._index)
         self.n_experts, self.top_k, self.max_tokens, self.bias = n_experts, top_k, max_tokens, bias
         self.desc = api.RouterDesc(
             n_experts, top_k, n_groups, top_groups, group_top,
             api.MOE_SCORE_SIGMOID if score == "sigmoid" else api.MOE_SCORE_SOFTMAX,
             1 if renorm else 0, scale)
-        self._idx = torch.empty(max_tokens * top_k, dtype=torch.int32, device=self.device)
-        self._w = torch.empty(max_tokens * top_k, dtype=torch.float32, device=self.device)
+        self._idx = torch.empty((max_tokens, top_k), dtype=torch.int32, device=self.device)
+        self._w = torch.empty((max_tokens, top_k), dtype=torch.float32, device=self.device)
+        self._n, self._views = None, None
         self._lib = api.load()
+        self._dref = ctypes.byref(self.desc)
         # the descriptor's own checks, before the first pass
         api._check(self._lib.moe_route_grouped(ctypes.byref(self.desc), None, api.MOE_F32,
                                                n_experts, None, 0, None, None, None),
@@ -236,19 +272,29 @@ class GroupedRouter:
         """(idx [n][k] int32, weights [n][k] float32) for logits [n][E] in
         float32, bfloat16 or float16 with contiguous rows; written to idx and
         weights if given (n·k contiguous elements), else to the router's own."""
-        if (logits.dim() != 2 or logits.shape[1] != self.n_experts or logits.stride(1) != 1 or
-                logits.dtype not in api.DTYPES or logits.device != self.device):
+        E, k, at = self.n_experts, self.top_k, self._index
+        dt = api.DTYPES.get(logits.dtype)
+        s = logits.stride()
+        if (logits.dim() != 2 or logits.shape[1] != E or s[1] != 1 or dt is None or
+                logits.get_device() != at):
             raise ValueError("logits must be a [n][%d] float32, bfloat16 or float16 tensor on %s "
-                             "with contiguous rows" % (self.n_experts, self.device))
-        n, k = logits.shape[0], self.top_k
-        if (idx is None or weights is None) and n > self.max_tokens:
-            raise ValueError("%d tokens, more than max_tokens %d" % (n, self.max_tokens))
-        idx = self._idx[:n * k] if idx is None else idx.view(-1)
-        weights = self._w[:n * k] if weights is None else weights.view(-1)
-        ip = _need(idx, "idx", torch.int32, [n * k], self.device)
-        wp = _need(weights, "weights", torch.float32, [n * k], self.device)
-        api._check(self._lib.moe_route_grouped(
-            ctypes.byref(self.desc), logits.data_ptr(), api.DTYPES[logits.dtype],
-            api._stride(logits, 0), None if self.bias is None else self.bias.data_ptr(), n, ip, wp,
-            api._stream(stream)), "moe_route_grouped")
-        return idx.view(n, k), weights.view(n, k)
+                             "with contiguous rows" % (E, self.device))
+        n = logits.shape[0]
+        if idx is None and weights is None:
+            if n != self._n:
+                if n > self.max_tokens:
+                    raise ValueError("%d tokens, more than max_tokens %d" % (n, self.max_tokens))
+                self._n, self._views = n, (self._idx[:n], self._w[:n])
+            idx, weights = self._views
+            ip, wp = idx.data_ptr(), weights.data_ptr()
+        elif idx is None or weights is None:
+            raise ValueError("give both idx and weights, or neither")
+        else:
+            idx, weights = idx.view(n, k), weights.view(n, k)
+            ip = _need(idx, "idx", torch.int32, (n, k), at)
+            wp = _need(weights, "weights", torch.float32, (n, k), at)
+        st = self._lib.moe_route_grouped(self._dref, logits.data_ptr(), dt, s[0] if n > 1 else E,
+                                         self._bias_ptr, n, ip, wp, _handle(stream, at))
+        if st:
+            api._check(st, "moe_route_grouped")
+        return idx, weights
