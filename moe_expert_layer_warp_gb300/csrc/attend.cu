@@ -24,10 +24,12 @@
 // number of 128-key tiles its rows see. All items' tiles in a row are cut
 // into equal ranges, one per CTA, wherever the cuts fall: every SM has the
 // same number of key tiles to go through whatever the mix of long and short
-// requests. Rows of an item that was cut leave (O, m, Σ) in the workspace,
-// and a second kernel joins them in key order, so results do not depend on
-// scheduling. The lengths are on the device: every CTA works out the cuts
-// from them by itself.
+// requests. The lengths are on the device: every CTA works out the cuts from
+// them by itself. A CTA whose range ends inside an item leaves (O, m, Σ) of
+// the item's rows in the workspace, and the CTA with the item's last tile
+// joins the parts in key order, so results do not depend on scheduling. It
+// waits (bounded) for lower-numbered CTAs only, which leave their parts
+// before they wait themselves.
 //
 // Warps (one CTA per SM):
 //   0-3    softmax of stream 0 over the first 64 keys of a tile, one thread per
@@ -42,6 +44,9 @@
 #include <limits.h>
 #include <math.h>
 #include <string.h>
+
+#include <atomic>
+#include <chrono>
 
 #include "batch_launch.h"
 #include "common.cuh"
@@ -80,19 +85,17 @@ struct Sizes {
   static constexpr size_t kSlotFloats = size_t(2 * kTile) * (kDim + 2);
 };
 
-// What a CTA leaves for the join: the item that ends in its range but began
-// in an earlier one.
-struct JoinRec {
-  int valid, row0, ntok, head0, first_cta, pad[3];
-};
-
 struct Params {
   CUtensorMap kmap, vmap, qmap;
   AttendArgs a;
   int page_shift;
   int tpt;       // tokens per query tile, 128 / group
   float* part;   // [2 per CTA][kSlotFloats]
-  JoinRec* rec;  // [CTAs]
+  // [CTAs]: `call` when the CTA has left the part of its last item. The CTA
+  // that reads it sets it to 0; what an unused workspace holds is not `call`,
+  // a number of 64 mixed bits that no two calls share.
+  unsigned long long* left;
+  unsigned long long call;
 };
 
 // A block of new tokens of one request for one key head.
@@ -164,10 +167,8 @@ struct Walker {
   Request r;
   int b, h;  // of the present part
 
-  MOE_DEV Walker(const Params& prm, const Walk& start) : p(prm), w(start), b(start.b), h(start.h) {
-    bool bad;
-    r = request(p.a, p.page_shift, min(w.b, p.a.n_requests - 1), &bad);
-  }
+  MOE_DEV Walker(const Params& prm, const Walk& start, const Request& first)
+      : p(prm), w(start), r(first), b(start.b), h(start.h) {}
 
   MOE_DEV bool next(Part* out) {
     const int fixed = 2 * p.tpt;
@@ -200,8 +201,12 @@ struct Walker {
 
 struct Start {
   Walk w;
-  int has_rec;
-  JoinRec rec;
+  Request r;       // of w.b
+  // the CTA has the last tile of an item that began in an earlier range: the
+  // item's rows, and the unit of its first tile
+  int joins, row0, ntok, head0;
+  long long unit;
+  long long each, more;  // units per CTA; the first `more` have one more
 };
 
 MOE_DEV long long divide(long long a, long long b) {  // of non-negative numbers
@@ -229,16 +234,19 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   Request req[kPerThread];
   long long count[kPerThread], sum = 0;
   bool any_bad = false;
+  const int per = (a.n_requests + kPlanThreads - 1) / kPlanThreads;  // requests per thread
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
+    const int b = tid * per + i;
     bool bad = false;
     req[i] = Request{0, 0, 0};
-    if (b < a.n_requests) req[i] = request(a, p.page_shift, b, &bad);
+    if (i < per && b < a.n_requests) req[i] = request(a, p.page_shift, b, &bad);
     any_bad |= bad;
   }
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
+    count[i] = 0;
+    if (i >= per) continue;
     // a request of one block by its own thread, longer ones by the warp
     count[i] = req[i].q > 0 ? make_item(a, req[i], 0, fixed).n + kItemCost : 0;
     uint32_t longer = __ballot_sync(kAll, req[i].q > fixed);
@@ -277,7 +285,9 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   if (tid == 0) {
     out->w.b = 0;
     out->w.left = (int)(w1 - w0);
-    out->has_rec = 0;
+    out->joins = 0;
+    out->each = each;
+    out->more = more;
   }
   asm volatile("bar.sync 1, 256;" ::: "memory");
   if (w1 == w0) return;
@@ -289,7 +299,7 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   for (int i = 0; i < kPerThread; ++i) {
     const long long n = count[i] * H;
     if (w0 >= before && w0 < before + n) {
-      b = tid * kPerThread + i;
+      b = tid * per + i;
       r = req[i];
       h = (int)divide(w0 - before, count[i]);
       rem = w0 - before - h * count[i];
@@ -324,14 +334,13 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
       out->w.h = h;
       out->w.block = q;
       out->w.u0 = (int)u0;
-      // the item's last tile is here and its first in an earlier range: this
-      // CTA's record
+      out->r = r;
       if (u0 > kItemCost && n - u0 <= w1 - w0) {
-        const long long s = w0 - u0 + kItemCost;  // unit of the item's first tile
-        const long long head = more * (each + 1);
-        const long long c0 = s < head ? divide(s, each + 1) : more + divide(s - head, each);
-        out->has_rec = 1;
-        out->rec = JoinRec{1, it.row0, it.ntok, h * a.group, (int)c0, {0, 0, 0}};
+        out->joins = 1;
+        out->row0 = it.row0;
+        out->ntok = it.ntok;
+        out->head0 = h * a.group;
+        out->unit = w0 - u0 + kItemCost;
       }
     }
     const long long block_sum = __shfl_sync(kAll, upto, 31);
@@ -425,6 +434,65 @@ MOE_DEV void quad_transpose(uint4 (&v)[4], int lane) {
   }
 }
 
+// The parts of an item in key order, a thread per (row, 4 columns). All
+// softmax threads of the CTA that has the item's last tile call it.
+template <int kDim, bool kF16>
+MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* abort_flag) {
+  using Z = Sizes<kDim>;
+  const AttendArgs& a = p.a;
+  // the CTA with the item's first tile
+  const long long head = st.more * (st.each + 1);
+  const int first = (int)(st.unit < head ? divide(st.unit, st.each + 1)
+                                         : st.more + divide(st.unit - head, st.each));
+  const int last = blockIdx.x;
+  if (first + (int)threadIdx.x < last) {
+    unsigned long long* word = p.left + first + threadIdx.x;
+    const unsigned long long t0 = global_ns();
+    for (unsigned int i = 0;; ++i) {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
+      if (v == p.call) break;
+      if ((i & 63u) == 63u && (*abort_flag || global_ns() - t0 > kWaitLimitNs)) {
+        report_error(a.err, ERR_TIMEOUT, 0xA70);
+        break;
+      }
+    }
+    *word = 0ull;
+  }
+  __threadfence();
+  asm volatile("bar.sync 2, 512;" ::: "memory");
+  const int G = a.group, rows = st.ntok * G, per_tile = p.tpt * G;
+  for (int i = threadIdx.x; i < rows * (kDim / 4); i += 512) {
+    const int c4 = i / rows, rr = i - c4 * rows;
+    // rows of the second tile start at 128
+    const int prow = rr < per_tile ? rr : kTile + rr - per_tile;
+    float m = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = first; c <= last; ++c) {
+      const float* slot = p.part + (size_t)(2 * c + (c == last ? 0 : 1)) * Z::kSlotFloats;
+      const float* stat = slot + (size_t)2 * kTile * kDim;
+      const float mc = __ldcg(stat + prow), sc = __ldcg(stat + 2 * kTile + prow);
+      const float4 oc =
+          __ldcg(reinterpret_cast<const float4*>(slot) + c4 * (2 * kTile) + prow);
+      if (mc == -INFINITY) continue;
+      const float top = fmaxf(m, mc);
+      const float keep = m == -INFINITY ? 0.f : exp2_approx(m - top), add = exp2_approx(mc - top);
+      m = top;
+      sum = sum * keep + sc * add;
+      o.x = o.x * keep + oc.x * add;
+      o.y = o.y * keep + oc.y * add;
+      o.z = o.z * keep + oc.z * add;
+      o.w = o.w * keep + oc.w * add;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int tok = rr / G, g = rr - tok * G;
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(st.row0 + tok) * a.out_token_stride +
+                    (int64_t)(st.head0 + g) * a.out_head_stride + c4 * 4;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(narrow<kF16>(o.x * inv, o.y * inv), narrow<kF16>(o.z * inv, o.w * inv));
+  }
+}
+
 // Barriers and words behind the ring.
 struct Misc {
   uint64_t full[10], empty[10];
@@ -488,14 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
-  if (threadIdx.x == 0) {
-    JoinRec& rec = p.rec[blockIdx.x];
-    if (m.start.has_rec) {
-      rec = m.start.rec;
-    } else {
-      rec.valid = 0;
-    }
-  }
   bool ok = true;  // no wait of this role has been lost
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int site) {
     ok = __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, abort_flag, a.err, site));
@@ -507,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   if (warp == 16) {
     // ------------------------------------------------------------- loader --
-    Walker walk(p, m.start.w);
+    Walker walk(p, m.start.w, m.start.r);
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
@@ -575,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // ------------------------------------------------------------ queries --
     // a box is the 128 / group tokens of a tile, times the group's heads, in
     // the order of the tile's rows
-    Walker walk(p, m.start.w);
+    Walker walk(p, m.start.w, m.start.r);
     const uint64_t policy = l2_evict_normal_policy();
     int slot = 0;
     uint32_t phase = 0;
@@ -604,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // order: a barrier tells only the parity of its phase, so a warp that
     // passed over a tile could take an older phase for the one it wants. A
     // tile that is the other stream's alone is released as soon as it is there.
-    Walker walk(p, m.start.w);
+    Walker walk(p, m.start.w, m.start.r);
     const int s = (warp - 17) >> 1;                    // stream
     const uint32_t id_s = umma::idesc_f16(kTile, kTile, kF16, false);
     const uint32_t id_o = umma::idesc_f16(kTile, kDim, kF16, true);
@@ -730,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    Walker walk(p, m.start.w);
+    Walker walk(p, m.start.w, m.start.r);
     const int s = warp >> 3, half = warp >> 2 & 1;  // stream, and half of a tile's keys
     const int row = threadIdx.x & 127;               // row of the tile, TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // 32·(warp % 4) in the upper half
@@ -750,6 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       asm volatile("bar.sync %0, 64;" ::"r"(3 + 4 * s + (warp & 3)) : "memory");
     };
     uint32_t s_phase = 0, o_phase = 0;
+    bool open = false;                               // the last part does not end its item
     while (walk.next(&pt)) {
       const Item& it = pt.it;
       const int n = pt.t1 - pt.t0;
@@ -855,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       pair_sync();
       if (!two) *mine = half == 0 ? ref : sum;
       const bool ends = pt.t1 == it.n, whole_item = ends && pt.t0 == 0;
+      open = !ends;
       // factors of the two streams' O, and this thread's columns
       float f0 = 1.f, f1 = 0.f;
       int c_first = half * (kDim / 2), c_end = c_first + kDim / 2;
@@ -946,56 +1008,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         asm volatile("bar.sync 2, 512;" ::: "memory");
       }
     }
+    if (open) {                                      // the part left behind is complete
+      __threadfence();
+      asm volatile("bar.sync 2, 512;" ::: "memory");
+      if (threadIdx.x == 0)
+        asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.left + blockIdx.x), "l"(p.call)
+                     : "memory");
+    }
+    if (m.start.joins) join_parts<kDim, kF16>(p, m.start, abort_flag);
   }
   umma::fence_before_sync();
   __syncthreads();
   if (warp == 17) umma::tmem_dealloc(tmem, kCols);
-}
-
-// ------------------------------------------------------------------ join --
-// One CTA per record: the parts of the record's item in key order, a thread
-// per (row, 4 columns).
-constexpr int kJoinThreads = 256;
-
-template <int kDim, bool kF16>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const __grid_constant__ Params p) {
-  using Z = Sizes<kDim>;
-  pdl_wait();
-  pdl_trigger();
-  const JoinRec rec = p.rec[blockIdx.x];
-  if (!rec.valid) return;
-  const AttendArgs& a = p.a;
-  const int G = a.group, rows = rec.ntok * G, per_tile = p.tpt * G;
-  const int last = blockIdx.x;
-  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < rows * (kDim / 4);
-       i += gridDim.y * kJoinThreads) {
-    const int c4 = i / rows, rr = i - c4 * rows;
-    // rows of the second tile start at 128
-    const int prow = rr < per_tile ? rr : kTile + rr - per_tile;
-    float m = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = rec.first_cta; c <= last; ++c) {
-      const float* slot = p.part + (size_t)(2 * c + (c == last ? 0 : 1)) * Z::kSlotFloats;
-      const float* st = slot + (size_t)2 * kTile * kDim;
-      const float mc = st[prow], sc = st[2 * kTile + prow];
-      const float4 oc = reinterpret_cast<const float4*>(slot)[c4 * (2 * kTile) + prow];
-      if (mc == -INFINITY) continue;
-      const float top = fmaxf(m, mc);
-      const float keep = m == -INFINITY ? 0.f : exp2_approx(m - top), add = exp2_approx(mc - top);
-      m = top;
-      sum = sum * keep + sc * add;
-      o.x = o.x * keep + oc.x * add;
-      o.y = o.y * keep + oc.y * add;
-      o.z = o.z * keep + oc.z * add;
-      o.w = o.w * keep + oc.w * add;
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int tok = rr / G, g = rr - tok * G;
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(rec.row0 + tok) * a.out_token_stride +
-                    (int64_t)(rec.head0 + g) * a.out_head_stride + c4 * 4;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(narrow<kF16>(o.x * inv, o.y * inv), narrow<kF16>(o.z * inv, o.w * inv));
-  }
 }
 
 template <int kDim, bool kF16>
@@ -1010,16 +1034,28 @@ cudaError_t launch_t(Params& p, int ctas, cudaStream_t stream) {
     if (e == cudaSuccess) configured_device = dev;
   }
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), Z::kSmem, stream, p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attend_join_kernel<kDim, kF16>, dim3(ctas, 2), dim3(kJoinThreads), 0, stream, p);
+  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), Z::kSmem, stream, p);
+}
+
+constexpr size_t kLeftBytes = (kMaxCtas * sizeof(unsigned long long) + 255) / 256 * 256;
+
+// A number that no other call of the process, and no leftover word in a
+// workspace, has but by a chance of 2^-64: a count from a start taken from
+// the clock and an address, its bits mixed by multiplications and shifts.
+unsigned long long call_number() {
+  static std::atomic<unsigned long long> next{
+      (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() * 4096ull ^
+      (unsigned long long)reinterpret_cast<uintptr_t>(&next)};
+  unsigned long long v = next.fetch_add(1, std::memory_order_relaxed) * 0x9e3779b97f4a7c15ull;
+  v = (v ^ (v >> 31)) * 0xd6e8feb86659fd93ull;
+  return (v ^ (v >> 32)) | 1ull;
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int head_dim) {
   const size_t slot = head_dim == 128 ? Sizes<128>::kSlotFloats : Sizes<64>::kSlotFloats;
-  return size_t(kMaxCtas) * sizeof(JoinRec) + 2 * kMaxCtas * slot * sizeof(float);
+  return kLeftBytes + 2 * kMaxCtas * slot * sizeof(float);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream) {
@@ -1028,8 +1064,9 @@ cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream)
   p.a = a;
   p.page_shift = 31 - __builtin_clz(a.cache.page_size);
   p.tpt = kTile / a.group;
-  p.rec = static_cast<JoinRec*>(a.workspace);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kMaxCtas * sizeof(JoinRec));
+  p.left = static_cast<unsigned long long*>(a.workspace);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + kLeftBytes);
+  p.call = call_number();
   const moe_kv_cache& c = a.cache;
   // [page][row][head][dim], one 64-column piece of a head's rows per box
   const cuuint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.n_kv_heads, (uint64_t)c.page_size,
