@@ -63,7 +63,7 @@ constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 constexpr int kPlanThreads = 256;
 constexpr int kPerThread = MOE_MAX_REQUESTS / kPlanThreads;
 // What an item costs beside its tiles, in tiles, when the work is cut.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 3;
 // The reference m follows the row's maximum only when that has grown by more
 // than this (in powers of two): until then weights are up to 2^8 instead of
 // 1, which fp32 sums and both 16-bit types hold, and O needs no rescaling.
@@ -468,21 +468,37 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* abort_fl
     const int prow = rr < per_tile ? rr : kTile + rr - per_tile;
     float m = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = first; c <= last; ++c) {
-      const float* slot = p.part + (size_t)(2 * c + (c == last ? 0 : 1)) * Z::kSlotFloats;
-      const float* stat = slot + (size_t)2 * kTile * kDim;
-      const float mc = __ldcg(stat + prow), sc = __ldcg(stat + 2 * kTile + prow);
-      const float4 oc =
-          __ldcg(reinterpret_cast<const float4*>(slot) + c4 * (2 * kTile) + prow);
-      if (mc == -INFINITY) continue;
-      const float top = fmaxf(m, mc);
-      const float keep = m == -INFINITY ? 0.f : exp2_approx(m - top), add = exp2_approx(mc - top);
+    // the loads of several parts in flight together
+    constexpr int kBatch = 4;
+    for (int c0 = first; c0 <= last; c0 += kBatch) {
+      float mc[kBatch], sc[kBatch];
+      float4 oc[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int c = min(c0 + j, last);
+        const float* slot = p.part + (size_t)(2 * c + (c == last ? 0 : 1)) * Z::kSlotFloats;
+        const float* stat = slot + (size_t)2 * kTile * kDim;
+        mc[j] = c0 + j <= last ? __ldcg(stat + prow) : -INFINITY;
+        sc[j] = __ldcg(stat + 2 * kTile + prow);
+        oc[j] = __ldcg(reinterpret_cast<const float4*>(slot) + c4 * (2 * kTile) + prow);
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, mc[j]);
+      if (top == -INFINITY) continue;              // (the parts hold zeros)
+      const float keep = exp2_approx(m - top);
       m = top;
-      sum = sum * keep + sc * add;
-      o.x = o.x * keep + oc.x * add;
-      o.y = o.y * keep + oc.y * add;
-      o.z = o.z * keep + oc.z * add;
-      o.w = o.w * keep + oc.w * add;
+      sum *= keep;
+      o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float add = exp2_approx(mc[j] - top);
+        sum = fmaf(sc[j], add, sum);
+        o.x = fmaf(oc[j].x, add, o.x);
+        o.y = fmaf(oc[j].y, add, o.y);
+        o.z = fmaf(oc[j].z, add, o.z);
+        o.w = fmaf(oc[j].w, add, o.w);
+      }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const int tok = rr / G, g = rr - tok * G;
