@@ -32,15 +32,16 @@
 // before they wait themselves.
 //
 // Warps (one CTA per SM):
-//   0-3    softmax of stream 0 over the first 64 keys of a tile, one thread per
-//          row, and a share of its results out
-//   4-7    the same over the last 64 keys; the two halves agree on a row's
-//          maximum through shared memory
-//   8-15   the same for stream 1
-//   16     TMA: key and value tiles into a ring, a box per page and 64 columns
-//   18     TMA: query tiles into two slots, the next as soon as one is free
-//   17, 19 MMA issue of stream 0 and of stream 1; they also clear value rows
+//   0, 2   TMA: key and value tiles into a ring, a box per page and 64 columns,
+//          every other box each; warp 2 also query tiles into two slots, the
+//          next as soon as one is free
+//   1, 3   MMA issue of stream 0 and of stream 1; they also clear value rows
 //          that no row of the item sees
+//   4-7    softmax of stream 0 over the first 64 keys of a tile, one thread per
+//          row, and a share of its results out
+//   8-11   the same over the last 64 keys; the two halves agree on a row's
+//          maximum through shared memory
+//   12-19  the same for stream 1
 #include <limits.h>
 #include <math.h>
 #include <string.h>
@@ -76,7 +77,7 @@ template <int kDim>
 struct Sizes {
   static constexpr int kTileBytes = kTile * kDim * 2;
   static constexpr int kStages = kDim == 128 ? 5 : 10;
-  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffRing = 2 * kTileBytes;  // behind the query slots
   static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
   static constexpr int kMiscBytes = 512 + 2048;  // Misc, then the streams' row statistics
   static constexpr int kSmem = kOffMisc + kMiscBytes;
@@ -368,6 +369,10 @@ MOE_DEV void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+MOE_DEV uint32_t low_bits(int n) {  // the n lowest bits; none for n ≤ 0, all for n ≥ 32
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 MOE_DEV float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -445,8 +450,9 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* abort_fl
   const int first = (int)(st.unit < head ? divide(st.unit, st.each + 1)
                                          : st.more + divide(st.unit - head, st.each));
   const int last = blockIdx.x;
-  if (first + (int)threadIdx.x < last) {
-    unsigned long long* word = p.left + first + threadIdx.x;
+  const int tid = threadIdx.x - 128;
+  if (first + tid < last) {
+    unsigned long long* word = p.left + first + tid;
     const unsigned long long t0 = global_ns();
     for (unsigned int i = 0;; ++i) {
       unsigned long long v;
@@ -462,7 +468,7 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* abort_fl
   __threadfence();
   asm volatile("bar.sync 2, 512;" ::: "memory");
   const int G = a.group, rows = st.ntok * G, per_tile = p.tpt * G;
-  for (int i = threadIdx.x; i < rows * (kDim / 4); i += 512) {
+  for (int i = tid; i < rows * (kDim / 4); i += 512) {
     const int c4 = i / rows, rr = i - c4 * rows;
     // rows of the second tile start at 128
     const int prow = rr < per_tile ? rr : kTile + rr - per_tile;
@@ -526,21 +532,20 @@ constexpr int kOffStat = 512;  // then [2 streams][2][128 rows] floats
 template <int kDim, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Params p) {
   using Z = Sizes<kDim>;
-  constexpr int kStages = Z::kStages;
   constexpr int kHalves = kDim / 64;           // 64-column halves of a row
   constexpr int kHalfBytes = kTile * 128;
   constexpr uint32_t kCols = 512;              // S0 S1 O0 O1, 128 columns each
+  constexpr int kStages = Z::kStages;
   const AttendArgs& a = p.a;
   extern __shared__ __align__(1024) unsigned char smem[];
   if (smem_addr(smem) & 1023u) {               // the tiles' swizzle needs it
     if (threadIdx.x == 0) report_error(a.err, ERR_CHECK, 0xA23);
     return;
   }
-  unsigned char* ring = smem + Z::kOffRing;
   Misc& m = *reinterpret_cast<Misc*>(smem + Z::kOffMisc);
   volatile int* abort_flag = &m.abort_flag;
   // the same value in every lane, and known to be
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) - 4;  // of the softmax warps
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -560,8 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     m.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 17) umma::tmem_alloc(&m.tmem, kCols);
-  if (threadIdx.x == 16 * 32) {
+  if (warp == -3) umma::tmem_alloc(&m.tmem, kCols);
+  if (threadIdx.x == 0) {
     prefetch_tmap(&p.kmap);
     prefetch_tmap(&p.vmap);
   }
@@ -578,115 +583,138 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   };
   Part pt;
 
-  if (warp >= 16) {
+  if (warp < 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   }
-  if (warp == 16) {
-    // ------------------------------------------------------------- loader --
+  if (warp == -4 || warp == -2) {
+    // ------------------------------------------------------------ loaders --
+    // A box takes its issuing lane 75 to 100 cycles, one lane after the other:
+    // 16 boxes of a tile in small pages took one warp longer than the tile
+    // took to arrive. So two warps go through the same tiles, each with every
+    // other box.
     Walker walk(p, m.start.w, m.start.r);
+    const int which = warp == -2;
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
     const uint64_t policy = l2_evict_normal_policy();
-    int stage = 0;
-    uint32_t phase = 0;
+    // this lane's boxes in the ring
+    const uint32_t ring = smem_addr(smem) + Z::kOffRing + lane * rows * 128;
+    int stage = 0, slot = 0, queries = 0, q_row = 0, q_head = 0;
+    uint32_t phase = 0, q_phase = 0;
+    // the next query tile, if its slot is free: a box is the 128 / group
+    // tokens of a tile, times the group's heads, in the order of the tile's rows
+    auto try_queries = [&]() {
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&m.q_empty[slot], q_phase ^ 1u))) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&m.q_full[slot], p.tpt * a.group * kDim * 2);
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half)
+          tma_load_3d(smem + slot * Z::kTileBytes + half * kHalfBytes, &p.qmap, half * 64, q_head,
+                      q_row, &m.q_full[slot], policy);
+      }
+      __syncwarp();
+      --queries;
+      q_row += p.tpt;
+      if (slot) q_phase ^= 1u;
+      slot ^= 1;
+    };
+    // waits for a free stage of the ring (or for nothing), and meanwhile for
+    // the slots of the queries still to load
+    auto wait_free = [&](uint64_t* bar) {
+      const unsigned long long t0 = global_ns();
+      for (unsigned int i = 0; ok && i < kWaitLimitIters; ++i) {
+        if (queries > 0) try_queries();
+        if (bar ? __all_sync(0xffffffffu, mbar_try_wait(bar, phase ^ 1u)) : queries == 0) return;
+        if ((i & 63u) == 63u)
+          ok = __all_sync(0xffffffffu, !*abort_flag && global_ns() - t0 <= kWaitLimitNs);
+      }
+      if (!*abort_flag) report_error(a.err, ERR_TIMEOUT, 0xA30);
+      *abort_flag = 1;
+      ok = false;
+    };
     while (walk.next(&pt)) {
       const Item& it = pt.it;
       const int n = pt.t1 - pt.t0;
       const int lead = pt.two ? 1 : 2;          // key tiles ahead of the value tiles
+      if (which) {
+        queries = pt.two ? 2 : 1;
+        q_row = it.row0;
+        q_head = walk.h * a.group;
+      }
       const int32_t* table = a.block_table + (size_t)walk.b * a.max_blocks;
       // this lane's page of tile j (−1: it has none, or no row of it is seen)
       auto page_of = [&](int j) {
-        if (j >= n) return -1;
         const int r0 = tile_of(it, pt.t0 + j) * kTile + lane * rows;
-        const bool want = lane < n_pages && r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk);
-        if (!want) return -1;
-        const int pg = table[r0 >> p.page_shift];
-        if (pg >= 0 && pg < a.cache.n_pages) return pg;
-        report_error(a.err, ERR_CHECK, 0xA21);
-        return (int)a.cache.n_pages;            // out of the map: the box reads zeros
+        const bool want = j < n && lane < n_pages && r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk);
+        int pg = -1;
+        if (want) {
+          pg = table[r0 >> p.page_shift];
+          if (pg < 0 || pg >= a.cache.n_pages) {
+            report_error(a.err, ERR_CHECK, 0xA21);
+            pg = (int)a.cache.n_pages;          // out of the map: the box reads zeros
+          }
+        }
+        return pg;
       };
-      auto load = [&](const CUtensorMap* map, int j, int pg) {
+      // Keys 0..lead-1, then values j, keys j + lead, for j = 0..n-1.
+      int jk = 0, jv = 0;
+      // the pages of tiles jv .. jv + 3, fetched that far ahead
+      int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3 = page_of(3);
+      while (jv < n) {
+        const bool is_k = jk < n && jk < jv + lead;
+        const int j = is_k ? jk : jv, pg = is_k && jk != jv ? pg1 : pg0;
         const uint32_t wanted = __ballot_sync(0xffffffffu, pg >= 0);
-        wait(&m.empty[stage], phase ^ 1u, 0xA30);
+        wait_free(&m.empty[stage]);
         if (ok) {
-          unsigned char* dst = ring + stage * Z::kTileBytes;
-          if (lane == 0)
+          if (lane == 0 && !which)
             mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim * 2);
           __syncwarp();
-          if (pg >= 0) {
-            const int r0 = tile_of(it, pt.t0 + j) * kTile + lane * rows;
+          const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
+          const int row = tile_of(it, pt.t0 + j) * kTile & (page - 1);  // 0 in small pages
 #pragma unroll
-            for (int half = 0; half < kHalves; ++half)
-              tma_load_4d(dst + half * kHalfBytes + lane * rows * 128, map, half * 64, walk.h,
-                          r0 & (page - 1), pg, &m.full[stage], policy);
-          }
+          for (int half = 0; half < kHalves; ++half)
+            if (pg >= 0 && ((half * n_pages + lane) & 1) == which)
+              tma_load_4d_at(ring + stage * Z::kTileBytes + half * kHalfBytes, map, half * 64,
+                             walk.h, row, pg, &m.full[stage], policy);
         }
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
         }
-      };
-      // keys 0..lead-1, then values j, keys j + lead, for j = 0..n-1; the
-      // pages of a tile are fetched one tile ahead
-      int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
-      load(&p.kmap, 0, pg0);
-      if (lead == 2 && n > 1) load(&p.kmap, 1, pg1);
-      for (int j = 0; j < n; ++j) {
-        const int pg3 = page_of(j + 3);
-        load(&p.vmap, j, pg0);
-        if (j + lead < n) load(&p.kmap, j + lead, lead == 1 ? pg1 : pg2);
-        pg0 = pg1;
-        pg1 = pg2;
-        pg2 = pg3;
+        if (is_k) {
+          ++jk;
+        } else {
+          ++jv;
+          pg0 = pg1;
+          pg1 = pg2;
+          pg2 = pg3;
+          pg3 = page_of(jv + 3);
+        }
       }
+      if (queries > 0) wait_free(nullptr);
     }
     // After a lost wait the tiles still in flight must land before the CTA
-    // ends; without one, every tile has been waited for by the MMA warp.
+    // ends; without one, every tile has been waited for by the MMA warps.
     if (!ok && lane == 0) {
-      for (int i = 0; i < kStages; ++i)
-        for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_for(&m.full[i], ph, a.err, 0xA31, 1000000ull);
-    }
-  } else if (warp == 18) {
-    // ------------------------------------------------------------ queries --
-    // a box is the 128 / group tokens of a tile, times the group's heads, in
-    // the order of the tile's rows
-    Walker walk(p, m.start.w, m.start.r);
-    const uint64_t policy = l2_evict_normal_policy();
-    int slot = 0;
-    uint32_t phase = 0;
-    while (walk.next(&pt)) {
-      for (int q = 0; q < (pt.two ? 2 : 1); ++q) {
-        wait(&m.q_empty[slot], phase ^ 1u, 0xA60);
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&m.q_full[slot], p.tpt * a.group * kDim * 2);
-#pragma unroll
-          for (int half = 0; half < kHalves; ++half)
-            tma_load_3d(smem + slot * Z::kTileBytes + half * kHalfBytes, &p.qmap, half * 64,
-                        walk.h * a.group, pt.it.row0 + q * p.tpt, &m.q_full[slot], policy);
-        }
-        __syncwarp();
-        if (slot) phase ^= 1u;
-        slot ^= 1;
+      for (uint32_t ph = 0; ph < 2; ++ph) {
+        for (int i = 0; i < kStages; ++i) mbar_wait_for(&m.full[i], ph, a.err, 0xA31, 1000000ull);
+        for (int i = 0; i < 2; ++i) mbar_wait_for(&m.q_full[i], ph, a.err, 0xA61, 1000000ull);
       }
     }
-    if (!ok && lane == 0) {
-      for (int i = 0; i < 2; ++i)
-        for (uint32_t ph = 0; ph < 2; ++ph) mbar_wait_for(&m.q_full[i], ph, a.err, 0xA61, 1000000ull);
-    }
-  } else if (warp >= 16) {
+  } else if (warp < 0) {
     // ---------------------------------------------------------------- MMA --
     // Both warps follow every tile of the ring and of the query slots, in
     // order: a barrier tells only the parity of its phase, so a warp that
     // passed over a tile could take an older phase for the one it wants. A
     // tile that is the other stream's alone is released as soon as it is there.
     Walker walk(p, m.start.w, m.start.r);
-    const int s = (warp - 17) >> 1;                    // stream
+    const int s = (warp + 3) >> 1;                     // stream
     const uint32_t id_s = umma::idesc_f16(kTile, kTile, kF16, false);
     const uint32_t id_o = umma::idesc_f16(kTile, kDim, kF16, true);
     const uint32_t q_lo = umma::desc_lo(smem_addr(smem), 0);
-    const uint32_t k_lo = umma::desc_lo(smem_addr(ring), 0);
-    const uint32_t v_lo = umma::desc_lo(smem_addr(ring), kHalfBytes);
+    const uint32_t k_lo = umma::desc_lo(smem_addr(smem) + Z::kOffRing, 0);
+    const uint32_t v_lo = umma::desc_lo(smem_addr(smem) + Z::kOffRing, kHalfBytes);
     const uint32_t d_s = tmem + s * 128, d_o = tmem + 256 + s * 128;
     int stage = 0;
     uint32_t phase = 0, n_q = 0, p_phase = 0, turn = s ^ 1u;
@@ -762,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const int key0 = tile_of(it, pt.t0 + j) * kTile;
         const bool now = sees(j);
         if (ok && now && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
-          unsigned char* v = ring + vt * Z::kTileBytes;
+          unsigned char* v = smem + Z::kOffRing + vt * Z::kTileBytes;
           for (int i = lane; i < kTile * kHalves * 8; i += 32) {
             const int key = key0 + ((i >> 3) & (kTile - 1));
             if (key >= it.hi || (key < it.lo && key >= it.sk))
@@ -858,10 +886,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const bool whole =
               !valid || (key0 + kHalf <= hi && (key0 >= lo || key0 + kHalf <= a.sinks));
           if (!__all_sync(0xffffffffu, whole)) {
-            const int e_hi = hi - key0, e_lo = lo - key0, e_sk = a.sinks - key0;
+            // bit c of `seen`: key key0 + 32·w + c
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c)
-              if (!(c < e_hi && (c >= e_lo || c < e_sk))) x[c] = 0xff800000u;  // −inf
+            for (int w = 0; w < kHalf / 32; ++w) {
+              const int at = key0 + 32 * w;
+              const uint32_t seen =
+                  low_bits(hi - at) & (~low_bits(lo - at) | low_bits(a.sinks - at));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                x[32 * w + c] = seen >> c & 1u ? x[32 * w + c] : 0xff800000u;  // −inf
+            }
           }
           float t4[4];
 #pragma unroll
@@ -1027,7 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     if (open) {                                      // the part left behind is complete
       __threadfence();
       asm volatile("bar.sync 2, 512;" ::: "memory");
-      if (threadIdx.x == 0)
+      if (threadIdx.x == 128)
         asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.left + blockIdx.x), "l"(p.call)
                      : "memory");
     }
@@ -1035,7 +1069,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == 17) umma::tmem_dealloc(tmem, kCols);
+  if (warp == -3) umma::tmem_dealloc(tmem, kCols);
 }
 
 template <int kDim, bool kF16>
