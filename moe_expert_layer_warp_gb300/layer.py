@@ -6,7 +6,7 @@ the library's entry points: forward() makes one moe_verify_pass call
 (moe_route_union → moe_verify_perslot or moe_verify_dedup → moe_combine), or
 one moe_verify_pass_fused call (the combine inside the expert kernel);
 gate(), route(), build_union(), route_union(), experts() and combine() make
-the single calls. Buffers are allocated
+the single calls; route_grouped() routes with a batch.GroupedRouter instead. Buffers are allocated
 once, through torch, at construction, and so are the C arguments that point
 at them: a call only marshals x and the stream.
 """
@@ -109,6 +109,19 @@ class PassRunner:
                                                   self._bias_w, xp, x.shape[0], self._idx,
                                                   self._tw, self._ws, self._ws_bytes,
                                                   api._stream(stream)), "moe_route_biased")
+
+    def route_grouped(self, x: torch.Tensor, router, stream=None):
+        """The gate, then `router` (a batch.GroupedRouter of this layer's
+        experts and top-k) on its logits, into the runner's routing buffers:
+        build_union(), experts() and combine() go on from there."""
+        sh = self.shape
+        if router.n_experts != sh.n_experts or router.top_k != sh.top_k:
+            raise ValueError("the router picks %d of %d experts, the layer %d of %d"
+                             % (router.top_k, router.n_experts, sh.top_k, sh.n_experts))
+        n = x.shape[0]
+        self.gate(x, stream)
+        return router.route(self.logits[: n * sh.n_experts].view(n, sh.n_experts),
+                            self.topk_idx[: n * sh.top_k], self.topk_w[: n * sh.top_k], stream)
 
     def build_union(self, n: int, stream=None):
         api._check(self._lib.moe_build_union(self._desc, self._idx, n, self._uref,

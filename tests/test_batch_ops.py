@@ -1,6 +1,7 @@
 """GPU checks of include/moe_batch.h's operators against their definitions in
 64 bits (tests/batch_oracle.py), at the sizes and masks where they can go
 wrong. Tolerances are the oracle's bounds."""
+import functools
 import random
 
 import numpy as np
@@ -231,56 +232,66 @@ class Attend:
 
 
 B16, F16 = torch.bfloat16, torch.float16
+def spec(*args, **kwargs):     # of an Attend, which is built on the GPU
+    return args, kwargs
+
+
 ATTENDS = {
-    "one token, one key": Attend([1], [1], 1, 1, 64, B16, 16),
-    "one token": Attend([1], [130], 4, 2, 128, F16, 16),
-    "pass of five": Attend([5], [77], 16, 16, 128, B16, 64),
-    "first tokens of a request": Attend([9], [9], 8, 2, 64, B16, 16),
-    "tile edges": Attend([1, 2, 3, 1, 2, 3, 1], [127, 128, 129, 255, 256, 257, 64], 8, 2, 64, F16,
+    "one token, one key": spec([1], [1], 1, 1, 64, B16, 16),
+    "one token": spec([1], [130], 4, 2, 128, F16, 16),
+    "pass of five": spec([5], [77], 16, 16, 128, B16, 64),
+    "first tokens of a request": spec([9], [9], 8, 2, 64, B16, 16),
+    "tile edges": spec([1, 2, 3, 1, 2, 3, 1], [127, 128, 129, 255, 256, 257, 64], 8, 2, 64, F16,
                          64, heads_first=True),
-    "ragged passes": Attend([1, 9, 5, 3, 16, 2], [700, 33, 5, 1030, 128, 450], 8, 2, 128, B16, 32),
-    "seven heads per key head": Attend([4, 20], [50, 300], 14, 2, 64, F16, 16),
-    "three heads per key head": Attend([50], [190], 3, 1, 128, B16, 128),
-    "sixteen heads, one key head": Attend([7, 9], [300, 200], 16, 1, 128, B16, 256),
-    "128 heads per key head": Attend([3], [150], 128, 1, 64, B16, 64),
-    "48 heads per key head": Attend([6, 1], [40, 400], 96, 2, 128, F16, 64),
-    "chunk": Attend([300], [300], 2, 2, 128, B16, 64),
-    "chunk over a cache": Attend([200, 77], [520, 500], 4, 1, 64, F16, 16, heads_first=True),
-    "chunk beside passes": Attend([1, 260, 4], [600, 413, 90], 8, 4, 128, B16, 16),
-    "empty requests": Attend([3, 0, 2, 0], [0, 0, 40, 70], 4, 2, 64, B16, 16),
-    "only empty rows": Attend([3, 5], [0, 0], 4, 2, 128, B16, 16),
-    "cache shorter than the pass": Attend([6, 300], [4, 140], 4, 2, 64, B16, 16),
-    "window of one": Attend([5, 140], [60, 300], 4, 2, 64, B16, 16, window=1),
-    "window": Attend([5, 9, 1], [700, 45, 129], 8, 2, 128, F16, 16, window=40),
-    "window and sinks": Attend([5, 9, 1], [700, 45, 390], 8, 2, 128, B16, 16, window=40, sinks=4),
-    "sinks past a tile": Attend([5, 200], [900, 700], 4, 2, 64, B16, 64, window=33, sinks=130),
-    "sinks alone beside one": Attend([3], [400], 4, 1, 64, F16, 128, window=1, sinks=1),
-    "window over a chunk": Attend([400], [650], 4, 2, 128, B16, 32, window=100, sinks=3),
-    "window longer than the cache": Attend([5], [200], 4, 2, 64, B16, 16, window=5000, sinks=9),
-    "peaked scores": Attend([9, 150], [800, 400], 4, 2, 128, B16, 64, spread=12.0),
-    "peaked scores in fp16": Attend([9, 150], [800, 400], 4, 2, 128, F16, 64, spread=12.0),
-    "large scale": Attend([4], [300], 4, 2, 64, B16, 16, scale=3.0),
+    "ragged passes": spec([1, 9, 5, 3, 16, 2], [700, 33, 5, 1030, 128, 450], 8, 2, 128, B16, 32),
+    "seven heads per key head": spec([4, 20], [50, 300], 14, 2, 64, F16, 16),
+    "three heads per key head": spec([50], [190], 3, 1, 128, B16, 128),
+    "sixteen heads, one key head": spec([7, 9], [300, 200], 16, 1, 128, B16, 256),
+    "128 heads per key head": spec([3], [150], 128, 1, 64, B16, 64),
+    "48 heads per key head": spec([6, 1], [40, 400], 96, 2, 128, F16, 64),
+    "chunk": spec([300], [300], 2, 2, 128, B16, 64),
+    "chunk over a cache": spec([200, 77], [520, 500], 4, 1, 64, F16, 16, heads_first=True),
+    "chunk beside passes": spec([1, 260, 4], [600, 413, 90], 8, 4, 128, B16, 16),
+    "empty requests": spec([3, 0, 2, 0], [0, 0, 40, 70], 4, 2, 64, B16, 16),
+    "only empty rows": spec([3, 5], [0, 0], 4, 2, 128, B16, 16),
+    "cache shorter than the pass": spec([6, 300], [4, 140], 4, 2, 64, B16, 16),
+    "window of one": spec([5, 140], [60, 300], 4, 2, 64, B16, 16, window=1),
+    "window": spec([5, 9, 1], [700, 45, 129], 8, 2, 128, F16, 16, window=40),
+    "window and sinks": spec([5, 9, 1], [700, 45, 390], 8, 2, 128, B16, 16, window=40, sinks=4),
+    "sinks past a tile": spec([5, 200], [900, 700], 4, 2, 64, B16, 64, window=33, sinks=130),
+    "sinks alone beside one": spec([3], [400], 4, 1, 64, F16, 128, window=1, sinks=1),
+    "window over a chunk": spec([400], [650], 4, 2, 128, B16, 32, window=100, sinks=3),
+    "window longer than the cache": spec([5], [200], 4, 2, 64, B16, 16, window=5000, sinks=9),
+    "peaked scores": spec([9, 150], [800, 400], 4, 2, 128, B16, 64, spread=12.0),
+    "peaked scores in fp16": spec([9, 150], [800, 400], 4, 2, 128, F16, 64, spread=12.0),
+    "large scale": spec([4], [300], 4, 2, 64, B16, 16, scale=3.0),
     # several tiles and several items per CTA
-    "many passes": Attend([1 + i % 9 for i in range(40)], [100 + 97 * i for i in range(40)], 16, 4,
+    "many passes": spec([1 + i % 9 for i in range(40)], [100 + 97 * i for i in range(40)], 16, 4,
                           128, B16, 64),
-    "many passes, small pages": Attend([1 + i % 5 for i in range(60)], [3000 - 49 * i for i in
+    "many passes, small pages": spec([1 + i % 5 for i in range(60)], [3000 - 49 * i for i in
                                        range(60)], 12, 4, 64, F16, 16, heads_first=True),
-    "long chunks": Attend([900, 1100], [2600, 1100], 8, 2, 128, B16, 64),
-    "long chunks, odd groups": Attend([700, 333, 40], [3000, 333, 2000], 15, 3, 64, F16, 32),
-    "mixed batch": Attend([500, 3, 9, 0, 260, 1] + [4] * 30, [1500, 0, 2500, 9, 2000, 1] +
+    "long chunks": spec([900, 1100], [2600, 1100], 8, 2, 128, B16, 64),
+    "long chunks, odd groups": spec([700, 333, 40], [3000, 333, 2000], 15, 3, 64, F16, 32),
+    "mixed batch": spec([500, 3, 9, 0, 260, 1] + [4] * 30, [1500, 0, 2500, 9, 2000, 1] +
                           [600 + 31 * i for i in range(30)], 28, 4, 128, F16, 16),
-    "many windows": Attend([1 + i % 9 for i in range(40)], [200 + 190 * i for i in range(40)], 16,
+    "many windows": spec([1 + i % 9 for i in range(40)], [200 + 190 * i for i in range(40)], 16,
                            4, 64, B16, 16, window=700, sinks=5),
-    "long windows over chunks": Attend([1500, 800], [2500, 4000], 8, 4, 128, B16, 128, window=900,
+    "long windows over chunks": spec([1500, 800], [2500, 4000], 8, 4, 128, B16, 128, window=900,
                                        sinks=200),
-    "peaked long chunks": Attend([900, 1100], [2600, 1500], 8, 2, 128, F16, 64, spread=10.0),
-    "tiny scale": Attend([4], [300], 4, 2, 64, F16, 16, scale=1e-20),
+    "peaked long chunks": spec([900, 1100], [2600, 1500], 8, 2, 128, F16, 64, spread=10.0),
+    "tiny scale": spec([4], [300], 4, 2, 64, F16, 16, scale=1e-20),
 }
+
+
+@functools.lru_cache(maxsize=None)
+def problem(name):
+    args, kwargs = ATTENDS[name]
+    return Attend(*args, **kwargs)
 
 
 @pytest.mark.parametrize("name", ATTENDS)
 def test_attend(lib, name):
-    a = ATTENDS[name]
+    a = problem(name)
     r = a.runner()
     out = torch.full(a.q.shape, float("nan"), dtype=a.q.dtype, device="cuda")
     r.attend(*a.args(), out=out)
@@ -305,7 +316,7 @@ def test_attend_rising_scores(lib):
 
 
 def test_attend_leaves_rows_of_no_request(lib):
-    a = ATTENDS["ragged passes"]
+    a = problem("ragged passes")
     q, qs, kv, table = a.args()
     wide = torch.cat([q, q[:2]])
     out = torch.full(wide.shape, 7.0, dtype=q.dtype, device="cuda")
@@ -316,7 +327,7 @@ def test_attend_leaves_rows_of_no_request(lib):
 
 def test_attend_strides(lib):
     """Queries inside a joint projection, results in [heads][tokens] order."""
-    a = ATTENDS["chunk beside passes"]
+    a = problem("chunk beside passes")
     q, qs, kv, table = a.args()
     T, H, D = q.shape
     joint = torch.randn(T, H + 8, D, device="cuda").to(q.dtype)
@@ -327,7 +338,7 @@ def test_attend_strides(lib):
 
 
 def test_attend_other_stream_and_graph(lib):
-    a = ATTENDS["window and sinks"]
+    a = problem("window and sinks")
     r, args = a.runner(), a.args()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -349,7 +360,7 @@ def test_attend_reports_bad_pages_and_lengths(lib):
     """A table entry outside the pool, a cache length past the table and
     request bounds past the rows are reported; nothing is read out of range,
     and other requests are not touched by it."""
-    a = ATTENDS["ragged passes"]
+    a = problem("ragged passes")
     q, qs, kv, table = a.args()
     for spoil in ("page", "negative page", "length", "negative length", "bounds", "order"):
         qs2, kv2, t2 = qs.clone(), kv.clone(), table.clone()
