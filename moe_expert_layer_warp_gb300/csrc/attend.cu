@@ -62,7 +62,6 @@ constexpr int kThreads = 640;
 constexpr int kHalf = kTile / 2;  // keys of one softmax thread
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 constexpr int kPlanThreads = 256;
-constexpr int kPerThread = MOE_MAX_REQUESTS / kPlanThreads;
 // What an item costs beside its tiles, in tiles, when the work is cut.
 constexpr int kItemCost = 3;
 // The reference m follows the row's maximum only when that has grown by more
@@ -210,58 +209,74 @@ struct Start {
   long long each, more;  // units per CTA; the first `more` have one more
 };
 
-MOE_DEV long long divide(long long a, long long b) {  // of non-negative numbers
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// The units of one request for one key head; every lane of the warp has the
-// same request.
-MOE_DEV long long warp_units(const AttendArgs& a, const Request& r, int fixed) {
-  long long n = 0;
-  for (int q = threadIdx.x & 31; q * fixed < r.q; q += 32)
-    n += make_item(a, r, q, fixed).n + kItemCost;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
+// a / b of non-negative numbers below 2^62, b > 0; short for 32 bits, and small
+// for more (64-bit division is 350 instructions at every place it stands).
+MOE_DEV long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  unsigned long long q = 0, r = 0;
+#pragma unroll 1
+  for (int i = 61; i >= 0; --i) {
+    r = 2 * r + (a >> i & 1);
+    q *= 2;
+    if (r >= (unsigned long long)b) {
+      r -= b;
+      ++q;
+    }
+  }
+  return q;
 }
 
 // The CTA's range: prefix sums over the requests' units, then the place of
-// its first one. The first kPlanThreads threads call it, warps converged.
-MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
+// its first one. The first kPlanThreads threads call it, warps converged;
+// `count` [MOE_MAX_REQUESTS] and `part` [8] are shared memory. (Every loop
+// stays a loop: unrolled, this took a quarter of the kernel's instructions,
+// which are fetched anew by every launch.)
+MOE_DEV void find_start(const Params& p, long long* count, long long* part, Start* out) {
   const AttendArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int fixed = 2 * p.tpt, H = a.cache.n_kv_heads;
+  const int fixed = 2 * p.tpt, H = a.cache.n_kv_heads, B = a.n_requests;
   constexpr uint32_t kAll = 0xffffffffu;
-  Request req[kPerThread];
-  long long count[kPerThread], sum = 0;
-  bool any_bad = false;
-  const int per = (a.n_requests + kPlanThreads - 1) / kPlanThreads;  // requests per thread
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * per + i;
+  // units of every request for one key head: a request of one block by its
+  // own thread, longer ones by the warp
+#pragma unroll 1
+  for (int b0 = warp * 32; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + lane;
+    Request mine = {0, 0, 0};
     bool bad = false;
-    req[i] = Request{0, 0, 0};
-    if (i < per && b < a.n_requests) req[i] = request(a, p.page_shift, b, &bad);
-    any_bad |= bad;
-  }
+    if (b < B) mine = request(a, p.page_shift, b, &bad);
+    if (bad && blockIdx.x == 0) report_error(a.err, ERR_CHECK, 0xA20);
+    long long units = 0;
+    uint32_t todo = __ballot_sync(kAll, mine.q > 0);
+    const uint32_t longer = __ballot_sync(kAll, mine.q > fixed);
+    // first all short ones together (a turn of their own threads), then the
+    // long ones one after the other
+#pragma unroll 1
+    while (todo) {
+      const bool together = (todo & ~longer) != 0;
+      const int from = together ? lane : __ffs(todo) - 1;
+      todo &= together ? longer : todo - 1;
+      Request r;
+      r.first = 0;
+      r.q = __shfl_sync(kAll, mine.q, from);
+      r.len = __shfl_sync(kAll, mine.len, from);
+      const bool skip = together && (r.q == 0 || r.q > fixed);
+      long long n = 0;
+#pragma unroll 1
+      for (int q = together ? 0 : lane; !skip && q * fixed < r.q; q += 32)
+        n += make_item(a, r, q, fixed).n + kItemCost;
+      if (!together) {
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    count[i] = 0;
-    if (i >= per) continue;
-    // a request of one block by its own thread, longer ones by the warp
-    count[i] = req[i].q > 0 ? make_item(a, req[i], 0, fixed).n + kItemCost : 0;
-    uint32_t longer = __ballot_sync(kAll, req[i].q > fixed);
-    while (longer) {
-      const int from = __ffs(longer) - 1;
-      longer &= longer - 1;
-      const Request r = {__shfl_sync(kAll, req[i].first, from), __shfl_sync(kAll, req[i].q, from),
-                         __shfl_sync(kAll, req[i].len, from)};
-      const long long n = warp_units(a, r, fixed);
-      if (lane == from) count[i] = n;
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
+      }
+      if (together ? !skip : lane == from) units = n;
     }
-    sum += count[i];
+    if (b < B) count[b] = units;
   }
-  if (any_bad && blockIdx.x == 0) report_error(a.err, ERR_CHECK, 0xA20);
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+  const int per = (B + kPlanThreads - 1) / kPlanThreads, mine0 = tid * per;
+  long long sum = 0;
+#pragma unroll 1
+  for (int b = mine0; b < min(mine0 + per, B); ++b) sum += count[b];
   long long incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -278,6 +293,7 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   }
   total *= H;
   before *= H;
+  sum *= H;
   // no more CTAs than units, so that no range among them is empty: the first
   // `more` ranges are one unit longer than the others
   const long long C = min((long long)gridDim.x, total), c = blockIdx.x;
@@ -286,35 +302,22 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   if (tid == 0) {
     out->w.b = 0;
     out->w.left = (int)(w1 - w0);
-    out->joins = 0;
     out->each = each;
     out->more = more;
   }
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-  if (w1 == w0) return;
-  // the request whose units hold w0, then the warp looks through its blocks
-  Request r = {0, 0, 0};
-  int b = -1, h = 0;
-  long long rem = 0;
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const long long n = count[i] * H;
-    if (w0 >= before && w0 < before + n) {
-      b = tid * per + i;
-      r = req[i];
-      h = (int)divide(w0 - before, count[i]);
-      rem = w0 - before - h * count[i];
-    }
-    before += n;
-  }
-  const uint32_t here = __ballot_sync(kAll, b >= 0);
+  // the warp with the request whose units hold w0 looks through its blocks
+  const uint32_t here = __ballot_sync(kAll, w1 > w0 && w0 >= before && w0 < before + sum);
   if (here == 0) return;
   const int from = __ffs(here) - 1;
-  r = Request{__shfl_sync(kAll, r.first, from), __shfl_sync(kAll, r.q, from),
-              __shfl_sync(kAll, r.len, from)};
-  b = __shfl_sync(kAll, b, from);
-  h = __shfl_sync(kAll, h, from);
-  rem = __shfl_sync(kAll, rem, from);
+  int b = __shfl_sync(kAll, mine0, from);
+  long long rem = w0 - __shfl_sync(kAll, before, from);
+#pragma unroll 1
+  while (rem >= count[b] * H) rem -= count[b++] * H;
+  const int h = (int)divide(rem, count[b]);
+  rem -= h * count[b];
+  bool bad;
+  const Request r = request(a, p.page_shift, b, &bad);
+#pragma unroll 1
   for (int q0 = 0; q0 * fixed < r.q; q0 += 32) {
     const int q = q0 + lane;
     Item it;
@@ -336,13 +339,11 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
       out->w.block = q;
       out->w.u0 = (int)u0;
       out->r = r;
-      if (u0 > kItemCost && n - u0 <= w1 - w0) {
-        out->joins = 1;
-        out->row0 = it.row0;
-        out->ntok = it.ntok;
-        out->head0 = h * a.group;
-        out->unit = w0 - u0 + kItemCost;
-      }
+      out->joins = u0 > kItemCost && n - u0 <= w1 - w0;
+      out->row0 = it.row0;
+      out->ntok = it.ntok;
+      out->head0 = h * a.group;
+      out->unit = w0 - u0 + kItemCost;
     }
     const long long block_sum = __shfl_sync(kAll, upto, 31);
     if (rem < block_sum) return;
@@ -350,19 +351,42 @@ MOE_DEV void find_start(const Params& p, long long* part, Start* out) {
   }
 }
 
-// Bounded wait that gives up at once when any role of the CTA has.
-MOE_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                           unsigned int* err, unsigned int site) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  for (unsigned int i = 0; i < kWaitLimitIters; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if ((i & 63u) == 63u && global_ns() - t0 > kWaitLimitNs) break;
-  }
-  report_error(err, ERR_TIMEOUT, site);
-  *abort_flag = 1;
-  return false;
+// Bounded wait that gives up at once when any role of the CTA has: `lost`
+// then holds the site of the first wait given up, which is reported at the
+// kernel's end. Kept short, for it stands in twenty places: the kernel's warps
+// run four different programs, and what does not fit the SM's instruction
+// cache is fetched again at every turn of an item. A try suspends the warp for
+// up to kTryNs; the limit is about half a second of them.
+constexpr uint32_t kTryNs = 2000u;
+constexpr int kTries = 1 << 18;
+MOE_DEV bool try_longer(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return done != 0;
+}
+MOE_DEV bool try_now(uint64_t* bar, uint32_t parity) {  // without suspending
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+MOE_DEV bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* lost, int site) {
+  bool done = mbar_try_wait(bar, parity);
+#pragma unroll 1
+  for (int i = 0; !done && i < kTries && *lost == 0; ++i) done = try_longer(bar, parity);
+  if (!done && *lost == 0) *lost = site;
+  return done;
 }
 
 MOE_DEV void fence_proxy_async_smem() {
@@ -442,7 +466,7 @@ MOE_DEV void quad_transpose(uint4 (&v)[4], int lane) {
 // The parts of an item in key order, a thread per (row, 4 columns). All
 // softmax threads of the CTA that has the item's last tile call it.
 template <int kDim, bool kF16>
-MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* abort_flag) {
+MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
   using Z = Sizes<kDim>;
   const AttendArgs& a = p.a;
   // the CTA with the item's first tile
@@ -458,8 +482,8 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* abort_fl
       unsigned long long v;
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
       if (v == p.call) break;
-      if ((i & 63u) == 63u && (*abort_flag || global_ns() - t0 > kWaitLimitNs)) {
-        report_error(a.err, ERR_TIMEOUT, 0xA70);
+      if ((i & 63u) == 63u && (*lost || global_ns() - t0 > kWaitLimitNs)) {
+        *lost = 0xA70;
         break;
       }
     }
@@ -524,7 +548,7 @@ struct Misc {
   Start start;
   long long part[8];
   uint32_t tmem;
-  int abort_flag;
+  int lost;
 };
 static_assert(sizeof(Misc) <= 512, "misc words");
 constexpr int kOffStat = 512;  // then [2 streams][2][128 rows] floats
@@ -543,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     return;
   }
   Misc& m = *reinterpret_cast<Misc*>(smem + Z::kOffMisc);
-  volatile int* abort_flag = &m.abort_flag;
+  volatile int* lost = &m.lost;
   // the same value in every lane, and known to be
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) - 4;  // of the softmax warps
   const int lane = threadIdx.x & 31;
@@ -562,7 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(&m.turn[s], 1);
       mbar_init(&m.drain[s], 1);
     }
-    m.abort_flag = 0;
+    m.lost = 0;
+    m.start.joins = 0;
     fence_mbar_init();
   }
   if (warp == -3) umma::tmem_alloc(&m.tmem, kCols);
@@ -572,14 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < kPlanThreads) find_start(p, m.part, &m.start);
+  // (the ring holds the plan's counts until the first tiles are on their way)
+  if (threadIdx.x < kPlanThreads)
+    find_start(p, reinterpret_cast<long long*>(smem + Z::kOffRing), m.part, &m.start);
+  fence_proxy_async_smem();
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
   bool ok = true;  // no wait of this role has been lost
-  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int site) {
-    ok = __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, abort_flag, a.err, site));
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+    ok = __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, lost, site));
   };
   Part pt;
 
@@ -605,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // the next query tile, if its slot is free: a box is the 128 / group
     // tokens of a tile, times the group's heads, in the order of the tile's rows
     auto try_queries = [&]() {
-      if (!__all_sync(0xffffffffu, mbar_try_wait(&m.q_empty[slot], q_phase ^ 1u))) return;
+      if (!__all_sync(0xffffffffu, try_now(&m.q_empty[slot], q_phase ^ 1u))) return;
       if (lane == 0) {
         mbar_arrive_expect_tx(&m.q_full[slot], p.tpt * a.group * kDim * 2);
 #pragma unroll
@@ -618,20 +646,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       q_row += p.tpt;
       if (slot) q_phase ^= 1u;
       slot ^= 1;
-    };
-    // waits for a free stage of the ring (or for nothing), and meanwhile for
-    // the slots of the queries still to load
-    auto wait_free = [&](uint64_t* bar) {
-      const unsigned long long t0 = global_ns();
-      for (unsigned int i = 0; ok && i < kWaitLimitIters; ++i) {
-        if (queries > 0) try_queries();
-        if (bar ? __all_sync(0xffffffffu, mbar_try_wait(bar, phase ^ 1u)) : queries == 0) return;
-        if ((i & 63u) == 63u)
-          ok = __all_sync(0xffffffffu, !*abort_flag && global_ns() - t0 <= kWaitLimitNs);
-      }
-      if (!*abort_flag) report_error(a.err, ERR_TIMEOUT, 0xA30);
-      *abort_flag = 1;
-      ok = false;
     };
     while (walk.next(&pt)) {
       const Item& it = pt.it;
@@ -657,27 +671,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         return pg;
       };
-      // Keys 0..lead-1, then values j, keys j + lead, for j = 0..n-1.
-      int jk = 0, jv = 0;
-      // the pages of tiles jv .. jv + 3, fetched that far ahead
-      int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3 = page_of(3);
-      while (jv < n) {
-        const bool is_k = jk < n && jk < jv + lead;
+      // Keys 0..lead-1, then values j, keys j + lead, for j = 0..n-1; and at the
+      // end the queries that are still to load.
+      int jk = 0, jv = 0, fetched = 0;
+      int pg0 = -1, pg1 = -1, pg2 = -1, pg3 = -1;  // pages of tiles jv .. jv + 3
+      while (ok && (jv < n || queries > 0)) {
+#pragma unroll 1
+        for (; fetched < jv + 4; ++fetched) {
+          pg0 = pg1;
+          pg1 = pg2;
+          pg2 = pg3;
+          pg3 = page_of(fetched);
+        }
+        const bool is_k = jk < n && jk < jv + lead, tiles = jv < n;
         const int j = is_k ? jk : jv, pg = is_k && jk != jv ? pg1 : pg0;
         const uint32_t wanted = __ballot_sync(0xffffffffu, pg >= 0);
-        wait_free(&m.empty[stage]);
-        if (ok) {
-          if (lane == 0 && !which)
-            mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim * 2);
-          __syncwarp();
-          const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
-          const int row = tile_of(it, pt.t0 + j) * kTile & (page - 1);  // 0 in small pages
-#pragma unroll
-          for (int half = 0; half < kHalves; ++half)
-            if (pg >= 0 && ((half * n_pages + lane) & 1) == which)
-              tma_load_4d_at(ring + stage * Z::kTileBytes + half * kHalfBytes, map, half * 64,
-                             walk.h, row, pg, &m.full[stage], policy);
+        // a free stage of the ring, and meanwhile free slots for the queries
+        bool free = false;
+#pragma unroll 1
+        for (int i = 0; ok && i < 64 * kTries; ++i) {
+          if (queries > 0) try_queries();
+          free = tiles && __all_sync(0xffffffffu, queries > 0
+                                                      ? try_now(&m.empty[stage], phase ^ 1u)
+                                                      : try_longer(&m.empty[stage], phase ^ 1u));
+          if (free || (!tiles && queries == 0)) break;
+          ok = i + 1 < 64 * kTries && __all_sync(0xffffffffu, *lost == 0);
         }
+        if (!ok && *lost == 0) *lost = 0xA30;
+        if (!free) continue;
+        if (lane == 0 && !which)
+          mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim * 2);
+        __syncwarp();
+        const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
+        const int row = tile_of(it, pt.t0 + j) * kTile & (page - 1);  // 0 in small pages
+#pragma unroll
+        for (int half = 0; half < kHalves; ++half)
+          if (pg >= 0 && ((half * n_pages + lane) & 1) == which)
+            tma_load_4d_at(ring + stage * Z::kTileBytes + half * kHalfBytes, map, half * 64, walk.h,
+                           row, pg, &m.full[stage], policy);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
@@ -686,20 +717,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           ++jk;
         } else {
           ++jv;
-          pg0 = pg1;
-          pg1 = pg2;
-          pg2 = pg3;
-          pg3 = page_of(jv + 3);
         }
       }
-      if (queries > 0) wait_free(nullptr);
     }
     // After a lost wait the tiles still in flight must land before the CTA
     // ends; without one, every tile has been waited for by the MMA warps.
-    if (!ok && lane == 0) {
-      for (uint32_t ph = 0; ph < 2; ++ph) {
-        for (int i = 0; i < kStages; ++i) mbar_wait_for(&m.full[i], ph, a.err, 0xA31, 1000000ull);
-        for (int i = 0; i < 2; ++i) mbar_wait_for(&m.q_full[i], ph, a.err, 0xA61, 1000000ull);
+    if (!ok) {
+#pragma unroll 1
+      for (int i = 0; i < 2 * 500 * (kStages + 2); ++i) {      // a millisecond for each, or two
+        const int b = i / 1000;
+        try_longer(b < kStages ? &m.full[b] : &m.q_full[b - kStages], i & 1);
       }
     }
   } else if (warp < 0) {
@@ -766,29 +793,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int lead = two ? 1 : 2;                    // the next key tile of the stream
       const int last = two ? n - 1 : ((n - 1 - s) & ~1) + s;  // its last tile (< s: it has none)
       bool first = true;
-      for (int j = 0; j < min(lead, n); ++j) {
-        const int st = next_tile();
-        if (!two && j != s) {
-          pass(&m.empty[st]);
-        } else {
-          if (sees(j)) scores(slot, st);
-          commit(&m.empty[st]);
-        }
-      }
-      if (last < lead) commit(&m.q_empty[slot]);
-      for (int j = 0; j < n; ++j) {
-        const bool more = j + lead < n, mine = two || (j & 1) == s;
-        const int vt = next_tile();
+      if (last < 0) pass(&m.q_empty[slot]);            // no tile of its own at all
+      for (int j = -lead; j < n; ++j) {
+        // V_j and K_{j+lead}, in the ring's order
+        const bool has_v = j >= 0, more = j + lead < n;
+        const bool mine = two || (j & 1) == s;         // (lead is even where that matters)
+        if (!has_v && !more) continue;
+        const int vt = has_v ? next_tile() : 0;
         const int kt = more ? next_tile() : 0;
         if (!mine) {
-          pass(&m.empty[vt]);
+          if (has_v) pass(&m.empty[vt]);
           if (more) pass(&m.empty[kt]);
           continue;
         }
         // rows of V that no row of the item sees may hold anything: their
         // weights are 0, and 0 · NaN is not
         const int key0 = tile_of(it, pt.t0 + j) * kTile;
-        const bool now = sees(j);
+        const bool now = has_v && sees(j);
         if (ok && now && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
           unsigned char* v = smem + Z::kOffRing + vt * Z::kTileBytes;
           for (int i = lane; i < kTile * kHalves * 8; i += 32) {
@@ -804,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // issued in one piece. Were they mixed with the other's, both scores
         // would be ready late and together, both softmaxes would run at the
         // same time, and the tensor cores would wait for them.
-        if (two) {
+        if (two && has_v) {
           wait(&m.turn[s], turn, 0xA44);
           turn ^= 1u;
         }
@@ -819,9 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           first = false;
         }
         if (more && sees(j + lead)) scores(slot, kt);  // into S, behind the product that reads P
-        if (two) pass(&m.turn[s ^ 1]);
+        if (two && has_v) pass(&m.turn[s ^ 1]);
         if (j == last && !first) commit(&m.o_full[s]);
-        commit(&m.empty[vt]);
+        if (has_v) commit(&m.empty[vt]);
         if (more) commit(&m.empty[kt]);
         if (more && j + lead == last) commit(&m.q_empty[slot]);  // the last scores are issued
       }
@@ -829,7 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // Every MMA, and every arrival that hangs on one, is done before tensor
     // memory is released.
     umma::commit_elect(&m.drain[s]);
-    mbar_wait(&m.drain[s], 0, a.err, 0xA43);
+#pragma unroll 1
+    for (int i = 0; i < kTries && !try_longer(&m.drain[s], 0); ++i) {
+    }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax --
@@ -1065,10 +1088,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.left + blockIdx.x), "l"(p.call)
                      : "memory");
     }
-    if (m.start.joins) join_parts<kDim, kF16>(p, m.start, abort_flag);
+    if (m.start.joins) join_parts<kDim, kF16>(p, m.start, lost);
   }
   umma::fence_before_sync();
   __syncthreads();
+  if (threadIdx.x == 0 && m.lost) report_error(a.err, ERR_TIMEOUT, m.lost);
   if (warp == -3) umma::tmem_dealloc(tmem, kCols);
 }
 
