@@ -15,6 +15,15 @@
 // the token's. (Everything in fp64 took 848 us for 20011 tokens of 256
 // experts; close tokens whole in fp64, 81 us.) Without a bias, c is monotone
 // in the logit, and experts are compared by their logits, exactly.
+//
+// 20011 tokens of 256 experts in 8 groups (sigmoid, bias, bf16) take 19.4 us;
+// the logits alone would take 1.7. What bounds it is issuing a token's some
+// 700 instructions and waiting for one lane's after another's: scores 5 us,
+// groups 4, the (k + 1)-th best 1, candidates and ranks 4, weights 4. A group's
+// experts lie in its own lanes, so its sum takes log2(lanes) steps and no
+// shared memory (groups across lanes: 28 us). Warps that stay and load the
+// next token ahead were slower (22.9 us): the tokens that take fp64 then hold
+// up others. 64 tokens take 3.8 us, 9 take 2.6: a launch and one token's chain.
 #include <limits.h>
 #include <math.h>
 
@@ -25,6 +34,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kPerSm = 8;  // blocks, of 64 registers a thread: what is rare spills (6: 21.3 us for 19.4)
 constexpr uint32_t kAll = 0xffffffffu;
 
 template <typename T>
@@ -52,14 +62,21 @@ MOE_DEV float load_logit(const T* p) {
   return v <= lowest<T>() ? -INFINITY : v;
 }
 
-// Order-preserving integer keys of floats (−0 and +0 have one key); kNone is
-// below every float's key.
-constexpr int kNone = INT_MIN;
-MOE_DEV int order_key(float f) {
-  const int u = __float_as_int(f + 0.f);
-  return u ^ ((u >> 31) & 0x7fffffff);
+// What experts are compared by: kMasked for a masked expert, kAbsent for one
+// that is not there or not among the groups kept; every other is above both.
+constexpr float kAbsent = -INFINITY;
+constexpr float kMasked = -3.402823466e+38f;
+
+MOE_DEV float warp_most(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
-MOE_DEV float key_value(int key) { return __int_as_float(key ^ ((key >> 31) & 0x7fffffff)); }
+MOE_DEV float warp_least(float v) {
+  float r;
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 
 MOE_DEV double warp_max(double v) {
 #pragma unroll
@@ -75,9 +92,13 @@ MOE_DEV double warp_add(double v) {
 
 // One token by one warp, everything in fp64: the chosen expert j and its
 // weight in lane j. Expert e is in lane e % 32, register e / 32.
+struct Chosen {
+  int e;
+  float w;
+};
 template <typename T>
-__device__ __noinline__ void route_exact(const moe_router_desc& r, const T* row,
-                                         const float* bias, int* expert, float* weight) {
+__device__ __noinline__ Chosen route_exact(const moe_router_desc& r, const T* row,
+                                           const float* bias) {
   constexpr int kPerLane = MOE_MAX_EXPERTS / 32;
   const int lane = threadIdx.x & 31;
   const int E = r.n_experts, size = E / r.n_groups;
@@ -113,6 +134,13 @@ __device__ __noinline__ void route_exact(const moe_router_desc& r, const T* row,
     const int e = lane + 32 * i;
     c[i] = l[i] == -INFINITY ? -INFINITY : s[i] + (bias ? (double)bias[e] : 0.0);
   }
+  // groups of one choice each, and experts, compare by logits if no bias is
+  // there: scores may be too small even for fp64
+  auto by_logit = [&] {
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) c[i] = l[i];
+  };
+  if (!bias && r.group_top != 2) by_logit();
   if (r.top_groups < r.n_groups) {
     // lane g ends with group g's score
     double mine = -INFINITY;
@@ -149,6 +177,7 @@ __device__ __noinline__ void route_exact(const moe_router_desc& r, const T* row,
       if (e < E && !((kept >> (e / size)) & 1u)) left &= ~(1u << i);
     }
   }
+  if (!bias) by_logit();
   int my_e = 0;
   double my_s = 0;
   for (int j = 0; j < r.top_k; ++j) {
@@ -187,8 +216,7 @@ __device__ __noinline__ void route_exact(const moe_router_desc& r, const T* row,
     const double sum = warp_add(w);
     w = sum > 0.0 ? w / sum : 0.0;
   }
-  *expert = my_e;
-  *weight = (float)(w * r.scale);
+  return Chosen{my_e, (float)(w * r.scale)};
 }
 
 // Order-preserving integer key of a double.
@@ -237,25 +265,29 @@ MOE_DEV float reciprocal_fast(float x) {  // good to 2^-23
   return y;
 }
 
-// The descriptor, and what follows from it.
+// The descriptor, and what follows from it. Every group (all experts, if none
+// is left out) has the same number of lanes, a power of two, and they have its
+// experts in order, `per` each; the last ones may have fewer.
 struct Router {
   moe_router_desc d;
-  int size;         // experts of a group
-  int to_group;     // e / size = e·to_group >> 16, for e < 256
-  int share_shift;  // log2 of the lanes that look through one group
-  int wide;         // rows are whole, aligned 16-byte pieces
+  int groups, size, per;
+  int shift;      // log2 of the lanes of a group
+  int whole;      // every lane has kPer experts
+  int wide;       // a lane's logits are aligned 16-byte pieces, or it has none
+  int wide_bias;  // and its bias is
 };
 
-// One warp per token; lane holds kPer consecutive experts.
+// One warp per token; a lane has kPer experts or fewer, consecutive ones.
 template <typename T, int kPer>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, kPerSm)
     route_grouped_kernel(const __grid_constant__ Router p, const T* __restrict__ logits,
                          int64_t row_stride, const float* __restrict__ bias, int n,
                          int32_t* __restrict__ topk_idx, float* __restrict__ topk_w) {
-  // choices of the warp's token, one float of padding after every 32
-  __shared__ float choice[kWarps][32 * kPer + kPer];
-  // the experts that may be among the k, with their keys; then by rank
-  __shared__ int2 cand[kWarps][32];
+  // what the experts of the warp's token are compared by
+  __shared__ alignas(16) float choice[kWarps][32][kPer];
+  // the experts that may be among the k; then by rank
+  __shared__ alignas(16) float cand_c[kWarps][32];
+  __shared__ int cand_e[kWarps][32];
   pdl_wait();
   pdl_trigger();
   const moe_router_desc& r = p.d;
@@ -266,7 +298,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   const T* row = logits + t * row_stride;
   const bool sigmoid = r.score == MOE_SCORE_SIGMOID;
   const bool by_logit = bias == nullptr;   // experts compare by their logits
-  const bool grouped = r.top_groups < r.n_groups;
+  const bool grouped = p.groups > 1;
+  const int share = 1 << p.shift;
+  const int g = lane >> p.shift, sub = lane & (share - 1);
+  const int first = g * p.size + sub * p.per;
+  const int have = g < p.groups ? max(0, min(p.per, p.size - sub * p.per)) : 0;
 
   float l[kPer];
   if (p.wide) {
@@ -274,25 +310,16 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int v = 0; v < kPer; v += kVec) {
       alignas(16) T piece[kVec];
-      if (lane * kPer + v < E) {
-        if constexpr (kVec * sizeof(T) == 16) {
-          *reinterpret_cast<uint4*>(piece) =
-              __ldg(reinterpret_cast<const uint4*>(row + lane * kPer + v));
-        } else {
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) piece[i] = row[lane * kPer + v + i];
-        }
+      if constexpr (kVec * sizeof(T) == 16) {
+        if (have)
+          *reinterpret_cast<uint4*>(piece) = __ldg(reinterpret_cast<const uint4*>(row + first + v));
       }
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const float x = lane * kPer + v < E ? widen<T>(piece[i]) : -INFINITY;
-        l[v + i] = x <= lowest<T>() ? -INFINITY : x;
-      }
+      for (int i = 0; i < kVec; ++i) l[v + i] = have ? widen<T>(piece[i]) : -INFINITY;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      l[i] = lane * kPer + i < E ? load_logit(row + lane * kPer + i) : -INFINITY;
+    for (int i = 0; i < kPer; ++i) l[i] = i < have ? widen<T>(row[first + i]) : -INFINITY;
   }
 
   // softmax: the row's maximum and sum, for the choices and the weights
@@ -301,113 +328,149 @@ __global__ void __launch_bounds__(kWarps * 32)
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) m = fmaxf(m, l[i]);
-    top = key_value(__reduce_max_sync(kAll, order_key(m)));
-    if (top == -INFINITY) top = 0.f;       // every expert masked: scores 0
+    top = warp_most(m);
+    if (top <= lowest<T>()) top = 0.f;     // every expert masked: scores 0
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += expf(l[i] - top);
+    for (int i = 0; i < kPer; ++i) sum += l[i] <= lowest<T>() ? 0.f : expf(l[i] - top);
     sum = warp_sum(sum);
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
 
-  // what experts are compared by, as keys
-  int key[kPer];
-  bool unsure = false;
-  if (by_logit) {
+  // what experts, and groups, are compared by
+  const bool sums = grouped && r.group_top == 2;
+  float c[kPer];
+  auto store_choices = [&] {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) key[i] = lane * kPer + i < E ? order_key(l[i]) : kNone;
-  }
-  if (!by_logit || (grouped && r.group_top == 2)) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane * kPer + i;
-      const float s =
-          sigmoid ? reciprocal_fast(1.f + exp_fast(-l[i])) : exp_fast(l[i] - top) * inv;
-      float c = -INFINITY;
-      if (e < E && l[i] != -INFINITY) c = by_logit ? s : s + __ldg(bias + e);
-      if (!by_logit) key[i] = e < E ? order_key(c) : kNone;
-      if (grouped) choice[warp][e + (e >> 5)] = c;
+    for (int i = 0; i < kPer; i += kPer < 4 ? 2 : 4) {
+      if constexpr (kPer < 4)
+        *reinterpret_cast<float2*>(&choice[warp][lane][i]) = make_float2(c[i], c[i + 1]);
+      else
+        *reinterpret_cast<float4*>(&choice[warp][lane][i]) =
+            make_float4(c[i], c[i + 1], c[i + 2], c[i + 3]);
     }
-  } else if (grouped) {                    // groups by their largest logit
+  };
+  auto take_logits = [&] {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane * kPer + i;
-      choice[warp][e + (e >> 5)] = l[i];
+    for (int i = 0; i < kPer; ++i)
+      c[i] = i >= have ? kAbsent : l[i] <= lowest<T>() ? kMasked : l[i];
+  };
+  if (!by_logit || sums) {
+    if (sigmoid) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = reciprocal_fast(1.f + exp_fast(-l[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = exp_fast(l[i] - top) * inv;
     }
-  }
-
-  if (grouped) {
-    __syncwarp();
-    const int G = r.n_groups, size = p.size, share = 1 << p.share_shift;
-    const int g = lane >> p.share_shift, sub = lane & (share - 1);
-    float a = -INFINITY, b = -INFINITY;    // best and second best
-    if (g < G) {
-      for (int i = sub; i < size; i += share) {
-        const int e = g * size + i;
-        const float c = choice[warp][e + (e >> 5)];
-        b = fmaxf(b, fminf(a, c));
-        a = fmaxf(a, c);
+    if (!by_logit) {
+      float b[kPer];
+      if (p.wide_bias) {
+        if constexpr (kPer >= 4) {
+#pragma unroll
+          for (int i = 0; i < kPer; i += 4) {
+            const float4 f = have ? __ldg(reinterpret_cast<const float4*>(bias + first + i))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            b[i] = f.x;
+            b[i + 1] = f.y;
+            b[i + 2] = f.z;
+            b[i + 3] = f.w;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) b[i] = i < have ? __ldg(bias + first + i) : 0.f;
       }
+      // (a finite bias may be as low as kMasked)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = fmaxf(c[i] + b[i], -0x1.fffffcp127f);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c[i] = l[i] <= lowest<T>() ? kMasked : c[i];
+    if (!p.whole) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) c[i] = i < have ? c[i] : kAbsent;
+    }
+  } else {
+    take_logits();
+  }
+  store_choices();
+
+  bool unsure = false;
+  if (grouped) {
+    const int G = p.groups;
+    float a = c[0], b = kAbsent;           // best and second best
+#pragma unroll
+    for (int i = 1; i < kPer; ++i) {
+      b = fmaxf(b, fminf(a, c[i]));
+      a = fmaxf(a, c[i]);
     }
     for (int o = 1; o < share; o <<= 1) {
       const float a2 = __shfl_xor_sync(kAll, a, o), b2 = __shfl_xor_sync(kAll, b, o);
       b = fmaxf(fmaxf(b, b2), fminf(a, a2));
       a = fmaxf(a, a2);
     }
-    const float mine = g < G ? (r.group_top == 2 ? a + b : a) : -INFINITY;
+    a = a > kMasked ? a : -INFINITY;
+    b = b > kMasked ? b : -INFINITY;
+    const float mine = r.group_top == 2 ? a + b : a;
+    // how many groups come before this one: its lanes share the others
     int before = 0;
-    for (int o = 0; o < G; ++o) {
-      const float other = __shfl_sync(kAll, mine, o << p.share_shift);
-      before += other > mine || (other == mine && o < g);
+    for (int o = sub; o - sub < G; o += share) {
+      const float other = __shfl_sync(kAll, mine, o << p.shift);
+      before += o < G && (other > mine || (other == mine && o < g));
     }
+    for (int o = 1; o < share; o <<= 1) before += __shfl_xor_sync(kAll, before, o);
     bool keep = g < G && before < r.top_groups;
     // Group sums compare only by a margin. A score is off by less than
     // 2^-19.4: s·|x| ≤ 0.37 for a softmax's x = l − top, s·(1 − s)·|x| ≤ 0.28
     // for a sigmoid, and the rest is relative to s ≤ 1; four scores make
-    // 2^-17.4. Roundings of c and of the sums go by the largest |a| + |b|.
+    // 2^-17.4, and one group's two 2^-18.4. Roundings of c and of the sums go
+    // by |a| + |b|.
     if (!by_logit || r.group_top == 2) {
       const float size_ab = (a == -INFINITY ? 0.f : fabsf(a)) + (b == -INFINITY ? 0.f : fabsf(b));
-      const float largest =
-          __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(g < G ? size_ab : 0.f)));
-      const float worst_kept =
-          key_value(__reduce_min_sync(kAll, keep ? order_key(mine) : order_key(INFINITY)));
-      const float best_left =
-          key_value(__reduce_max_sync(kAll, order_key(g < G && !keep ? mine : -INFINITY)));
-      const float margin = 0x1p-17f + largest * 0x1p-21f;
-      if (worst_kept != -INFINITY && !(worst_kept - best_left > margin)) {
+      const float margin = 0x1p-18f + size_ab * 0x1p-22f;
+      const float worst_kept = warp_least(keep ? mine - margin : INFINITY);
+      const float best_left = warp_most(g < G && !keep ? mine + margin : -INFINITY);
+      if (worst_kept != -INFINITY && !(worst_kept > best_left)) {
         // the groups' sums in fp64, a group in a lane: its two best choices,
         // if they are its two best for certain
-        float c1 = -INFINITY, c2 = -INFINITY, c3 = -INFINITY;
+        float c1 = kMasked, c2 = kMasked, c3 = kMasked;
         int e1 = 0, e2 = 0;
+        __syncwarp();
         if (lane < G) {
-          for (int i = 0; i < size; ++i) {
-            const int e = lane * size + i;
-            const float c = choice[warp][e + (e >> 5)];
-            if (c > c1) {
+          for (int i = 0, from = lane * share, at = 0; i < p.size; ++i, ++at) {
+            if (at == p.per) {
+              ++from;
+              at = 0;
+            }
+            const float o = choice[warp][from][at];
+            const int e = lane * p.size + i;
+            if (o > c1) {
               c3 = c2;
               c2 = c1;
               e2 = e1;
-              c1 = c;
+              c1 = o;
               e1 = e;
-            } else if (c > c2) {
+            } else if (o > c2) {
               c3 = c2;
-              c2 = c;
+              c2 = o;
               e2 = e;
             } else {
-              c3 = fmaxf(c3, c);
+              c3 = fmaxf(c3, o);
             }
           }
         }
         const float next = r.group_top == 2 ? c3 : c2, last = r.group_top == 2 ? c2 : c1;
-        unsure |= __any_sync(kAll, next != -INFINITY && !(last - next > margin));
+        const float apart = 0x1p-17f + warp_most(size_ab) * 0x1p-21f;
+        unsure |= __any_sync(kAll, next != kMasked && !(last - next > apart));
         const RowSum q = sigmoid ? RowSum{0.0, 0.0} : row_sum64(row, E);
         double sum = -INFINITY;
-        if (c1 != -INFINITY) {
+        if (c1 != kMasked) {
           sum = choice64(load_logit(row + e1), bias ? bias[e1] : 0.f, sigmoid, q);
           if (r.group_top == 2)
-            sum = c2 == -INFINITY ? -INFINITY
-                                  : sum + choice64(load_logit(row + e2), bias ? bias[e2] : 0.f,
-                                                   sigmoid, q);
+            sum = c2 == kMasked ? -INFINITY
+                                : sum + choice64(load_logit(row + e2), bias ? bias[e2] : 0.f,
+                                                 sigmoid, q);
         }
         const unsigned long long mine64 = order_key64(sum);
         int rank = 0;
@@ -419,81 +482,117 @@ __global__ void __launch_bounds__(kWarps * 32)
         keep = g < G && ((kept64 >> g) & 1u);
       }
     }
-    const uint32_t kept = __ballot_sync(kAll, keep && sub == 0);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = lane * kPer + i;
-      if (!((kept >> ((e * p.to_group >> 16) << p.share_shift)) & 1u)) key[i] = kNone;
+    if (by_logit && sums) {                // the groups' by their scores: now the experts'
+      take_logits();
+      __syncwarp();
+      store_choices();
     }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c[i] = keep ? c[i] : kAbsent;
   }
 
   // At least k + 1 experts are no worse than the (k + 1)-th best of the lanes'
   // best ones, and few more: they go one to a lane and are ranked against
   // each other. Beside a bias, those that lie below it by no more than the
   // choices may be off come along.
-  auto best_below = [&](int limit) {       // this lane's largest key under `limit`
-    int m = kNone;
+  auto best_of_lane = [&] {
+    float m = c[0];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) m = max(m, key[i] < limit ? key[i] : kNone);
+    for (int i = 1; i < kPer; ++i) m = fmaxf(m, c[i]);
     return m;
   };
-  int best = best_below(INT_MAX);
-  // (with experts left in k lanes or fewer, a lane's next best takes its turn)
-  const bool few = __popc(__ballot_sync(kAll, best != kNone)) <= k;
-  int least = kNone;
-  for (int j = 0; j <= k; ++j) {
-    least = __reduce_max_sync(kAll, best);
-    if (best == least) best = few ? best_below(least) : kNone;
+  float best = best_of_lane(), least = kAbsent;
+  if (__popc(__ballot_sync(kAll, best != kAbsent)) > k) {
+    for (int j = 0; j <= k; ++j) {
+      least = warp_most(best);
+      if (best == least) best = kAbsent;
+    }
+  } else {  // experts left in k lanes or fewer: a lane's next best takes its turn
+    for (int j = 0; j <= k; ++j) {
+      least = warp_most(best);
+      if (best == least) {
+        best = kAbsent;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) best = fmaxf(best, c[i] < least ? c[i] : kAbsent);
+      }
+    }
   }
   // what a choice near `least` may be off by: see bound() below
-  const float off_max = (sigmoid ? 0x1p-20f : 0x1p-18f) + fabsf(key_value(least)) * 0x1p-22f;
-  if (!by_logit && least > order_key(-INFINITY)) least = order_key(key_value(least) - 2.f * off_max);
-  int count = 0;
+  if (!by_logit && least > kMasked)
+    least -= 2.f * ((sigmoid ? 0x1p-20f : 0x1p-18f) + fabsf(least) * 0x1p-22f);
+  least = fmaxf(least, kMasked);
+  uint32_t in = 0;                         // this lane's, a bit each
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const bool in = key[i] != kNone && key[i] >= least;
-    const uint32_t who = __ballot_sync(kAll, in);
+  for (int i = 0; i < kPer; ++i) in |= c[i] >= least ? 1u << i : 0u;
+  cand_c[warp][lane] = kAbsent;
+  __syncwarp();
+  int count = 0;
+  for (uint32_t who; (who = __ballot_sync(kAll, in != 0)) != 0;) {
     const int at = count + __popc(who & ((1u << lane) - 1u));
-    if (in && at < 32) cand[warp][at] = make_int2(key[i], lane * kPer + i);
+    if (in) {
+      const int i = __ffs(in) - 1;
+      if (at < 32) {
+        cand_c[warp][at] = choice[warp][lane][i];
+        cand_e[warp][at] = first + i;
+      }
+      in &= in - 1;
+    }
     count += __popc(who);
   }
   const bool crowd = count > 32;
   __syncwarp();
+  float my_c = kAbsent;
+  int my_e = 0;
   if (!crowd) {
-    const int2 my = lane < count ? cand[warp][lane] : make_int2(kNone, 0);
+    if (lane < count) {
+      my_c = cand_c[warp][lane];
+      my_e = cand_e[warp][lane];
+    }
     int rank = 0;
-    for (int o = 0; o < count; ++o) {
-      const int2 other = cand[warp][o];
-      rank += other.x > my.x || (other.x == my.x && other.y < my.y);
+    for (int o = 0; o < count; o += 4) {   // (none is below those past `count`)
+      const float4 other = *reinterpret_cast<const float4*>(&cand_c[warp][o]);
+      rank += (other.x > my_c) + (other.y > my_c) + (other.z > my_c) + (other.w > my_c);
+    }
+    if (__popc(__reduce_or_sync(kAll, lane < count ? 1u << rank : 0u)) != count) {
+      // equal ones: the lower expert's first
+      for (int o = 0; o < count; ++o)
+        rank += cand_c[warp][o] == my_c && cand_e[warp][o] < my_e;
     }
     __syncwarp();
-    if (lane < count) cand[warp][rank] = my;
+    if (lane < count) {
+      cand_c[warp][rank] = my_c;
+      cand_e[warp][rank] = my_e;
+    }
   } else {
-    // many equal ones: the largest key left k + 1 times, of equal ones the
-    // lowest expert's, which is in the lowest lane
+    // many equal ones: the largest left k + 1 times, of equal ones the lowest
+    // expert's, which is in the lowest lane
     count = k + 1;
     for (int j = 0; j <= k; ++j) {
-      const int mine = best_below(INT_MAX), most = __reduce_max_sync(kAll, mine);
+      const float mine = best_of_lane(), most = warp_most(mine);
       const int from = __ffs(__ballot_sync(kAll, mine == most)) - 1;
       if (lane == from) {
         int at = 0;
 #pragma unroll
         for (int i = kPer - 1; i >= 0; --i)
-          if (key[i] == most) at = i;
+          if (c[i] == most) at = i;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          if (i == at) key[i] = kNone;
-        cand[warp][j] = make_int2(most, lane * kPer + at);
+          if (i == at) c[i] = kAbsent;
+        cand_c[warp][j] = most;
+        cand_e[warp][j] = first + at;
       }
     }
   }
   __syncwarp();
-  const int2 my = lane < count ? cand[warp][lane] : make_int2(kNone, 0);
-  int my_e = my.y;                         // rank j's expert in lane j
+  // rank j's expert in lane j
+  my_c = lane < count ? cand_c[warp][lane] : kAbsent;
+  my_e = lane < count ? cand_e[warp][lane] : 0;
 
   // the chosen experts' scores, accurately
   auto score_of = [&](float x) {
-    return x == -INFINITY ? 0.f : sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - top) * inv;
+    return x == -INFINITY ? 0.f
+           : sigmoid      ? reciprocal_fast(1.f + expf(-x))
+                          : expf(x - top) * inv;
   };
   float x = lane < count ? load_logit(row + my_e) : -INFINITY;
   float s = score_of(x);
@@ -501,50 +600,56 @@ __global__ void __launch_bounds__(kWarps * 32)
     // Neighbours in the order must differ by more than their bounds — for a
     // sigmoid s·((1 − s)·(|x|·2^-23.4 + 2^-22) + 2^-22), (1 − s)·|x| ≤ 0.28
     // for x > 0; for a softmax s·(|x|·2^-23.4 + 2^-19.4) — or be equal in
-    // logit and bias: then the index decides, here as exactly.
-    auto bound = [&](float v_s, float v_x, float v_c) {
-      return (sigmoid ? v_s * 0x1.6ap-21f + fmaxf(-v_x, 0.f) * v_s * 0x1p-23f
-                      : v_s * (fabsf(v_x - top) * 0x1p-23f + 0x1p-19f)) +
-             fabsf(v_c) * 0x1p-23f;
-    };
-    const float b = lane < count ? __ldg(bias + my_e) : 0.f;
-    const float c = key_value(my.x);
-    const float off = lane < count && x != -INFINITY ? bound(s, x, c) : 0.f;
-    const float x2 = __shfl_down_sync(kAll, x, 1), b2 = __shfl_down_sync(kAll, b, 1);
-    const float c2 = __shfl_down_sync(kAll, c, 1), off2 = __shfl_down_sync(kAll, off, 1);
-    const bool close = lane < k && lane + 1 < count && x2 != -INFINITY && !(c - c2 > off + off2) &&
-                       !(x == x2 && b == b2);
-    if (!__any_sync(kAll, close)) {
-    } else if (crowd) {
-      unsure = true;                       // others may be as close
-    } else {                               // all candidates by fp64
-      const RowSum q = sigmoid ? RowSum{0.0, 0.0} : row_sum64(row, E);
-      const unsigned long long mine64 =
-          lane < count ? order_key64(choice64(x, b, sigmoid, q)) : 0ull;
-      int rank = 0;
-      for (int o = 0; o < count; ++o) {
-        const unsigned long long other = __shfl_sync(kAll, mine64, o);
-        const int e_o = __shfl_sync(kAll, my_e, o);
-        rank += other > mine64 || (other == mine64 && e_o < my_e);
+    // logit and bias: then the index decides, here as exactly. Most tokens'
+    // do by what no bound exceeds.
+    const float c2 = __shfl_down_sync(kAll, my_c, 1);
+    const bool next = lane < k && lane + 1 < count && c2 > kMasked;
+    const float off_most = (sigmoid ? 0x1p-19f : 0x1p-17f) + (fabsf(my_c) + fabsf(c2)) * 0x1p-23f;
+    if (__any_sync(kAll, next && !(my_c - c2 > off_most))) {
+      auto bound = [&](float v_s, float v_x, float v_c) {
+        return (sigmoid ? v_s * 0x1.6ap-21f + fmaxf(-v_x, 0.f) * v_s * 0x1p-23f
+                        : v_s * (fabsf(v_x - top) * 0x1p-23f + 0x1p-19f)) +
+               fabsf(v_c) * 0x1p-23f;
+      };
+      const float b = lane < count ? __ldg(bias + my_e) : 0.f;
+      const float off = lane < count && x != -INFINITY ? bound(s, x, my_c) : 0.f;
+      const float x2 = __shfl_down_sync(kAll, x, 1), b2 = __shfl_down_sync(kAll, b, 1);
+      const float off2 = __shfl_down_sync(kAll, off, 1);
+      const bool close = next && !(my_c - c2 > off + off2) && !(x == x2 && b == b2);
+      if (!__any_sync(kAll, close)) {
+      } else if (crowd) {
+        unsure = true;                     // others may be as close
+      } else {                             // all candidates by fp64
+        const RowSum q = sigmoid ? RowSum{0.0, 0.0} : row_sum64(row, E);
+        const unsigned long long mine64 =
+            lane < count ? order_key64(choice64(x, b, sigmoid, q)) : 0ull;
+        int rank = 0;
+        for (int o = 0; o < count; ++o) {
+          const unsigned long long other = __shfl_sync(kAll, mine64, o);
+          const int e_o = __shfl_sync(kAll, my_e, o);
+          rank += other > mine64 || (other == mine64 && e_o < my_e);
+        }
+        __syncwarp();
+        if (lane < count) cand_e[warp][rank] = my_e;
+        __syncwarp();
+        my_e = cand_e[warp][lane < count ? lane : 0];
+        x = lane < count ? load_logit(row + my_e) : -INFINITY;
+        s = score_of(x);
       }
-      __syncwarp();
-      if (lane < count) cand[warp][rank].y = my_e;
-      __syncwarp();
-      my_e = cand[warp][lane < count ? lane : 0].y;
-      x = lane < count ? load_logit(row + my_e) : -INFINITY;
-      s = score_of(x);
     }
   }
-  // sigmoids that fp32 cannot hold, of which quotients are wanted
-  if (sigmoid && r.renorm && lane < k && x != -INFINITY && s < 0x1p-100f) unsure = true;
+  // scores that fp32 cannot hold, of which quotients are wanted
+  if (r.renorm && lane < k && x != -INFINITY && s < 0x1p-100f) unsure = true;
   float w;
   if (__any_sync(kAll, unsure)) {
-    route_exact<T>(r, row, bias, &my_e, &w);
+    const Chosen exact = route_exact<T>(r, row, bias);
+    my_e = exact.e;
+    w = exact.w;
   } else {
     w = lane < k ? s : 0.f;
     if (r.renorm) {
       const float sum = warp_sum(w);
-      w = sum > 0.f ? w / sum : 0.f;
+      w = sum > 0.f ? __fdividef(w, sum) : 0.f;  // 2^-100 < sum ≤ 16: good to two steps
     }
     w *= r.scale;
   }
@@ -555,18 +660,13 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 template <typename T, int kPer>
-cudaError_t launch_t(const moe_router_desc& r, const T* logits, int64_t row_stride,
-                     const float* bias, int n, int32_t* topk_idx, float* topk_w,
-                     cudaStream_t stream) {
-  Router p;
-  p.d = r;
-  p.size = r.n_experts / r.n_groups;
-  p.to_group = (65536 + p.size - 1) / p.size;
-  p.share_shift = 0;
-  while ((2 << p.share_shift) * r.n_groups <= 32) ++p.share_shift;
-  // rows in whole pieces: every lane's experts exist or none does
-  p.wide = r.n_experts % kPer == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0 &&
-           row_stride * sizeof(T) % 16 == 0 && kPer * sizeof(T) % 16 == 0;
+cudaError_t launch_t(Router p, const T* logits, int64_t row_stride, const float* bias, int n,
+                     int32_t* topk_idx, float* topk_w, cudaStream_t stream) {
+  const bool pieces = p.per == kPer && p.size % kPer == 0;  // a lane has kPer experts or none
+  p.whole = pieces && p.groups * p.size == 32 * kPer;
+  p.wide = pieces && kPer * sizeof(T) % 16 == 0 && row_stride * sizeof(T) % 16 == 0 &&
+           (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
+  p.wide_bias = pieces && kPer >= 4 && (reinterpret_cast<uintptr_t>(bias) & 15u) == 0;
   return launch_pdl(route_grouped_kernel<T, kPer>, dim3((n - 1) / kWarps + 1), dim3(kWarps * 32), 0,
                     stream, p, logits, row_stride, bias, n, topk_idx, topk_w);
 }
@@ -576,10 +676,17 @@ cudaError_t launch_e(const moe_router_desc& r, const void* logits, int64_t row_s
                      const float* bias, int n, int32_t* topk_idx, float* topk_w,
                      cudaStream_t stream) {
   const T* l = static_cast<const T*>(logits);
-  if (r.n_experts <= 64) return launch_t<T, 2>(r, l, row_stride, bias, n, topk_idx, topk_w, stream);
-  if (r.n_experts <= 128)
-    return launch_t<T, 4>(r, l, row_stride, bias, n, topk_idx, topk_w, stream);
-  return launch_t<T, 8>(r, l, row_stride, bias, n, topk_idx, topk_w, stream);
+  Router p;
+  p.d = r;
+  p.groups = r.top_groups < r.n_groups ? r.n_groups : 1;
+  p.size = r.n_experts / p.groups;
+  p.shift = 0;
+  while ((2 << p.shift) * p.groups <= 32) ++p.shift;
+  p.per = ((p.size - 1) >> p.shift) + 1;   // 16 at most: more than 16 / groups lanes a group
+  if (p.per <= 2) return launch_t<T, 2>(p, l, row_stride, bias, n, topk_idx, topk_w, stream);
+  if (p.per <= 4) return launch_t<T, 4>(p, l, row_stride, bias, n, topk_idx, topk_w, stream);
+  if (p.per <= 8) return launch_t<T, 8>(p, l, row_stride, bias, n, topk_idx, topk_w, stream);
+  return launch_t<T, 16>(p, l, row_stride, bias, n, topk_idx, topk_w, stream);
 }
 
 }  // namespace

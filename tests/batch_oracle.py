@@ -112,7 +112,9 @@ def route(logits, bias, topk, groups, top_groups, group_top, score, renorm, scal
             spread = float(np.ptp(live)) if live.size else 0.0
         c = [-math.inf if off[t, e] else s[e] + b[e] for e in range(E)]
         size = E // groups
-        best = [sum(sorted(c[g * size:(g + 1) * size], reverse=True)[:group_top])
+        # (so for groups of one choice each)
+        value = c if bias is not None or group_top == 2 else np.where(off[t], -np.inf, x[t]).tolist()
+        best = [sum(sorted(value[g * size:(g + 1) * size], reverse=True)[:group_top])
                 for g in range(groups)]
         kept = sorted(range(groups), key=lambda g: (-best[g], g))[:top_groups]
         pool = [e for g in kept for e in range(g * size, (g + 1) * size)]

@@ -504,6 +504,22 @@ def test_route_extreme_logits(lib):
     _route(lib, x[:, :6].contiguous(), 2, 2, 1, 2, "softmax", torch.zeros(6), True, 1.0)
 
 
+def test_route_scores_below_fp32(lib):
+    """Scores that fp32 flushes to zero, of which the quotients are asked for;
+    below fp64 too, the logits still order the experts."""
+    x = -100 - 0.25 * torch.arange(64, dtype=torch.float32)
+    x = x[(torch.arange(64) * 29) % 64].repeat(3, 1)
+    x[1, 40] = 0.0
+    x[2] *= 9
+    _route(lib, x, 4, 1, 1, 1, "sigmoid", None, True, 1.0)
+    _route(lib, x, 4, 8, 2, 1, "sigmoid", None, True, 2.5)
+    _route(lib, x[:2], 4, 8, 2, 2, "sigmoid", None, True, 1.0)
+    bias = torch.zeros(64)
+    bias[:16] = 2.0
+    _route(lib, x[:2], 5, 1, 1, 1, "softmax", bias, True, 1.0)
+    _route(lib, x[:2], 5, 8, 2, 2, "softmax", bias, True, 1.0)
+
+
 def test_route_row_stride_and_buffers(lib):
     from moe_expert_layer_warp_gb300 import batch
     g = torch.Generator().manual_seed(1)
