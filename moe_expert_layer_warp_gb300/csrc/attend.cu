@@ -21,9 +21,9 @@
 //   a few tokens: bound by reading the cache), joined at the end.
 //
 // Work. An item is (request, key head, block of tokens); its length is the
-// number of 128-key tiles its rows see. All items' tiles in a row are cut
-// into equal ranges, one per CTA, wherever the cuts fall: every SM has the
-// same number of key tiles to go through whatever the mix of long and short
+// number of 128-key tiles its rows see, weighted by what they cost. All items'
+// tiles in a row are cut into equal ranges, one per CTA, wherever the cuts
+// fall: every SM has the same work whatever the mix of long and short
 // requests. The lengths are on the device: every CTA works out the cuts from
 // them by itself. A CTA whose range ends inside an item leaves (O, m, Σ) of
 // the item's rows in the workspace, and the CTA with the item's last tile
@@ -62,8 +62,13 @@ constexpr int kThreads = 640;
 constexpr int kHalf = kTile / 2;  // keys of one softmax thread
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 constexpr int kPlanThreads = 256;
-// What an item costs beside its tiles, in tiles, when the work is cut.
-constexpr int kItemCost = 3;
+// What an item costs beside its tiles when the work is cut, in units: a key
+// tile is one unit for a block of one query tile, and two for a block of two,
+// which are gone through beside each other but by all of the CTA's warps.
+// (Three prompt chunks among 21 verification passes, 8 key heads of 64 columns:
+// 35.2 us; with 2 and 4 units for an item, 34.2 and 37.4, but for 128 columns
+// 50.5 and 48.0 beside 49.4; with one unit for either kind of tile 40.8.)
+constexpr int kItemUnits = 3;
 // The reference m follows the row's maximum only when that has grown by more
 // than this (in powers of two): until then weights are up to 2^8 instead of
 // 1, which fp32 sums and both 16-bit types hold, and O needs no rescaling.
@@ -145,8 +150,24 @@ MOE_DEV Item make_item(const AttendArgs& a, const Request& r, int block, int fix
   return it;
 }
 
-// Where a CTA is in its range; every role walks it by itself. Units are key
-// tiles, with kItemCost more at the head of every item.
+// An item's units: first `cost`, then one for every key tile of a block of one
+// query tile, two for one of a block of two. A tile belongs to the CTA whose
+// range has its first unit.
+struct Units {
+  int cost, each, all;
+  MOE_DEV int tiles(int u) const {  // that begin before unit u
+    return (max(0, u - cost) + each - 1) >> (each - 1);
+  }
+};
+MOE_DEV Units units_of(const Params& p, const Item& it) {
+  Units u;
+  u.cost = it.hi > 0 ? kItemUnits : 0;  // (rows that see nothing are only cleared)
+  u.each = it.ntok > p.tpt ? 2 : 1;
+  u.all = u.cost + it.n * u.each;
+  return u;
+}
+
+// Where a CTA is in its range; every role walks it by itself.
 struct Walk {
   int b, h, block, u0, left;
 };
@@ -174,10 +195,11 @@ struct Walker {
     const int fixed = 2 * p.tpt;
     while (w.left > 0) {
       const Item it = make_item(p.a, r, w.block, fixed);
-      const int u1 = min(w.u0 + w.left, it.n + kItemCost);
+      const Units units = units_of(p, it);
+      const int u1 = min(w.u0 + w.left, units.all);
       out->it = it;
-      out->t0 = max(0, w.u0 - kItemCost);
-      out->t1 = max(0, u1 - kItemCost);
+      out->t0 = units.tiles(w.u0);
+      out->t1 = units.tiles(u1);
       out->two = it.ntok > p.tpt;
       b = w.b;
       h = w.h;
@@ -238,6 +260,7 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
   constexpr uint32_t kAll = 0xffffffffu;
   // units of every request for one key head: a request of one block by its
   // own thread, longer ones by the warp
+  int any_two = 0;
 #pragma unroll 1
   for (int b0 = warp * 32; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + lane;
@@ -246,6 +269,7 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
     if (b < B) mine = request(a, p.page_shift, b, &bad);
     if (bad && blockIdx.x == 0) report_error(a.err, ERR_CHECK, 0xA20);
     long long units = 0;
+    any_two |= mine.q > p.tpt;
     uint32_t todo = __ballot_sync(kAll, mine.q > 0);
     const uint32_t longer = __ballot_sync(kAll, mine.q > fixed);
     // first all short ones together (a turn of their own threads), then the
@@ -263,7 +287,7 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
       long long n = 0;
 #pragma unroll 1
       for (int q = together ? 0 : lane; !skip && q * fixed < r.q; q += 32)
-        n += make_item(a, r, q, fixed).n + kItemCost;
+        n += units_of(p, make_item(a, r, q, fixed)).all;
       if (!together) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(kAll, n, o);
@@ -284,7 +308,13 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
     if (lane >= o) incl += t;
   }
   if (lane == 31) part[warp] = incl;
-  asm volatile("bar.sync 1, 256;" ::: "memory");
+  int least = any_two;                     // units of a range, at least
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %0, 0;\n\t"
+      "bar.red.or.pred q, 1, 256, p;\n\t"
+      "selp.s32 %0, 2, 1, q;\n\t}"
+      : "+r"(least)::"memory");
   long long before = incl - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
@@ -294,9 +324,9 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
   total *= H;
   before *= H;
   sum *= H;
-  // no more CTAs than units, so that no range among them is empty: the first
-  // `more` ranges are one unit longer than the others
-  const long long C = min((long long)gridDim.x, total), c = blockIdx.x;
+  // every range inside an item begins a tile; the first `more` ranges are one
+  // unit longer than the others
+  const long long C = min((long long)gridDim.x, total >> (least - 1)), c = blockIdx.x;
   const long long each = C > 0 ? divide(total, C) : 0, more = total - each * C;
   const long long w0 = c * each + min(c, more), w1 = c < C ? w0 + each + (c < more ? 1 : 0) : w0;
   if (tid == 0) {
@@ -321,10 +351,12 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
   for (int q0 = 0; q0 * fixed < r.q; q0 += 32) {
     const int q = q0 + lane;
     Item it;
+    Units units;
     long long n = 0, upto;
     if (q * fixed < r.q) {
       it = make_item(a, r, q, fixed);
-      n = it.n + kItemCost;
+      units = units_of(p, it);
+      n = units.all;
     }
     upto = n;
 #pragma unroll
@@ -339,11 +371,12 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
       out->w.block = q;
       out->w.u0 = (int)u0;
       out->r = r;
-      out->joins = u0 > kItemCost && n - u0 <= w1 - w0;
+      const int t0 = units.tiles((int)u0);
+      out->joins = t0 > 0 && t0 < it.n && units.tiles((int)min(n, u0 + w1 - w0)) == it.n;
       out->row0 = it.row0;
       out->ntok = it.ntok;
       out->head0 = h * a.group;
-      out->unit = w0 - u0 + kItemCost;
+      out->unit = w0 - u0 + units.cost;
     }
     const long long block_sum = __shfl_sync(kAll, upto, 31);
     if (rem < block_sum) return;
@@ -463,8 +496,81 @@ MOE_DEV void quad_transpose(uint4 (&v)[4], int lane) {
   }
 }
 
-// The parts of an item in key order, a thread per (row, 4 columns). All
-// softmax threads of the CTA that has the item's last tile call it.
+// The parts of an item joined in key order, those of CTAs `first` to this one:
+// a thread per row and kQuads · 4 columns, the loads of kBatch parts in flight.
+template <int kDim, bool kF16, int kQuads, int kBatch>
+MOE_DEV void join_rows(const Params& p, const Start& st, int first) {
+  using Z = Sizes<kDim>;
+  const AttendArgs& a = p.a;
+  const int last = blockIdx.x;
+  const int G = a.group, rows = st.ntok * G, per_tile = p.tpt * G;
+#pragma unroll 1
+  for (int i = threadIdx.x - 128; i < rows * (kDim / 4 / kQuads); i += 512) {
+    const int c4 = i / rows * kQuads, rr = i % rows;
+    // rows of the second tile start at 128
+    const int prow = rr < per_tile ? rr : kTile + rr - per_tile;
+    float m = -INFINITY, sum = 0.f;
+    float4 o[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c0 = first; c0 <= last; c0 += kBatch) {
+      float mc[kBatch], sc[kBatch];
+      float4 oc[kBatch][kQuads];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int c = c0 + j;
+        const float* slot = p.part + (size_t)(2 * c + (c == last ? 0 : 1)) * Z::kSlotFloats;
+        const float* stat = slot + (size_t)2 * kTile * kDim;
+        mc[j] = -INFINITY;
+        sc[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) oc[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c <= last) {
+          mc[j] = __ldcg(stat + prow);
+          sc[j] = __ldcg(stat + 2 * kTile + prow);
+#pragma unroll
+          for (int k = 0; k < kQuads; ++k)
+            oc[j][k] = __ldcg(reinterpret_cast<const float4*>(slot) + (c4 + k) * (2 * kTile) + prow);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, mc[j]);
+      if (top == -INFINITY) continue;              // (the parts hold zeros)
+      const float keep = exp2_approx(m - top);
+      m = top;
+      sum *= keep;
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k)
+        o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float add = exp2_approx(mc[j] - top);
+        sum = fmaf(sc[j], add, sum);
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+          o[k].x = fmaf(oc[j][k].x, add, o[k].x);
+          o[k].y = fmaf(oc[j][k].y, add, o[k].y);
+          o[k].z = fmaf(oc[j][k].z, add, o[k].z);
+          o[k].w = fmaf(oc[j][k].w, add, o[k].w);
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int tok = rr / G, g = rr - tok * G;
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(st.row0 + tok) * a.out_token_stride +
+                    (int64_t)(st.head0 + g) * a.out_head_stride + c4 * 4;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k)
+      reinterpret_cast<uint2*>(dst)[k] =
+          make_uint2(narrow<kF16>(o[k].x * inv, o[k].y * inv), narrow<kF16>(o[k].z * inv, o[k].w * inv));
+  }
+}
+
+// All softmax threads of the CTA that has the item's last tile call it. (What
+// the other CTAs' threads left is ordered before their flags' releases by
+// their barrier, and before this CTA's reads by the acquires and this one.)
 template <int kDim, bool kF16>
 MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
   using Z = Sizes<kDim>;
@@ -489,54 +595,13 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
     }
     *word = 0ull;
   }
-  __threadfence();
   asm volatile("bar.sync 2, 512;" ::: "memory");
-  const int G = a.group, rows = st.ntok * G, per_tile = p.tpt * G;
-  for (int i = tid; i < rows * (kDim / 4); i += 512) {
-    const int c4 = i / rows, rr = i - c4 * rows;
-    // rows of the second tile start at 128
-    const int prow = rr < per_tile ? rr : kTile + rr - per_tile;
-    float m = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the loads of several parts in flight together
-    constexpr int kBatch = 4;
-    for (int c0 = first; c0 <= last; c0 += kBatch) {
-      float mc[kBatch], sc[kBatch];
-      float4 oc[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int c = min(c0 + j, last);
-        const float* slot = p.part + (size_t)(2 * c + (c == last ? 0 : 1)) * Z::kSlotFloats;
-        const float* stat = slot + (size_t)2 * kTile * kDim;
-        mc[j] = c0 + j <= last ? __ldcg(stat + prow) : -INFINITY;
-        sc[j] = __ldcg(stat + 2 * kTile + prow);
-        oc[j] = __ldcg(reinterpret_cast<const float4*>(slot) + c4 * (2 * kTile) + prow);
-      }
-      float top = m;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) top = fmaxf(top, mc[j]);
-      if (top == -INFINITY) continue;              // (the parts hold zeros)
-      const float keep = exp2_approx(m - top);
-      m = top;
-      sum *= keep;
-      o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const float add = exp2_approx(mc[j] - top);
-        sum = fmaf(sc[j], add, sum);
-        o.x = fmaf(oc[j].x, add, o.x);
-        o.y = fmaf(oc[j].y, add, o.y);
-        o.z = fmaf(oc[j].z, add, o.z);
-        o.w = fmaf(oc[j].w, add, o.w);
-      }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int tok = rr / G, g = rr - tok * G;
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(st.row0 + tok) * a.out_token_stride +
-                    (int64_t)(st.head0 + g) * a.out_head_stride + c4 * 4;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(narrow<kF16>(o.x * inv, o.y * inv), narrow<kF16>(o.z * inv, o.w * inv));
-  }
+  // few rows: a thread has 4 columns and loads 8 parts at once; many rows: 8
+  // columns of 4 parts
+  if (st.ntok * a.group * (kDim / 4) <= 512)
+    join_rows<kDim, kF16, 1, 8>(p, st, first);
+  else
+    join_rows<kDim, kF16, 2, 4>(p, st, first);
 }
 
 // Barriers and words behind the ring.
@@ -1082,7 +1147,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
     }
     if (open) {                                      // the part left behind is complete
-      __threadfence();
       asm volatile("bar.sync 2, 512;" ::: "memory");
       if (threadIdx.x == 128)
         asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.left + blockIdx.x), "l"(p.call)

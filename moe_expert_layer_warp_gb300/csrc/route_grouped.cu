@@ -34,7 +34,9 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kPerSm = 8;  // blocks, of 64 registers a thread: what is rare spills (6: 21.3 us for 19.4)
+// Blocks of an SM: 64 registers a thread, and what is rare spills. (With 6
+// blocks of 80 registers, 20011 tokens took 21.3 us for 19.4.)
+constexpr int kPerSm = 8;
 constexpr uint32_t kAll = 0xffffffffu;
 
 template <typename T>
