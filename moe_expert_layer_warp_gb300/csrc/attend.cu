@@ -302,12 +302,12 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
 #pragma unroll 1
   for (int b = mine0; b < min(mine0 + per, B); ++b) sum += count[b];
   long long incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+  for (int o = 1; o < min(B, 32); o <<= 1) {
     const long long t = __shfl_up_sync(kAll, incl, o);
     if (lane >= o) incl += t;
   }
-  if (lane == 31) part[warp] = incl;
+  if (lane == min(B, 32) - 1) part[warp] = incl;
   int least = any_two;                     // units of a range, at least
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -316,8 +316,8 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
       "selp.s32 %0, 2, 1, q;\n\t}"
       : "+r"(least)::"memory");
   long long before = incl - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+#pragma unroll 1
+  for (int w = 0; w < kPlanThreads / 32 && w * 32 * per < B; ++w) {
     if (w < warp) before += part[w];
     total += part[w];
   }
@@ -359,8 +359,8 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
       n = units.all;
     }
     upto = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+    for (int o = 1; o < 32 && (q0 + o) * fixed < r.q; o <<= 1) {
       const long long t = __shfl_up_sync(kAll, upto, o);
       if (lane >= o) upto += t;
     }
@@ -596,12 +596,12 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
     *word = 0ull;
   }
   asm volatile("bar.sync 2, 512;" ::: "memory");
-  // few rows: a thread has 4 columns and loads 8 parts at once; many rows: 8
-  // columns of 4 parts
+  // few rows: a thread has 4 columns and loads 8 parts at once; many rows: 16
+  // columns of 2 parts
   if (st.ntok * a.group * (kDim / 4) <= 512)
     join_rows<kDim, kF16, 1, 8>(p, st, first);
   else
-    join_rows<kDim, kF16, 2, 4>(p, st, first);
+    join_rows<kDim, kF16, 4, 2>(p, st, first);
 }
 
 // Barriers and words behind the ring.
@@ -659,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     prefetch_tmap(&p.kmap);
     prefetch_tmap(&p.vmap);
+    prefetch_tmap(&p.qmap);
   }
   pdl_wait();
   pdl_trigger();
