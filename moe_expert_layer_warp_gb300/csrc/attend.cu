@@ -87,9 +87,10 @@ constexpr int kPlanThreads = 256;
 // tile is one unit for a block of one query tile, and two for a block of two,
 // which are gone through beside each other but by all of the CTA's warps.
 // (Three prompt chunks among 21 verification passes, 8 key heads of 64 columns:
-// 35.2 us; with 2 and 4 units for an item, 34.2 and 37.4, but for 128 columns
-// 50.5 and 48.0 beside 49.4; with one unit for either kind of tile 40.8.)
-constexpr int kItemUnits = 3;
+// 33.2 us; with 1 and 3 units for an item 37.3 and 34.8; with 3, and one unit
+// for either kind of tile, 40.8. 200 passes over caches of up to 6000 keys: 243.5
+// us, with 3 units 246.4.)
+constexpr int kItemUnits = 2;
 // The reference m follows the row's maximum only when that has grown by more
 // than this (in powers of two): until then weights are up to 2^8 instead of
 // 1, which fp32 sums and both 16-bit types hold, and O needs no rescaling.
@@ -116,6 +117,7 @@ struct Params {
   AttendArgs a;
   int page_shift;
   int tpt;       // tokens per query tile, 128 / group
+  int block;     // tokens per block, tpt or 2·tpt
   float* part;   // [2 per CTA][kSlotFloats]
   // [CTAs]: `call` when the CTA has left the part of its last item. The CTA
   // that reads it sets it to 0; what an unused workspace holds is not `call`,
@@ -155,7 +157,7 @@ MOE_DEV Request request(const AttendArgs& a, int page_shift, int b, bool* bad) {
   return r;
 }
 
-// `fixed`: the block's tokens, 2·tpt.
+// `fixed`: the tokens of a block.
 MOE_DEV Item make_item(const AttendArgs& a, const Request& r, int block, int fixed) {
   Item it;
   const int tok0 = block * fixed;
@@ -213,7 +215,7 @@ struct Walker {
       : p(prm), w(start), r(first), b(start.b), h(start.h) {}
 
   MOE_DEV bool next(Part* out) {
-    const int fixed = 2 * p.tpt;
+    const int fixed = p.block;
     while (w.left > 0) {
       const Item it = make_item(p.a, r, w.block, fixed);
       const Units units = units_of(p, it);
@@ -277,7 +279,7 @@ MOE_DEV long long divide(long long a, long long b) {
 MOE_DEV void find_start(const Params& p, long long* count, long long* part, Start* out) {
   const AttendArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int fixed = 2 * p.tpt, H = a.cache.n_kv_heads, B = a.n_requests;
+  const int fixed = p.block, H = a.cache.n_kv_heads, B = a.n_requests;
   constexpr uint32_t kAll = 0xffffffffu;
   // units of every request for one key head: a request of one block by its
   // own thread, longer ones by the warp
@@ -1257,6 +1259,12 @@ cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream)
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  // Blocks of two query tiles halve what is read; but with fewer of them than
+  // CTAs most are cut, and their parts' joins take longer than the reads: a
+  // prompt of 1024 tokens (32 heads on 8) 32.6 us in blocks of two, 27.5 in blocks
+  // of one; of 2048 tokens 53.0 and 56.0.
+  const long long blocks = (long long)((a.n_tokens - 1) / (2 * p.tpt) + 1) * c.n_kv_heads;
+  p.block = blocks < ctas ? p.tpt : 2 * p.tpt;
   const bool f16 = c.dtype == MOE_F16;
   if (c.head_dim == 128)
     return f16 ? launch_t<128, true>(p, ctas, stream) : launch_t<128, false>(p, ctas, stream);
