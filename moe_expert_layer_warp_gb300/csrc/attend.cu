@@ -1130,6 +1130,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&m.p_full[s]);
       }
       // ---- results out
+      const bool ends = pt.t1 == it.n, whole_item = ends && pt.t0 == 0;
+      open = !ends;
+        // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
+        const uint64_t dst = reinterpret_cast<uint64_t>(
+            static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
+            (int64_t)(walk.h * a.group + g_in) * a.out_head_stride);
+        const uint32_t quad_valid = __ballot_sync(0xffffffffu, valid) >> (lane & ~3) & 15u;
+        uint16_t* quad_dst[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          quad_dst[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, dst, (lane & ~3) + i));
       if (began) {
         wait(&m.o_full[s], o_phase, 0xA52);
         o_phase ^= 1u;
@@ -1141,8 +1152,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       sum += *theirs;
       pair_sync();
       if (!two) *mine = half == 0 ? ref : sum;
-      const bool ends = pt.t1 == it.n, whole_item = ends && pt.t0 == 0;
-      open = !ends;
       // factors of the two streams' O, and this thread's columns
       float f0 = 1.f, f1 = 0.f;
       int c_first = half * (kDim / 2), c_end = c_first + kDim / 2;
@@ -1170,15 +1179,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         const bool any0 = f0 > 0.f && sum > 0.f, any1 = f1 > 0.f;
         const bool warp_any1 = __any_sync(0xffffffffu, any1);
         const uint32_t from = lanes + 256 + (two ? s * 128 : 0);
-        // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
-        const uint64_t dst = reinterpret_cast<uint64_t>(
-            static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
-            (int64_t)(walk.h * a.group + g_in) * a.out_head_stride);
-        const uint32_t quad_valid = __ballot_sync(0xffffffffu, valid) >> (lane & ~3) & 15u;
-        uint16_t* quad_dst[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          quad_dst[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, dst, (lane & ~3) + i));
         float* slot = p.part + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * Z::kSlotFloats;
         const int prow = (two ? s * kTile : 0) + row;
 #pragma unroll 1
