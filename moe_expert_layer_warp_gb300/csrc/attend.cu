@@ -43,26 +43,26 @@
 //          maximum through shared memory
 //   12-19  the same for stream 1
 //
-// What bounds it, with 32 query heads on 8 key heads of 128 bf16 columns where
-// nothing else is said:
+// What bounds it; 32 query heads on 8 key heads of 128 bf16 columns where nothing
+// else is said:
 //   verification passes (64 requests of 1 to 9 tokens, caches up to 16000 keys,
 //   906 MB): 153 us, 5.9 TB/s, 87 % of a copy's rate. The rest is the start
 //   (plan 2 us, first loads 3), turns between items, during which the ring
-//   holds only 2.5 tiles, and the joins (3 us). Windows of 4096 keys of 56
-//   heads: 146 us for 804 MB; tiles at the windows' ends cost 7 % more bytes;
-//   long prompt chunks (957 GFLOP): 670 us cold and 725 us under the power
+//   holds only 2.5 tiles, and the joins (2 us). Windows of 4096 keys of 56
+//   heads: 146 us for 804 MB; tiles at the windows' ends cost 7 % more bytes.
+//   Long prompt chunks (957 GFLOP): 670 us cold and 725 us under the power
 //   cap, 1.43 and 1.32 PFLOP/s. A stream's chain of softmax (1450 cycles a
 //   tile) and products (1024, and 475 of hand-overs) runs beside the other
-//   stream's: the tensor cores work 70 % of a period. Tensor memory is full,
-//   so a stream's next scores cannot be computed beside its weights; for 64
-//   columns they can, which gained 1 % and is not done. Both maxima or exact
-//   references elsewhere, shifting the exponentials among the steps, and one
-//   issuing warp for both streams were slower;
-//   a mixed batch (3 prompt chunks, 20 passes, 56 heads of 64 columns, pages of
-//   16, 69 MB): 35 us, the longest range's 25 us of item turns and small
-//   boxes, the start and one join;
-//   one pass of 5 tokens over 777 keys: 12.5 us, one chain of plan (2 us), loads
-//   and products (5), a part's hand-over (2) and join (1.2), and the launch.
+//   stream's: the tensor cores work 70 % of a period. Tensor memory is full, so
+//   a stream's next scores cannot be computed beside its weights.
+//   A mixed batch (3 prompt chunks, 20 passes, 56 heads of 64 columns, pages of
+//   16, 69 MB): 33.4 us, of which 25 are the longest range's item turns and
+//   small boxes, the others the start and one join.
+//   A prompt of 512 tokens: 18 us; 200 passes within windows of 512 keys: 125 us,
+//   for an item's turn (products, results out, the next item's place: 3 us)
+//   stands against 5 tiles' loads.
+//   One pass of 5 tokens over 777 keys: 12.5 us, one chain of plan (2), loads and
+//   products (5), a part's hand-over (2), join (1.2) and the launch.
 #include <limits.h>
 #include <math.h>
 #include <string.h>
@@ -86,10 +86,9 @@ constexpr int kPlanThreads = 256;
 // What an item costs beside its tiles when the work is cut, in units: a key
 // tile is one unit for a block of one query tile, and two for a block of two,
 // which are gone through beside each other but by all of the CTA's warps.
-// (Three prompt chunks among 21 verification passes, 8 key heads of 64 columns:
-// 33.2 us; with 1 and 3 units for an item 37.3 and 34.8; with 3, and one unit
-// for either kind of tile, 40.8. 200 passes over caches of up to 6000 keys: 243.5
-// us, with 3 units 246.4.)
+// (Three prompt chunks among 20 passes, 8 key heads of 64 columns: 33.4 us; with
+// 1 and 3 units for an item 36.5 and 35.2; with one unit for either kind of tile
+// 38.0. 200 passes over caches of up to 6000 keys: 243 us, with 3 units 248.)
 constexpr int kItemUnits = 2;
 // The reference m follows the row's maximum only when that has grown by more
 // than this (in powers of two): until then weights are up to 2^8 instead of
@@ -1325,8 +1324,8 @@ cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream)
   const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   // Blocks of two query tiles halve what is read; but with fewer of them than
   // CTAs most are cut, and their parts' joins take longer than the reads: a
-  // prompt of 1024 tokens (32 heads on 8) 32.6 us in blocks of two, 27.5 in blocks
-  // of one; of 2048 tokens 53.0 and 56.0.
+  // prompt of 1024 tokens (32 heads on 8) takes 28.4 us in blocks of two and 26.4
+  // in blocks of one, one of 2048 tokens 49.2 and 54.5.
   const long long blocks = (long long)((a.n_tokens - 1) / (2 * p.tpt) + 1) * c.n_kv_heads;
   p.block = blocks < ctas ? p.tpt : 2 * p.tpt;
   const bool f16 = c.dtype == MOE_F16;
