@@ -280,6 +280,14 @@ ATTENDS = {
                                        sinks=200),
     "peaked long chunks": spec([900, 1100], [2600, 1500], 8, 2, 128, F16, 64, spread=10.0),
     "tiny scale": spec([4], [300], 4, 2, 64, F16, 16, scale=1e-20),
+    # more blocks of two query tiles than SMs
+    "blocks of two": spec([700, 333], [900, 333], 64, 4, 64, B16, 64),
+    "blocks of two, odd groups, windows": spec([611, 40, 290], [700, 1000, 1300], 56, 8, 128, F16,
+                                               16, heads_first=True, window=150, sinks=3),
+    "blocks of two beside passes": spec([600, 3, 9, 0, 160, 1, 33, 17, 16], [1500, 0, 2500, 9, 100,
+                                          1, 600, 17, 900], 64, 8, 64, B16, 32),
+    "blocks of two, peaked": spec([1250], [2100], 32, 8, 128, B16, 256, spread=12.0),
+    "blocks of two, one key head": spec([640, 9], [640, 3000], 128, 1, 64, F16, 128),
 }
 
 
