@@ -18,7 +18,9 @@
 //   two query tiles of the same keys, when a block of tokens fills more than
 //   one tile (each key tile is then read once for 256 rows), or
 //   the even and the odd key tiles of one query tile (verification passes of
-//   a few tokens: bound by reading the cache), joined at the end.
+//   a few tokens: bound by reading the cache), joined at the end, or
+//   two whole items of a request that differ in their key head only, where the
+//   CTA has both: nothing is joined, and an item's turn is one for both.
 //
 // Work. An item is (request, key head, block of tokens); its length is the
 // number of 128-key tiles its rows see, weighted by what they cost. All items'
@@ -58,9 +60,10 @@
 //   A mixed batch (3 prompt chunks, 20 passes, 56 heads of 64 columns, pages of
 //   16, 69 MB): 33.4 us, of which 25 are the longest range's item turns and
 //   small boxes, the others the start and one join.
-//   A prompt of 512 tokens: 18 us; 200 passes within windows of 512 keys: 125 us,
+//   A prompt of 512 tokens: 18 us; 200 passes within windows of 512 keys: 122 us,
 //   for an item's turn (products, results out, the next item's place: 3 us)
-//   stands against 5 tiles' loads.
+//   stands against 5 tiles' loads, or a pair's against 10. Without pairs this took
+//   125 us, and 40 passes of 16 heads over 8 to 71 keys 21.1 for 18.9.
 //   One pass of 5 tokens over 777 keys: 12.5 us, one chain of plan (2), loads and
 //   products (5), a part's hand-over (2), join (1.2) and the launch.
 #include <limits.h>
@@ -194,11 +197,16 @@ struct Walk {
   int b, h, block, u0, left;
 };
 
-// The CTA's part of an item: tiles [t0, t1).
+// The CTA's part of an item: tiles [t0, t1). Or two whole items of one request
+// that differ in their key head only (`pair`), a stream for each: the ring's
+// tile j is then tile j / 2 of head h + j % 2.
 struct Part {
   Item it;
   int t0, t1;
+  int n;     // tiles of the ring
   bool two;  // the block's tokens fill more than one query tile
+  int pair;  // 0 or 1
+  MOE_DEV int tile(int j) const { return tile_of(it, t0 + (j >> pair)); }
 };
 
 // The next part of the walk with tiles in it, which is then behind the walk;
@@ -225,8 +233,17 @@ struct Walker {
       out->two = it.ntok > p.tpt;
       b = w.b;
       h = w.h;
+      const bool whole = out->t0 == 0 && out->t1 == it.n;
       w.left -= u1 - w.u0;
       w.u0 = 0;
+      out->pair = 0;
+      if (whole && !out->two && r.q <= fixed && w.h + 1 < p.a.cache.n_kv_heads &&
+          units.tiles(w.left) >= it.n) {
+        out->pair = 1;
+        w.left -= min(w.left, units.all);
+        ++w.h;
+      }
+      out->n = (out->t1 - out->t0) << out->pair;
       if (w.left > 0 && ++w.block * fixed >= r.q) {
         w.block = 0;
         if (++w.h == p.a.cache.n_kv_heads) {
@@ -798,23 +815,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       __syncwarp();
       --queries;
-      q_row += p.tpt;
+      if (pt.pair) {
+        q_head += a.group;
+      } else {
+        q_row += p.tpt;
+      }
       if (slot) q_phase ^= 1u;
       slot ^= 1;
     };
     while (walk.next(&pt)) {
       const Item& it = pt.it;
-      const int n = pt.t1 - pt.t0;
+      const int n = pt.n;
       const int lead = pt.two ? 1 : 2;          // key tiles ahead of the value tiles
       if (which) {
-        queries = pt.two ? 2 : 1;
+        queries = pt.two || pt.pair ? 2 : 1;
         q_row = it.row0;
         q_head = walk.h * a.group;
       }
       const int32_t* table = a.block_table + (size_t)walk.b * a.max_blocks;
       // this lane's page of tile j (−1: it has none, or no row of it is seen)
       auto page_of = [&](int j) {
-        const int r0 = tile_of(it, pt.t0 + j) * kTile + lane * rows;
+        const int r0 = pt.tile(j) * kTile + lane * rows;
         const bool want = j < n && lane < n_pages && r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk);
         int pg = -1;
         if (want) {
@@ -858,11 +879,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim * 2);
         __syncwarp();
         const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
-        const int row = tile_of(it, pt.t0 + j) * kTile & (page - 1);  // 0 in small pages
+        const int row = page > kTile ? pt.tile(j) * kTile & (page - 1) : 0;
+        const int head = walk.h + (j & pt.pair);
 #pragma unroll
         for (int half = 0; half < kHalves; ++half)
           if (pg >= 0 && ((half * n_pages + lane) & 1) == which)
-            tma_load_4d_at(ring + stage * Z::kTileBytes + half * kHalfBytes, map, half * 64, walk.h,
+            tma_load_4d_at(ring + stage * Z::kTileBytes + half * kHalfBytes, map, half * 64, head,
                            row, pg, &m.full[stage], policy);
         if (++stage == kStages) {
           stage = 0;
@@ -925,21 +947,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     };
     while (walk.next(&pt)) {
       const Item& it = pt.it;
-      const int n = pt.t1 - pt.t0;
+      const int n = pt.n;
       const bool two = pt.two;
       // the stream sees something of a tile that begins at key0
       const int t_first = two ? s * p.tpt : 0, t_last = two && s == 0 ? p.tpt : it.ntok;
       const int hi = it.pos0 + t_last;
       const int lo = a.window > 0 ? it.pos0 + t_first - a.window + 1 - (kTile - 1) : INT_MIN;
       auto sees = [&](int j) {
-        const int key0 = tile_of(it, pt.t0 + j) * kTile;
+        const int key0 = pt.tile(j) * kTile;
         return (two || (j & 1) == s) && key0 < hi && (key0 >= lo || key0 < a.sinks);
       };
       // the query tiles: the stream's own, and the other one's
       uint32_t slot = 0;
-      for (int q = 0; q < (two ? 2 : 1); ++q, ++n_q) {
+      const bool own = two || pt.pair;                 // a query tile for either stream
+      for (int q = 0; q < (own ? 2 : 1); ++q, ++n_q) {
         wait(&m.q_full[n_q & 1u], n_q >> 1 & 1u, 0xA42);
-        if (!two || q == s) {
+        if (!own || q == s) {
           slot = n_q & 1u;
         } else {
           pass(&m.q_empty[n_q & 1u]);
@@ -963,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         // rows of V that no row of the item sees may hold anything: their
         // weights are 0, and 0 · NaN is not
-        const int key0 = tile_of(it, pt.t0 + j) * kTile;
+        const int key0 = pt.tile(j) * kTile;
         const bool now = has_v && sees(j);
         if (ok && now && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
           unsigned char* v = smem + Z::kOffRing + vt * Z::kTileBytes;
@@ -1035,8 +1058,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     bool open = false;                               // the last part does not end its item
     while (walk.next(&pt)) {
       const Item& it = pt.it;
-      const int n = pt.t1 - pt.t0;
-      const bool two = pt.two;
+      const int n = pt.n;
+      const bool two = pt.two, own = two || pt.pair;
       const int t_first = two ? s * p.tpt : 0, t_last = two && s == 0 ? p.tpt : it.ntok;
       const int tok = t_first + t_in;
       const bool valid = t_in < p.tpt && tok < t_last;
@@ -1049,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       float ref = -INFINITY, sum = 0.f;
       bool began = false;
       for (int j = two ? 0 : s; j < n; j += two ? 1 : 2) {
-        int key0 = tile_of(it, pt.t0 + j) * kTile;
+        int key0 = pt.tile(j) * kTile;
         if (!(key0 < s_hi && (key0 >= s_lo || key0 < a.sinks))) continue;
         key0 += half * kHalf;                        // this thread's keys
         wait(&m.s_full[s], s_phase, 0xA51);
@@ -1137,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
         const uint64_t dst = reinterpret_cast<uint64_t>(
             static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
-            (int64_t)(walk.h * a.group + g_in) * a.out_head_stride);
+            (int64_t)((walk.h + (s & pt.pair)) * a.group + g_in) * a.out_head_stride);
         const uint32_t quad_valid = __ballot_sync(0xffffffffu, valid) >> (lane & ~3) & 15u;
         uint16_t* quad_dst[4];
 #pragma unroll
@@ -1153,11 +1176,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       pair_sync();
       sum += *theirs;
       pair_sync();
-      if (!two) *mine = half == 0 ? ref : sum;
+      if (!own) *mine = half == 0 ? ref : sum;
       // factors of the two streams' O, and this thread's columns
       float f0 = 1.f, f1 = 0.f;
       int c_first = half * (kDim / 2), c_end = c_first + kDim / 2;
-      if (!two) {
+      if (!own) {
         // both streams hold sums of the same rows: every warp of a row joins
         // its share of the columns, 32 at least
         asm volatile("bar.sync 2, 512;" ::: "memory");
@@ -1180,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // number to be scaled
         const bool any0 = f0 > 0.f && sum > 0.f, any1 = f1 > 0.f;
         const bool warp_any1 = __any_sync(0xffffffffu, any1);
-        const uint32_t from = lanes + 256 + (two ? s * 128 : 0);
+        const uint32_t from = lanes + 256 + (own ? s * 128 : 0);
         float* slot = p.part + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * Z::kSlotFloats;
         const int prow = (two ? s * kTile : 0) + row;
 #pragma unroll 1
@@ -1230,7 +1253,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       // joined O and statistics have been read before either stream goes on
       umma::fence_before_sync();
-      if (two) {
+      if (own) {
         pair_sync();
       } else {
         asm volatile("bar.sync 2, 512;" ::: "memory");

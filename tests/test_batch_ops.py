@@ -287,6 +287,13 @@ ATTENDS = {
     "blocks of two beside passes": spec([600, 3, 9, 0, 160, 1, 33, 17, 16], [1500, 0, 2500, 9, 100,
                                           1, 600, 17, 900], 64, 8, 64, B16, 32),
     "blocks of two, peaked": spec([1250], [2100], 32, 8, 128, B16, 256, spread=12.0),
+    # more whole items than SMs: a CTA's go in pairs
+    "short items": spec([1 + i % 7 for i in range(120)], [1 + (i * 37) % 300 for i in range(120)],
+                        16, 8, 128, B16, 16),
+    "short items, odd heads": spec([1 + i % 3 for i in range(200)], [0 if i % 9 == 4 else 200 + i
+                                     for i in range(200)], 9, 3, 64, F16, 32, heads_first=True),
+    "short items, windows": spec([i % 6 for i in range(150)], [40 + 11 * i for i in range(150)], 28,
+                                 4, 64, B16, 256, window=200, sinks=2),
     "blocks of two, one key head": spec([640, 9], [640, 3000], 128, 1, 64, F16, 128),
 }
 
