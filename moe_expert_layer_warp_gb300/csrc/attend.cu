@@ -51,9 +51,9 @@
 //   906 MB): 153 us, 5.9 TB/s, 87 % of a copy's rate. The rest is the start
 //   (plan 2 us, first loads 3), turns between items, during which the ring
 //   holds only 2.5 tiles, and the joins (2 us). Windows of 4096 keys of 56
-//   heads: 146 us for 804 MB; tiles at the windows' ends cost 7 % more bytes.
-//   Long prompt chunks (957 GFLOP): 670 us cold and 725 us under the power
-//   cap, 1.43 and 1.32 PFLOP/s. A stream's chain of softmax (1450 cycles a
+//   heads: 144 us for 804 MB; tiles at the windows' ends cost 7 % more bytes.
+//   Long prompt chunks (957 GFLOP): 670 us cold and 730 us under the power
+//   cap, 1.43 and 1.31 PFLOP/s. A stream's chain of softmax (1450 cycles a
 //   tile) and products (1024, and 475 of hand-overs) runs beside the other
 //   stream's: the tensor cores work 70 % of a period. Tensor memory is full, so
 //   a stream's next scores cannot be computed beside its weights.
@@ -73,9 +73,9 @@
 #include <atomic>
 #include <chrono>
 
+#include "attend_mma.cuh"
 #include "batch_launch.h"
 #include "common.cuh"
-#include "tcgen05.cuh"
 #include "tmap.h"
 
 namespace moe {

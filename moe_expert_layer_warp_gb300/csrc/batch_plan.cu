@@ -20,6 +20,8 @@
 // writes whole lines whatever the order of the slots. 12345 tokens of 8 heads
 // of 128 columns (fp32 rounded to fp16, 149 MB) take 24 us, 6.2 TB/s, 91 % of a
 // copy's rate; 36 tokens 2.0 us, the launch.
+#include <cuda_fp16.h>
+
 #include "batch_launch.h"
 #include "common.cuh"
 

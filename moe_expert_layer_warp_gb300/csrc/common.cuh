@@ -6,7 +6,6 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -152,20 +151,14 @@ MOE_DEV void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int 
       : "memory");
 }
 
-// (dst: an address in the shared window)
-MOE_DEV void tma_load_4d_at(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                            uint64_t* bar, uint64_t policy) {
+MOE_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                         uint64_t* bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar)),
       "l"(policy)
       : "memory");
-}
-
-MOE_DEV void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                         uint64_t* bar, uint64_t policy) {
-  tma_load_4d_at(smem_addr(dst), map, c0, c1, c2, c3, bar, policy);
 }
 
 MOE_DEV void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,

@@ -24,6 +24,7 @@
 // shared memory (groups across lanes: 28 us). Warps that stay and load the
 // next token ahead were slower (22.9 us): the tokens that take fp64 then hold
 // up others. 64 tokens take 3.8 us, 9 take 2.6: a launch and one token's chain.
+#include <cuda_fp16.h>
 #include <limits.h>
 #include <math.h>
 
