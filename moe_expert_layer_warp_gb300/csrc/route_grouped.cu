@@ -17,8 +17,8 @@
 // in the logit, and experts are compared by their logits, exactly.
 //
 // 20011 tokens of 256 experts in 8 groups (sigmoid, bias, bf16) take 19.4 us;
-// the logits alone would take 1.7. What bounds it is issuing a token's some
-// 700 instructions and waiting for one lane's after another's: scores 5 us,
+// the logits alone would take 1.7. What bounds it is issuing a token's
+// 790 instructions and waiting for one lane's after another's: scores 5 us,
 // groups 4, the (k + 1)-th best 1, candidates and ranks 4, weights 4. A group's
 // experts lie in its own lanes, so its sum takes log2(lanes) steps and no
 // shared memory (groups across lanes: 28 us). Warps that stay and load the
