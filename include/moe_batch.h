@@ -43,6 +43,7 @@ extern "C" {
 #define MOE_MAX_REQUESTS 1024   /* requests per call */
 #define MOE_MAX_GROUPS 32       /* expert groups */
 #define MOE_MAX_HEAD_GROUP 128  /* query heads per key head */
+#define MOE_MAX_CACHE_LEN 2147483391 /* kv_len of moe_attend: 2^31 − 257, so that tile ends fit */
 
 /* Element types of the calls below (the first two are moe_wdtype's values). */
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
@@ -118,7 +119,8 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, const void* v
 typedef struct {
   int32_t n_heads; /* query heads, a multiple of n_kv_heads: head h reads key head
                       h / (n_heads / n_kv_heads) */
-  int32_t window;  /* 0: all earlier keys; W > 0: the W newest, the token's own included */
+  int32_t window;  /* 0: all earlier keys; W > 0: the W newest, the token's own included
+                      (any W up to 2^31 − 1) */
   int32_t sinks;   /* with a window: this many first keys of the request stay visible */
   float scale;     /* of the products q·k; finite, > 0 */
 } moe_attn_desc;
@@ -136,8 +138,9 @@ size_t moe_attend_workspace_bytes(const moe_kv_cache* cache, const moe_attn_desc
  * themselves are read from the cache: append them first.
  *   q         [n_tokens][n_heads][head_dim] of the cache's type, strides
  *             positive multiples of 8, 16-byte aligned.
- *   q_start   [n_requests+1], kv_len [n_requests], block_table
- *             [n_requests][max_blocks]: as moe_plan_batch writes them.
+ *   q_start   [n_requests+1], kv_len [n_requests] (each ≤ MOE_MAX_CACHE_LEN),
+ *             block_table [n_requests][max_blocks]: as moe_plan_batch writes
+ *             them.
  *   out       same shape and type, with its own strides (multiples of 8,
  *             16-byte aligned). Rows of no request are not written.
  * Table entries of pages that hold no key any new token of the request sees

@@ -31,6 +31,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_build_union", "moe_verify_p
 
 MOE_F32, MOE_BF16, MOE_F16 = range(3)
 MOE_MAX_REQUESTS, MOE_MAX_GROUPS, MOE_MAX_HEAD_GROUP = 1024, 32, 128
+MOE_MAX_CACHE_LEN = 2 ** 31 - 257
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 

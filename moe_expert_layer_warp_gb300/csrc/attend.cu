@@ -152,12 +152,17 @@ MOE_DEV Request request(const AttendArgs& a, int page_shift, int b, bool* bad) {
   r.q = last - r.first;
   r.len = len;
   *bad = f != r.first || l != last;
-  if (len < 0 || len > ((int64_t)a.max_blocks << page_shift)) {
+  if (len < 0 || len > MOE_MAX_CACHE_LEN || len > ((int64_t)a.max_blocks << page_shift)) {
     r.len = 0;
     *bad = true;
   }
   return r;
 }
+
+// The first key that a token at position `pos` sees, or below 0. (A cache shorter
+// than the pass has negative positions, and a window may be as long as the
+// longest cache: their difference passes 32 bits, and says no more than 0's.)
+MOE_DEV int window_from(int pos, int window) { return max(pos, 0) - window + 1; }
 
 // `fixed`: the tokens of a block.
 MOE_DEV Item make_item(const AttendArgs& a, const Request& r, int block, int fixed) {
@@ -167,7 +172,7 @@ MOE_DEV Item make_item(const AttendArgs& a, const Request& r, int block, int fix
   it.ntok = min(fixed, r.q - tok0);
   it.pos0 = r.len - r.q + tok0;
   it.hi = max(0, it.pos0 + it.ntok);
-  it.lo = a.window > 0 ? min(it.hi, max(0, it.pos0 - a.window + 1)) : 0;
+  it.lo = a.window > 0 ? min(it.hi, max(0, window_from(it.pos0, a.window))) : 0;
   it.sk = min(a.sinks, it.lo);
   it.lo_tile = it.lo / kTile;
   it.ns = min((it.sk + kTile - 1) / kTile, it.lo_tile);
@@ -952,7 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // the stream sees something of a tile that begins at key0
       const int t_first = two ? s * p.tpt : 0, t_last = two && s == 0 ? p.tpt : it.ntok;
       const int hi = it.pos0 + t_last;
-      const int lo = a.window > 0 ? it.pos0 + t_first - a.window + 1 - (kTile - 1) : INT_MIN;
+      const int lo =
+          a.window > 0 ? window_from(it.pos0 + t_first, a.window) - (kTile - 1) : INT_MIN;
       auto sees = [&](int j) {
         const int key0 = pt.tile(j) * kTile;
         return (two || (j & 1) == s) && key0 < hi && (key0 >= lo || key0 < a.sinks);
@@ -1066,9 +1072,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const int pos = it.pos0 + tok;
       const int hi = valid ? max(0, pos + 1) : 0;
-      const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      const int lo = a.window > 0 ? max(0, window_from(pos, a.window)) : 0;
       const int s_hi = it.pos0 + t_last;
-      const int s_lo = a.window > 0 ? it.pos0 + t_first - a.window + 1 - (kTile - 1) : INT_MIN;
+      const int s_lo =
+          a.window > 0 ? window_from(it.pos0 + t_first, a.window) - (kTile - 1) : INT_MIN;
       float ref = -INFINITY, sum = 0.f;
       bool began = false;
       for (int j = two ? 0 : s; j < n; j += two ? 1 : 2) {

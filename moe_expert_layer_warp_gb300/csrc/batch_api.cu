@@ -156,8 +156,10 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_attn_desc* attn, cons
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < moe::attend_workspace_bytes(cache->head_dim))
     return bad("workspace null, not 256-byte aligned or too small");
+  // a window beyond the longest cache is one of its length
+  const int window = attn->window < MOE_MAX_CACHE_LEN ? attn->window : MOE_MAX_CACHE_LEN;
   int sms;
-  moe::AttendArgs a = {*cache, attn->n_heads, attn->n_heads / cache->n_kv_heads, attn->window,
+  moe::AttendArgs a = {*cache, attn->n_heads, attn->n_heads / cache->n_kv_heads, window,
                        attn->window > 0 ? attn->sinks : 0, attn->scale, q, q_token_stride,
                        q_head_stride, n_tokens, n_requests, max_blocks, q_start, kv_len,
                        block_table, out, out_token_stride, out_head_stride, workspace, nullptr};
