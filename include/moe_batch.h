@@ -5,6 +5,7 @@
  *   moe_plan_batch     block tables, slots and positions from request lengths
  *   moe_kv_append      the pass's keys and values into a paged cache
  *   moe_attend         every new token's attention over that cache
+ *                      (moe_attend_padded: and zeros for rows of no request)
  *   moe_route_grouped  experts from router logits: softmax or sigmoid scores,
  *                      balance bias, groups, top-k, renormalised weights
  * and then moe_build_union, an expert engine and moe_combine of moe_warp.h.
@@ -154,6 +155,15 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_attn_desc* attn, cons
                       int32_t max_blocks, int32_t n_requests, void* workspace,
                       size_t workspace_bytes, void* out, int64_t out_token_stride,
                       int64_t out_head_stride, void* stream);
+
+/* moe_attend for batches padded to a fixed number of tokens: rows of `out` that
+ * belong to no request (those from q_start[n_requests] on) are written zeros. */
+moe_status moe_attend_padded(const moe_kv_cache* cache, const moe_attn_desc* attn, const void* q,
+                             int64_t q_token_stride, int64_t q_head_stride, int32_t n_tokens,
+                             const int32_t* q_start, const int32_t* kv_len,
+                             const int32_t* block_table, int32_t max_blocks, int32_t n_requests,
+                             void* workspace, size_t workspace_bytes, void* out,
+                             int64_t out_token_stride, int64_t out_head_stride, void* stream);
 
 /* --------------------------------------------------------------- routing --*/
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;

@@ -27,7 +27,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_build_union", "moe_verify_p
             "moe_last_cuda_error_string", "moe_verify_dedup_noalloc", "moe_noalloc_scratch_limit",
             "moe_diag_bounded_wait", "moe_route_biased", "moe_route_union", "moe_verify_pass",
             "moe_verify_pass_fused", "moe_gate", "moe_plan_batch", "moe_kv_append",
-            "moe_attend_workspace_bytes", "moe_attend", "moe_route_grouped")
+            "moe_attend_workspace_bytes", "moe_attend", "moe_attend_padded", "moe_route_grouped")
 
 MOE_F32, MOE_BF16, MOE_F16 = range(3)
 MOE_MAX_REQUESTS, MOE_MAX_GROUPS, MOE_MAX_HEAD_GROUP = 1024, 32, 128
@@ -131,8 +131,10 @@ def load(path: str = LIB_PATH):
     lib.moe_attend_workspace_bytes.argtypes = [C, A]
     lib.moe_attend_workspace_bytes.restype = SZ
     lib.moe_attend.argtypes = [C, A, P, I64, I64, I32, P, P, P, I32, I32, P, SZ, P, I64, I64, P]
+    lib.moe_attend_padded.argtypes = lib.moe_attend.argtypes
     lib.moe_route_grouped.argtypes = [ctypes.POINTER(RouterDesc), P, I32, I64, P, I32, P, P, P]
-    for f in ("moe_plan_batch", "moe_kv_append", "moe_attend", "moe_route_grouped"):
+    for f in ("moe_plan_batch", "moe_kv_append", "moe_attend", "moe_attend_padded",
+              "moe_route_grouped"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_route", "moe_build_union", "moe_verify_perslot", "moe_verify_dedup",
               "moe_combine", "moe_last_device_error", "moe_verify_dedup_noalloc",

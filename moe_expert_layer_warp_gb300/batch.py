@@ -213,21 +213,22 @@ class PagedAttention:
         """q: [n][n_heads][head_dim] of the cache's type; q_start [B+1], kv_len
         [B] and block_table [B][M] int32 as BatchPlanner.plan leaves them.
         Returns `out` (same shape and type, rows contiguous), or the object's
-        own buffer. Rows of no request keep what `out` held."""
+        own buffer. Rows of no request (a padded batch's) keep what `out` held,
+        and are zeros in the object's own buffer."""
         c, n, i32 = self.cache, q.shape[0], torch.int32
-        at = c._index
+        at, call = c._index, self._lib.moe_attend
         if out is None:
             if n != self._n:
                 if n > self.max_tokens:
                     raise ValueError("%d tokens, more than max_tokens %d" % (n, self.max_tokens))
                 self._n, self._view = n, self._out[:n]
-            out = self._view
+            out, call = self._view, self._lib.moe_attend_padded
         q_token, q_head = self._check("q", q, n)
         out_token, out_head = self._check("out", out, n)
         if block_table.dim() != 2:
             raise ValueError("block_table must be [requests][blocks]")
         B, M = block_table.shape
-        st = self._lib.moe_attend(
+        st = call(
             c._cref, self._dref, q.data_ptr(), q_token, q_head, n,
             _need(q_start, "q_start", i32, (B + 1,), at), _need(kv_len, "kv_len", i32, (B,), at),
             _need(block_table, "block_table", i32, (B, M), at), M, B, self._ws_ptr,

@@ -715,6 +715,22 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
     join_many<kDim, kF16>(p, st, first, rows);
 }
 
+// Rows before the first request's and behind the last one's become zeros; the
+// softmax threads of all CTAs share them.
+template <int kDim>
+__device__ __noinline__ void clear_rows(const AttendArgs& a) {
+  const int first = min(max(a.q_start[0], 0), a.n_tokens);
+  const int last = min(max(a.q_start[a.n_requests], first), a.n_tokens);
+  const int64_t n = (int64_t)(first + (a.n_tokens - last)) * a.n_heads * (kDim / 8);
+  for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x - 128; i < n; i += gridDim.x * 512) {
+    const int64_t row = i / (kDim / 8);
+    const int64_t t = row / a.n_heads, token = t < first ? t : t - first + last;
+    uint16_t* to = static_cast<uint16_t*>(a.out) + token * a.out_token_stride +
+                   (row - t * a.n_heads) * a.out_head_stride;
+    reinterpret_cast<uint4*>(to)[i % (kDim / 8)] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // Barriers and words behind the ring.
 struct Misc {
   uint64_t full[10], empty[10];
@@ -1041,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   } else {
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (a.clear) clear_rows<kDim>(a);                // while the first tiles are on their way
     Walker walk(p, m.start.w, m.start.r);
     const int s = warp >> 3, half = warp >> 2 & 1;  // stream, and half of a tile's keys
     const int row = threadIdx.x & 127;               // row of the tile, TMEM lane

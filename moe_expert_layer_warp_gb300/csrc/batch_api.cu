@@ -56,6 +56,50 @@ const char* attn_fault(const moe_kv_cache* c, const moe_attn_desc* a, moe_status
   return nullptr;
 }
 
+// moe_attend and moe_attend_padded.
+moe_status attend(const moe_kv_cache* cache, const moe_attn_desc* attn, const void* q,
+                  int64_t q_token_stride, int64_t q_head_stride, int32_t n_tokens,
+                  const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                  int32_t max_blocks, int32_t n_requests, void* workspace, size_t workspace_bytes,
+                  void* out, int64_t out_token_stride, int64_t out_head_stride, void* stream,
+                  const char* fn, bool padded) {
+  moe_status st;
+  if (const char* why = attn_fault(cache, attn, &st)) return moe::refuse(st, fn, why);
+  auto bad = [&](const char* why) { return moe::refuse(MOE_EINVAL, fn, why); };
+  if (n_requests < 1 || n_requests > MOE_MAX_REQUESTS) return bad("n_requests out of range");
+  if (n_tokens < 0 || max_blocks < 1) return bad("n_tokens or max_blocks out of range");
+  if (q_token_stride < 1 || q_head_stride < 1 || q_token_stride % 8 != 0 ||
+      q_head_stride % 8 != 0 || q_token_stride >= kMaxStride || q_head_stride >= kMaxStride)
+    return bad("q strides must be positive multiples of 8 elements");
+  // rows of out must not overlap: either order of tokens and heads
+  const int64_t D = cache->head_dim, H = attn->n_heads;
+  const bool heads_in = out_head_stride >= D && (n_tokens < 2 || out_token_stride >= H * out_head_stride);
+  const bool tokens_in = out_token_stride >= D && (H < 2 || out_head_stride >= n_tokens * out_token_stride);
+  if (out_token_stride % 8 != 0 || out_head_stride % 8 != 0 || !(heads_in || tokens_in))
+    return bad("out strides must be multiples of 8 elements and rows must not overlap");
+  if (n_tokens == 0) return MOE_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16))
+    return bad("q or out null or not 16-byte aligned");
+  if (!q_start || !kv_len || !block_table || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
+      !aligned(block_table, 4))
+    return bad("q_start, kv_len or block_table null or misaligned");
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < moe::attend_workspace_bytes(cache->head_dim))
+    return bad("workspace null, not 256-byte aligned or too small");
+  // a window beyond the longest cache is one of its length
+  const int window = attn->window < MOE_MAX_CACHE_LEN ? attn->window : MOE_MAX_CACHE_LEN;
+  int sms;
+  moe::AttendArgs a = {*cache, attn->n_heads, attn->n_heads / cache->n_kv_heads, window,
+                       attn->window > 0 ? attn->sinks : 0, attn->scale, q, q_token_stride,
+                       q_head_stride, n_tokens, n_requests, max_blocks, q_start, kv_len,
+                       block_table, out, out_token_stride, out_head_stride, padded ? 1 : 0, workspace,
+                       nullptr};
+  st = moe::call_device(&sms, &a.err);
+  if (st != MOE_OK) return st;
+  const cudaError_t e = moe::launch_attend(a, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : moe::fail_cuda(e, fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -132,41 +176,20 @@ moe_status moe_attend(const moe_kv_cache* cache, const moe_attn_desc* attn, cons
                       int32_t max_blocks, int32_t n_requests, void* workspace,
                       size_t workspace_bytes, void* out, int64_t out_token_stride,
                       int64_t out_head_stride, void* stream) {
-  const char* fn = "moe_attend";
-  moe_status st;
-  if (const char* why = attn_fault(cache, attn, &st)) return moe::refuse(st, fn, why);
-  auto bad = [&](const char* why) { return moe::refuse(MOE_EINVAL, fn, why); };
-  if (n_requests < 1 || n_requests > MOE_MAX_REQUESTS) return bad("n_requests out of range");
-  if (n_tokens < 0 || max_blocks < 1) return bad("n_tokens or max_blocks out of range");
-  if (q_token_stride < 1 || q_head_stride < 1 || q_token_stride % 8 != 0 ||
-      q_head_stride % 8 != 0 || q_token_stride >= kMaxStride || q_head_stride >= kMaxStride)
-    return bad("q strides must be positive multiples of 8 elements");
-  // rows of out must not overlap: either order of tokens and heads
-  const int64_t D = cache->head_dim, H = attn->n_heads;
-  const bool heads_in = out_head_stride >= D && (n_tokens < 2 || out_token_stride >= H * out_head_stride);
-  const bool tokens_in = out_token_stride >= D && (H < 2 || out_head_stride >= n_tokens * out_token_stride);
-  if (out_token_stride % 8 != 0 || out_head_stride % 8 != 0 || !(heads_in || tokens_in))
-    return bad("out strides must be multiples of 8 elements and rows must not overlap");
-  if (n_tokens == 0) return MOE_OK;
-  if (!q || !out || !aligned(q, 16) || !aligned(out, 16))
-    return bad("q or out null or not 16-byte aligned");
-  if (!q_start || !kv_len || !block_table || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
-      !aligned(block_table, 4))
-    return bad("q_start, kv_len or block_table null or misaligned");
-  if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < moe::attend_workspace_bytes(cache->head_dim))
-    return bad("workspace null, not 256-byte aligned or too small");
-  // a window beyond the longest cache is one of its length
-  const int window = attn->window < MOE_MAX_CACHE_LEN ? attn->window : MOE_MAX_CACHE_LEN;
-  int sms;
-  moe::AttendArgs a = {*cache, attn->n_heads, attn->n_heads / cache->n_kv_heads, window,
-                       attn->window > 0 ? attn->sinks : 0, attn->scale, q, q_token_stride,
-                       q_head_stride, n_tokens, n_requests, max_blocks, q_start, kv_len,
-                       block_table, out, out_token_stride, out_head_stride, workspace, nullptr};
-  st = moe::call_device(&sms, &a.err);
-  if (st != MOE_OK) return st;
-  const cudaError_t e = moe::launch_attend(a, sms, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? MOE_OK : moe::fail_cuda(e, "moe_attend launch");
+  return attend(cache, attn, q, q_token_stride, q_head_stride, n_tokens, q_start, kv_len,
+                block_table, max_blocks, n_requests, workspace, workspace_bytes, out,
+                out_token_stride, out_head_stride, stream, "moe_attend", false);
+}
+
+moe_status moe_attend_padded(const moe_kv_cache* cache, const moe_attn_desc* attn, const void* q,
+                             int64_t q_token_stride, int64_t q_head_stride, int32_t n_tokens,
+                             const int32_t* q_start, const int32_t* kv_len,
+                             const int32_t* block_table, int32_t max_blocks, int32_t n_requests,
+                             void* workspace, size_t workspace_bytes, void* out,
+                             int64_t out_token_stride, int64_t out_head_stride, void* stream) {
+  return attend(cache, attn, q, q_token_stride, q_head_stride, n_tokens, q_start, kv_len,
+                block_table, max_blocks, n_requests, workspace, workspace_bytes, out,
+                out_token_stride, out_head_stride, stream, "moe_attend_padded", true);
 }
 
 moe_status moe_route_grouped(const moe_router_desc* r, const void* logits, int32_t dtype,

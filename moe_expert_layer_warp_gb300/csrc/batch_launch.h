@@ -45,6 +45,7 @@ struct AttendArgs {
   const int32_t* block_table;
   void* out;
   int64_t out_token_stride, out_head_stride;
+  int clear;           // rows of no request become zeros
   void* workspace;
   unsigned int* err;
 };

@@ -1,0 +1,19 @@
+"""Host-only checks of include/moe_batch.h's entry points and their Python
+objects beyond their refusals: nothing is launched (no GPU is touched)."""
+import ctypes
+
+import pytest
+
+from moe_expert_layer_warp_gb300 import api
+from tests.test_batch_abi import ONE, _cache, _why, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("at,value,reason", [
+    (0, ONE + 8, "q or out"), (1, 100, "q strides"), (8, 0, "n_requests"), (10, 16, "workspace"),
+    (13, 32, "out strides")])
+def test_padded_attend_refuses_what_attend_refuses(lib, at, value, reason):
+    c, a = _cache(), api.AttnDesc(8, 0, 0, 0.125)
+    args = [ONE, 512, 64, 4, ONE, ONE, ONE, 4, 2, ONE, 1 << 30, ONE, 512, 64]
+    args[at] = value
+    assert lib.moe_attend_padded(ctypes.byref(c), ctypes.byref(a), *args, None) == api.MOE_EINVAL
+    assert reason in _why() and "moe_attend_padded" in _why()

@@ -50,3 +50,22 @@ def test_lengths_near_the_limit(lib):
         out = r.attend(q, qs, kv + (shift + more), far)
         assert lib.moe_last_device_error() == lib.MOE_EDEVICE
         assert (out == 0).all()
+
+
+# ------------------------------------------------------- padded batches -----
+@pytest.mark.parametrize("q_len,kv_len,pad", [([3, 5], [40, 300], 7), ([0, 0], [5, 0], 4),
+                                              ([400], [600], 300), ([2], [0], 1)])
+def test_rows_of_no_request_are_zeros_in_the_objects_buffer(lib, q_len, kv_len, pad):
+    """Padding rows of a batch of fixed size: neither what the buffer held at
+    first nor an earlier call's results."""
+    from moe_expert_layer_warp_gb300 import batch
+    a = Attend(q_len, kv_len, 6, 2, 128, B16, 16)
+    q, qs, kv, table = a.args()
+    n = q.shape[0]
+    wide = torch.cat([q, torch.randn(pad, *q.shape[1:], device="cuda").to(q.dtype)])
+    r = batch.PagedAttention(batch.PagedCache(a.k, a.v), 6, n + pad)
+    r.attend(wide, qs, kv, table).fill_(float("nan"))       # what an earlier call left
+    out = r.attend(wide, qs, kv, table)
+    assert lib.moe_last_device_error() == lib.MOE_OK
+    assert (out[n:] == 0).all()
+    a.check(out[:n])
