@@ -543,6 +543,10 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
     count += __popc(who);
   }
   const bool crowd = count > 32;
+  // what the bounds of two choices (see bound() below) never exceed together
+  auto bounds_most = [&](float c1, float c2) {
+    return (sigmoid ? 0x1p-19f : 0x1p-17f) + (fabsf(c1) + fabsf(c2)) * 0x1p-23f;
+  };
   __syncwarp();
   float my_c = kAbsent;
   int my_e = 0;
@@ -585,6 +589,19 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
         cand_e[warp][j] = first + at;
       }
     }
+    if (!by_logit) {
+      // those left must lie below the k-th by what no bound exceeds, or equal
+      // it in logit and bias (and come after it)
+      __syncwarp();
+      const float c_k = cand_c[warp][k - 1];
+      const float x_k = load_logit(row + cand_e[warp][k - 1]);
+      const float b_k = __ldg(bias + cand_e[warp][k - 1]);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (c[i] > kMasked && !(c_k - c[i] > bounds_most(c_k, c[i])) &&
+            !(load_logit(row + first + i) == x_k && __ldg(bias + first + i) == b_k))
+          unsure = true;
+    }
   }
   __syncwarp();
   // rank j's expert in lane j
@@ -600,15 +617,16 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
   float x = lane < count ? load_logit(row + my_e) : -INFINITY;
   float s = score_of(x);
   if (!by_logit) {
-    // Neighbours in the order must differ by more than their bounds — for a
-    // sigmoid s·((1 − s)·(|x|·2^-23.4 + 2^-22) + 2^-22), (1 − s)·|x| ≤ 0.28
+    // Neighbours in the order of the k must differ by more than their bounds — for
+    // a sigmoid s·((1 − s)·(|x|·2^-23.4 + 2^-22) + 2^-22), (1 − s)·|x| ≤ 0.28
     // for x > 0; for a softmax s·(|x|·2^-23.4 + 2^-19.4) — or be equal in
-    // logit and bias: then the index decides, here as exactly. Most tokens'
-    // do by what no bound exceeds.
+    // logit and bias: then the index decides, here as exactly. So must the last
+    // of the k and every other candidate, not the next one alone: a large score
+    // beside a negative bias has a larger bound than those before it. Most
+    // tokens' do by what no bound exceeds.
     const float c2 = __shfl_down_sync(kAll, my_c, 1);
     const bool next = lane < k && lane + 1 < count && c2 > kMasked;
-    const float off_most = (sigmoid ? 0x1p-19f : 0x1p-17f) + (fabsf(my_c) + fabsf(c2)) * 0x1p-23f;
-    if (__any_sync(kAll, next && !(my_c - c2 > off_most))) {
+    if (__any_sync(kAll, next && !(my_c - c2 > bounds_most(my_c, c2)))) {
       auto bound = [&](float v_s, float v_x, float v_c) {
         return (sigmoid ? v_s * 0x1.6ap-21f + fmaxf(-v_x, 0.f) * v_s * 0x1p-23f
                         : v_s * (fabsf(v_x - top) * 0x1p-23f + 0x1p-19f)) +
@@ -616,9 +634,12 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
       };
       const float b = lane < count ? __ldg(bias + my_e) : 0.f;
       const float off = lane < count && x != -INFINITY ? bound(s, x, my_c) : 0.f;
-      const float x2 = __shfl_down_sync(kAll, x, 1), b2 = __shfl_down_sync(kAll, b, 1);
-      const float off2 = __shfl_down_sync(kAll, off, 1);
-      const bool close = next && !(my_c - c2 > off + off2) && !(x == x2 && b == b2);
+      // the one before: of a candidate behind the k, the last of the k
+      const int ahead = lane < k ? max(lane - 1, 0) : k - 1;
+      const float c1 = __shfl_sync(kAll, my_c, ahead), off1 = __shfl_sync(kAll, off, ahead);
+      const float x1 = __shfl_sync(kAll, x, ahead), b1 = __shfl_sync(kAll, b, ahead);
+      const bool close = lane > 0 && lane < count && my_c > kMasked &&
+                         !(c1 - my_c > off1 + off) && !(x1 == x && b1 == b);
       if (!__any_sync(kAll, close)) {
       } else if (crowd) {
         unsure = true;                     // others may be as close

@@ -69,3 +69,57 @@ def test_rows_of_no_request_are_zeros_in_the_objects_buffer(lib, q_len, kv_len, 
     assert lib.moe_last_device_error() == lib.MOE_OK
     assert (out[n:] == 0).all()
     a.check(out[:n])
+
+
+# ------------------------------------------------------------- near ties ----
+def test_route_near_tie_past_its_neighbour(lib):
+    """The three best choices lie within 3e-8: the second's bound is small, the
+    third's, a large score beside a negative bias, is not, and the third is the
+    largest of the three."""
+    x = torch.tensor([[-25.0, -25.0, 1.1229205131530762]])
+    bias = torch.tensor([0.05000002682209015, 0.050000011920928955, -0.7045300006866455])
+    _route(lib, x, 1, 1, 1, 1, "sigmoid", bias, False, 1.0)
+    _route(lib, x, 2, 1, 1, 1, "sigmoid", bias, True, 1.0)
+
+
+def _near_ties(score, E, n, seed):
+    """Rows whose choices lie within some 1e-7 of each other: half of the
+    experts by their bias alone, the others by a large score beside a bias that
+    takes it back, their logits a few roundings away from a tie."""
+    g = torch.Generator().manual_seed(seed)
+    half = E // 2
+    x = torch.full((n, E), -25.0)
+    x[:, half:] = (torch.rand(E - half, generator=g) * 2).expand(n, -1)
+    step = 2.0 ** -23 * torch.randint(-6, 7, (n, E - half), generator=g)
+    x[:, half:] += step.float() * x[:, half:]
+    s = torch.sigmoid(x[0].double()) if score == "sigmoid" else torch.softmax(x[0].double(), 0)
+    near = 0.05 + (torch.rand(E, generator=g).double() - 0.5) * 6e-8
+    order = torch.randperm(E, generator=g)
+    return x[:, order].contiguous(), (near - s).float()[order].contiguous()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,k,G,tg,top", [(8, 1, 1, 1, 1), (16, 3, 1, 1, 1), (32, 8, 1, 1, 1),
+                                          (64, 6, 1, 1, 1), (24, 2, 4, 2, 1), (64, 8, 8, 3, 2),
+                                          (256, 16, 8, 4, 2)])
+def test_route_near_ties_of_unequal_bounds(lib, score, E, k, G, tg, top):
+    x, bias = _near_ties(score, E, 300, E + k)
+    _route(lib, x, k, G, tg, top, score, bias, False, 1.0)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_near_ties_among_many_equal_choices(lib, score):
+    """Forty experts of one logit and one bias, and others whose choices lie a
+    few roundings above or below theirs."""
+    x, bias = _near_ties(score, 64, 300, 1)
+    low = x[0] == -25.0
+    few = low.nonzero().flatten()
+    x[:, few[20:]] = -30.0
+    bias[few[20:]] = -1.0
+    more = (~low).nonzero().flatten()[:20]
+    x[:, more] = -25.0
+    s = torch.sigmoid(x.double()) if score == "sigmoid" else torch.softmax(x.double(), 1)
+    bias[~low] -= (s[0] + bias.double() - 0.05)[~low].float()
+    bias[more] = bias[few[:20]] = 0.05
+    for k in (1, 5, 16):
+        _route(lib, x, k, 1, 1, 1, score, bias, False, 1.0)
