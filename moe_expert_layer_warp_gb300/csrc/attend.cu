@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&m.full[i], 1);
+      mbar_init(&m.full[i], 2);                // either loader, with the bytes of its boxes
       mbar_init(&m.empty[i], 2);
     }
     for (int s = 0; s < 2; ++s) {
@@ -821,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const uint64_t policy = l2_evict_normal_policy();
     // this lane's boxes in the ring
     const uint32_t ring = smem_addr(smem) + Z::kOffRing + lane * rows * 128;
+    constexpr uint32_t kEven = 0x55555555u;     // even lanes
     int stage = 0, slot = 0, queries = 0, q_row = 0, q_head = 0;
     uint32_t phase = 0, q_phase = 0;
     // the next query tile, if its slot is free: a box is the 128 / group
@@ -896,8 +897,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         if (!ok && *lost == 0) *lost = 0xA30;
         if (!free) continue;
-        if (lane == 0 && !which)
-          mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim * 2);
+        // Either loader arrives, boxes or none: a stage can then not be filled
+        // and emptied twice past one of them, which would take the older phase
+        // of `empty` for the one it waits for.
+        if (lane == 0) {
+          int mine = 0;
+#pragma unroll
+          for (int half = 0; half < kHalves; ++half)
+            mine += __popc(wanted & (((half * n_pages) & 1) == which ? kEven : ~kEven));
+          mbar_arrive_expect_tx(&m.full[stage], mine * rows * 128);
+        }
         __syncwarp();
         const CUtensorMap* map = is_k ? &p.kmap : &p.vmap;
         const int row = page > kTile ? pt.tile(j) * kTile & (page - 1) : 0;

@@ -123,3 +123,19 @@ def test_route_near_ties_among_many_equal_choices(lib, score):
     bias[more] = bias[few[:20]] = 0.05
     for k in (1, 5, 16):
         _route(lib, x, k, 1, 1, 1, score, bias, False, 1.0)
+
+
+# ------------------------------------------------ tiles of one loader's boxes
+@pytest.mark.parametrize("page", [128, 256])
+@pytest.mark.parametrize("q_len,kv_len,Hq,H,window", [
+    ([3], [30000], 4, 1, 0), ([2] * 40, [4000 + 900 * i for i in range(40)], 8, 4, 0),
+    ([600, 5, 900], [6000, 9000, 900], 16, 8, 0), ([9] * 12, [20000] * 12, 4, 2, 9000)])
+def test_items_longer_than_the_ring_in_one_box_a_tile(lib, page, q_len, kv_len, Hq, H, window):
+    """Heads of 64 columns in pages of a tile or two: a tile is one box, and the
+    second loader has none of its own for more tiles than the ring holds."""
+    a = Attend(q_len, kv_len, Hq, H, 64, B16, page, window=window)
+    r = a.runner()
+    for _ in range(3):
+        out = r.attend(*a.args())
+        assert lib.moe_last_device_error() == lib.MOE_OK
+    a.check(out)
