@@ -150,8 +150,11 @@ __global__ void __launch_bounds__(kPlanThreads)
     int32_t* dst = b.block_table + (size_t)r * b.max_blocks + p.held;
     for (int i = lane; i < p.given; i += 32) dst[i] = b.free_pages[p.take + i];
   }
-  // slots and positions, a thread per token
-  for (int t = blockIdx.x * kPlanThreads + tid; t < n_tokens; t += gridDim.x * kPlanThreads) {
+  // slots and positions, a thread per token (64 bits: a step of the grid from a t
+  // near 2^31 passes 32)
+  for (int64_t at0 = blockIdx.x * kPlanThreads + tid; at0 < n_tokens;
+       at0 += gridDim.x * kPlanThreads) {
+    const int t = (int)at0;
     int64_t slot = -1;
     int pos = -1;
     if (t < total) {

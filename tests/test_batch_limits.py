@@ -139,3 +139,21 @@ def test_items_longer_than_the_ring_in_one_box_a_tile(lib, page, q_len, kv_len, 
         out = r.attend(*a.args())
         assert lib.moe_last_device_error() == lib.MOE_OK
     a.check(out)
+
+
+# --------------------------------------------------------- padded plans -----
+def test_plan_padded_to_the_types_limit(lib):
+    """Rows of padding up to 2^31 - 1: all written, none beside them."""
+    from moe_expert_layer_warp_gb300 import batch
+    n = 2 ** 31 - 1
+    P = batch.BatchPlanner(16, 2, n)
+    P._slots.fill_(7)
+    P._positions.fill_(7)
+    table = i32([[3, -1], [5, 6]])
+    r = P.plan(i32([4, 3]), i32([14, 15]), i32([1, 2]), i32([9, 8]), i32([0, 2]), table, n)
+    assert lib.moe_last_device_error() == lib.MOE_OK
+    assert r.slots[:7].tolist() == [62, 63, 144, 145, 95, 96, 97]
+    assert r.positions[:7].tolist() == [14, 15, 16, 17, 15, 16, 17]
+    for t in (r.slots, r.positions):
+        for part in t[7:].split(2 ** 28):
+            assert bool((part == -1).all())
