@@ -135,8 +135,9 @@ size_t moe_attend_workspace_bytes(const moe_kv_cache* cache, const moe_attn_desc
  * token i of request b is at position p = kv_len[b] − q_len_b + i, q_len_b =
  * q_start[b+1] − q_start[b], and sees keys j ≤ p, with a window only those
  * with p − j < window or j < sinks. A token that sees no key (kv_len 0, or
- * shorter than the pass) gets zeros. The keys and values of the new tokens
- * themselves are read from the cache: append them first.
+ * shorter than the pass) gets zeros, one with NaN among its scores NaN. The
+ * keys and values of the new tokens themselves are read from the cache: append
+ * them first.
  *   q         [n_tokens][n_heads][head_dim] of the cache's type, strides
  *             positive multiples of 8, 16-byte aligned.
  *   q_start   [n_requests+1], kv_len [n_requests] (each ≤ MOE_MAX_CACHE_LEN),

@@ -520,6 +520,10 @@ MOE_DEV uint32_t narrow(float lo, float hi) {
   }
 }
 
+// 1 / Σ of a row's weights; 0 for a row that sees no key. NaN among the scores a
+// row sees makes its Σ, and so its result, NaN.
+MOE_DEV float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+
 // v[i] of lane 4q + j  <->  v[j] of lane 4q + i.
 MOE_DEV uint4 shfl_xor4(uint4 v, int mask) {
   return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask),
@@ -598,7 +602,11 @@ MOE_DEV void join_few(const Params& p, const Start& st, int first, int rows) {
       float top = m;
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, mc[j]);
-      if (top == -INFINITY) continue;              // (the parts hold zeros)
+      if (top == -INFINITY) {                      // (the parts hold zeros, or sums of NaN)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += sc[j];
+        continue;
+      }
       const float keep = exp2_approx(m - top);
       m = top;
       sum *= keep;
@@ -613,7 +621,7 @@ MOE_DEV void join_few(const Params& p, const Start& st, int first, int rows) {
         o.w = fmaf(oc[j].w, add, o.w);
       }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = inverse(sum);
     *reinterpret_cast<uint2*>(out[row] + c4 * 4) =
         make_uint2(narrow<kF16>(o.x * inv, o.y * inv), narrow<kF16>(o.z * inv, o.w * inv));
   }
@@ -646,7 +654,10 @@ MOE_DEV void join_many(const Params& p, const Start& st, int first, int rows) {
       for (int k = 0; k < 8; ++k)
         oc[k] = __ldcg(reinterpret_cast<const float4*>(part) + (c / 4 + k) * (2 * kTile) + prow);
       const float top = fmaxf(m, mc);
-      if (top == -INFINITY) continue;              // (the part holds zeros)
+      if (top == -INFINITY) {                      // (the part holds zeros, or a sum of NaN)
+        sum += sc;
+        continue;
+      }
       const float keep = exp2_approx(m - top), add = exp2_approx(mc - top);
       m = top;
       sum = fmaf(sc, add, sum * keep);
@@ -659,7 +670,7 @@ MOE_DEV void join_many(const Params& p, const Start& st, int first, int rows) {
       }
     }
     __syncwarp();
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = inverse(sum);
     uint4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1228,13 +1239,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       umma::fence_after_sync();
       if (ok && warp_valid) {
         if (whole_item) {
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          const float inv = inverse(sum);
           f0 *= inv;
           f1 *= inv;
         }
         // a stream that saw no key never wrote its O: what is there is not a
-        // number to be scaled
-        const bool any0 = f0 > 0.f && sum > 0.f, any1 = f1 > 0.f;
+        // number to be scaled. (Factors of NaN are not 0. Where every row is one
+        // stream's there is no other O: its place is past tensor memory's end.)
+        const bool any0 = f0 != 0.f && sum != 0.f, any1 = !own && f1 != 0.f;
         const bool warp_any1 = __any_sync(0xffffffffu, any1);
         const uint32_t from = lanes + 256 + (own ? s * 128 : 0);
         float* slot = p.part + (size_t)(2 * blockIdx.x + (ends ? 0 : 1)) * Z::kSlotFloats;

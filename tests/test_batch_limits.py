@@ -157,3 +157,77 @@ def test_plan_padded_to_the_types_limit(lib):
     for t in (r.slots, r.positions):
         for part in t[7:].split(2 ** 28):
             assert bool((part == -1).all())
+
+
+# ------------------------------------------------- values that are not finite
+def _by_definition(a, kc, vc):
+    """out [T][Hq][D] in 64 bits, every row over the keys that it sees alone."""
+    q, out = a.q.double().cuda(), torch.zeros(a.q.shape, dtype=torch.float64, device="cuda")
+    H = kc.shape[2]
+    per = q.shape[1] // H
+    for b, m in enumerate(a.kv_len):
+        for i in range(a.q_len[b]):
+            t, pos = a.q_start[b] + i, m - a.q_len[b] + i
+            j = torch.arange(max(0, pos + 1), device="cuda")
+            if a.window:
+                j = j[(pos - j < a.window) | (j < a.sinks)]
+            if not j.numel():
+                continue
+            page = a.table[b].long().cuda()[j // a.page]
+            k, v = kc[page, j % a.page].double(), vc[page, j % a.page].double()
+            s = torch.einsum("hpd,jhd->hpj", q[t].view(H, per, -1), k) * a.scale
+            y = (torch.softmax(s, 2)[..., None] * v.permute(1, 0, 2)[:, None]).sum(2)
+            out[t] = y.reshape(-1, y.shape[-1])
+    return out
+
+
+def _check_not_finite(a, got):
+    """Rows that see nothing but numbers as ever; the others by the definition:
+    NaN, or the infinity of one sign."""
+    want = _by_definition(a, a.kc.cuda(), a.vc.cuda())
+    plain = [torch.nan_to_num(p.cuda(), nan=0.0, posinf=0.0, neginf=0.0) for p in (a.kc, a.vc)]
+    q = torch.nan_to_num(a.q.cuda(), nan=0.0, posinf=0.0, neginf=0.0)
+    _, bound = oracle.attend(q, *plain, a.q_start, a.kv_len, a.table.cuda(), a.scale, a.window,
+                             a.sinks)
+    got, fine = got.double(), torch.isfinite(want)
+    assert torch.isfinite(got[fine]).all(), "%d numbers lost" % (~torch.isfinite(got[fine])).sum()
+    assert ((got - want).abs() <= bound)[fine].all()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)])
+
+
+def _place(a, pool, b, j):
+    return pool[int(a.table[b, j // a.page]), j % a.page]
+
+
+NOT_FINITE = {
+    "pass": dict(q_len=[5, 1, 9], kv_len=[77, 40, 300], Hq=16, H=4, D=128, dtype=F16, page=16),
+    "pass at a tile's edge": dict(q_len=[6], kv_len=[131], Hq=8, H=2, D=64, dtype=B16, page=64),
+    "chunk": dict(q_len=[300], kv_len=[420], Hq=8, H=2, D=128, dtype=B16, page=64),
+    "chunk, heads of their own": dict(q_len=[500], kv_len=[520], Hq=2, H=2, D=64, dtype=F16,
+                                      page=32, heads_first=True),
+    "window": dict(q_len=[9, 130], kv_len=[700, 400], Hq=4, H=2, D=128, dtype=B16, page=16,
+                   window=50, sinks=3),
+    "sinks past a tile": dict(q_len=[40], kv_len=[600], Hq=4, H=1, D=64, dtype=F16, page=16,
+                              window=20, sinks=140),
+    "odd groups": dict(q_len=[61, 9], kv_len=[100, 400], Hq=56, H=8, D=128, dtype=F16, page=16,
+                       window=50, sinks=3),
+    "blocks of two": dict(q_len=[700, 9], kv_len=[900, 60], Hq=64, H=8, D=64, dtype=B16, page=64),
+    "short items": dict(q_len=[1 + i % 5 for i in range(80)], kv_len=[9 + 7 * i for i in range(80)],
+                        Hq=8, H=4, D=128, dtype=B16, page=16),
+}
+
+
+@pytest.mark.parametrize("name", NOT_FINITE)
+def test_scores_not_finite(lib, name):
+    """A query of NaN, and a key of NaN, give NaN to the rows they belong to
+    and to those that see them, not zeros."""
+    a = Attend(**NOT_FINITE[name])
+    last = len(a.q_len) - 1
+    _place(a, a.kc, last, a.kv_len[last] - 1)[0, 3] = float("nan")
+    a.k.copy_(a.kc)
+    a.q[0, 1, 2] = float("nan")
+    a.q[a.q_start[-1] // 2, 0] = float("nan")
+    out = a.runner().attend(*a.args())
+    assert lib.moe_last_device_error() == lib.MOE_OK
+    _check_not_finite(a, out)
