@@ -146,8 +146,9 @@ size_t moe_attend_workspace_bytes(const moe_kv_cache* cache, const moe_attn_desc
  *   out       same shape and type, with its own strides (multiples of 8,
  *             16-byte aligned). Rows of no request are not written.
  * Table entries of pages that hold no key any new token of the request sees
- * are not read, and whatever lies in the cache at unseen positions (beyond
- * kv_len, or behind the window) has no effect, NaN and infinities included.
+ * are not read, and what lies in the cache at a position that a token does not
+ * see (beyond kv_len, a later token's, behind the window) has no effect on it,
+ * NaN and infinities included.
  * Scores, softmax statistics and sums are fp32; softmax weights are rounded
  * to the cache's type before the product with v. Deterministic.             */
 moe_status moe_attend(const moe_kv_cache* cache, const moe_attn_desc* attn, const void* q,

@@ -37,8 +37,8 @@
 //   0, 2   TMA: key and value tiles into a ring, a box per page and 64 columns,
 //          every other box each; warp 2 also query tiles into two slots, the
 //          next as soon as one is free
-//   1, 3   MMA issue of stream 0 and of stream 1; they also clear value rows
-//          that no row of the item sees
+//   1, 3   MMA issue of stream 0 and of stream 1; they also take out of the
+//          values what rows that do not see it must not meet
 //   4-7    softmax of stream 0 over the first 64 keys of a tile, one thread per
 //          row, and a share of its results out
 //   8-11   the same over the last 64 keys; the two halves agree on a row's
@@ -178,6 +178,17 @@ MOE_DEV Item make_item(const AttendArgs& a, const Request& r, int block, int fix
   it.ns = min((it.sk + kTile - 1) / kTile, it.lo_tile);
   it.n = max(1, it.ns + (it.hi + kTile - 1) / kTile - it.lo_tile);
   return it;
+}
+
+// Whether some rows of the item see `key` and others do not (for a key that no
+// row sees it may be either), and whether a tile that begins at key0 has such.
+MOE_DEV bool some_see(const AttendArgs& a, const Item& it, int key) {
+  return key > it.pos0 ||
+         (a.window > 0 && key >= a.sinks && key < window_from(it.hi - 1, a.window));
+}
+MOE_DEV bool tile_some_see(const AttendArgs& a, const Item& it, int key0) {
+  return key0 + kTile - 1 > it.pos0 ||
+         (a.window > 0 && key0 + kTile > a.sinks && key0 < window_from(it.hi - 1, a.window));
 }
 
 // An item's units: first `cost`, then one for every key tile of a block of one
@@ -524,6 +535,21 @@ MOE_DEV uint32_t narrow(float lo, float hi) {
 // row sees makes its Σ, and so its result, NaN.
 MOE_DEV float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
 
+// Two values of V, and which are not finite: bit 15 of the lower, 31 of the upper.
+template <bool kF16>
+MOE_DEV uint32_t not_finite(uint32_t w) {
+  return ((w & (kF16 ? 0x7c007c00u : 0x7f807f80u)) + (kF16 ? 0x04000400u : 0x00800080u)) &
+         0x80008000u;
+}
+template <bool kF16>
+MOE_DEV uint32_t only_finite(uint32_t w) {  // zeros in their place
+  return w & ~((not_finite<kF16>(w) >> 15) * 0xffffu);
+}
+template <bool kF16>
+MOE_DEV float widen(uint32_t v16) {
+  return kF16 ? __half2float(__ushort_as_half((unsigned short)v16)) : __uint_as_float(v16 << 16);
+}
+
 // v[i] of lane 4q + j  <->  v[j] of lane 4q + i.
 MOE_DEV uint4 shfl_xor4(uint4 v, int mask) {
   return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask),
@@ -742,6 +768,118 @@ __device__ __noinline__ void clear_rows(const AttendArgs& a) {
   }
 }
 
+// Takes out of a tile of V, by one warp, what must not meet a weight of 0, for
+// 0 · NaN is not 0: the rows that no row of the item sees, whatever they hold,
+// and of those that some see and others do not what is not finite (`bad` is
+// then set). A call of its own: within the MMA warps' loop it slowed down every
+// tile (chunks 735 -> 830 us).
+template <int kDim, bool kF16>
+__device__ __noinline__ void clean_values(const AttendArgs& a, int v_at, int key0, int pos0, int lo,
+                                          int hi, int sk, volatile int* bad) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  constexpr int kHalves = kDim / 64;
+  unsigned char* v = smem + v_at;
+  const int lane = threadIdx.x & 31;
+  auto in_tile = [&](int key) { return min(max(key - key0, 0), kTile); };
+  auto clear = [&](int r0, int r1) {
+#pragma unroll 1
+    for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        *reinterpret_cast<uint4*>(v + h * (kTile * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+  };
+  auto filter = [&](int r0, int r1) {
+#pragma unroll 1
+    for (int i0 = r0 * 8 + lane; i0 < r1 * 8; i0 += 64) {
+      uint4 x[2 * kHalves];
+#pragma unroll
+      for (int k = 0; k < 2 * kHalves; ++k) {
+        const int i = i0 + (k & 1) * 32;
+        x[k] = i < r1 * 8 ? *reinterpret_cast<const uint4*>(v + (k >> 1) * (kTile * 128) + i * 16)
+                          : make_uint4(0, 0, 0, 0);
+      }
+      uint32_t any = 0;
+#pragma unroll
+      for (int k = 0; k < 2 * kHalves; ++k)
+        any |= not_finite<kF16>(x[k].x) | not_finite<kF16>(x[k].y) | not_finite<kF16>(x[k].z) |
+               not_finite<kF16>(x[k].w);
+      if (any) {
+        *bad = 1;
+        __threadfence_block();                       // known before it is gone
+#pragma unroll
+        for (int k = 0; k < 2 * kHalves; ++k) {
+          const int i = i0 + (k & 1) * 32;
+          if (i < r1 * 8)
+            *reinterpret_cast<uint4*>(v + (k >> 1) * (kTile * 128) + i * 16) =
+                make_uint4(only_finite<kF16>(x[k].x), only_finite<kF16>(x[k].y),
+                           only_finite<kF16>(x[k].z), only_finite<kF16>(x[k].w));
+        }
+      }
+    }
+  };
+  clear(in_tile(hi), kTile);
+  filter(in_tile(pos0 + 1), in_tile(hi));
+  if (a.window > 0) {
+    clear(in_tile(sk), in_tile(lo));
+    filter(in_tile(max(lo, a.sinks)), in_tile(min(window_from(hi - 1, a.window), pos0 + 1)));
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Rows whose O lacks the values that are not finite and that not all rows of
+// the item see: the MMA warps took them out of V. Each is added to the rows
+// that see its key (their weight of it is not 0), in this thread's columns
+// [c0, c1). Rare, and slow: it goes through the keys in question once more.
+template <int kDim, bool kF16>
+__device__ __noinline__ void add_not_finite(const Params& p, const Part& pt, int b, int kv_head,
+                                            int first, int step, int hi, int lo, uint32_t o_addr,
+                                            int c0, int c1) {
+  const AttendArgs& a = p.a;
+  const moe_kv_cache& cache = a.cache;
+  const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    uint32_t o[32];
+    umma::ld_x32(o_addr + c, o);
+    umma::wait_ld();
+#pragma unroll 1
+    for (int j = first; j < pt.n; j += step) {
+      const int key0 = pt.tile(j) * kTile;
+      if (!tile_some_see(a, pt.it, key0)) continue;
+      const int end = min(key0 + kTile, pt.it.hi);
+#pragma unroll 1
+      for (int key = key0; key < end; ++key) {
+        if (!some_see(a, pt.it, key) || (key < pt.it.lo && key >= pt.it.sk)) continue;
+        const int page = table[key >> p.page_shift];
+        if (page < 0 || page >= cache.n_pages) continue;
+        const uint4* v = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(cache.v) + page * cache.page_stride +
+            (key & ((1 << p.page_shift) - 1)) * cache.token_stride + kv_head * cache.head_stride +
+            c);
+        const bool seen = key < hi && (key >= lo || key < a.sinks);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = v[i];
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bad = not_finite<kF16>(w[k]);
+            const int at = 8 * i + 2 * k;
+            if (seen && (bad & 0x8000u))
+              o[at] = __float_as_uint(__uint_as_float(o[at]) + widen<kF16>(w[k] & 0xffffu));
+            if (seen && (bad >> 31))
+              o[at + 1] = __float_as_uint(__uint_as_float(o[at + 1]) + widen<kF16>(w[k] >> 16));
+          }
+        }
+      }
+    }
+    umma::st_x32(o_addr + c, o);
+    umma::wait_st();
+  }
+  umma::fence_before_sync();
+}
+
 // Barriers and words behind the ring.
 struct Misc {
   uint64_t full[10], empty[10];
@@ -752,6 +890,7 @@ struct Misc {
   long long part[8];
   uint32_t tmem;
   int lost;
+  int bad;  // values that are not finite were taken out of some V
 };
 static_assert(sizeof(Misc) <= 512, "misc words");
 constexpr int kOffStat = 512;  // then [2 streams][2][128 rows] floats
@@ -785,11 +924,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(&m.q_empty[s], 2);
       mbar_init(&m.s_full[s], 1);
       mbar_init(&m.p_full[s], 8);
-      mbar_init(&m.o_full[s], 1);
+      mbar_init(&m.o_full[s], 2);              // the products, and what is known of their V
       mbar_init(&m.turn[s], 1);
       mbar_init(&m.drain[s], 1);
     }
     m.lost = 0;
+    m.bad = 0;
     m.start.joins = 0;
     fence_mbar_init();
   }
@@ -1026,20 +1166,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (more) pass(&m.empty[kt]);
           continue;
         }
-        // rows of V that no row of the item sees may hold anything: their
-        // weights are 0, and 0 · NaN is not
-        const int key0 = pt.tile(j) * kTile;
         const bool now = has_v && sees(j);
-        if (ok && now && (key0 + kTile > it.hi || (key0 < it.lo && key0 + kTile > it.sk))) {
-          unsigned char* v = smem + Z::kOffRing + vt * Z::kTileBytes;
-          for (int i = lane; i < kTile * kHalves * 8; i += 32) {
-            const int key = key0 + ((i >> 3) & (kTile - 1));
-            if (key >= it.hi || (key < it.lo && key >= it.sk))
-              *reinterpret_cast<uint4*>(v + (size_t)i * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+        if (ok && now && tile_some_see(a, it, pt.tile(j) * kTile))
+          clean_values<kDim, kF16>(a, Z::kOffRing + vt * Z::kTileBytes, pt.tile(j) * kTile, it.pos0,
+                                   it.lo, it.hi, it.sk, &m.bad);
         if (now) wait(&m.p_full[s], p_phase, 0xA41);
         // Two query tiles take turns: a stream's P·V and its next scores are
         // issued in one piece. Were they mixed with the other's, both scores
@@ -1061,7 +1191,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         if (more && sees(j + lead)) scores(slot, kt);  // into S, behind the product that reads P
         if (two && has_v) pass(&m.turn[s ^ 1]);
-        if (j == last && !first) commit(&m.o_full[s]);
+        if (j == last && !first) {
+          commit(&m.o_full[s]);
+          pass(&m.o_full[s]);
+        }
         if (has_v) commit(&m.empty[vt]);
         if (more) commit(&m.empty[kt]);
         if (more && j + lead == last) commit(&m.q_empty[slot]);  // the last scores are issued
@@ -1213,6 +1346,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       if (began) {
         wait(&m.o_full[s], o_phase, 0xA52);
         o_phase ^= 1u;
+        if (ok && __any_sync(0xffffffffu, *static_cast<volatile int*>(&m.bad))) {
+          umma::fence_after_sync();
+          const Part copy = pt;                      // (pt itself stays in registers)
+          add_not_finite<kDim, kF16>(p, copy, walk.b, walk.h + (s & pt.pair), two ? 0 : s,
+                                     two ? 1 : 2, hi, lo, o_addr, half * (kDim / 2),
+                                     (half + 1) * (kDim / 2));
+        }
       }
       // the halves' sums, then (one query tile) both streams' statistics; the
       // other half has read the last maximum: O is complete, its weights are in

@@ -231,3 +231,24 @@ def test_scores_not_finite(lib, name):
     out = a.runner().attend(*a.args())
     assert lib.moe_last_device_error() == lib.MOE_OK
     _check_not_finite(a, out)
+
+
+@pytest.mark.parametrize("name", NOT_FINITE)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_values_not_finite_reach_only_rows_that_see_them(lib, name, value):
+    """A drafted token whose value overflowed; one that a window leaves behind
+    in the middle of a pass."""
+    a = Attend(**NOT_FINITE[name])
+    for b, (n, m) in enumerate(zip(a.q_len, a.kv_len)):
+        if len(a.q_len) > 9 and b % 3:
+            continue
+        _place(a, a.vc, b, m - 1)[0, 5] = value                    # the newest token's
+        _place(a, a.vc, b, m - 1 - n // 2)[-1, a.q.shape[2] - 1] = value
+        if a.window and m - n - a.window + 1 > 0:                  # the first to leave the window
+            _place(a, a.vc, b, m - n - a.window + 1)[0, 7] = value
+        if a.sinks:
+            _place(a, a.vc, b, a.sinks - 1)[-1, 2] = -value        # seen by every row
+    a.v.copy_(a.vc)
+    out = a.runner().attend(*a.args())
+    assert lib.moe_last_device_error() == lib.MOE_OK
+    _check_not_finite(a, out)
