@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from moe_expert_layer_warp_gb300 import api
+from moe_expert_layer_warp_gb300 import api, batch
 from tests.test_batch_abi import ONE, _cache, _why, lib  # noqa: F401
 
 
@@ -17,3 +17,13 @@ def test_padded_attend_refuses_what_attend_refuses(lib, at, value, reason):
     args[at] = value
     assert lib.moe_attend_padded(ctypes.byref(c), ctypes.byref(a), *args, None) == api.MOE_EINVAL
     assert reason in _why() and "moe_attend_padded" in _why()
+
+
+def test_objects_of_another_device_than_the_current_one_are_refused(monkeypatch):
+    monkeypatch.setattr(batch, "_several_devices", True)
+    monkeypatch.setattr(batch, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        batch._handle(None, 1)
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        batch._handle(ctypes.c_void_p(0), 1)
+    assert batch._handle(ctypes.c_void_p(5), 0).value == 5

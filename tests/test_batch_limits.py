@@ -252,3 +252,26 @@ def test_values_not_finite_reach_only_rows_that_see_them(lib, name, value):
     out = a.runner().attend(*a.args())
     assert lib.moe_last_device_error() == lib.MOE_OK
     _check_not_finite(a, out)
+
+
+# ---------------------------------------------------------------- devices ---
+def test_calls_beside_another_current_device_are_refused(lib, monkeypatch):
+    from moe_expert_layer_warp_gb300 import batch
+    a = Attend([3], [20], 4, 2, 64, B16, 16)
+    cache = batch.PagedCache(a.k, a.v)
+    planner, attention = batch.BatchPlanner(16, 1, 4), a.runner()
+    router = batch.GroupedRouter(8, 2, 4)
+    args, new = a.args(), torch.zeros(3, 2, 64, dtype=B16, device="cuda")
+    calls = [lambda: planner.plan(i32([3]), i32([0]), i32([0]), i32([1]), i32([0, 1]), i32([[0]]), 3),
+             lambda: cache.append(new, new, torch.arange(3, device="cuda")),
+             lambda: attention.attend(*args),
+             lambda: router.route(torch.zeros(4, 8, device="cuda"))]
+    current = torch.cuda.current_device()
+    for call in calls:
+        call()
+        with monkeypatch.context() as m:
+            m.setattr(batch, "_several_devices", True)
+            m.setattr(batch, "_current_device", lambda: current + 1)
+            with pytest.raises(ValueError, match="current device"):
+                call()
+    assert lib.moe_last_device_error() == lib.MOE_OK
