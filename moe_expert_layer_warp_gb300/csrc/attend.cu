@@ -122,8 +122,9 @@ struct Params {
   int block;     // tokens per block, tpt or 2·tpt
   float* part;   // [2 per CTA][kSlotFloats]
   // [CTAs]: `call` when the CTA has left the part of its last item. The CTA
-  // that reads it sets it to 0; what an unused workspace holds is not `call`,
-  // a number of 64 mixed bits that no two calls share.
+  // that reads it sets it to 0, for a replayed graph's call has its number
+  // again; what an unused workspace holds is not `call`, a number of 64 mixed
+  // bits that no two calls share.
   unsigned long long* left;
   unsigned long long call;
 };
@@ -717,6 +718,18 @@ MOE_DEV void join_many(const Params& p, const Start& st, int first, int rows) {
   }
 }
 
+// What stands in `left` for a part that is no longer waited for (calls' numbers
+// are odd).
+MOE_DEV unsigned long long given_up(unsigned long long call) { return call ^ 1ull; }
+MOE_DEV unsigned long long exchange(unsigned long long* word, unsigned long long v) {
+  unsigned long long old;
+  asm volatile("atom.exch.acq_rel.gpu.global.b64 %0, [%1], %2;"
+               : "=l"(old)
+               : "l"(word), "l"(v)
+               : "memory");
+  return old;
+}
+
 // All softmax threads of the CTA that has the item's last tile call it. (What
 // the other CTAs' threads left is ordered before their flags' releases by
 // their barrier, and before this CTA's reads by the acquires and this one.)
@@ -739,10 +752,14 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
       if (v == p.call) break;
       if ((i & 63u) == 63u && (*lost || global_ns() - t0 > kWaitLimitNs)) {
         *lost = 0xA70;
+        // a part that comes later is not to be taken for a replayed graph's,
+        // whose call has the same number: its CTA finds this and clears the word
+        if (exchange(word, given_up(p.call)) == p.call) break;
+        word = nullptr;
         break;
       }
     }
-    *word = 0ull;
+    if (word) *word = 0ull;
   }
   asm volatile("bar.sync 2, 512;" ::: "memory");
   const int rows = st.ntok * a.group;
@@ -1444,13 +1461,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         asm volatile("bar.sync 2, 512;" ::: "memory");
       }
     }
+    unsigned long long before = 0;                   // (used at the end: it takes a while)
     if (open) {                                      // the part left behind is complete
       asm volatile("bar.sync 2, 512;" ::: "memory");
-      if (threadIdx.x == 128)
-        asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.left + blockIdx.x), "l"(p.call)
-                     : "memory");
+      if (threadIdx.x == 128) before = exchange(p.left + blockIdx.x, p.call);
     }
     if (m.start.joins) join_parts<kDim, kF16>(p, m.start, lost);
+    if (before == given_up(p.call)) p.left[blockIdx.x] = 0ull;
   }
   umma::fence_before_sync();
   __syncthreads();

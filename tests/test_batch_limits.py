@@ -275,3 +275,58 @@ def test_calls_beside_another_current_device_are_refused(lib, monkeypatch):
             with pytest.raises(ValueError, match="current device"):
                 call()
     assert lib.moe_last_device_error() == lib.MOE_OK
+
+
+# ------------------------------------------------ graphs, streams, threads --
+CUT = {     # items cut among several CTAs, whose parts are joined
+    "one pass": dict(q_len=[5], kv_len=[777], Hq=16, H=16, D=128, dtype=B16, page=64),
+    "passes": dict(q_len=[3, 9, 1, 5], kv_len=[6000, 900, 20, 9000], Hq=8, H=2, D=64, dtype=F16,
+                   page=16),
+    "chunk beside passes": dict(q_len=[300, 4, 260], kv_len=[1500, 5000, 300], Hq=32, H=8, D=128,
+                                dtype=B16, page=32),
+}
+
+
+@pytest.mark.parametrize("name", CUT)
+def test_a_graph_replayed_over_changing_inputs(lib, name):
+    """Every replay has the same call number: parts of the replay before must
+    not pass for its own."""
+    a = Attend(**CUT[name], unseen=0.0)
+    r, (q, qs, kv, table) = a.runner(), a.args()
+    out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    r.attend(q, qs, kv, table, out=out)
+    with torch.cuda.graph(graph):
+        r.attend(q, qs, kv, table, out=out)
+    lengths = list(a.kv_len)
+    g = torch.Generator().manual_seed(1)
+    for i in range(8):
+        a.q = (torch.randn(a.q.shape, generator=g) * (0.5 + i)).to(a.q.dtype)
+        a.kv_len = [max(n, m - 97 * i if i % 2 else m // (i + 1)) for n, m in
+                    zip(a.q_len, lengths)]
+        a.vc = torch.randn(a.vc.shape, generator=g).to(a.vc.dtype)
+        q.copy_(a.q), kv.copy_(i32(a.kv_len)), a.v.copy_(a.vc), out.fill_(float("nan"))
+        graph.replay()
+        assert lib.moe_last_device_error() == lib.MOE_OK
+        a.check(out)
+        again = out.clone()
+        graph.replay()
+        graph.replay()
+        assert torch.equal(again, out)
+    assert lib.moe_last_device_error() == lib.MOE_OK
+
+
+def test_two_objects_on_two_streams(lib):
+    """Calls that overlap, each with its object's workspace."""
+    problems = [Attend(**CUT["passes"]), Attend(**CUT["chunk beside passes"], seed=3)]
+    runners, args = [a.runner() for a in problems], [a.args() for a in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    outs = [torch.empty_like(a[0]) for a in args]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for r, x, out, s in zip(runners, args, outs, streams):
+            r.attend(*x, out=out, stream=s)
+    torch.cuda.synchronize()
+    assert lib.moe_last_device_error() == lib.MOE_OK
+    for a, out in zip(problems, outs):
+        a.check(out)
