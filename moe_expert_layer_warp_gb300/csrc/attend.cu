@@ -1532,23 +1532,32 @@ cudaError_t launch_attend(const AttendArgs& a, int num_sms, cudaStream_t stream)
   const uint32_t steps[4] = {1, 1, 1, 1};
   const EncodeFn encode = encode_fn();
   if (!encode) return cudaErrorNotSupported;
-  for (int i = 0; i < 2; ++i)
-    if (encode(i ? &p.vmap : &p.kmap, type, 4, i ? c.v : c.k, dims, strides, box, steps,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
   // queries as [token][head][dim]: a box is the rows of a query tile
   const cuuint64_t q_dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)a.n_heads,
                                 (cuuint64_t)a.n_tokens};
   const cuuint64_t q_strides[2] = {(cuuint64_t)a.q_head_stride * 2,
                                    (cuuint64_t)a.q_token_stride * 2};
   const uint32_t q_box[3] = {64, (uint32_t)a.group, (uint32_t)p.tpt};
-  if (encode(&p.qmap, type, 3, const_cast<void*>(a.q), q_dims, q_strides, q_box, steps,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  auto encode_maps = [&] {
+    auto map = [&](CUtensorMap* to, int rank, const void* at, const cuuint64_t* size,
+                   const cuuint64_t* stride, const uint32_t* piece) {
+      return encode(to, type, rank, const_cast<void*>(at), size, stride, piece, steps,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(&p.kmap, 4, c.k, dims, strides, box) && map(&p.vmap, 4, c.v, dims, strides, box) &&
+           map(&p.qmap, 3, a.q, q_dims, q_strides, q_box);
+  };
+  if (!encode_maps()) {
+    // a host thread that has called nothing but this library has no context yet,
+    // and encoding, a driver's call, makes none
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (!encode_maps()) return cudaErrorInvalidValue;
+  }
   const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
   // Blocks of two query tiles halve what is read; but with fewer of them than
   // CTAs most are cut, and their parts' joins take longer than the reads: a

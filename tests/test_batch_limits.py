@@ -330,3 +330,56 @@ def test_two_objects_on_two_streams(lib):
     assert lib.moe_last_device_error() == lib.MOE_OK
     for a, out in zip(problems, outs):
         a.check(out)
+
+
+def test_two_host_threads(lib):
+    """First calls of each kernel from two threads at once, an object each."""
+    import threading
+    problems = [Attend(**dict(CUT["passes"], D=D, dtype=dtype), seed=i)
+                for i, (D, dtype) in enumerate([(64, B16), (128, F16), (64, B16), (128, F16)])]
+    runners, args = [a.runner() for a in problems], [a.args() for a in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    outs, faults = [torch.empty_like(a[0]) for a in args], []
+    start = threading.Barrier(len(problems))
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            start.wait(30)
+            for _ in range(100):
+                runners[i].attend(*args[i], out=outs[i], stream=streams[i])
+        except Exception as e:                                # reported below
+            faults.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(problems))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    assert not faults
+    assert lib.moe_last_device_error() == lib.MOE_OK
+    for a, out in zip(problems, outs):
+        a.check(out)
+
+
+def test_first_call_of_a_host_thread(lib):
+    """A thread that has made no CUDA call before."""
+    import threading
+    a = Attend(**CUT["passes"])
+    r, args = a.runner(), a.args()
+    out, faults, stream = torch.empty_like(args[0]), [], torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            r.attend(*args, out=out, stream=stream)
+        except Exception as e:                                # reported below
+            faults.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join(60)
+    stream.synchronize()
+    assert not faults
+    a.check(out)
