@@ -1479,12 +1479,15 @@ template <int kDim, bool kF16>
 cudaError_t launch_t(Params& p, int ctas, cudaStream_t stream) {
   using Z = Sizes<kDim>;
   auto* kernel = attend_kernel<kDim, kF16>;
-  static int configured_device = -1;
+  // a bit for each device whose kernel may have that much shared memory (two
+  // threads that find it missing both ask for it, to the same effect)
+  static std::atomic<unsigned long long> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && configured_device != dev) {
+  const unsigned long long bit = 1ull << (dev & 63);     // call_device takes devices below 64
+  if (e == cudaSuccess && !(configured.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kSmem);
-    if (e == cudaSuccess) configured_device = dev;
+    if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_release);
   }
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(ctas), dim3(kThreads), Z::kSmem, stream, p);
