@@ -71,10 +71,16 @@ moe_status attend(const moe_kv_cache* cache, const moe_attn_desc* attn, const vo
   if (q_token_stride < 1 || q_head_stride < 1 || q_token_stride % 8 != 0 ||
       q_head_stride % 8 != 0 || q_token_stride >= kMaxStride || q_head_stride >= kMaxStride)
     return bad("q strides must be positive multiples of 8 elements");
-  // rows of out must not overlap: either order of tokens and heads
+  // rows of out must not overlap: a token's heads before the next token, or a
+  // head's tokens before the next head, whatever lies between
   const int64_t D = cache->head_dim, H = attn->n_heads;
-  const bool heads_in = out_head_stride >= D && (n_tokens < 2 || out_token_stride >= H * out_head_stride);
-  const bool tokens_in = out_token_stride >= D && (H < 2 || out_head_stride >= n_tokens * out_token_stride);
+  auto holds = [D](int64_t outer, int64_t inner, int64_t n) {  // n rows `inner` apart
+    return outer >= D && (outer - D) / inner >= n - 1;
+  };
+  const bool heads_in = out_head_stride >= D &&
+                        (n_tokens < 2 || holds(out_token_stride, out_head_stride, H));
+  const bool tokens_in = out_token_stride >= D &&
+                         (H < 2 || holds(out_head_stride, out_token_stride, n_tokens));
   if (out_token_stride % 8 != 0 || out_head_stride % 8 != 0 || !(heads_in || tokens_in))
     return bad("out strides must be multiples of 8 elements and rows must not overlap");
   if (n_tokens == 0) return MOE_OK;

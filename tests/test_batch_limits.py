@@ -383,3 +383,18 @@ def test_first_call_of_a_host_thread(lib):
     stream.synchronize()
     assert not faults
     a.check(out)
+
+
+# ---------------------------------------------------------------- strides ---
+def test_results_with_gaps_between_heads_and_tokens(lib):
+    """Every other one of an odd number of heads, or of tokens."""
+    a = Attend(**CUT["chunk beside passes"])
+    q, qs, kv, table = a.args()
+    T, H, D = q.shape
+    for shape, order in (((T, 2 * H - 1, D), lambda t: t[:, ::2]),
+                         ((H, 2 * T - 1, D), lambda t: t[:, ::2].transpose(0, 1))):
+        whole = torch.full(shape, 7.0, dtype=q.dtype, device="cuda")
+        a.runner().attend(q, qs, kv, table, out=order(whole))
+        assert lib.moe_last_device_error() == lib.MOE_OK
+        a.check(order(whole))
+        assert (whole[:, 1::2] == 7.0).all()
