@@ -97,21 +97,26 @@ def main(argv=None):
     p.add_argument("--requests", type=int, default=12)
     p.add_argument("--steps", type=int, default=20)
     a = p.parse_args(argv)
+    # an expert pass takes 128 tokens at most: every request brings one at least
+    if not 1 <= a.requests <= 128 or a.steps < 1:
+        p.error("1 to 128 requests and one step at least")
     rng = random.Random(1)
-    draft = max(1, min(5, 128 // a.requests))
-    block = Block(a.requests, max_tokens=min(128, a.requests * 10), max_blocks=24)
-    total = 0
+    prompt, draft = min(10, 128 // a.requests), min(5, 128 // a.requests)
+    # pages for the longest request: every draft kept
+    block = Block(a.requests, max_tokens=min(128, a.requests * 10),
+                  max_blocks=(prompt + a.steps * draft - 1) // PAGE + 1)
+    total, timed_from = 0, min(2, a.steps - 1)            # the first steps warm up
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for step in range(a.steps):
-        longest = min(10, 128 // a.requests) if step == 0 else draft
+        longest = prompt if step == 0 else draft
         q = [rng.randint(1, longest) for _ in range(a.requests)]
         x = torch.randn((sum(q), SHAPE.d), device="cuda")
-        if step == 2:
+        if step == timed_from:
             start.record()
         y, _ = block.step(x, torch.tensor(q, dtype=torch.int32, device="cuda"))
         kept = [n if step == 0 else rng.randint(1, n) for n in q]
         block.accept(torch.tensor(kept, dtype=torch.int32, device="cuda"))
-        total += sum(kept) if step >= 2 else 0
+        total += sum(kept) if step >= timed_from else 0
     end.record()
     status = api.moe_last_device_error()
     if status != api.MOE_OK:

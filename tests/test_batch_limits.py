@@ -398,3 +398,28 @@ def test_results_with_gaps_between_heads_and_tokens(lib):
         assert lib.moe_last_device_error() == lib.MOE_OK
         a.check(order(whole))
         assert (whole[:, 1::2] == 7.0).all()
+
+
+# ---------------------------------------------------------------- example ---
+@pytest.mark.parametrize("requests,steps", [(2, 1), (3, 2), (128, 4), (2, 200)])
+def test_example_runs_at_any_size(lib, capsys, monkeypatch, requests, steps):
+    """Fewer steps than it warms up with, as many requests as a pass holds, and
+    caches longer than a few pages: no request is refused."""
+    from examples import verify_step as ex
+    step = ex.Block.step
+
+    def checked(self, x, q_len):
+        out = step(self, x, q_len)
+        assert (out[1]["plan"].kv_len == self.cached + q_len).all()
+        return out
+
+    monkeypatch.setattr(ex.Block, "step", checked)
+    ex.main(["--requests", str(requests), "--steps", str(steps)])
+    assert "%d requests, %d steps" % (requests, steps) in capsys.readouterr().out
+
+
+def test_example_refuses_what_a_pass_cannot_hold(lib):
+    from examples import verify_step as ex
+    for args in (["--requests", "129"], ["--requests", "0"], ["--steps", "0"]):
+        with pytest.raises(SystemExit):
+            ex.main(args)
