@@ -315,16 +315,40 @@ def make_cache(k: torch.Tensor, v: torch.Tensor) -> KvCacheC:
                     DTYPES[k.dtype], _stride(k, 0), _stride(k, 1), _stride(k, 2))
 
 
+def _shaped(name, t, dtype, shape):
+    """ValueError unless `t` is of that type and shape (None: any size)."""
+    if t.dtype is not dtype or t.dim() != len(shape) or any(
+            want is not None and want != got for want, got in zip(shape, t.shape)):
+        raise ValueError("%s must be a %s tensor of shape %s, got %s %s"
+                         % (name, str(dtype)[6:], ["?" if v is None else v for v in shape],
+                            str(t.dtype)[6:], list(t.shape)))
+
+
+def _holding(name, t, dtype, n):
+    """ValueError unless `t` is of that type with n elements at least."""
+    if t.dtype is not dtype or t.numel() < n:
+        raise ValueError("%s must be a %s tensor of %d elements or more, got %s %s"
+                         % (name, str(dtype)[6:], n, str(t.dtype)[6:], list(t.shape)))
+
+
 def moe_plan_batch(batch: BatchC, n_tokens, slots, positions, stream=None):
+    _holding("slots", slots, torch.int64, n_tokens)
+    _holding("positions", positions, torch.int32, n_tokens)
     _check(load().moe_plan_batch(ctypes.byref(batch), n_tokens, _ptr(slots), _ptr(positions),
                                  _stream(stream)), "moe_plan_batch")
 
 
 def moe_kv_append(cache: KvCacheC, k, v, slots, stream=None):
     """k, v: [n_tokens][n_kv_heads][head_dim], last dimension contiguous."""
-    if k.shape != v.shape or k.dtype != v.dtype or k.stride(2) != 1 or v.stride(2) != 1 or any(
+    row = (cache.n_kv_heads, cache.head_dim)
+    _shaped("k", k, k.dtype, (None, *row))
+    _shaped("v", v, k.dtype, k.shape)
+    _holding("slots", slots, torch.int64, k.shape[0])
+    if k.stride(2) != 1 or v.stride(2) != 1 or any(
             _stride(k, i) != _stride(v, i) for i in range(2)):
-        raise ValueError("k and v must share type, shape and strides, their rows contiguous")
+        raise ValueError("k and v must share their strides, their rows contiguous")
+    if k.dtype not in DTYPES:
+        raise ValueError("k and v must be float32, bfloat16 or float16")
     _check(load().moe_kv_append(ctypes.byref(cache), _raw(k), _raw(v), DTYPES[k.dtype],
                                 _stride(k, 0), _stride(k, 1), k.shape[0], _ptr(slots),
                                 _stream(stream)), "moe_kv_append")
@@ -335,22 +359,37 @@ def moe_attend_workspace_bytes(cache: KvCacheC, attn: AttnDesc) -> int:
 
 
 def moe_attend(cache: KvCacheC, attn: AttnDesc, q, q_start, kv_len, block_table, workspace, out,
-               stream=None):
-    """q, out: [n_tokens][n_heads][head_dim], last dimension contiguous."""
-    if q.stride(2) != 1 or out.stride(2) != 1 or q.shape != out.shape:
-        raise ValueError("q and out must have one shape and contiguous rows")
-    _check(load().moe_attend(ctypes.byref(cache), ctypes.byref(attn), _raw(q), _stride(q, 0),
-                             _stride(q, 1), q.shape[0], _ptr(q_start), _ptr(kv_len),
-                             _ptr(block_table), block_table.shape[1], kv_len.shape[0],
-                             _ptr(workspace), workspace.numel() * workspace.element_size(),
-                             _raw(out), _stride(out, 0), _stride(out, 1), _stream(stream)),
-           "moe_attend")
+               stream=None, padded: bool = False):
+    """q, out: [n_tokens][n_heads][head_dim], last dimension contiguous; padded:
+    moe_attend_padded."""
+    if DTYPES.get(q.dtype) != cache.dtype:
+        raise ValueError("q must be of the cache's type, got %s" % str(q.dtype)[6:])
+    _shaped("q", q, q.dtype, (None, attn.n_heads, cache.head_dim))
+    _shaped("out", out, q.dtype, q.shape)
+    _shaped("kv_len", kv_len, torch.int32, (None,))
+    n = kv_len.shape[0]
+    _holding("q_start", q_start, torch.int32, n + 1)
+    _shaped("block_table", block_table, torch.int32, (None, None))
+    _holding("block_table", block_table, torch.int32, n * block_table.shape[1])
+    if q.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("the rows of q and out must be contiguous")
+    call = load().moe_attend_padded if padded else load().moe_attend
+    _check(call(ctypes.byref(cache), ctypes.byref(attn), _raw(q), _stride(q, 0), _stride(q, 1),
+                q.shape[0], _ptr(q_start), _ptr(kv_len), _ptr(block_table), block_table.shape[1],
+                n, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                _raw(out), _stride(out, 0), _stride(out, 1), _stream(stream)),
+           "moe_attend_padded" if padded else "moe_attend")
 
 
 def moe_route_grouped(router: RouterDesc, logits, bias, topk_idx, topk_w, stream=None):
     """logits: [n][E] float32, bfloat16 or float16, last dimension contiguous."""
-    if logits.stride(1) != 1:
-        raise ValueError("the rows of logits must be contiguous")
+    _shaped("logits", logits, logits.dtype, (None, router.n_experts))
+    if logits.dtype not in DTYPES or logits.stride(1) != 1:
+        raise ValueError("logits must be float32, bfloat16 or float16 with contiguous rows")
+    _holding("topk_idx", topk_idx, torch.int32, logits.shape[0] * router.top_k)
+    _holding("topk_w", topk_w, torch.float32, logits.shape[0] * router.top_k)
+    if bias is not None:
+        _holding("bias", bias, torch.float32, router.n_experts)
     _check(load().moe_route_grouped(ctypes.byref(router), _raw(logits), DTYPES[logits.dtype],
                                     _stride(logits, 0), _ptr(bias),
                                     logits.shape[0], _ptr(topk_idx), _ptr(topk_w),

@@ -3,6 +3,7 @@ objects beyond their refusals: nothing is launched (no GPU is touched)."""
 import ctypes
 
 import pytest
+import torch
 
 from moe_expert_layer_warp_gb300 import api, batch
 from tests.test_batch_abi import ONE, _cache, _why, lib  # noqa: F401
@@ -43,3 +44,41 @@ def test_attend_out_strides(lib, token, head, ok):
     assert lib.moe_attend(ctypes.byref(c), ctypes.byref(a), None, 512, 64, 4, ONE, ONE, ONE, 4, 2,
                           ONE, 1 << 30, ONE, token, head, None) == api.MOE_EINVAL
     assert ("q or out null" if ok else "out strides") in _why()
+
+
+def test_binding_refuses_tensors_of_another_kind(lib):
+    """What the calls cannot see: types and shapes behind the pointers. (None of
+    these tensors is on a GPU; each refusal comes before that is asked.)"""
+    B16, I32 = torch.bfloat16, torch.int32
+    c, a = _cache(), api.AttnDesc(8, 0, 0, 0.125)
+    q, ws = torch.zeros(4, 8, 64, dtype=B16), torch.zeros(16, dtype=torch.uint8)
+    start, length, table = (torch.zeros(n, dtype=I32) for n in (3, 2, 8))
+    table = table.view(2, 4)
+    good = dict(q=q, q_start=start, kv_len=length, block_table=table, workspace=ws, out=q)
+    for over, reason in [
+            (dict(q=q.half(), out=q.half()), "cache's type"), (dict(q=q[:, :7], out=q[:, :7]), "q"),
+            (dict(out=q[:3]), "out"), (dict(out=q.float()), "out"),
+            (dict(q_start=start[:2]), "q_start"), (dict(kv_len=length.long()), "kv_len"),
+            (dict(block_table=table[0]), "block_table"),
+            (dict(q=q.transpose(0, 2).contiguous().transpose(0, 2)), "contiguous")]:
+        for padded in (False, True):
+            with pytest.raises(ValueError, match=reason):
+                api.moe_attend(c, a, **dict(good, **over), padded=padded)
+    k, slots = torch.zeros(4, 2, 64, dtype=B16), torch.zeros(4, dtype=torch.int64)
+    for args, reason in [((k[:, :1], k[:, :1], slots), "k must"), ((k, k.float(), slots), "v must"),
+                         ((k, k, slots[:3]), "slots"), ((k, k, slots.int()), "slots"),
+                         ((k.double(), k.double(), slots), "float32"),
+                         ((k, k.transpose(0, 1).contiguous().transpose(0, 1), slots), "strides")]:
+        with pytest.raises(ValueError, match=reason):
+            api.moe_kv_append(c, *args)
+    r = api.RouterDesc(8, 2, 1, 1, 1, 0, 1, 1.0)
+    x, idx, w = torch.zeros(3, 8), torch.zeros(3, 2, dtype=I32), torch.zeros(3, 2)
+    for args, reason in [((x[:, :7], None, idx, w), "logits"), ((x.double(), None, idx, w), "logits"),
+                         ((x, x[0].half(), idx, w), "bias"), ((x, None, idx.long(), w), "topk_idx"),
+                         ((x, None, idx, w[:2]), "topk_w")]:
+        with pytest.raises(ValueError, match=reason):
+            api.moe_route_grouped(r, *args)
+    with pytest.raises(ValueError, match="slots"):
+        api.moe_plan_batch(api.BatchC(), 4, slots.int(), slots.int())
+    with pytest.raises(ValueError, match="positions"):
+        api.moe_plan_batch(api.BatchC(), 4, slots, slots)

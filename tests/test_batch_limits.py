@@ -423,3 +423,34 @@ def test_example_refuses_what_a_pass_cannot_hold(lib):
     for args in (["--requests", "129"], ["--requests", "0"], ["--steps", "0"]):
         with pytest.raises(SystemExit):
             ex.main(args)
+
+
+# ---------------------------------------------------------------- binding ---
+def test_binding_calls_agree_with_the_objects(lib):
+    from moe_expert_layer_warp_gb300 import batch
+    a = Attend(**CUT["passes"])
+    q, qs, kv, table = a.args()
+    want = a.runner().attend(q, qs, kv, table)
+    cache, attn = lib.make_cache(a.k, a.v), lib.AttnDesc(8, 0, 0, a.scale)
+    ws = torch.empty(lib.moe_attend_workspace_bytes(cache, attn), dtype=torch.uint8, device="cuda")
+    for padded in (False, True):
+        out = torch.full_like(q, 7.0)
+        lib.moe_attend(cache, attn, q, qs, kv, table, ws, out, padded=padded)
+        assert torch.equal(out, want)
+    x = torch.randn(9, 64, device="cuda")
+    idx, w = torch.empty(9, 6, dtype=torch.int32, device="cuda"), torch.empty(9, 6, device="cuda")
+    lib.moe_route_grouped(lib.RouterDesc(64, 6, 1, 1, 1, 0, 1, 1.0), x, None, idx, w)
+    want_idx, want_w = batch.GroupedRouter(64, 6, 9).route(x)
+    assert torch.equal(idx, want_idx) and torch.equal(w, want_w)
+    # plan and append, one request of 20 tokens into 2 pages
+    q_len, cached, held, free, ends = i32([20]), i32([0]), i32([0]), i32([4, 1, 2]), i32([0, 3])
+    outs = [i32([-1, -1]), i32([0]), i32([0]), i32([0]), i32([[-1, -1]])]
+    slots = torch.empty(20, dtype=torch.int64, device="cuda")
+    pos = torch.empty(20, dtype=torch.int32, device="cuda")
+    p = [t.data_ptr() for t in (q_len, cached, held, free, ends, outs[4], *outs[:4])]
+    lib.moe_plan_batch(lib.BatchC(1, 2, 16, 3, *p), 20, slots, pos)
+    assert slots.tolist() == list(range(64, 80)) + list(range(16, 20))
+    k = torch.randn(20, 2, 64, device="cuda").half()
+    lib.moe_kv_append(cache, k, -k, slots)
+    assert torch.equal(a.k[4, :16], k[:16]) and torch.equal(a.v[1, :4], -k[16:])
+    assert lib.moe_last_device_error() == lib.MOE_OK
