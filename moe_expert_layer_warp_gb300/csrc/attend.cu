@@ -76,6 +76,7 @@
 #include "attend_mma.cuh"
 #include "batch_launch.h"
 #include "common.cuh"
+#include "round16.cuh"
 #include "tmap.h"
 
 namespace moe {
@@ -522,16 +523,6 @@ MOE_DEV uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <bool kF16>
-MOE_DEV uint32_t narrow(float lo, float hi) {
-  if constexpr (kF16) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    return pack_bf16x2(lo, hi);
-  }
-}
-
 // 1 / Σ of a row's weights; 0 for a row that sees no key. NaN among the scores a
 // row sees makes its Σ, and so its result, NaN.
 MOE_DEV float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
@@ -650,7 +641,7 @@ MOE_DEV void join_few(const Params& p, const Start& st, int first, int rows) {
     }
     const float inv = inverse(sum);
     *reinterpret_cast<uint2*>(out[row] + c4 * 4) =
-        make_uint2(narrow<kF16>(o.x * inv, o.y * inv), narrow<kF16>(o.z * inv, o.w * inv));
+        make_uint2(round16<kF16>(o.x * inv, o.y * inv), round16<kF16>(o.z * inv, o.w * inv));
   }
 }
 
@@ -701,10 +692,10 @@ MOE_DEV void join_many(const Params& p, const Start& st, int first, int rows) {
     uint4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[k].x = narrow<kF16>(o[8 * k] * inv, o[8 * k + 1] * inv);
-      v[k].y = narrow<kF16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
-      v[k].z = narrow<kF16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
-      v[k].w = narrow<kF16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
+      v[k].x = round16<kF16>(o[8 * k] * inv, o[8 * k + 1] * inv);
+      v[k].y = round16<kF16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv);
+      v[k].z = round16<kF16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv);
+      v[k].w = round16<kF16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv);
     }
     quad_transpose(v, lane);
     const uint64_t dst = reinterpret_cast<uint64_t>(out[row] + c);
@@ -735,7 +726,6 @@ MOE_DEV unsigned long long exchange(unsigned long long* word, unsigned long long
 // their barrier, and before this CTA's reads by the acquires and this one.)
 template <int kDim, bool kF16>
 MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
-  using Z = Sizes<kDim>;
   const AttendArgs& a = p.a;
   // the CTA with the item's first tile
   const long long head = st.more * (st.each + 1);
@@ -1335,7 +1325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             p0 = exp2_approx(p0);
             p1 = exp2_approx(p1);
             sums[(c >> 1) & 3] = add2(sums[(c >> 1) & 3], pair_f(p0, p1));
-            x[c >> 1] = narrow<kF16>(p0, p1);
+            x[c >> 1] = round16<kF16>(p0, p1);
           }
           umma::st_x32(p_addr, x);
           float s0, s1;
@@ -1351,15 +1341,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // ---- results out
       const bool ends = pt.t1 == it.n, whole_item = ends && pt.t0 == 0;
       open = !ends;
-        // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
-        const uint64_t dst = reinterpret_cast<uint64_t>(
-            static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
-            (int64_t)((walk.h + (s & pt.pair)) * a.group + g_in) * a.out_head_stride);
-        const uint32_t quad_valid = __ballot_sync(0xffffffffu, valid) >> (lane & ~3) & 15u;
-        uint16_t* quad_dst[4];
+      // the results of rows 4·(lane / 4) + i, for i = 0..3, and which of them exist
+      const uint64_t dst = reinterpret_cast<uint64_t>(
+          static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
+          (int64_t)((walk.h + (s & pt.pair)) * a.group + g_in) * a.out_head_stride);
+      const uint32_t quad_valid = __ballot_sync(0xffffffffu, valid) >> (lane & ~3) & 15u;
+      uint16_t* quad_dst[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          quad_dst[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, dst, (lane & ~3) + i));
+      for (int i = 0; i < 4; ++i)
+        quad_dst[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, dst, (lane & ~3) + i));
       if (began) {
         wait(&m.o_full[s], o_phase, 0xA52);
         o_phase ^= 1u;
@@ -1428,10 +1418,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             uint4 v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              v[i].x = narrow<kF16>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]));
-              v[i].y = narrow<kF16>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
-              v[i].z = narrow<kF16>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
-              v[i].w = narrow<kF16>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
+              v[i].x = round16<kF16>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1]));
+              v[i].y = round16<kF16>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3]));
+              v[i].z = round16<kF16>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5]));
+              v[i].w = round16<kF16>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7]));
             }
             // four lanes turn their 4 rows × 4 pieces, so that a store covers
             // 64 bytes of 8 rows instead of 16 bytes of 32
