@@ -454,3 +454,26 @@ def test_binding_calls_agree_with_the_objects(lib):
     lib.moe_kv_append(cache, k, -k, slots)
     assert torch.equal(a.k[4, :16], k[:16]) and torch.equal(a.v[1, :4], -k[16:])
     assert lib.moe_last_device_error() == lib.MOE_OK
+
+
+@pytest.mark.parametrize("name", NOT_FINITE)
+def test_values_not_finite_change_no_other_bit(lib, name):
+    """What is finite is the same, bit for bit, whatever stands where it is not
+    seen; and a call after one with such values is as ever."""
+    a = Attend(**NOT_FINITE[name])
+    r, args = a.runner(), a.args()
+    clean = r.attend(*args).clone()
+    for b, (n, m) in enumerate(zip(a.q_len, a.kv_len)):
+        _place(a, a.vc, b, m - 1)[0, 5] = float("inf")
+        _place(a, a.vc, b, m - 1 - n // 2)[-1, 11] = float("nan")
+    a.v.copy_(a.vc)
+    spoilt = r.attend(*args).clone()
+    again = r.attend(*args).clone()
+    assert torch.equal(spoilt.view(torch.int16), again.view(torch.int16))
+    fine = torch.isfinite(_by_definition(a, a.kc.cuda(), a.vc.cuda()))
+    assert not fine.all()
+    assert torch.equal(spoilt[fine], clean[fine])
+    a.v.copy_(torch.nan_to_num(a.vc, nan=0.0, posinf=0.0))
+    a.vc.copy_(a.v.cpu())
+    a.check(r.attend(*args))
+    assert lib.moe_last_device_error() == lib.MOE_OK
