@@ -711,6 +711,10 @@ MOE_DEV void join_many(const Params& p, const Start& st, int first, int rows) {
   }
 }
 
+// A part is waited for this long: ranges take equal times, but one that is gone
+// through again (see Misc::bad) five times as long as the others, and a prompt
+// of 128 k tokens takes 0.1 s.
+constexpr unsigned long long kJoinLimitNs = 2000ull * 1000ull * 1000ull;
 // What stands in `left` for a part that is no longer waited for (calls' numbers
 // are odd).
 MOE_DEV unsigned long long given_up(unsigned long long call) { return call ^ 1ull; }
@@ -742,7 +746,7 @@ MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
       unsigned long long v;
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
       if (v == p.call) break;
-      if ((i & 63u) == 63u && (*lost || global_ns() - t0 > kWaitLimitNs)) {
+      if ((i & 63u) == 63u && (*lost || global_ns() - t0 > kJoinLimitNs)) {
         *lost = 0xA70;
         // a part that comes later is not to be taken for a replayed graph's,
         // whose call has the same number: its CTA finds this and clears the word
