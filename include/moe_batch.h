@@ -8,12 +8,16 @@
  *                      (moe_attend_padded: and zeros for rows of no request)
  *   moe_route_grouped  experts from router logits: softmax or sigmoid scores,
  *                      balance bias, groups, top-k, renormalised weights
- * and then moe_build_union, an expert engine and moe_combine of moe_warp.h.
+ * and then moe_build_union, an expert engine and moe_combine of moe_warp.h. One
+ * expert pass takes MOE_MAX_TOKENS tokens and MOE_MAX_PAIRS (token, expert)
+ * pairs at most (128 and 512: 64 tokens at top 8), far fewer than one call
+ * here may hold. A larger step goes through the experts in several passes over
+ * slices of moe_route_grouped's rows, which the caller cuts.
  *
  * A verification pass of a request is its n = γ+1 newest tokens; a prompt
- * that enters in chunks is a longer pass of the same kind. The new tokens of
- * all requests are packed one request after the other: request b owns rows
- * q_start[b] .. q_start[b+1]-1 of every [n_tokens] array.
+ * that enters in chunks is, for these calls, a longer pass of the same kind.
+ * The new tokens of all requests are packed one request after the other:
+ * request b owns rows q_start[b] .. q_start[b+1]-1 of every [n_tokens] array.
  *
  * Conventions
  *   - The descriptors are host structs, read during the call only; every
@@ -150,7 +154,10 @@ size_t moe_attend_workspace_bytes(const moe_kv_cache* cache, const moe_attn_desc
  * see (beyond kv_len, a later token's, behind the window) has no effect on it,
  * NaN and infinities included.
  * Scores, softmax statistics and sums are fp32; softmax weights are rounded
- * to the cache's type before the product with v. Deterministic.             */
+ * to the cache's type before the product with v. Deterministic for the batch:
+ * the same inputs give the same bits. Keys are cut among the SMs by all
+ * requests' lengths, so a request's last bits may change with its neighbours'.
+ */
 moe_status moe_attend(const moe_kv_cache* cache, const moe_attn_desc* attn, const void* q,
                       int64_t q_token_stride, int64_t q_head_stride, int32_t n_tokens,
                       const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,

@@ -37,8 +37,8 @@
 //   0, 2   TMA: key and value tiles into a ring, a box per page and 64 columns,
 //          every other box each; warp 2 also query tiles into two slots, the
 //          next as soon as one is free
-//   1, 3   MMA issue of stream 0 and of stream 1; they also take out of the
-//          values what rows that do not see it must not meet
+//   1, 3   MMA issue of stream 0 and of stream 1; they also clear value rows
+//          that no row of the item sees
 //   4-7    softmax of stream 0 over the first 64 keys of a tile, one thread per
 //          row, and a share of its results out
 //   8-11   the same over the last 64 keys; the two halves agree on a row's
@@ -52,20 +52,21 @@
 //   (plan 2 us, first loads 3), turns between items, during which the ring
 //   holds only 2.5 tiles, and the joins (2 us). Windows of 4096 keys of 56
 //   heads: 144 us for 804 MB; tiles at the windows' ends cost 7 % more bytes.
-//   Long prompt chunks (957 GFLOP): 670 us cold and 730 us under the power
-//   cap, 1.43 and 1.31 PFLOP/s. A stream's chain of softmax (1450 cycles a
+//   Long prompt chunks (957 GFLOP): 670 us cold and 720 us under the power
+//   cap, 1.43 and 1.33 PFLOP/s. A stream's chain of softmax (1450 cycles a
 //   tile) and products (1024, and 475 of hand-overs) runs beside the other
 //   stream's: the tensor cores work 70 % of a period. Tensor memory is full, so
 //   a stream's next scores cannot be computed beside its weights.
 //   A mixed batch (3 prompt chunks, 20 passes, 56 heads of 64 columns, pages of
-//   16, 69 MB): 33.4 us, of which 25 are the longest range's item turns and
+//   16, 69 MB): 33 us, of which 25 are the longest range's item turns and
 //   small boxes, the others the start and one join.
 //   A prompt of 512 tokens: 18 us; 200 passes within windows of 512 keys: 122 us,
 //   for an item's turn (products, results out, the next item's place: 3 us)
 //   stands against 5 tiles' loads, or a pair's against 10. Without pairs this took
-//   125 us, and 40 passes of 16 heads over 8 to 71 keys 21.1 for 18.9.
-//   One pass of 5 tokens over 777 keys: 12.5 us, one chain of plan (2), loads and
-//   products (5), a part's hand-over (2), join (1.2) and the launch.
+//   125 us, and 40 passes of 16 heads over 8 to 71 keys 21.1 for 19.
+//   One pass of 5 tokens over 777 keys: 12 to 13 us by the card, one chain of
+//   plan (2), loads and products (5), a part's hand-over (2), join (1.2) and the
+//   launch.
 #include <limits.h>
 #include <math.h>
 #include <string.h>

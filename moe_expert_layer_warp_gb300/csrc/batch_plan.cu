@@ -11,15 +11,15 @@
 // which costs less than handing them over through a second launch, and then
 // maps its own tokens and fills its own share of the table rows. No CTA reads
 // what another writes: a token's page is read from the table only below h_b,
-// from the free list otherwise. One request takes 3.0 us of GPU time, 1000
-// requests (20 of them prompts in chunks of up to 2048 tokens) 4.5 us; a launch
-// alone takes 2.
+// from the free list otherwise. One request takes 2.6 us of GPU time, 1000
+// requests (20 of them prompts in chunks of up to 2048 tokens) 4.1 us; a launch
+// alone takes 1.6.
 //
 // Append. A thread moves 8 elements of one head's row, 16 bytes of the cache:
 // with heads of 64 or 128 columns a row is 8 or 16 such pieces, so a warp
 // writes whole lines whatever the order of the slots. 12345 tokens of 8 heads
-// of 128 columns (fp32 rounded to fp16, 149 MB) take 24 us, 6.2 TB/s, 91 % of a
-// copy's rate; 36 tokens 2.0 us, the launch.
+// of 128 columns (fp32 rounded to fp16, 149 MB) take 23.6 us, 6.3 TB/s, 93 % of a
+// copy's rate; 36 tokens 1.6 us, the launch.
 #include "batch_launch.h"
 #include "common.cuh"
 #include "round16.cuh"

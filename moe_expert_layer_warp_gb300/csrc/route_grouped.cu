@@ -16,14 +16,14 @@
 // experts; close tokens whole in fp64, 81 us.) Without a bias, c is monotone
 // in the logit, and experts are compared by their logits, exactly.
 //
-// 20011 tokens of 256 experts in 8 groups (sigmoid, bias, bf16) take 19.4 us;
+// 20011 tokens of 256 experts in 8 groups (sigmoid, bias, bf16) take 18.8 us;
 // the logits alone would take 1.7. What bounds it is issuing a token's
 // 790 instructions and waiting for one lane's after another's: scores 5 us,
 // groups 4, the (k + 1)-th best 1, candidates and ranks 4, weights 4. A group's
 // experts lie in its own lanes, so its sum takes log2(lanes) steps and no
 // shared memory (groups across lanes: 28 us). Warps that stay and load the
 // next token ahead were slower (22.9 us): the tokens that take fp64 then hold
-// up others. 64 tokens take 3.8 us, 9 take 2.6: a launch and one token's chain.
+// up others. 64 tokens take 3.4 us, 9 take 2.6: a launch and one token's chain.
 #include <cuda_fp16.h>
 #include <limits.h>
 #include <math.h>
