@@ -1,6 +1,6 @@
 """Thin ctypes binding of libmoewarp.so — the same entry points as the C ABI
-in include/moe_warp.h and include/moe_batch.h, taking torch CUDA tensors for
-the device pointers.
+in include/moe_warp.h, include/moe_batch.h and include/moe_kv8.h, taking torch
+CUDA tensors for the device pointers.
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels. If the library has not been built, or no CUDA device is present,
@@ -27,7 +27,9 @@ EXPORTED = ("moe_workspace_bytes", "moe_route", "moe_build_union", "moe_verify_p
             "moe_last_cuda_error_string", "moe_verify_dedup_noalloc", "moe_noalloc_scratch_limit",
             "moe_diag_bounded_wait", "moe_route_biased", "moe_route_union", "moe_verify_pass",
             "moe_verify_pass_fused", "moe_gate", "moe_plan_batch", "moe_kv_append",
-            "moe_attend_workspace_bytes", "moe_attend", "moe_attend_padded", "moe_route_grouped")
+            "moe_attend_workspace_bytes", "moe_attend", "moe_attend_padded", "moe_route_grouped",
+            "moe_rotary_turns", "moe_rotary", "moe_kv8_append", "moe_kv8_read",
+            "moe_attend8_workspace_bytes", "moe_attend8", "moe_attend8_padded")
 
 MOE_F32, MOE_BF16, MOE_F16 = range(3)
 MOE_MAX_REQUESTS, MOE_MAX_GROUPS, MOE_MAX_HEAD_GROUP = 1024, 32, 128
@@ -86,6 +88,29 @@ class RouterDesc(ctypes.Structure):
                   "renorm")] + [("scale", ctypes.c_float)])
 
 
+class RotaryDesc(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int32) for name in
+                 ("head_dim", "n_rotated", "first", "interleaved")] +
+                [("amplitude", ctypes.c_float), ("turns", ctypes.c_void_p)])
+
+
+class RotaryRows(ctypes.Structure):
+    # "in" is a Python word: in_
+    _fields_ = ([("in_", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                 ("n_heads", ctypes.c_int32)] +
+                [(name, ctypes.c_int64) for name in
+                 ("in_token_stride", "in_head_stride", "out_token_stride", "out_head_stride")])
+
+
+class Kv8CacheC(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_void_p) for name in ("k", "v", "k_scale", "v_scale")] +
+                [("n_pages", ctypes.c_int64)] +
+                [(name, ctypes.c_int32) for name in
+                 ("page_size", "n_kv_heads", "head_dim", "block")] +
+                [(name, ctypes.c_int64) for name in
+                 ("page_stride", "token_stride", "head_stride")])
+
+
 _lib = None
 
 
@@ -135,6 +160,19 @@ def load(path: str = LIB_PATH):
     lib.moe_route_grouped.argtypes = [ctypes.POINTER(RouterDesc), P, I32, I64, P, I32, P, P, P]
     for f in ("moe_plan_batch", "moe_kv_append", "moe_attend", "moe_attend_padded",
               "moe_route_grouped"):
+        getattr(lib, f).restype = ctypes.c_int
+    C8, R = ctypes.POINTER(Kv8CacheC), ctypes.POINTER(RotaryRows)
+    lib.moe_rotary_turns.argtypes = [P, I32, P]
+    lib.moe_rotary.argtypes = [ctypes.POINTER(RotaryDesc), I32, R, R, P, I32, P]
+    lib.moe_kv8_append.argtypes = [C8, P, P, I32, I64, I64, I32, P, P]
+    lib.moe_kv8_read.argtypes = [C8, P, I32, I32, P, P, I64, I64, P]
+    lib.moe_attend8_workspace_bytes.argtypes = [C8, A]
+    lib.moe_attend8_workspace_bytes.restype = SZ
+    lib.moe_attend8.argtypes = [C8, A, I32, P, I64, I64, I32, P, P, P, I32, I32, P, SZ, P, I64, I64,
+                                P]
+    lib.moe_attend8_padded.argtypes = lib.moe_attend8.argtypes
+    for f in ("moe_rotary_turns", "moe_rotary", "moe_kv8_append", "moe_kv8_read", "moe_attend8",
+              "moe_attend8_padded"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("moe_route", "moe_build_union", "moe_verify_perslot", "moe_verify_dedup",
               "moe_combine", "moe_last_device_error", "moe_verify_dedup_noalloc",
@@ -394,3 +432,122 @@ def moe_route_grouped(router: RouterDesc, logits, bias, topk_idx, topk_w, stream
                                     _stride(logits, 0), _ptr(bias),
                                     logits.shape[0], _ptr(topk_idx), _ptr(topk_w),
                                     _stream(stream)), "moe_route_grouped")
+
+
+# ---- include/moe_kv8.h -------------------------------------------------------
+def moe_rotary_turns(radians) -> torch.Tensor:
+    """[n] int64 on the host, the bits of the library's uint64 table, for angles
+    per position in radians (any sequence of numbers)."""
+    n = len(radians)
+    angles = (ctypes.c_double * n)(*radians)
+    turns = torch.empty(n, dtype=torch.int64)
+    _check(load().moe_rotary_turns(angles, n, turns.data_ptr()), "moe_rotary_turns")
+    return turns
+
+
+def make_rotary_rows(x: torch.Tensor, out: torch.Tensor) -> RotaryRows:
+    """x, out: [n][heads][head_dim] of one type and shape, last dimension contiguous."""
+    _shaped("out", out, x.dtype, x.shape)
+    if x.dim() != 3 or x.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("rows must be [tokens][heads][dim] with contiguous rows")
+    return RotaryRows(_raw(x), _raw(out), x.shape[1], _stride(x, 0), _stride(x, 1),
+                      _stride(out, 0), _stride(out, 1))
+
+
+def moe_rotary(rotary: RotaryDesc, q, k, positions, q_out=None, k_out=None, stream=None):
+    """q, k (or None): [n][heads][head_dim]; q_out, k_out None: in place."""
+    n, given = positions.shape[0], [x for x in (q, k) if x is not None]
+    _shaped("positions", positions, torch.int32, (None,))
+    if not given:
+        raise ValueError("give q or k")
+    dtype = given[0].dtype
+    if dtype not in DTYPES or any(x.dtype is not dtype for x in given):
+        raise ValueError("q and k must be of one type: float32, bfloat16 or float16")
+    rows = []
+    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
+        if x is not None:
+            _shaped(name, x, dtype, (n, None, rotary.head_dim))
+            x = ctypes.byref(make_rotary_rows(x, x if out is None else out))
+        rows.append(x)
+    _check(load().moe_rotary(ctypes.byref(rotary), DTYPES[dtype], rows[0], rows[1],
+                             _ptr(positions), n, _stream(stream)), "moe_rotary")
+
+
+def make_cache8(k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                v_scale: torch.Tensor) -> Kv8CacheC:
+    """From pools of codes [n_pages][page_size][n_kv_heads][head_dim] in
+    float8_e4m3fn, the last dimension contiguous, both with the same strides, and
+    their scales [n_pages][n_kv_heads][page_size / block] in float32."""
+    if k.dim() != 4 or k.shape != v.shape or any(
+            _stride(k, i) != _stride(v, i) for i in range(4)):
+        raise ValueError("k and v must be [pages][rows][heads][dim] of one shape and strides")
+    if (k.dtype is not torch.float8_e4m3fn or v.dtype is not torch.float8_e4m3fn or
+            k.stride(3) != 1 or v.stride(3) != 1):
+        raise ValueError("cache pages must be float8_e4m3fn with contiguous rows")
+    pages, page, heads, dim = k.shape
+    for name, s in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _shaped(name, s, torch.float32, (pages, heads, None))
+        if not s.is_contiguous() or s.shape != k_scale.shape or not s.shape[2] or page % s.shape[2]:
+            raise ValueError("%s must be contiguous, [pages][heads][blocks of a page]" % name)
+    return Kv8CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, page,
+                     heads, dim, page // k_scale.shape[2], _stride(k, 0), _stride(k, 1),
+                     _stride(k, 2))
+
+
+def moe_kv8_append(cache: Kv8CacheC, k, v, slots, stream=None):
+    """k, v: [n_tokens][n_kv_heads][head_dim], last dimension contiguous."""
+    _shaped("k", k, k.dtype, (None, cache.n_kv_heads, cache.head_dim))
+    _shaped("v", v, k.dtype, k.shape)
+    _holding("slots", slots, torch.int64, k.shape[0])
+    if k.stride(2) != 1 or v.stride(2) != 1 or any(
+            _stride(k, i) != _stride(v, i) for i in range(2)):
+        raise ValueError("k and v must share their strides, their rows contiguous")
+    if k.dtype not in DTYPES:
+        raise ValueError("k and v must be float32, bfloat16 or float16")
+    _check(load().moe_kv8_append(ctypes.byref(cache), _raw(k), _raw(v), DTYPES[k.dtype],
+                                 _stride(k, 0), _stride(k, 1), k.shape[0], _ptr(slots),
+                                 _stream(stream)), "moe_kv8_append")
+
+
+def moe_kv8_read(cache: Kv8CacheC, slots, k, v, stream=None):
+    """k, v: [n][n_kv_heads][head_dim] out, of one type and strides."""
+    _shaped("slots", slots, torch.int64, (None,))
+    n = slots.shape[0]
+    _shaped("k", k, k.dtype, (n, cache.n_kv_heads, cache.head_dim))
+    _shaped("v", v, k.dtype, k.shape)
+    if k.stride(2) != 1 or v.stride(2) != 1 or any(
+            _stride(k, i) != _stride(v, i) for i in range(2)):
+        raise ValueError("k and v must share their strides, their rows contiguous")
+    if k.dtype not in DTYPES:
+        raise ValueError("k and v must be float32, bfloat16 or float16")
+    _check(load().moe_kv8_read(ctypes.byref(cache), _ptr(slots), n, DTYPES[k.dtype], _raw(k),
+                               _raw(v), _stride(k, 0), _stride(k, 1), _stream(stream)),
+           "moe_kv8_read")
+
+
+def moe_attend8_workspace_bytes(cache: Kv8CacheC, attn: AttnDesc) -> int:
+    return int(load().moe_attend8_workspace_bytes(ctypes.byref(cache), ctypes.byref(attn)))
+
+
+def moe_attend8(cache: Kv8CacheC, attn: AttnDesc, q, q_start, kv_len, block_table, workspace, out,
+                stream=None, padded: bool = False):
+    """q, out: [n_tokens][n_heads][head_dim] bfloat16 or float16, last dimension
+    contiguous; padded: moe_attend8_padded."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q must be bfloat16 or float16, got %s" % str(q.dtype)[6:])
+    _shaped("q", q, q.dtype, (None, attn.n_heads, cache.head_dim))
+    _shaped("out", out, q.dtype, q.shape)
+    _shaped("kv_len", kv_len, torch.int32, (None,))
+    n = kv_len.shape[0]
+    _holding("q_start", q_start, torch.int32, n + 1)
+    _shaped("block_table", block_table, torch.int32, (None, None))
+    _holding("block_table", block_table, torch.int32, n * block_table.shape[1])
+    if q.stride(2) != 1 or out.stride(2) != 1:
+        raise ValueError("the rows of q and out must be contiguous")
+    call = load().moe_attend8_padded if padded else load().moe_attend8
+    _check(call(ctypes.byref(cache), ctypes.byref(attn), DTYPES[q.dtype], _raw(q), _stride(q, 0),
+                _stride(q, 1), q.shape[0], _ptr(q_start), _ptr(kv_len), _ptr(block_table),
+                block_table.shape[1], n, _ptr(workspace),
+                workspace.numel() * workspace.element_size(), _raw(out), _stride(out, 0),
+                _stride(out, 1), _stream(stream)),
+           "moe_attend8_padded" if padded else "moe_attend8")

@@ -1,5 +1,5 @@
 """A verification step of several requests, through the C ABI of
-include/moe_batch.h.
+include/moe_batch.h and include/moe_kv8.h.
 
 ``BatchPlanner`` turns request lengths into block tables, slots and
 positions; ``PagedCache`` holds pages of keys and values and takes new ones;
@@ -11,6 +11,12 @@ them in that order, then an expert engine (``layer.PassRunner``):
     cache.append(k, v, plan.slots)
     y = attention.attend(q, plan.q_start, plan.kv_len, table)
     idx, w = router.route(logits)
+
+``Rotary`` gives queries and keys their positions before that, and
+``PagedCache8`` with ``PagedAttention8`` is the same cache and attention with
+keys and values held in 8 bits:
+
+    rotary.rotate(q, k, plan.positions)
 
 Each object allocates its buffers once, through torch, at construction; a
 call only checks and marshals its arguments, returns views of those buffers
@@ -246,6 +252,274 @@ class PagedAttention:
             self._ws_bytes, out.data_ptr(), out_token, out_head, _handle(stream, at))
         if st:
             api._check(st, "moe_attend")
+        return out
+
+
+def rotary_frequencies(n_rotated: int, base: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, original: int = 4096, fast: float = 32.0,
+                       slow: float = 1.0) -> list:
+    """Angles per position in radians of n_rotated / 2 pairs, base^(-2i/n_rotated),
+    stretched for contexts `factor` times as long as `original` positions:
+
+      "linear"  every angle divided by factor;
+      "base"    the base times factor^(n/(n-2)): the slowest pair is stretched by
+                the factor, the fastest not at all;
+      "ramp"    pairs that turn less than `slow` times within `original` positions
+                divided, those that turn more than `fast` times kept, the pairs
+                between by their index (usual with an amplitude of
+                0.1 ln(factor) + 1);
+      "bands"   the same by the number of turns itself.
+    """
+    n = n_rotated
+    if n < 2 or n % 2 or not base > 0 or not factor > 0 or original < 1 or not 0 < slow < fast:
+        raise ValueError("n_rotated must be even and positive, base, factor and original positive, "
+                         "and slow below fast")
+    if scaling == "base":
+        if n < 4:
+            raise ValueError("scaling the base takes two pairs at least")
+        base *= factor ** (n / (n - 2))
+    f = [base ** (-2.0 * i / n) for i in range(n // 2)]
+    if scaling in ("none", "base"):
+        return f
+    if scaling == "linear":
+        return [v / factor for v in f]
+    if scaling == "bands":
+        keep = [(original * v / (2 * math.pi) - slow) / (fast - slow) for v in f]
+    elif scaling == "ramp":
+        if base == 1.0:
+            raise ValueError("a ramp takes a base other than 1")
+
+        def index(turns):
+            return n * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(0.0, math.floor(index(fast))), min(n - 1.0, math.ceil(index(slow)))
+        keep = [1.0 - (i - lo) / max(hi - lo, 0.001) for i in range(n // 2)]
+    else:
+        raise ValueError("scaling must be 'none', 'linear', 'base', 'ramp' or 'bands'")
+    keep = [min(1.0, max(0.0, v)) for v in keep]
+    return [v * w + v / factor * (1.0 - w) for v, w in zip(f, keep)]
+
+
+class Rotary:
+    """Rotary positions of queries and keys (moe_rotary): of every head the
+    n_rotated columns from `first` on (None: all) are turned in pairs, halves of
+    them or neighbours (interleaved). frequencies: angles per position in radians,
+    n_rotated / 2 of them (None: rotary_frequencies(n_rotated))."""
+
+    def __init__(self, head_dim: int, n_rotated: Optional[int] = None, frequencies=None,
+                 first: int = 0, interleaved: bool = False, amplitude: float = 1.0, device="cuda"):
+        n = head_dim if n_rotated is None else n_rotated
+        if frequencies is None:
+            frequencies = rotary_frequencies(n)
+        frequencies = [float(v) for v in frequencies]
+        if len(frequencies) * 2 != n:
+            raise ValueError("%d rotated columns need %d frequencies, got %d"
+                             % (n, n // 2, len(frequencies)))
+        turns = api.moe_rotary_turns(frequencies)
+        self.device = _cuda(device)
+        self.head_dim, self.n_rotated, self.frequencies = head_dim, n, frequencies
+        self._turns = turns.to(self.device)
+        self.desc = api.RotaryDesc(head_dim, n, first, 1 if interleaved else 0, amplitude,
+                                   self._turns.data_ptr())
+        self._lib, self._index, self._dref = api.load(), self.device.index, ctypes.byref(self.desc)
+        self._q, self._k = api.RotaryRows(), api.RotaryRows()
+        self._qref, self._kref = ctypes.byref(self._q), ctypes.byref(self._k)
+        # the descriptor's own checks, before the first step
+        api._check(self._lib.moe_rotary(self._dref, api.MOE_F32, None, None, None, 0, None),
+                   "Rotary")
+
+    def _rows(self, c, name, x, out, n):
+        D = self.head_dim
+        s = x.stride()
+        if x.dim() != 3 or x.shape[0] != n or x.shape[2] != D or x.get_device() != self._index or (
+                s[2] != 1):
+            raise ValueError("%s must be a [%d][heads][%d] tensor on %s with contiguous rows"
+                             % (name, n, D, self.device))
+        H = x.shape[1]
+        c.n_heads = H
+        c.in_ = x.data_ptr()
+        c.in_token_stride, c.in_head_stride = s[0] if n > 1 else D, s[1] if H > 1 else D
+        if out is None:
+            out = x
+        elif out.shape != x.shape or out.dtype is not x.dtype or (
+                out.get_device() != self._index or out.stride(2) != 1):
+            raise ValueError("%s_out must be a %s %s tensor on %s with contiguous rows"
+                             % (name, str(x.dtype)[6:], list(x.shape), self.device))
+        s = out.stride()
+        c.out = out.data_ptr()
+        c.out_token_stride, c.out_head_stride = s[0] if n > 1 else D, s[1] if H > 1 else D
+        return out
+
+    def rotate(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+               positions: torch.Tensor, q_out: Optional[torch.Tensor] = None,
+               k_out: Optional[torch.Tensor] = None, stream=None):
+        """q, k: [n][heads][head_dim] float32, bfloat16 or float16 with contiguous
+        rows, either may be None; positions [n] int32, as BatchPlanner.plan leaves
+        them. In place, or into q_out and k_out. Returns (q, k) rotated."""
+        n, x = positions.shape[0], k if q is None else q
+        if x is None or (q is not None and k is not None and q.dtype is not k.dtype) or (
+                x.dtype not in api.DTYPES):
+            raise ValueError("give q or k, of one type: float32, bfloat16 or float16")
+        if q is not None:
+            q = self._rows(self._q, "q", q, q_out, n)
+        if k is not None:
+            k = self._rows(self._k, "k", k, k_out, n)
+        st = self._lib.moe_rotary(
+            self._dref, api.DTYPES[x.dtype], None if q is None else self._qref,
+            None if k is None else self._kref,
+            _need(positions, "positions", torch.int32, (n,), self._index), n,
+            _handle(stream, self._index))
+        if st:
+            api._check(st, "moe_rotary")
+        return q, k
+
+
+class PagedCache8:
+    """Pages of keys and values in 8 bits: codes k, v
+    [n_pages][page_size][n_kv_heads][head_dim] in float8_e4m3fn, in any order in
+    memory that keeps head_dim contiguous, and scales k_scale, v_scale
+    [n_pages][n_kv_heads][page_size / block] in float32, one for each `block`
+    tokens of a page and head. An element stands for code · scale."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        if not k.is_cuda or any(t.device != k.device for t in (v, k_scale, v_scale)):
+            raise ValueError("codes and scales must live on one CUDA device")
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, k.device
+        self.c = api.make_cache8(k, v, k_scale, v_scale)
+        self.page_size, self.n_kv_heads, self.head_dim = k.shape[1:]
+        self.block = self.c.block
+        self._lib = api.load()
+        self._index, self._cref = self.device.index, ctypes.byref(self.c)
+        self._row = (self.n_kv_heads, self.head_dim)
+
+    @classmethod
+    def allocate(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
+                 block: int = 16, device="cuda", heads_first: bool = False) -> "PagedCache8":
+        """A pool of its own, not initialised; heads_first: heads before rows
+        within a page."""
+        if block < 1 or page_size % block:
+            raise ValueError("block must divide page_size")
+        shape = ((n_pages, n_kv_heads, page_size, head_dim) if heads_first else
+                 (n_pages, page_size, n_kv_heads, head_dim))
+        device = _cuda(device)
+        k, v = (torch.empty(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2))
+        ks, vs = (torch.empty((n_pages, n_kv_heads, page_size // block), device=device)
+                  for _ in range(2))
+        return cls(k.transpose(1, 2), v.transpose(1, 2), ks, vs) if heads_first else cls(k, v, ks,
+                                                                                          vs)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        """New keys and values [n][n_kv_heads][head_dim] (float32, bfloat16 or
+        float16) to their slots, rounded to codes (moe_kv8_append). A block's
+        scale grows with what comes into it, and starts anew when its first row
+        is written; the tokens of a block are consecutive rows of the call. Rows
+        must be contiguous; token and head strides may be any multiple of 16
+        bytes."""
+        n, dt, at = k.shape[0], k.dtype, self._index
+        sk, sv = k.stride(), v.stride()
+        if (k.shape != (n, *self._row) or v.shape != k.shape or v.dtype is not dt or
+                dt not in api.DTYPES or k.get_device() != at or v.get_device() != at or
+                sk[2] != 1 or sv[2] != 1 or (n > 1 and sk[0] != sv[0]) or
+                (self.n_kv_heads > 1 and sk[1] != sv[1])):
+            raise ValueError("k and v must be [n][%d][%d] float32, bfloat16 or float16 tensors on "
+                             "%s with contiguous rows and equal strides" % (*self._row, self.device))
+        D = self.head_dim                      # for the stride of a dimension of one entry
+        st = self._lib.moe_kv8_append(self._cref, k.data_ptr(), v.data_ptr(), api.DTYPES[dt],
+                                      sk[0] if n > 1 else D, sk[1] if self.n_kv_heads > 1 else D, n,
+                                      _need(slots, "slots", torch.int64, (n,), at),
+                                      _handle(stream, at))
+        if st:
+            api._check(st, "moe_kv8_append")
+
+    def read(self, slots: torch.Tensor, dtype=torch.bfloat16, k: Optional[torch.Tensor] = None,
+             v: Optional[torch.Tensor] = None, stream=None):
+        """(keys, values) [n][n_kv_heads][head_dim] that the rows of slots [n] int64
+        stand for (moe_kv8_read), zeros for slot -1, written to k and v if given
+        (of one type and strides), else to new tensors of `dtype`."""
+        n, at = slots.shape[0], self._index
+        if k is None and v is None:
+            k, v = (torch.empty((n, *self._row), dtype=dtype, device=self.device)
+                    for _ in range(2))
+        elif k is None or v is None:
+            raise ValueError("give both k and v, or neither")
+        sk, sv = k.stride(), v.stride()
+        if (k.shape != (n, *self._row) or v.shape != k.shape or v.dtype is not k.dtype or
+                k.dtype not in api.DTYPES or k.get_device() != at or v.get_device() != at or
+                sk[2] != 1 or sv[2] != 1 or (n > 1 and sk[0] != sv[0]) or
+                (self.n_kv_heads > 1 and sk[1] != sv[1])):
+            raise ValueError("k and v must be [%d][%d][%d] float32, bfloat16 or float16 tensors on "
+                             "%s with contiguous rows and equal strides"
+                             % (n, *self._row, self.device))
+        D = self.head_dim
+        st = self._lib.moe_kv8_read(self._cref, _need(slots, "slots", torch.int64, (n,), at), n,
+                                    api.DTYPES[k.dtype], k.data_ptr(), v.data_ptr(),
+                                    sk[0] if n > 1 else D, sk[1] if self.n_kv_heads > 1 else D,
+                                    _handle(stream, at))
+        if st:
+            api._check(st, "moe_kv8_read")
+        return k, v
+
+
+class PagedAttention8:
+    """PagedAttention over a cache in 8 bits (moe_attend8): queries and results
+    are of `dtype`, bfloat16 or float16."""
+
+    def __init__(self, cache: PagedCache8, n_heads: int, max_tokens: int, dtype=torch.bfloat16,
+                 scale: Optional[float] = None, window: int = 0, sinks: int = 0):
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("dtype must be bfloat16 or float16")
+        self.cache, self.n_heads, self.max_tokens, self.dtype = cache, n_heads, max_tokens, dtype
+        self.desc = api.AttnDesc(n_heads, window, sinks, 1.0 / math.sqrt(cache.head_dim)
+                                 if scale is None else scale)
+        nbytes = api.moe_attend8_workspace_bytes(cache.c, self.desc)
+        if nbytes == 0:
+            raise ValueError("cache or attention shape not covered by this library: %d heads over "
+                             "%d of %d, pages of %d, blocks of %d, window %d, sinks %d"
+                             % (n_heads, cache.n_kv_heads, cache.head_dim, cache.page_size,
+                                cache.block, window, sinks))
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+        self._out = torch.empty((max_tokens, n_heads, cache.head_dim), dtype=dtype,
+                                device=cache.device)
+        self._lib = api.load()
+        self._dref, self._ws_ptr, self._ws_bytes = (ctypes.byref(self.desc),
+                                                    self.workspace.data_ptr(), nbytes)
+        self._type = api.DTYPES[dtype]
+        self._n, self._view = None, None
+
+    def _check(self, name, t, n):
+        """The token and head strides of q or out."""
+        c, H = self.cache, self.n_heads
+        s = t.stride()
+        if (t.shape != (n, H, c.head_dim) or t.dtype is not self.dtype or
+                t.get_device() != c._index or s[2] != 1):
+            raise ValueError("%s must be a %s %s tensor on %s with contiguous rows"
+                             % (name, str(self.dtype)[6:], [n, H, c.head_dim], c.device))
+        return s[0] if n > 1 else c.head_dim, s[1] if H > 1 else c.head_dim
+
+    def attend(self, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+               block_table: torch.Tensor, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+        """As PagedAttention.attend."""
+        c, n, i32 = self.cache, q.shape[0], torch.int32
+        at, call = c._index, self._lib.moe_attend8
+        if out is None:
+            if n != self._n:
+                if n > self.max_tokens:
+                    raise ValueError("%d tokens, more than max_tokens %d" % (n, self.max_tokens))
+                self._n, self._view = n, self._out[:n]
+            out, call = self._view, self._lib.moe_attend8_padded
+        q_token, q_head = self._check("q", q, n)
+        out_token, out_head = self._check("out", out, n)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [requests][blocks]")
+        B, M = block_table.shape
+        st = call(
+            c._cref, self._dref, self._type, q.data_ptr(), q_token, q_head, n,
+            _need(q_start, "q_start", i32, (B + 1,), at), _need(kv_len, "kv_len", i32, (B,), at),
+            _need(block_table, "block_table", i32, (B, M), at), M, B, self._ws_ptr,
+            self._ws_bytes, out.data_ptr(), out_token, out_head, _handle(stream, at))
+        if st:
+            api._check(st, "moe_attend8")
         return out
 
 
