@@ -2,125 +2,1103 @@
 // e4m3 codes: causal, optionally within a sliding window beside a few first
 // keys that stay visible.
 //
-// For a query row q at position p, with s_j = scale·ks_j·(q·k_j) over the keys
-// it sees, out = Σ_j e^(s_j − m) vs_j·v_j / Σ_j e^(s_j − m). A warp per row
-// walks its keys one after the other with the running maximum and sums.
-#include <math.h>
+// For a query row q at position p, over the keys j that it sees, with codes K_j
+// and V_j and scales ks_j and vs_j of their blocks,
+//   s_j = scale · ks_j · (q · K_j)          (in powers of two: times log2 e)
+//   out = Σ_j 2^(s_j + log2 vs_j − m) V_j / Σ_j 2^(s_j − m),
+// the reference m and the two sums carried along in one pass over the keys as in
+// attend.cu. m follows t_j = s_j + log2 vs_j: the weights w_j = 2^(t_j − m) that
+// meet the codes are then largest at 1 whatever the scales, and the second sum is
+// that of w_j / vs_j.
+//
+// Codes go to the tensor cores as they lie in the cache (tcgen05 kind::f8f6f4):
+// nothing is widened, and half the bytes of a 16-bit cache are read. Their other
+// operands are sums of e4m3 numbers: a query row, divided by a power of two,
+// is hi + lo/16 (+ lolo/256), each number the rounding of 16 times what the ones
+// before it left; e4m3 has 4 significant bits, so two numbers hold the 8 of bf16
+// exactly, three the 11 of fp16, as long as they are within 2^-14 of the row's
+// largest. Weights are split likewise, times 2^7: m follows growth beyond 2^1.5
+// only, so they stay below 2^8.5, and 448 is e4m3's largest. The numbers are
+// columns of one operand beside each other, so a product takes them at once.
+//
+// Tiles. Keys are the rows of both products, query rows their columns:
+//   Sᵀ = K · Qᵀ   128 keys × (16 to 64 query rows, times 2 or 3), and
+//   Oᵀ += Vᵀ · Pᵀ  head_dim × the same columns,
+// so that a pass of a few tokens pays for its 16 columns and not for 128 rows
+// (an instruction takes 64 cycles for any width up to 128 columns), K and V are
+// read in the order in which they lie, and a key's scales are one thread's. A
+// softmax thread has one key and 16 query rows. Its rows' references are those of
+// its group of four warps, which hold the tile's 128 keys: they change only when
+// some weight passes 2^8.5 (asked by one barrier's vote), and then by the exact
+// maximum over the tile.
+//
+// Work is cut into equal ranges as in attend.cu (attend_range.cuh): an item is
+// (request, key head, block of tokens with at most 64 rows), a CTA whose range
+// ends inside an item leaves (O, m, Σ) of its rows, and the CTA with the item's
+// last tile joins the parts in key order. Within a CTA an item of at most 32 (16)
+// rows runs as two (four) streams over every second (fourth) tile, each with its
+// own sums, joined at the end.
+//
+// Warps (one CTA per SM):
+//   0      TMA: key tiles into a ring, a box per page
+//   1      MMA issue
+//   2      TMA: value tiles into the same ring; the tiles' scales
+//   3      query rows into e4m3 numbers, the next item's ahead
+//   4-19   softmax, four groups of four warps: 16 columns of a tile each, or the
+//          tiles of a stream
+//
+// Values that are not finite (NaN; e4m3 has no infinities). A weight of 0 times
+// NaN is NaN: rows of V that no row of the item sees are cleared, and NaN in rows
+// that some see and others do not is taken out of the tile and noted for the rows
+// that do see it (in `spoiled`, a bit per column of V and row).
+#include <string.h>
 
-#include "batch_launch.h"
-#include "common.cuh"
+#include "attend8_mma.cuh"
+#include "attend_range.cuh"
 #include "fp8.cuh"
 #include "kv8_launch.h"
 #include "round16.cuh"
+#include "tmap.h"
 
 namespace moe {
 namespace {
 
-template <int kDim, bool kF16>
-__global__ void __launch_bounds__(256) attend8_kernel(const __grid_constant__ Attend8Args a,
-                                                      int page_shift, int block_shift) {
-  constexpr int kN = kDim / 32;                  // columns of a lane
-  pdl_wait();
-  pdl_trigger();
-  const moe_kv8_cache& c = a.cache;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int64_t t = row / a.n_heads;
-  const int h = (int)(row - t * a.n_heads), kh = h / a.group;
-  if (t >= a.n_tokens) return;
-  // the token's request: the last that begins at or before it
-  int b = -1, first = 0, len = 0, q = 0;
-  for (int i = 0; i < a.n_requests; ++i) {
-    const int f = a.q_start[i], l = a.q_start[i + 1];
-    if (f < 0 || l < f || l > a.n_tokens) report_error(a.err, ERR_CHECK, 0xB30);
-    if (f <= t && t < l) {
-      b = i;
-      first = f;
-      q = min(l, a.n_tokens) - f;
+constexpr int kThreads = 640;
+constexpr int kRows = 64;         // query rows of an item, at most
+constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
+// What an item costs beside its tiles when the work is cut, in tiles.
+constexpr int kItemUnits = 3;
+constexpr float kBase = 7.f;      // weights are held 2^7 larger
+constexpr float kGrow = 1.5f;     // m follows growth beyond this (powers of two)
+// Registers per thread: launched with 96, the 16 softmax warps take 104 and
+// the 4 others leave 64 (4·104 + 64 = 5·96).
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
+constexpr int kScaleSlots = 6;    // tiles whose scales are there
+constexpr int kScaleBlocks = kTile / 16;
+
+// kDim: columns of a head; kNum: e4m3 numbers of a query's element or a weight.
+template <int kDim, int kNum>
+struct Sizes {
+  static constexpr int kWide = kNum == 2 ? 2 : 4;  // columns set aside for a row's numbers
+  static constexpr int kTileBytes = kTile * kDim;
+  static constexpr int kQBytes = kRows * kNum * kDim;
+  static constexpr int kPBytes = kTile * kRows * kWide;  // in 128-byte columns, kTile rows each
+  static constexpr int kStages = kDim == 64 ? 16 : kNum == 2 ? 11 : 9;
+  static constexpr int kOffP = 2 * kQBytes;
+  static constexpr int kOffRing = kOffP + kPBytes;
+  static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
+  static constexpr int kMiscBytes = 3072;
+  static constexpr int kSmem = kOffMisc + kMiscBytes;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kTileBytes % 1024 == 0, "tiles");
+  static constexpr uint32_t kCols = kNum == 2 ? 256 : 512;  // tensor memory: S, then O
+  static constexpr uint32_t kColO = kRows * kWide;
+};
+// one slot of the workspace: O as [64 rows][dim] floats, then m and Σ
+constexpr size_t slot_floats(int dim) { return size_t(kRows) * (dim + 2); }
+
+struct Params {
+  CUtensorMap kmap, vmap;
+  Attend8Args a;
+  int page_shift;
+  int blocks_shift;  // log2 of a page's blocks
+  int tpt, block;    // tokens per item, 64 / group (both: see find_start)
+  float* part;       // [2 per CTA][slot]
+  // [CTAs][128]: see Misc::spoils
+  unsigned long long* spoiled;
+  // [CTAs]: `call` when the CTA has left the part of its last item; see attend.cu
+  unsigned long long* left;
+  unsigned long long call;
+};
+
+MOE_DEV Units units_of(const Params&, const Item& it) {
+  Units u;
+  u.cost = it.hi > 0 ? kItemUnits : 0;  // (rows that see nothing are only cleared)
+  u.each = 1;
+  u.all = u.cost + it.n;
+  return u;
+}
+
+// The CTA's part of an item: tiles [t0, t0 + n).
+struct Part {
+  Item it;
+  int t0, n;          // n 0: its rows see nothing
+  bool whole, ends;   // all of the item; its last tile
+  int rows, wide;     // query rows, and those rounded up: 16, 32, 48 or 64
+  int streams, shift; // 4, 2 or 1, and its logarithm
+  MOE_DEV int tile(int j) const { return tile_of(it, t0 + j); }
+  // places in the ring behind the part's first: K_0 .. K_{streams-1}, then
+  // K_{j + streams} and V_j for j = 0, 1, ..
+  MOE_DEV int place_k(int j) const { return j < streams ? j : 2 * j - streams; }
+  MOE_DEV int place_v(int j) const { return j + streams < n ? 2 * j + streams + 1 : n + j; }
+};
+
+// The next part of the walk; every role walks it by itself.
+struct Walker {
+  const Params& p;
+  Walk w;
+  Request r;
+  int b, h;  // of the present part
+
+  MOE_DEV Walker(const Params& prm, const Start& s) : p(prm), w(s.w), r(s.r), b(s.w.b), h(s.w.h) {}
+
+  MOE_DEV bool next(Part* out) {
+#pragma unroll 1
+    while (w.left > 0) {
+      const Item it = make_item(p.a, r, w.block, p.block);
+      const Units units = units_of(p, it);
+      const int u1 = min(w.u0 + w.left, units.all);
+      out->it = it;
+      out->t0 = units.tiles(w.u0);
+      const int t1 = units.tiles(u1), n = t1 - out->t0;
+      out->n = it.hi > 0 ? n : 0;
+      out->whole = n == it.n;
+      out->ends = t1 == it.n;
+      out->rows = it.ntok * p.a.group;
+      out->wide = (out->rows + 15) & ~15;
+      out->shift = out->wide == 16 ? 2 : out->wide == 32 ? 1 : 0;
+      out->streams = 1 << out->shift;
+      b = w.b;
+      h = w.h;
+      w.left -= u1 - w.u0;
+      w.u0 = 0;
+      if (w.left > 0 && ++w.block * p.block >= r.q) {
+        w.block = 0;
+        if (++w.h == p.a.cache.n_kv_heads) {
+          w.h = 0;
+          bool bad;
+          do {
+            r = request(p.a, p.page_shift, ++w.b, &bad);
+          } while (r.q == 0 && w.b + 1 < p.a.n_requests);
+        }
+      }
+      if (n > 0) return true;
     }
+    return false;
   }
-  uint16_t* out = static_cast<uint16_t*>(a.out) + t * a.out_token_stride + h * a.out_head_stride +
-                  lane * kN;
-  if (b < 0) {
-    if (a.clear)
-      for (int i = 0; i < kN; ++i) out[i] = 0;
+};
+
+// A place in the ring, counted modulo twice its stages: the stage, and the parity
+// of its filling.
+template <int kStages>
+struct Place {
+  int at;
+  MOE_DEV explicit Place(unsigned from) : at((int)from) {}
+  MOE_DEV int stage() const { return at >= kStages ? at - kStages : at; }
+  MOE_DEV uint32_t parity() const { return at >= kStages; }
+};
+
+// How many tiles each of the four streams has had, modulo 256, a byte each: all
+// roles count alike, and a barrier's parity follows from its stream's count.
+MOE_DEV uint32_t count_of(uint32_t counts, int s) { return counts >> (8 * s) & 255u; }
+MOE_DEV uint32_t add_counts(uint32_t counts, const Part& pt) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int more = s < pt.streams && pt.n > s ? ((pt.n - 1 - s) >> pt.shift) + 1 : 0;
+    r |= (count_of(counts, s) + (uint32_t)more & 255u) << (8 * s);
+  }
+  return r;
+}
+
+// Barriers and words behind the ring.
+template <int kStages>
+struct Misc {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
+  uint64_t s_full[4], s_empty[4], p_full[4], p_done[4];  // of a stream
+  uint64_t drain;
+  Start start;
+  long long part[8];
+  uint32_t tmem;
+  int lost;
+  // NaN has been noted in the CTA's `spoiled` for the present item
+  int spoils;
+};
+constexpr int kOffRef = 704;                    // [4 groups][16] −m of a column
+constexpr int kOffQScale = kOffRef + 256;       // [2][64] a row's factor
+constexpr int kOffStat = kOffQScale + 512;      // [4 groups][4 warps][16]
+constexpr int kOffScale = kOffStat + 1024;      // [slots][3][8 blocks]: ks, log2 vs + 7, 1 / vs
+static_assert(kOffScale + kScaleSlots * 3 * kScaleBlocks * 4 <= 3072, "misc words");
+
+// ln 2's reciprocal: scores are kept in powers of two.
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Row `row`, byte `at` of a tile of kRow-byte rows, swizzled at that width.
+template <int kRow>
+MOE_DEV uint32_t swizzled(uint32_t row, uint32_t at) {
+  const uint32_t o = row * kRow + at;
+  return o ^ (o >> 3 & (kRow == 128 ? 0x70u : 0x30u));
+}
+
+// Two values' e4m3 numbers: each is 16 times what the ones before it left. (In
+// fp16: the differences of numbers and their multiples by 16 are exact.)
+template <int kNum>
+MOE_DEV void numbers_of(float lo, float hi, uint16_t (&out)[kNum]) {
+  __half2 rest = __floats2half2_rn(lo, hi);
+#pragma unroll
+  for (int i = 0; i < kNum; ++i) {
+    out[i] = e4m3_of(rest);
+    if (i + 1 < kNum)
+      rest = __hfma2(half2_of(out[i]), __float2half2_rn(-16.f),
+                     __hmul2(rest, __float2half2_rn(16.f)));
+  }
+}
+// What a number counts.
+MOE_DEV constexpr float number_unit(int i) { return i == 0 ? 1.f : i == 1 ? 0x1p-4f : 0x1p-8f; }
+
+// The largest of the warp's values; NaN are passed over.
+MOE_DEV float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Bytes of w that are NaN, 0x80 each.
+MOE_DEV uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+template <int kDim>
+MOE_DEV const float* part_of(const Params& p, int cta, bool ends) {
+  return p.part + (size_t)(2 * cta + (ends ? 0 : 1)) * slot_floats(kDim);
+}
+
+// The parts of an item joined in key order, those of CTAs `first` to this one: a
+// thread has 4 columns of a row and loads 8 parts at once. (Barriers and flags as
+// in attend.cu.)
+template <int kDim, bool kF16>
+MOE_DEV void join_parts(const Params& p, const Start& st, volatile int* lost) {
+  const Attend8Args& a = p.a;
+  const long long head = st.more * (st.each + 1);
+  const int first = (int)(st.unit < head ? divide(st.unit, st.each + 1)
+                                         : st.more + divide(st.unit - head, st.each));
+  const int last = blockIdx.x;
+  const int tid = threadIdx.x - 128;
+  if (first + tid < last) {
+    unsigned long long* word = p.left + first + tid;
+    const unsigned long long t0 = global_ns();
+    for (unsigned int i = 0;; ++i) {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(word) : "memory");
+      if (v == p.call) break;
+      if ((i & 63u) == 63u && (*lost || global_ns() - t0 > kJoinLimitNs)) {
+        *lost = 0xB70;
+        if (exchange(word, given_up(p.call)) == p.call) break;
+        word = nullptr;
+        break;
+      }
+    }
+    if (word) *word = 0ull;
+  }
+  asm volatile("bar.sync 2, 512;" ::: "memory");
+  const int rows = st.ntok * a.group;
+#pragma unroll 1
+  for (int i = tid; i < rows * (kDim / 4); i += 512) {
+    const int row = i / (kDim / 4), c4 = i % (kDim / 4);
+    float m = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int c0 = first; c0 <= last; c0 += 8) {
+      float mc[8], sc[8];
+      float4 oc[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mc[j] = -INFINITY;
+        sc[j] = 0.f;
+        oc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + j <= last) {
+          const float* part = part_of<kDim>(p, c0 + j, c0 + j == last);
+          mc[j] = __ldcg(part + kRows * kDim + row);
+          sc[j] = __ldcg(part + kRows * kDim + kRows + row);
+          oc[j] = __ldcg(reinterpret_cast<const float4*>(part + row * kDim) + c4);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, mc[j]);
+      if (top == -INFINITY) {                      // (the parts hold zeros, or sums of NaN)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += sc[j];
+        continue;
+      }
+      const float keep = exp2_approx(m - top);
+      m = top;
+      sum *= keep;
+      o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float add = exp2_approx(mc[j] - top);
+        sum = fmaf(sc[j], add, sum);
+        o.x = fmaf(oc[j].x, add, o.x);
+        o.y = fmaf(oc[j].y, add, o.y);
+        o.z = fmaf(oc[j].z, add, o.z);
+        o.w = fmaf(oc[j].w, add, o.w);
+      }
+    }
+    const float inv = inverse(sum);
+    const int t = row / a.group, g = row - t * a.group;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(st.row0 + t) * a.out_token_stride +
+                    (int64_t)(st.head0 + g) * a.out_head_stride;
+    *reinterpret_cast<uint2*>(out + c4 * 4) =
+        make_uint2(round16<kF16>(o.x * inv, o.y * inv), round16<kF16>(o.z * inv, o.w * inv));
+  }
+}
+
+template <int kDim, int kNum>
+__global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_constant__ Params p) {
+  using Z = Sizes<kDim, kNum>;
+  constexpr bool kF16 = kNum == 3;
+  constexpr int kStages = Z::kStages;
+  using M = Misc<kStages>;
+  static_assert(sizeof(M) <= kOffRef, "misc words");
+  const Attend8Args& a = p.a;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_addr(smem) & 1023u) {               // the tiles' swizzle needs it
+    if (threadIdx.x == 0) report_error(a.err, ERR_CHECK, 0xB23);
     return;
   }
-  len = a.kv_len[b];
-  if (len < 0 || len > MOE_MAX_CACHE_LEN || len > ((int64_t)a.max_blocks << page_shift)) {
-    report_error(a.err, ERR_CHECK, 0xB31);
-    len = 0;
-  }
-  const int pos = len - q + (int)(t - first);
-  float x[kN], o[kN];
-  for (int i = 0; i < kN; ++i) {
-    const uint16_t w = (static_cast<const uint16_t*>(a.q) + t * a.q_token_stride +
-                        h * a.q_head_stride)[lane * kN + i];
-    x[i] = (kF16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16)) *
-           a.scale;
-    o[i] = 0.f;
-  }
-  float m = -INFINITY, sum = 0.f;
-  const int lo = a.window > 0 ? max(0, max(pos, 0) - a.window + 1) : 0;
-  const int blocks = c.page_size >> block_shift;
-  for (int j = 0; j <= pos && j < len; ++j) {
-    if (j < lo && j >= a.sinks) {
-      j = lo - 1;
-      continue;
+  unsigned char* misc = smem + Z::kOffMisc;
+  M& m = *reinterpret_cast<M*>(misc);
+  float* refs = reinterpret_cast<float*>(misc + kOffRef);
+  float* qscale = reinterpret_cast<float*>(misc + kOffQScale);
+  float* stat = reinterpret_cast<float*>(misc + kOffStat);
+  float* scale_slots = reinterpret_cast<float*>(misc + kOffScale);
+  // the same value in every lane, and known to be
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) - 4;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
     }
-    const int page = a.block_table[(size_t)b * a.max_blocks + (j >> page_shift)];
-    float ks = 1.f, vs = 1.f;
-    uint32_t kw = 0, vw = 0;
-    if (page < 0 || page >= c.n_pages) {
-      report_error(a.err, ERR_CHECK, 0xB32);
-    } else {
-      const int r = j & (c.page_size - 1);
-      const int64_t at = page * c.page_stride + r * c.token_stride + kh * c.head_stride + lane * kN;
-      if (kN == 4) {
-        kw = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c.k) + at);
-        vw = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(c.v) + at);
-      } else {
-        kw = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(c.k) + at);
-        vw = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(c.v) + at);
-      }
-      const int64_t s = ((int64_t)page * c.n_kv_heads + kh) * blocks + (r >> block_shift);
-      ks = c.k_scale[s];
-      vs = c.v_scale[s];
-      const float least = pow2(MOE_KV8_MIN_EXP), most = pow2(MOE_KV8_MAX_EXP);
-      if (!(ks >= least && ks <= most && vs >= least && vs <= most)) {
-        report_error(a.err, ERR_CHECK, 0xB33);
-        ks = fminf(fmaxf(ks, least), most);
-        vs = fminf(fmaxf(vs, least), most);
-      }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.q_full[i], 1);
+      mbar_init(&m.q_empty[i], 2);             // the products with it, and its factors' readers
     }
-    const float4 k4 = floats_of(kw), v4 = floats_of(vw);
-    const float kf[4] = {k4.x, k4.y, k4.z, k4.w}, vf[4] = {v4.x, v4.y, v4.z, v4.w};
-    float s = 0.f;
-    for (int i = 0; i < kN; ++i) s = fmaf(x[i], kf[i], s);
-    s = warp_sum(s) * ks;
-    const float top = fmaxf(m, s);
-    const float keep = m == -INFINITY ? 0.f : expf(m - top), p = expf(s - top);
-    m = top;
-    sum = sum * keep + p;
-    for (int i = 0; i < kN; ++i) o[i] = fmaf(p * vs, vf[i], o[i] * keep);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&m.sc_full[i], 1);
+      mbar_init(&m.sc_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&m.s_full[i], 1);
+      mbar_init(&m.s_empty[i], 16);            // a warp counts 1, 2 or 4 (see below)
+      mbar_init(&m.p_full[i], 16);
+      mbar_init(&m.p_done[i], 1);
+    }
+    mbar_init(&m.drain, 1);
+    fence_mbar_init();
+    m.lost = m.spoils = 0;
+    m.start.joins = 0;
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int i = 0; i < kN; i += 2)
-    *reinterpret_cast<uint32_t*>(out + i) = round16<kF16>(o[i] * inv, o[i + 1] * inv);
+  if (warp == -3) umma::tmem_alloc(&m.tmem, Z::kCols);
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&p.kmap);
+    prefetch_tmap(&p.vmap);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x < 128) p.spoiled[blockIdx.x * 128 + threadIdx.x] = 0;
+  // (the ring holds the plan's counts until the first tiles are on their way)
+  if (threadIdx.x < kPlanThreads)
+    find_start(p, reinterpret_cast<long long*>(smem + Z::kOffRing), m.part, &m.start);
+  fence_proxy_async_smem();
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
+
+  volatile int* lost = &m.lost;
+  bool ok = true;  // no wait of this role has been lost
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+    ok = __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, lost, site));
+  };
+  Part pt;
+  Walker walk(p, m.start);
+  uint32_t counts = 0;
+  int ring = 0;     // place of the part's first tile, modulo twice the stages
+
+  if (warp < 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == -4 || warp == -2) {
+    // ------------------------------------------------------------ loaders --
+    const bool values = warp == -2;
+    const int page = 1 << p.page_shift;
+    const int rows = min(page, kTile);          // rows of a box
+    const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
+    const uint64_t policy = l2_evict_normal_policy();
+    const CUtensorMap* map = values ? &p.vmap : &p.kmap;
+    const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
+    int slot = 0;
+    uint32_t slot_parity = 1;
+    while (walk.next(&pt)) {
+      const Item& it = pt.it;
+      const int n = pt.n;
+      const int32_t* table = a.block_table + (size_t)walk.b * a.max_blocks;
+      // this lane's page of tile j (−1: it has none, or no row of it is seen)
+      auto page_of = [&](int j) {
+        int pg = -1;
+        if (j < n && lane < n_pages) {
+          const int r0 = pt.tile(j) * kTile + lane * rows;
+          if (r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk)) {
+            pg = table[r0 >> p.page_shift];
+            if (pg < 0 || pg >= a.cache.n_pages) {
+              report_error(a.err, ERR_CHECK, 0xB21);
+              pg = (int)a.cache.n_pages;        // out of the map: the box reads zeros
+            }
+          }
+        }
+        return pg;
+      };
+      // this lane's scale of tile j: lanes 0-7 those of its keys, by 16, 8-15 of
+      // its values (1 where there is none, or none is wanted)
+      auto scale_of = [&](int j, int pg) {
+        const int e = lane & 7;
+        const int mine = __shfl_sync(0xffffffffu, pg, e * 16 / rows);
+        float s = 1.f;
+        if (lane < 16 && mine >= 0 && mine < a.cache.n_pages) {
+          const int key = pt.tile(j) * kTile + e * 16;
+          if (key < it.hi && (key + 16 > it.lo || key < it.sk)) {
+            const int at = (key & (page - 1)) >> (p.page_shift - p.blocks_shift);
+            const float* from = lane < 8 ? a.cache.k_scale : a.cache.v_scale;
+            s = __ldg(from + ((((int64_t)mine * a.cache.n_kv_heads) + walk.h) << p.blocks_shift) +
+                      at);
+          }
+        }
+        return s;
+      };
+      // pages are asked for four tiles ahead, scales two
+      int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3 = page_of(3);
+      float s0 = 1.f, s1 = 1.f;
+      if (values) {
+        s0 = scale_of(0, pg0);
+        s1 = scale_of(1, pg1);
+      }
+#pragma unroll 1
+      for (int j = 0; ok && j < n; ++j) {
+        const int pg4 = page_of(j + 4);
+        float s2 = 1.f;
+        if (values) s2 = scale_of(j + 2, pg2);
+        const Place<kStages> at((unsigned)(ring + (values ? pt.place_v(j) : pt.place_k(j))) % (2u * kStages));
+        const int stage = at.stage();
+        if (values) {
+          wait(&m.sc_empty[slot], slot_parity, 0xB31);
+          const float least = pow2(MOE_KV8_MIN_EXP), most = pow2(MOE_KV8_MAX_EXP);
+          if (!(s0 >= least && s0 <= most)) {
+            report_error(a.err, ERR_CHECK, 0xB33);
+            s0 = s0 > most ? most : least;
+          }
+          float* sc = scale_slots + slot * 3 * kScaleBlocks + (lane & 7);
+          if (lane < 8) sc[0] = s0;
+          if (lane >= 8 && lane < 16) {
+            const uint32_t bits = __float_as_uint(s0);
+            const float l = bits & 0x7fffffu ? log2f(s0) : (float)((int)(bits >> 23) - 127);
+            sc[kScaleBlocks] = l + kBase;
+            sc[2 * kScaleBlocks] = 1.f / s0;
+          }
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&m.sc_full[slot]);
+          if (++slot == kScaleSlots) {
+            slot = 0;
+            slot_parity ^= 1u;
+          }
+        }
+        wait(&m.empty[stage], at.parity() ^ 1u, 0xB30);
+        if (ok) {
+          const uint32_t wanted = __ballot_sync(0xffffffffu, pg0 >= 0);
+          if (lane == 0) mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim);
+          __syncwarp();
+          const int row = page > kTile ? pt.tile(j) * kTile & (page - 1) : 0;
+          if (pg0 >= 0)
+            tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, walk.h, row, pg0, &m.full[stage],
+                           policy);
+          __syncwarp();
+        }
+        pg0 = pg1;
+        pg1 = pg2;
+        pg2 = pg3;
+        pg3 = pg4;
+        s0 = s1;
+        s1 = s2;
+      }
+      ring = (ring + 2 * n) % (2 * kStages);
+    }
+    // After a lost wait the tiles still in flight must land before the CTA
+    // ends; without one, every tile has been waited for by the MMA warp.
+    if (!ok) {
+#pragma unroll 1
+      for (int i = 0; i < 2 * 500 * kStages; ++i) try_longer(&m.full[i / 1000], i & 1);
+    }
+  } else if (warp == -3) {
+    // ---------------------------------------------------------------- MMA --
+    constexpr int kSteps = kDim / 32;
+    constexpr uint32_t kRowHi = umma::kDescHi8<kDim>, kPHi = umma::kDescHi8<128>;
+    constexpr uint32_t kOne = 1u << 16;                // (a K-major tile has no other distance)
+    const uint32_t ring_at = (smem_addr(smem) + Z::kOffRing) >> 4;
+    const uint32_t q_at = smem_addr(smem) >> 4;
+    const uint32_t p_at = (smem_addr(smem) + Z::kOffP) >> 4;
+    constexpr uint32_t kNextP = (kTile * 128u >> 4) << 16;  // the next 128 columns of P
+    int slot = 0, sc_slot = 0;
+    uint32_t q_parity = 0;
+    auto commit = [&](uint64_t* bar) {                 // arrives when the MMAs so far are done
+      if (ok) umma::commit_elect(bar);
+    };
+    while (walk.next(&pt)) {
+      const int n = pt.n, streams = pt.streams, cols = pt.wide * kNum;
+      const int pitch = pt.wide * Z::kWide;            // columns between streams
+      const uint32_t id_s = umma::idesc_e4m3(kTile, cols, false);
+      const uint32_t id_o = umma::idesc_e4m3(kDim, cols, true);
+      // S may be laid out anew once the last scores of every stream are read
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) wait(&m.s_empty[s], count_of(counts, s) & 1u ^ 1u, 0xB41);
+      wait(&m.q_full[slot], q_parity, 0xB42);
+      if (n == 0) {
+        if (ok && lane == 0) mbar_arrive(&m.q_empty[slot]);
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int j = -streams; j < n; ++j) {
+        const int s = (j + streams) & (streams - 1);
+        if (j + streams < n) {                         // the scores of tile j + streams
+          const int i = j + streams;
+          const uint32_t k = count_of(counts, s) + (uint32_t)(i >> pt.shift);
+          const Place<kStages> at((unsigned)(ring + pt.place_k(i)) % (2u * kStages));
+          wait(&m.full[at.stage()], at.parity(), 0xB43);
+          wait(&m.s_empty[s], k & 1u ^ 1u, 0xB44);
+          umma::fence_after_sync();
+          if (ok)
+            umma::mma_e4m3<kSteps, kRowHi, kRowHi, 2, 2>(
+                tmem + s * pitch, (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
+                (q_at + slot * (Z::kQBytes >> 4)) & 0x3fffu | kOne, id_s, 0u);
+          commit(&m.s_full[s]);
+          commit(&m.empty[at.stage()]);
+          if (i + 1 == n) commit(&m.q_empty[slot]);
+        }
+        if (j >= 0) {                                  // Oᵀ (+)= Vᵀ · Pᵀ of tile j
+          const uint32_t k = count_of(counts, s) + (uint32_t)(j >> pt.shift);
+          const Place<kStages> at((unsigned)(ring + pt.place_v(j)) % (2u * kStages));
+          wait(&m.full[at.stage()], at.parity(), 0xB45);
+          wait(&m.p_full[s], k & 1u, 0xB46);
+          umma::fence_after_sync();
+          const uint32_t first = s * pitch;            // column of P
+          if (ok)
+            umma::mma_e4m3<4, kRowHi, kPHi, (32 * kDim >> 4), (32 * 128 >> 4)>(
+                tmem + Z::kColO + s * pitch,
+                (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
+                (p_at + (first >> 7) * (kTile * 128 >> 4) + ((first & 127u) >> 4)) & 0x3fffu |
+                    kNextP,
+                id_o, j >= streams ? 1u : 0u);
+          commit(&m.p_done[s]);
+          commit(&m.empty[at.stage()]);
+          commit(&m.sc_empty[sc_slot]);
+          if (++sc_slot == kScaleSlots) sc_slot = 0;
+        }
+      }
+      counts = add_counts(counts, pt);
+      ring = (ring + 2 * n) % (2 * kStages);
+      if (slot) q_parity ^= 1u;
+      slot ^= 1;
+    }
+    // Every MMA, and every arrival that hangs on one, is done before tensor
+    // memory is released.
+    umma::commit_elect(&m.drain);
+#pragma unroll 1
+    for (int i = 0; i < kTries && !try_longer(&m.drain, 0); ++i) {
+    }
+    __syncwarp();
+  } else if (warp == -1) {
+    // ------------------------------------------------------------ queries --
+    constexpr int kMine = kDim / 32;                   // columns of a lane
+    const float to_log2 = a.scale * kLog2e;
+    int slot = 0;
+    uint32_t q_parity = 1;
+    while (walk.next(&pt)) {
+      wait(&m.q_empty[slot], q_parity, 0xB60);
+      unsigned char* q = smem + slot * Z::kQBytes;
+      const uint16_t* from = static_cast<const uint16_t*>(a.q) +
+                             (int64_t)pt.it.row0 * a.q_token_stride +
+                             (int64_t)walk.h * a.group * a.q_head_stride + lane * kMine;
+      constexpr int kAhead = 8;                        // rows loaded at once
+#pragma unroll 1
+      for (int r0 = 0; r0 < pt.rows; r0 += kAhead) {
+        uint32_t x[kAhead][kMine / 2];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int r = min(r0 + i, pt.rows - 1);
+          const int t = r / a.group, g = r - t * a.group;
+          const uint16_t* at = from + t * a.q_token_stride + g * a.q_head_stride;
+          if constexpr (kMine == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+            x[i][0] = v.x;
+            x[i][1] = v.y;
+          } else {
+            x[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int r = r0 + i;
+          float v[kMine];
+          float top = 0.f;
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) {
+            const uint32_t w = x[i][c / 2] >> (16 * (c & 1));
+            v[c] = kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
+                        : __uint_as_float(w << 16);
+            top = fmaxf(top, fabsf(v[c]));
+            if (v[c] != v[c]) top = INFINITY;
+          }
+          // 448 · 2^e is the row's largest size or up to twice it
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          const uint32_t bits = __float_as_uint(top);
+          int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+          e = min(max(e, -120), 120);
+          const float inv = pow2(-e);
+          if (r < pt.rows) {
+#pragma unroll
+            for (int c = 0; c < kMine; c += 2) {
+              uint16_t num[kNum];
+              numbers_of<kNum>(v[c] * inv, v[c + 1] * inv, num);
+#pragma unroll
+              for (int k = 0; k < kNum; ++k)
+                *reinterpret_cast<uint16_t*>(
+                    q + swizzled<kDim>(k * pt.wide + r, lane * kMine + c)) = num[k];
+            }
+            // (a row with NaN or an infinity has NaN for its factor)
+            if (lane == 0)
+              qscale[slot * kRows + r] = top <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&m.q_full[slot]);
+      if (slot) q_parity ^= 1u;
+      slot ^= 1;
+    }
+  } else {
+    // ------------------------------------------------------------ softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (a.clear) clear_rows<kDim>(a);                  // while the first tiles are on their way
+    const int g = warp >> 2, quarter = warp & 3;       // group, and the warp's quarter of a tile
+    const int kt = threadIdx.x & 127;                  // key of the tile, TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)quarter << 21);  // 32 · quarter in the upper half
+    float* ref = refs + g * 16;                        // −m of the group's columns
+    float* mine = stat + g * 64 + quarter * 16;
+    auto group_sync = [&]() {
+      asm volatile("bar.sync %0, 128;" ::"r"(3 + g) : "memory");
+    };
+    auto all_sync = [&]() { asm volatile("bar.sync 2, 512;" ::: "memory"); };
+    int sc_first = 0, slot = 0;                        // slots of the part's first scales, its queries
+    uint32_t sc_parity = 0, q_parity = 0;
+    bool open = false;                                 // the last part does not end its item
+    while (walk.next(&pt)) {
+      const Item& it = pt.it;
+      const int n = pt.n, streams = pt.streams, per = 4 / streams;  // groups of a stream
+      const int s = g / per, gl = g - s * per;
+      const int c0 = 16 * gl;                          // the group's first query row
+      const bool active = c0 < pt.wide;
+      const int pitch = pt.wide * Z::kWide;
+      const uint32_t s_addr = lanes + s * pitch + c0;
+      const uint32_t o_addr = lanes + Z::kColO + s * pitch + c0;
+      // a stream's barriers count 16: each of its 4·per warps arrives for 4 / per
+      const uint32_t weight = streams;
+      auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
+                           smem_addr(bar)),
+                       "r"(weight)
+                       : "memory");
+      };
+      // rows that do not exist stay out of every vote
+      if (quarter == 0 && lane < 16) ref[lane] = c0 + lane < pt.rows ? INFINITY : -INFINITY;
+      group_sync();
+      wait(&m.q_full[slot], q_parity, 0xB50);
+      const float* factor = qscale + slot * kRows + c0;
+      uint64_t sums[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sums[c] = 0;
+      uint32_t k = count_of(counts, s);
+      int sc_at = sc_first + s;                        // the next tile's scales
+      uint32_t sc_p = sc_parity;
+      if (sc_at >= kScaleSlots) sc_at -= kScaleSlots, sc_p ^= 1u;
+#pragma unroll 1
+      for (int j = s; j < n; j += streams, ++k) {
+        const int key0 = pt.tile(j) * kTile, key = key0 + kt;
+        wait(&m.s_full[s], k & 1u, 0xB51);
+        // (a lost wait leaves the sums wrong, and the barriers in step)
+        if (!active) {
+          arrive(&m.s_empty[s]);
+          wait(&m.p_done[s], k & 1u ^ 1u, 0xB52);
+        }
+        const bool edge = tile_some_see(a, it, key0) || key0 + kTile > it.hi ||
+                          (key0 < it.lo && key0 + kTile > it.sk);
+        // rows of the item that see the key: [n0, n1)
+        int n0 = 0, n1 = kRows;
+        if (edge) {
+          const long long g0 = (long long)key - it.pos0;
+          n0 = (int)min(max(g0, 0ll), (long long)it.ntok) * a.group;
+          n1 = it.ntok * a.group;
+          if (a.window > 0 && key >= a.sinks)
+            n1 = (int)min(max(g0 + a.window, 0ll), (long long)it.ntok) * a.group;
+        }
+        if (active) {
+          umma::fence_after_sync();
+          uint32_t x[16], y[kNum - 1][16];
+          umma::ld_x16(s_addr, x);
+#pragma unroll
+          for (int i = 1; i < kNum; ++i) umma::ld_x16(s_addr + i * pt.wide, y[i - 1]);
+          wait(&m.sc_full[sc_at], sc_p, 0xB53);
+          const float* sc = scale_slots + sc_at * 3 * kScaleBlocks + (kt >> 4);
+          sc_at += streams;
+          if (sc_at >= kScaleSlots) sc_at -= kScaleSlots, sc_p ^= 1u;
+          const float ks = sc[0], lv = sc[kScaleBlocks], iv = sc[2 * kScaleBlocks];
+          umma::wait_ld();
+          umma::fence_before_sync();
+          arrive(&m.s_empty[s]);
+          // q · K
+#pragma unroll
+          for (int i = 1; i < kNum; ++i) {
+            const uint64_t unit = pair_f(number_unit(i), number_unit(i));
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              float lo, hi;
+              split(fma2(pair(y[i - 1][c], y[i - 1][c + 1]), unit, pair(x[c], x[c + 1])), &lo, &hi);
+              x[c] = __float_as_uint(lo);
+              x[c + 1] = __float_as_uint(hi);
+            }
+          }
+          const uint64_t ks2 = pair_f(ks, ks), lv2 = pair_f(lv, lv), iv2 = pair_f(iv, iv);
+          const uint32_t seen = low_bits(n1 - c0) & ~low_bits(n0 - c0);
+          float t[16];
+          // t = q·K·factor·ks + log2 vs + 7 − m, −inf for what a row does not see
+          auto weights = [&]() {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(factor + c);
+              const float4 r = *reinterpret_cast<const float4*>(ref + c);
+              split(fma2(mul2(pair(x[c], x[c + 1]), pair_f(f.x, f.y)), ks2,
+                         add2(lv2, pair_f(r.x, r.y))), &t[c], &t[c + 1]);
+              split(fma2(mul2(pair(x[c + 2], x[c + 3]), pair_f(f.z, f.w)), ks2,
+                         add2(lv2, pair_f(r.z, r.w))), &t[c + 2], &t[c + 3]);
+            }
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) t[c] = seen >> c & 1u ? t[c] : -INFINITY;
+            }
+          };
+          weights();
+          float top = fmaxf(t[0], t[1]);
+#pragma unroll
+          for (int c = 2; c < 16; c += 2) top = max3(top, t[c], t[c + 1]);
+          int grown = top > kBase + kGrow;
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\t"
+              "setp.ne.s32 p, %0, 0;\n\t"
+              "bar.red.or.pred q, %1, 128, p;\n\t"
+              "selp.s32 %0, 1, 0, q;\n\t}"
+              : "+r"(grown)
+              : "r"(3 + g)
+              : "memory");
+          if (grown) {
+            // the tile's largest t of every column; the references that it passes
+            // follow it, and with them what has been summed up so far
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float f = factor[c];
+              float v = fmaf(__uint_as_float(x[c]) * f, ks, lv - kBase);
+              if (edge && !(seen >> c & 1u)) v = -INFINITY;
+              v = warp_max(v);
+              if (lane == c) mine[c] = v;
+            }
+            group_sync();
+            const int col = lane & 15;
+            float best = stat[g * 64 + col];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) best = fmaxf(best, stat[g * 64 + w * 16 + col]);
+            const float was = -ref[col];                // (+inf: a row that does not exist)
+            const bool follows = best > was + kGrow;
+            const float keep = follows ? exp2_approx(was - best) : 1.f;
+            group_sync();
+            if (quarter == 0 && lane < 16 && follows) ref[lane] = -best;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const uint64_t by = pair_f(__shfl_sync(0xffffffffu, keep, c),
+                                         __shfl_sync(0xffffffffu, keep, c + 1));
+              sums[c / 2] = mul2(sums[c / 2], by);
+            }
+            if (j >= streams) {
+              wait(&m.p_done[s], k & 1u ^ 1u, 0xB54);
+              umma::fence_after_sync();
+#pragma unroll 1
+              for (int i = 0; i < kNum; ++i) {
+                uint32_t o[16];
+                umma::ld_x16(o_addr + i * pt.wide, o);
+                umma::wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                  o[c] = __float_as_uint(__uint_as_float(o[c]) *
+                                         __shfl_sync(0xffffffffu, keep, c));
+                umma::st_x16(o_addr + i * pt.wide, o);
+              }
+              umma::wait_st();
+              umma::fence_before_sync();
+            }
+            group_sync();
+            weights();
+          }
+          // weights, their sum, and their numbers
+          uint32_t num[kNum][4];
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float p0 = exp2_approx(t[c]), p1 = exp2_approx(t[c + 1]);
+            sums[c / 2] = fma2(pair_f(p0, p1), iv2, sums[c / 2]);
+            uint16_t v[kNum];
+            numbers_of<kNum>(p0, p1, v);
+#pragma unroll
+            for (int i = 0; i < kNum; ++i)
+              num[i][c / 4] = c & 2 ? num[i][c / 4] | (uint32_t)v[i] << 16 : v[i];
+          }
+          // the product with the weights before them has read those
+          wait(&m.p_done[s], k & 1u ^ 1u, 0xB55);
+#pragma unroll
+          for (int i = 0; i < kNum; ++i) {
+            const uint32_t col = s * pitch + i * pt.wide + c0;
+            *reinterpret_cast<uint4*>(smem + Z::kOffP + (col >> 7) * (kTile * 128) +
+                                      swizzled<128>(kt, col & 127u)) =
+                make_uint4(num[i][0], num[i][1], num[i][2], num[i][3]);
+          }
+        }
+        if (edge) {
+          // the stream's groups share the tile's rows of V: what no row of the item
+          // sees becomes zeros, NaN that some see and others do not is taken out
+          const Place<kStages> at((unsigned)(ring + pt.place_v(j)) % (2u * kStages));
+          wait(&m.full[at.stage()], at.parity(), 0xB56);
+          const bool none = key >= it.hi || (key < it.lo && key >= it.sk);
+          if (ok && (none || some_see(a, it.pos0, it.hi, key))) {
+            unsigned char* v = smem + Z::kOffRing + at.stage() * Z::kTileBytes + kt * kDim;
+#pragma unroll 1
+            for (int c = gl; c < kDim / 16; c += per) {
+              uint4* to = reinterpret_cast<uint4*>(v + c * 16);
+              if (none) {
+                *to = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              uint32_t w[4] = {to->x, to->y, to->z, to->w};
+              if (!(nan_bytes(w[0]) | nan_bytes(w[1]) | nan_bytes(w[2]) | nan_bytes(w[3]))) continue;
+              const int d0 = (int)(swizzled<kDim>(kt, c * 16) - kt * kDim);  // its first column
+#pragma unroll 1
+              for (int i = 0; i < 16; ++i) {
+                if (!(nan_bytes(w[i >> 2]) >> (8 * (i & 3)) & 0x80u)) continue;
+                w[i >> 2] &= ~(0xffu << (8 * (i & 3)));
+                const unsigned long long rows =
+                    (n1 >= 64 ? ~0ull : (1ull << n1) - 1) & ~(n0 >= 64 ? ~0ull : (1ull << n0) - 1);
+                atomicOr(p.spoiled + blockIdx.x * 128 + d0 + i, n0 < n1 ? rows : 0ull);
+                *static_cast<volatile int*>(&m.spoils) = 1;
+              }
+              *to = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        arrive(&m.p_full[s]);
+      }
+      // ---- results out
+      // the sums over keys: 16 columns of 32 lanes, by halves
+      {
+        float v[16];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) split(sums[c], &v[2 * c], &v[2 * c + 1]);
+#pragma unroll
+        for (int half = 8; half > 0; half >>= 1) {
+          const bool up = lane & (2 * half);
+#pragma unroll
+          for (int i = 0; i < half; ++i) {
+            const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * half);
+          }
+        }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        if (!(lane & 1)) mine[lane >> 1] = v[0];
+      }
+      if (n > s) wait(&m.p_done[s], k & 1u ^ 1u, 0xB57);  // the stream's last product
+      all_sync();
+      umma::fence_after_sync();
+      const bool spoils = *static_cast<volatile int*>(&m.spoils);
+      // a thread has column d of V, and its group a quarter of the rows (of one
+      // stream: the group's own)
+      const int d = kDim == 128 ? kt : quarter * 16 + (lane & 15);
+      const bool valid = kDim == 128 || lane < 16;
+      const int take = streams == 1 ? 16 : streams == 2 ? 8 : 4, from = g * take;
+      const uint32_t o_from = lanes + Z::kColO + from;
+      float* part = p.part + (size_t)(2 * blockIdx.x + (pt.ends ? 0 : 1)) * slot_floats(kDim);
+      int tok = from / a.group, head = from - tok * a.group;
+#pragma unroll 1
+      for (int i = 0; ok && i < take && from + i < pt.rows; i += 4) {
+        float o[4], top[4], sum[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          o[c] = sum[c] = 0.f;
+          top[c] = -INFINITY;
+        }
+        const int at = (from + i) & 15, first = (from + i) >> 4;
+#pragma unroll 1
+        for (int z = 0; z < streams; ++z)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], -refs[(z * per + first) * 16 + at + c]);
+#pragma unroll 1
+        for (int z = 0; z < streams && z < n; ++z) {
+          uint32_t w[kNum][4];
+#pragma unroll
+          for (int e = 0; e < kNum; ++e) umma::ld_x4(o_from + z * pitch + e * pt.wide + i, w[e]);
+          umma::wait_ld();
+          const int gz = z * per + first;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float l = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) l += stat[gz * 64 + e * 16 + at + c];
+            const float was = -refs[gz * 16 + at + c];
+            // (a stream that saw none of the row's keys has zeros, or sums of NaN)
+            const float by = top[c] == -INFINITY ? 1.f : exp2_approx(was - top[c]);
+            float v = __uint_as_float(w[0][c]);
+#pragma unroll
+            for (int e = 1; e < kNum; ++e)
+              v = fmaf(__uint_as_float(w[e][c]), number_unit(e), v);
+            o[c] = fmaf(v, by, o[c]);
+            sum[c] = fmaf(l, by, sum[c]);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int r = from + i + c;
+          if (r < pt.rows && valid) {
+            if (spoils && (__ldcg(p.spoiled + blockIdx.x * 128 + d) >> r & 1ull)) o[c] = NAN;
+            if (pt.whole) {
+              const uint32_t v = round16<kF16>(o[c] * inverse(sum[c]), 0.f);
+              (static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
+               (int64_t)(walk.h * a.group + head) * a.out_head_stride)[d] = (uint16_t)v;
+            } else {
+              part[r * kDim + d] = o[c];
+              if (d == 0) {
+                part[kRows * kDim + r] = top[c];
+                part[kRows * kDim + kRows + r] = sum[c];
+              }
+            }
+          }
+          if (++head == a.group) {
+            head = 0;
+            ++tok;
+          }
+        }
+      }
+      open = !pt.ends;
+      umma::fence_before_sync();
+      // O, references and sums have been read before any stream goes on
+      all_sync();
+      if (threadIdx.x == 128) mbar_arrive(&m.q_empty[slot]);
+      if (spoils) {
+        if (threadIdx.x < 256) p.spoiled[blockIdx.x * 128 + threadIdx.x - 128] = 0;
+        if (threadIdx.x == 128) m.spoils = 0;
+        all_sync();
+      }
+      counts = add_counts(counts, pt);
+      ring = (ring + 2 * n) % (2 * kStages);
+      if (slot) q_parity ^= 1u;
+      slot ^= 1;
+      const unsigned upto = (unsigned)(sc_first + n);
+      sc_first = (int)(upto % kScaleSlots);
+      sc_parity ^= upto / kScaleSlots & 1u;
+    }
+    // The last part is left to the CTA that ends its item, and an item that began
+    // in earlier ranges joined, when all of the range's results are there.
+    if (open || m.start.joins) {
+      all_sync();
+      unsigned long long before = 0;                   // (used at the end: it takes a while)
+      if (open && threadIdx.x == 128) before = exchange(p.left + blockIdx.x, p.call);
+      if (m.start.joins) join_parts<kDim, kF16>(p, m.start, lost);
+      if (before == given_up(p.call)) p.left[blockIdx.x] = 0ull;
+    }
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && m.lost) report_error(a.err, ERR_TIMEOUT, m.lost);
+  if (warp == -3) umma::tmem_dealloc(tmem, Z::kCols);
 }
+
+template <int kDim, int kNum>
+cudaError_t launch_t(Params& p, int ctas, cudaStream_t stream) {
+  using Z = Sizes<kDim, kNum>;
+  auto* kernel = attend8_kernel<kDim, kNum>;
+  // a bit for each device whose kernel may have that much shared memory (two
+  // threads that find it missing both ask for it, to the same effect)
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const unsigned long long bit = 1ull << (dev & 63);     // call_device takes devices below 64
+  if (e == cudaSuccess && !(configured.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Z::kSmem);
+    if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_release);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(ctas), dim3(kThreads), Z::kSmem, stream, p);
+}
+
+constexpr size_t kLeftBytes = (kMaxCtas * sizeof(unsigned long long) + 255) / 256 * 256;
+constexpr size_t kSpoiledBytes = kMaxCtas * 128 * sizeof(unsigned long long);
 
 }  // namespace
 
-size_t attend8_workspace_bytes(int) { return 256; }
+size_t attend8_workspace_bytes(int head_dim) {
+  return kLeftBytes + kSpoiledBytes + 2 * kMaxCtas * slot_floats(head_dim) * sizeof(float);
+}
 
-cudaError_t launch_attend8(const Attend8Args& a, int, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.n_tokens * a.n_heads;
-  const dim3 grid((unsigned)((rows + 7) / 8));
-  const int ps = 31 - __builtin_clz(a.cache.page_size), bs = 31 - __builtin_clz(a.cache.block);
-  auto* kernel = a.cache.head_dim == 128
-                     ? (a.f16 ? attend8_kernel<128, true> : attend8_kernel<128, false>)
-                     : (a.f16 ? attend8_kernel<64, true> : attend8_kernel<64, false>);
-  return launch_pdl(kernel, grid, dim3(256), 0, stream, a, ps, bs);
+cudaError_t launch_attend8(const Attend8Args& a, int num_sms, cudaStream_t stream) {
+  Params p;
+  memset(&p, 0, sizeof p);
+  p.a = a;
+  const moe_kv8_cache& c = a.cache;
+  p.page_shift = 31 - __builtin_clz(c.page_size);
+  p.blocks_shift = 31 - __builtin_clz(c.page_size / c.block);
+  p.tpt = p.block = kRows / a.group;
+  char* ws = static_cast<char*>(a.workspace);
+  p.left = reinterpret_cast<unsigned long long*>(ws);
+  p.spoiled = reinterpret_cast<unsigned long long*>(ws + kLeftBytes);
+  p.part = reinterpret_cast<float*>(ws + kLeftBytes + kSpoiledBytes);
+  p.call = call_number();
+  // [page][row][head][dim]: a box is a head's rows of a page, or 128 of them
+  const cuuint64_t dims[4] = {(uint64_t)c.head_dim, (uint64_t)c.n_kv_heads, (uint64_t)c.page_size,
+                            (uint64_t)c.n_pages};
+  const cuuint64_t strides[3] = {(uint64_t)c.head_stride, (uint64_t)c.token_stride,
+                               (uint64_t)c.page_stride};
+  const uint32_t box[4] = {(uint32_t)c.head_dim, 1,
+                           (uint32_t)(c.page_size < kTile ? c.page_size : kTile), 1};
+  const uint32_t steps[4] = {1, 1, 1, 1};
+  const EncodeFn encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  auto encode_maps = [&] {
+    auto map = [&](CUtensorMap* to, const void* at) {
+      return encode(to, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(at), dims, strides, box,
+                    steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(&p.kmap, c.k) && map(&p.vmap, c.v);
+  };
+  if (!encode_maps()) {
+    // a host thread that has called nothing but this library has no context yet,
+    // and encoding, a driver's call, makes none
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    if (!encode_maps()) return cudaErrorInvalidValue;
+  }
+  const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  if (c.head_dim == 128)
+    return a.f16 ? launch_t<128, 3>(p, ctas, stream) : launch_t<128, 2>(p, ctas, stream);
+  return a.f16 ? launch_t<64, 3>(p, ctas, stream) : launch_t<64, 2>(p, ctas, stream);
 }
 
 }  // namespace moe

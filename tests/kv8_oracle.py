@@ -131,13 +131,15 @@ def attend(q, k, v, vs, q_start, kv_len, table, scale, window, sinks):
     [pages][rows][heads][D] with vs [pages][rows][heads] the scale of each row's
     values, both float64 [T][Hq][D], on q's device.
 
-    bound: a kernel may hold a query as a sum of e4m3 numbers, exact but for what
-    is below 2^-22 (two numbers) of its row's largest, and its weights as two (bf16)
-    or three (fp16), of which the first is off by half a step, 2^-4 of the weight or
-    2^-10 of a 2^7th of the largest weight, and each further one by 2^-4 of what
-    the one before left: with steps that go on 2^4 smaller, a weight w is off by at
-    most 2^-8 w + 2^-21 (2^-12 w + 2^-25) where 1 is the largest of w · scale. The
-    result is rounded to the type of q. Sums are fp32 (a score is off by at most
+    bound: a kernel may hold a query, and its weights, as sums of two (bf16) or three
+    (fp16) e4m3 numbers, each 16 times what the ones before it left, rounded. A
+    number above 2^-6 is off by at most 2^-4 of itself, one below by 2^-10.
+    Queries are scaled so that their row's largest is above 224: 8 (11) bits are
+    exact, but for what is below 2^-10 · 16^-1 (16^-2), 2^-21.8 (2^-25.8) of the largest.
+    Weights are scaled so that the largest w · vs is 2^7 or more, and rounded to
+    fp16 before (2^-11 of themselves): off by 2^-8 + 2^-11 (2^-11 + 2^-12) of themselves
+    and 2^-14 · 2^-7 (2^-18 · 2^-7) of the largest.
+    The result is rounded to the type of q. Sums are fp32 (a score is off by at most
     (D + 8)·2^-22·scale·Σ|q k|: the tensor cores add e4m3 products with 2^-22 of
     the sum of their sizes, which was measured; that moves a weight by as much,
     twice; statistics and exponentials 2^-20; sums over keys 2^-20)."""
@@ -145,8 +147,9 @@ def attend(q, k, v, vs, q_start, kv_len, table, scale, window, sinks):
     page, H = k.shape[1], k.shape[2]
     per = Hq // H
     f16 = q.dtype == torch.float16
-    eps, w_rel, w_abs = half_step(q.dtype), 2.0 ** (-11 if f16 else -8), 2.0 ** (-25 if f16 else -21)
-    q_abs = 2.0 ** (-26 if f16 else -22)
+    eps, w_rel, w_abs, q_abs = half_step(q.dtype), 2.0 ** -8 + 2.0 ** -11, 2.0 ** -21, 2.0 ** -21.8
+    if f16:
+        w_rel, w_abs, q_abs = 2.0 ** -11 + 2.0 ** -12, 2.0 ** -25, 2.0 ** -25.8
     tiny = 2.0 ** -25 if f16 else 2.0 ** -134
     out = torch.zeros((T, Hq, D), dtype=torch.float64, device=q.device)
     bound = torch.zeros((T, Hq, D), dtype=torch.float64, device=q.device)
