@@ -40,12 +40,12 @@
 // own sums, joined at the end.
 //
 // Warps (one CTA per SM):
-//   0      TMA: key tiles into a ring, a box per page
+//   0      TMA: key tiles into a ring, a box per page; the tiles' scales
 //   1      MMA issue
-//   2      TMA: value tiles into the same ring; the tiles' scales
-//   3      query rows into e4m3 numbers, the next item's ahead
+//   2      TMA: value tiles into the same ring
+//   3      query rows into shared memory, the next item's ahead
 //   4-19   softmax, four groups of four warps: 16 columns of a tile each, or the
-//          tiles of a stream
+//          tiles of a stream; and the next item's queries into e4m3 numbers
 //
 // Values that are not finite (NaN; e4m3 has no infinities). A weight of 0 times
 // NaN is NaN: rows of V that no row of the item sees are cleared, and NaN in rows
@@ -68,12 +68,12 @@ constexpr int kRows = 64;         // query rows of an item, at most
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 // What an item costs beside its tiles when the work is cut, in tiles.
 constexpr int kItemUnits = 3;
-constexpr float kBase = 7.f;      // weights are held 2^7 larger
-constexpr float kGrow = 1.5f;     // m follows growth beyond this (powers of two)
+constexpr float kBase = 4.f;      // weights are held 2^4 larger
+constexpr float kGrow = 4.5f;     // m follows growth beyond this (powers of two)
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
 // the 4 others leave 64 (4·104 + 64 = 5·96).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-constexpr int kScaleSlots = 6;    // tiles whose scales are there
+constexpr int kScaleSlots = 8;    // tiles whose scales are there
 constexpr int kScaleBlocks = kTile / 16;
 
 // kDim: columns of a head; kNum: e4m3 numbers of a query's element or a weight.
@@ -81,10 +81,12 @@ template <int kDim, int kNum>
 struct Sizes {
   static constexpr int kWide = kNum == 2 ? 2 : 4;  // columns set aside for a row's numbers
   static constexpr int kTileBytes = kTile * kDim;
-  static constexpr int kQBytes = kRows * kNum * kDim;
+  static constexpr int kQBytes = kRows * kNum * kDim;  // an item's queries as numbers
+  static constexpr int kRawBytes = kRows * kDim * 2;   // and the next one's as they come
   static constexpr int kPBytes = kTile * kRows * kWide;  // in 128-byte columns, kTile rows each
   static constexpr int kStages = kDim == 64 ? 16 : kNum == 2 ? 11 : 9;
-  static constexpr int kOffP = 2 * kQBytes;
+  static constexpr int kOffRaw = kQBytes;
+  static constexpr int kOffP = kOffRaw + kRawBytes;
   static constexpr int kOffRing = kOffP + kPBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
   static constexpr int kMiscBytes = 3072;
@@ -205,7 +207,8 @@ MOE_DEV uint32_t add_counts(uint32_t counts, const Part& pt) {
 template <int kStages>
 struct Misc {
   uint64_t full[kStages], empty[kStages];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t raw_full, raw_empty;  // queries as they come
+  uint64_t q_full;               // and as numbers
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
   uint64_t s_full[4], s_empty[4], p_full[4], p_done[4];  // of a stream
   uint64_t drain;
@@ -213,14 +216,15 @@ struct Misc {
   long long part[8];
   uint32_t tmem;
   int lost;
+  int raw_rows, raw_wide;  // of the queries as they come; no rows: there are no more
   // NaN has been noted in the CTA's `spoiled` for the present item
   int spoils;
 };
 constexpr int kOffRef = 704;                    // [4 groups][16] −m of a column
 constexpr int kOffQScale = kOffRef + 256;       // [2][64] a row's factor
 constexpr int kOffStat = kOffQScale + 512;      // [4 groups][4 warps][16]
-constexpr int kOffScale = kOffStat + 1024;      // [slots][3][8 blocks]: ks, log2 vs + 7, 1 / vs
-static_assert(kOffScale + kScaleSlots * 3 * kScaleBlocks * 4 <= 3072, "misc words");
+constexpr int kOffScale = kOffStat + 1024;      // [slots][2][8 blocks]: ks, log2 vs + kBase
+static_assert(kOffScale + kScaleSlots * 2 * kScaleBlocks * 4 <= 3072, "misc words");
 
 // ln 2's reciprocal: scores are kept in powers of two.
 constexpr float kLog2e = 1.4426950408889634f;
@@ -230,6 +234,13 @@ template <int kRow>
 MOE_DEV uint32_t swizzled(uint32_t row, uint32_t at) {
   const uint32_t o = row * kRow + at;
   return o ^ (o >> 3 & (kRow == 128 ? 0x70u : 0x30u));
+}
+
+// A wait that does not end at once (see wait_or_abort), kept out of the places
+// where it stands.
+MOE_DEV bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* lost,
+                                         int site) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, lost, site));
 }
 
 // Two values' e4m3 numbers: each is 16 times what the ones before it left. (In
@@ -372,10 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&m.q_full[i], 1);
-      mbar_init(&m.q_empty[i], 2);             // the products with it, and its factors' readers
-    }
+    mbar_init(&m.raw_full, 33);                // its lanes, with their copies, and its rows' number
+    mbar_init(&m.raw_empty, 16);
+    mbar_init(&m.q_full, 16);
     for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(&m.sc_full[i], 1);
       mbar_init(&m.sc_empty[i], 1);
@@ -411,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   volatile int* lost = &m.lost;
   bool ok = true;  // no wait of this role has been lost
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-    ok = __all_sync(0xffffffffu, ok && wait_or_abort(bar, parity, lost, site));
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+      ok = wait_longer(bar, parity, lost, site) && ok;
   };
   Part pt;
   Walker walk(p, m.start);
@@ -421,12 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   if (warp < 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == -4 || warp == -2) {
     // ------------------------------------------------------------ loaders --
-    const bool values = warp == -2;
+    const bool keys = warp == -4;
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
     const uint64_t policy = l2_evict_normal_policy();
-    const CUtensorMap* map = values ? &p.vmap : &p.kmap;
+    const CUtensorMap* map = keys ? &p.kmap : &p.vmap;
     const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
     int slot = 0;
     uint32_t slot_parity = 1;
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       // pages are asked for four tiles ahead, scales two
       int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3 = page_of(3);
       float s0 = 1.f, s1 = 1.f;
-      if (values) {
+      if (keys) {
         s0 = scale_of(0, pg0);
         s1 = scale_of(1, pg1);
       }
@@ -477,24 +488,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       for (int j = 0; ok && j < n; ++j) {
         const int pg4 = page_of(j + 4);
         float s2 = 1.f;
-        if (values) s2 = scale_of(j + 2, pg2);
-        const Place<kStages> at((unsigned)(ring + (values ? pt.place_v(j) : pt.place_k(j))) % (2u * kStages));
+        if (keys) s2 = scale_of(j + 2, pg2);
+        const Place<kStages> at((unsigned)(ring + (keys ? pt.place_k(j) : pt.place_v(j))) %
+                                (2u * kStages));
         const int stage = at.stage();
-        if (values) {
+        if (keys) {
           wait(&m.sc_empty[slot], slot_parity, 0xB31);
           const float least = pow2(MOE_KV8_MIN_EXP), most = pow2(MOE_KV8_MAX_EXP);
           if (!(s0 >= least && s0 <= most)) {
             report_error(a.err, ERR_CHECK, 0xB33);
             s0 = s0 > most ? most : least;
           }
-          float* sc = scale_slots + slot * 3 * kScaleBlocks + (lane & 7);
-          if (lane < 8) sc[0] = s0;
-          if (lane >= 8 && lane < 16) {
+          if (lane >= 8) {                             // (a power of two's is exact)
             const uint32_t bits = __float_as_uint(s0);
-            const float l = bits & 0x7fffffu ? log2f(s0) : (float)((int)(bits >> 23) - 127);
-            sc[kScaleBlocks] = l + kBase;
-            sc[2 * kScaleBlocks] = 1.f / s0;
+            s0 = (bits & 0x7fffffu ? log2f(s0) : (float)((int)(bits >> 23) - 127)) + kBase;
           }
+          if (lane < 16) scale_slots[slot * 2 * kScaleBlocks + lane] = s0;
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(&m.sc_full[slot]);
           if (++slot == kScaleSlots) {
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const uint32_t q_at = smem_addr(smem) >> 4;
     const uint32_t p_at = (smem_addr(smem) + Z::kOffP) >> 4;
     constexpr uint32_t kNextP = (kTile * 128u >> 4) << 16;  // the next 128 columns of P
-    int slot = 0, sc_slot = 0;
+    int sc_slot = 0;
     uint32_t q_parity = 0;
     auto commit = [&](uint64_t* bar) {                 // arrives when the MMAs so far are done
       if (ok) umma::commit_elect(bar);
@@ -550,11 +559,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       // S may be laid out anew once the last scores of every stream are read
 #pragma unroll 1
       for (int s = 0; s < 4; ++s) wait(&m.s_empty[s], count_of(counts, s) & 1u ^ 1u, 0xB41);
-      wait(&m.q_full[slot], q_parity, 0xB42);
-      if (n == 0) {
-        if (ok && lane == 0) mbar_arrive(&m.q_empty[slot]);
-        __syncwarp();
-      }
+      wait(&m.q_full, q_parity, 0xB42);
+      q_parity ^= 1u;
 #pragma unroll 1
       for (int j = -streams; j < n; ++j) {
         const int s = (j + streams) & (streams - 1);
@@ -568,10 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           if (ok)
             umma::mma_e4m3<kSteps, kRowHi, kRowHi, 2, 2>(
                 tmem + s * pitch, (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
-                (q_at + slot * (Z::kQBytes >> 4)) & 0x3fffu | kOne, id_s, 0u);
+                q_at & 0x3fffu | kOne, id_s, 0u);
           commit(&m.s_full[s]);
           commit(&m.empty[at.stage()]);
-          if (i + 1 == n) commit(&m.q_empty[slot]);
         }
         if (j >= 0) {                                  // Oᵀ (+)= Vᵀ · Pᵀ of tile j
           const uint32_t k = count_of(counts, s) + (uint32_t)(j >> pt.shift);
@@ -595,8 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       }
       counts = add_counts(counts, pt);
       ring = (ring + 2 * n) % (2 * kStages);
-      if (slot) q_parity ^= 1u;
-      slot ^= 1;
     }
     // Every MMA, and every arrival that hangs on one, is done before tensor
     // memory is released.
@@ -607,74 +610,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     __syncwarp();
   } else if (warp == -1) {
     // ------------------------------------------------------------ queries --
-    constexpr int kMine = kDim / 32;                   // columns of a lane
-    const float to_log2 = a.scale * kLog2e;
-    int slot = 0;
-    uint32_t q_parity = 1;
-    while (walk.next(&pt)) {
-      wait(&m.q_empty[slot], q_parity, 0xB60);
-      unsigned char* q = smem + slot * Z::kQBytes;
+    constexpr int kPieces = kDim / 8;                  // of a row, 16 bytes each
+    uint32_t parity = 1;
+    bool more = true;
+    while (more) {
+      more = walk.next(&pt);
+      wait(&m.raw_empty, parity, 0xB60);
+      parity ^= 1u;
+      const int rows = more && ok ? pt.rows : 0;
+      const uint32_t to = smem_addr(smem) + Z::kOffRaw;
       const uint16_t* from = static_cast<const uint16_t*>(a.q) +
                              (int64_t)pt.it.row0 * a.q_token_stride +
-                             (int64_t)walk.h * a.group * a.q_head_stride + lane * kMine;
-      constexpr int kAhead = 8;                        // rows loaded at once
+                             (int64_t)walk.h * a.group * a.q_head_stride;
 #pragma unroll 1
-      for (int r0 = 0; r0 < pt.rows; r0 += kAhead) {
-        uint32_t x[kAhead][kMine / 2];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int r = min(r0 + i, pt.rows - 1);
-          const int t = r / a.group, g = r - t * a.group;
-          const uint16_t* at = from + t * a.q_token_stride + g * a.q_head_stride;
-          if constexpr (kMine == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
-            x[i][0] = v.x;
-            x[i][1] = v.y;
-          } else {
-            x[i][0] = __ldg(reinterpret_cast<const uint32_t*>(at));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int r = r0 + i;
-          float v[kMine];
-          float top = 0.f;
-#pragma unroll
-          for (int c = 0; c < kMine; ++c) {
-            const uint32_t w = x[i][c / 2] >> (16 * (c & 1));
-            v[c] = kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
-                        : __uint_as_float(w << 16);
-            top = fmaxf(top, fabsf(v[c]));
-            if (v[c] != v[c]) top = INFINITY;
-          }
-          // 448 · 2^e is the row's largest size or up to twice it
-          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          const uint32_t bits = __float_as_uint(top);
-          int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-          e = min(max(e, -120), 120);
-          const float inv = pow2(-e);
-          if (r < pt.rows) {
-#pragma unroll
-            for (int c = 0; c < kMine; c += 2) {
-              uint16_t num[kNum];
-              numbers_of<kNum>(v[c] * inv, v[c + 1] * inv, num);
-#pragma unroll
-              for (int k = 0; k < kNum; ++k)
-                *reinterpret_cast<uint16_t*>(
-                    q + swizzled<kDim>(k * pt.wide + r, lane * kMine + c)) = num[k];
-            }
-            // (a row with NaN or an infinity has NaN for its factor)
-            if (lane == 0)
-              qscale[slot * kRows + r] = top <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
-          }
-        }
+      for (int i = lane; i < rows * kPieces; i += 32) {
+        const int r = i / kPieces, t = r / a.group;
+        const uint16_t* at = from + t * a.q_token_stride + (r - t * a.group) * a.q_head_stride +
+                             i % kPieces * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(at)
+                     : "memory");
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&m.q_full[slot]);
-      if (slot) q_parity ^= 1u;
-      slot ^= 1;
+      if (lane == 0) {
+        m.raw_rows = rows;
+        m.raw_wide = pt.wide;
+        mbar_arrive(&m.raw_full);
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                       smem_addr(&m.raw_full))
+                   : "memory");
     }
+    // the copies have landed when the last softmax warp has seen their barrier; a
+    // lost wait leaves that to this one
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -688,9 +655,67 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       asm volatile("bar.sync %0, 128;" ::"r"(3 + g) : "memory");
     };
     auto all_sync = [&]() { asm volatile("bar.sync 2, 512;" ::: "memory"); };
-    int sc_first = 0, slot = 0;                        // slots of the part's first scales, its queries
-    uint32_t sc_parity = 0, q_parity = 0;
+    int sc_first = 0, slot = 0;                        // slots of the part's first scales, factors
+    uint32_t sc_parity = 0, raw_parity = 0;
     bool open = false;                                 // the last part does not end its item
+    // The next item's queries into numbers: a warp takes every 16th row, divides it
+    // by the power of two that makes its largest size 224 to 448, and leaves that
+    // power with the scale as the row's factor.
+    auto next_queries = [&]() {
+      constexpr int kMine = kDim / 32;                 // columns of a lane
+      wait(&m.raw_full, raw_parity, 0xB58);
+      raw_parity ^= 1u;
+      const int rows = ok ? m.raw_rows : 0, wide = m.raw_wide;
+      const float to_log2 = a.scale * kLog2e;
+#pragma unroll 1
+      for (int r = warp; r < rows; r += 16) {
+        const unsigned char* at = smem + Z::kOffRaw + r * (kDim * 2) + lane * (kMine * 2);
+        uint32_t x[kMine / 2];
+        if constexpr (kMine == 4) {
+          const uint2 w = *reinterpret_cast<const uint2*>(at);
+          x[0] = w.x;
+          x[1] = w.y;
+        } else {
+          x[0] = *reinterpret_cast<const uint32_t*>(at);
+        }
+        float v[kMine];
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < kMine; ++c) {
+          const uint32_t w = x[c / 2] >> (16 * (c & 1));
+          v[c] = kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
+                      : __uint_as_float(w << 16);
+          top = fmaxf(top, fabsf(v[c]));
+          if (v[c] != v[c]) top = INFINITY;
+        }
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        const uint32_t bits = __float_as_uint(top);
+        int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+        e = min(max(e, -120), 120);
+        const float inv = pow2(-e);
+        uint16_t num[kMine / 2][kNum];
+#pragma unroll
+        for (int c = 0; c < kMine; c += 2) numbers_of<kNum>(v[c] * inv, v[c + 1] * inv, num[c / 2]);
+#pragma unroll
+        for (int k = 0; k < kNum; ++k) {
+          unsigned char* to = smem + swizzled<kDim>(k * wide + r, lane * kMine);
+          if constexpr (kMine == 4)
+            *reinterpret_cast<uint32_t*>(to) = num[0][k] | (uint32_t)num[1][k] << 16;
+          else
+            *reinterpret_cast<uint16_t*>(to) = num[0][k];
+        }
+        // (a row with NaN or an infinity has NaN for its factor)
+        if (lane == 0)
+          qscale[slot * kRows + r] = top <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&m.raw_empty);
+        mbar_arrive(&m.q_full);
+      }
+    };
+    next_queries();
     while (walk.next(&pt)) {
       const Item& it = pt.it;
       const int n = pt.n, streams = pt.streams, per = 4 / streams;  // groups of a stream
@@ -710,10 +735,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
                        "r"(weight)
                        : "memory");
       };
-      // rows that do not exist stay out of every vote
-      if (quarter == 0 && lane < 16) ref[lane] = c0 + lane < pt.rows ? INFINITY : -INFINITY;
+      // rows that do not exist stay out of every vote; the others' references are 0
+      // until they have seen a key
+      if (quarter == 0 && lane < 16) ref[lane] = c0 + lane < pt.rows ? 0.f : -INFINITY;
+      uint32_t fresh = low_bits(pt.rows - c0) & 0xffffu;
       group_sync();
-      wait(&m.q_full[slot], q_parity, 0xB50);
       const float* factor = qscale + slot * kRows + c0;
       uint64_t sums[8];
 #pragma unroll
@@ -736,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         // rows of the item that see the key: [n0, n1)
         int n0 = 0, n1 = kRows;
         if (edge) {
+          asm volatile("" ::: "memory");               // (a branch, and not selections for every tile)
           const long long g0 = (long long)key - it.pos0;
           n0 = (int)min(max(g0, 0ll), (long long)it.ntok) * a.group;
           n1 = it.ntok * a.group;
@@ -749,10 +776,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
 #pragma unroll
           for (int i = 1; i < kNum; ++i) umma::ld_x16(s_addr + i * pt.wide, y[i - 1]);
           wait(&m.sc_full[sc_at], sc_p, 0xB53);
-          const float* sc = scale_slots + sc_at * 3 * kScaleBlocks + (kt >> 4);
+          const float* sc = scale_slots + sc_at * 2 * kScaleBlocks + (kt >> 4);
           sc_at += streams;
           if (sc_at >= kScaleSlots) sc_at -= kScaleSlots, sc_p ^= 1u;
-          const float ks = sc[0], lv = sc[kScaleBlocks], iv = sc[2 * kScaleBlocks];
+          const float ks = sc[0], lv = sc[kScaleBlocks];
+          const float iv = exp2_approx(kBase - lv);    // 1 / vs
           umma::wait_ld();
           umma::fence_before_sync();
           arrive(&m.s_empty[s]);
@@ -769,29 +797,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             }
           }
           const uint64_t ks2 = pair_f(ks, ks), lv2 = pair_f(lv, lv), iv2 = pair_f(iv, iv);
-          const uint32_t seen = low_bits(n1 - c0) & ~low_bits(n0 - c0);
+          // t = q·K·factor·ks + log2 vs + kBase − m, −inf for what a row does not see
           float t[16];
-          // t = q·K·factor·ks + log2 vs + 7 − m, −inf for what a row does not see
-          auto weights = [&]() {
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(factor + c);
-              const float4 r = *reinterpret_cast<const float4*>(ref + c);
-              split(fma2(mul2(pair(x[c], x[c + 1]), pair_f(f.x, f.y)), ks2,
-                         add2(lv2, pair_f(r.x, r.y))), &t[c], &t[c + 1]);
-              split(fma2(mul2(pair(x[c + 2], x[c + 3]), pair_f(f.z, f.w)), ks2,
-                         add2(lv2, pair_f(r.z, r.w))), &t[c + 2], &t[c + 3]);
-            }
-            if (edge) {
+          for (int c = 0; c < 16; c += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(factor + c);
+            const float4 r = *reinterpret_cast<const float4*>(ref + c);
+            split(fma2(mul2(pair(x[c], x[c + 1]), pair_f(f.x, f.y)), ks2,
+                       add2(lv2, pair_f(r.x, r.y))), &t[c], &t[c + 1]);
+            split(fma2(mul2(pair(x[c + 2], x[c + 3]), pair_f(f.z, f.w)), ks2,
+                       add2(lv2, pair_f(r.z, r.w))), &t[c + 2], &t[c + 3]);
+          }
+          if (edge) {
+            asm volatile("" ::: "memory");
+            const uint32_t seen = low_bits(n1 - c0) & ~low_bits(n0 - c0);
 #pragma unroll
-              for (int c = 0; c < 16; ++c) t[c] = seen >> c & 1u ? t[c] : -INFINITY;
-            }
-          };
-          weights();
+            for (int c = 0; c < 16; ++c) t[c] = seen >> c & 1u ? t[c] : -INFINITY;
+          }
           float top = fmaxf(t[0], t[1]);
 #pragma unroll
           for (int c = 2; c < 16; c += 2) top = max3(top, t[c], t[c + 1]);
-          int grown = top > kBase + kGrow;
+          int grown = top > kBase + kGrow || fresh;
           asm volatile(
               "{\n\t.reg .pred p, q;\n\t"
               "setp.ne.s32 p, %0, 0;\n\t"
@@ -800,52 +826,38 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
               : "+r"(grown)
               : "r"(3 + g)
               : "memory");
+          uint32_t cols = 0;                           // columns whose reference moves,
+          float keep = 1.f;                            // and by how much (lane c: column c)
           if (grown) {
-            // the tile's largest t of every column; the references that it passes
-            // follow it, and with them what has been summed up so far
+            // the tile's largest t of every column: a reference that it passes follows
+            // it, and with it what has been summed up so far
+            const int col = lane & 15;
+            const float ref_was = ref[col];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              const float f = factor[c];
-              float v = fmaf(__uint_as_float(x[c]) * f, ks, lv - kBase);
-              if (edge && !(seen >> c & 1u)) v = -INFINITY;
-              v = warp_max(v);
+              const float v = warp_max(t[c]);
               if (lane == c) mine[c] = v;
             }
             group_sync();
-            const int col = lane & 15;
             float best = stat[g * 64 + col];
 #pragma unroll
             for (int w = 1; w < 4; ++w) best = fmaxf(best, stat[g * 64 + w * 16 + col]);
-            const float was = -ref[col];                // (+inf: a row that does not exist)
-            const bool follows = best > was + kGrow;
-            const float keep = follows ? exp2_approx(was - best) : 1.f;
-            group_sync();
-            if (quarter == 0 && lane < 16 && follows) ref[lane] = -best;
+            const bool first = fresh >> col & 1u;
+            const bool follows = best > (first ? -INFINITY : kBase + kGrow);
+            const float by = follows ? best - kBase : 0.f;
+            if (quarter == 0 && lane < 16 && follows) ref[lane] = ref_was - by;
+            if (!first) keep = exp2_approx(-by);
+            cols = __ballot_sync(0xffffffffu, follows) & 0xffffu;
+            fresh &= ~cols;
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
-              const uint64_t by = pair_f(__shfl_sync(0xffffffffu, keep, c),
-                                         __shfl_sync(0xffffffffu, keep, c + 1));
-              sums[c / 2] = mul2(sums[c / 2], by);
-            }
-            if (j >= streams) {
-              wait(&m.p_done[s], k & 1u ^ 1u, 0xB54);
-              umma::fence_after_sync();
-#pragma unroll 1
-              for (int i = 0; i < kNum; ++i) {
-                uint32_t o[16];
-                umma::ld_x16(o_addr + i * pt.wide, o);
-                umma::wait_ld();
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                  o[c] = __float_as_uint(__uint_as_float(o[c]) *
-                                         __shfl_sync(0xffffffffu, keep, c));
-                umma::st_x16(o_addr + i * pt.wide, o);
-              }
-              umma::wait_st();
-              umma::fence_before_sync();
+              if (!(cols >> c & 3u)) continue;
+              t[c] -= __shfl_sync(0xffffffffu, by, c);
+              t[c + 1] -= __shfl_sync(0xffffffffu, by, c + 1);
+              sums[c / 2] = mul2(sums[c / 2], pair_f(__shfl_sync(0xffffffffu, keep, c),
+                                                     __shfl_sync(0xffffffffu, keep, c + 1)));
             }
             group_sync();
-            weights();
           }
           // weights, their sum, and their numbers
           uint32_t num[kNum][4];
@@ -859,8 +871,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             for (int i = 0; i < kNum; ++i)
               num[i][c / 4] = c & 2 ? num[i][c / 4] | (uint32_t)v[i] << 16 : v[i];
           }
-          // the product with the weights before them has read those
+          // the product with the weights before them has read those, and added to O
           wait(&m.p_done[s], k & 1u ^ 1u, 0xB55);
+          if (cols && j >= streams) {
+            umma::fence_after_sync();
+#pragma unroll 1
+            for (uint32_t todo = cols; todo; todo &= todo - 1) {
+              const int c = __ffs(todo) - 1;
+              const float by = __shfl_sync(0xffffffffu, keep, c);
+              uint32_t o[kNum];
+#pragma unroll
+              for (int i = 0; i < kNum; ++i) o[i] = umma::ld_x1(o_addr + i * pt.wide + c);
+              umma::wait_ld();
+#pragma unroll
+              for (int i = 0; i < kNum; ++i)
+                umma::st_x1(o_addr + i * pt.wide + c, __float_as_uint(__uint_as_float(o[i]) * by));
+            }
+            umma::wait_st();
+            umma::fence_before_sync();
+          }
 #pragma unroll
           for (int i = 0; i < kNum; ++i) {
             const uint32_t col = s * pitch + i * pt.wide + c0;
@@ -921,52 +950,71 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
         if (!(lane & 1)) mine[lane >> 1] = v[0];
       }
+      counts = add_counts(counts, pt);
+      // the next item's queries, once the last products with these are done (the
+      // tensor cores begin with them while this item's results go out)
+#pragma unroll 1
+      for (int z = 0; z < 4; ++z) wait(&m.s_full[z], count_of(counts, z) & 1u ^ 1u, 0xB59);
+      slot ^= 1;
+      next_queries();
+      // (a column that saw no key has no reference)
+      if (quarter == 0 && lane < 16 && (fresh >> lane & 1u)) ref[lane] = INFINITY;
       if (n > s) wait(&m.p_done[s], k & 1u ^ 1u, 0xB57);  // the stream's last product
       all_sync();
       umma::fence_after_sync();
       const bool spoils = *static_cast<volatile int*>(&m.spoils);
+      float* part = p.part + (size_t)(2 * blockIdx.x + (pt.ends ? 0 : 1)) * slot_floats(kDim);
+      // what each column of each stream counts: its sums join those of the row's
+      // other streams, and are divided by Σ where the item is whole. The factors
+      // take the references' place; column i is that of row i % width of its stream.
+      const int width = kRows >> pt.shift;
+      if (warp < 2) {
+        const int i = threadIdx.x - 128, row = i & (width - 1);
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int z = row; z < kRows; z += width) top = fmaxf(top, -refs[z]);
+#pragma unroll 1
+        for (int z = row; z < kRows; z += width) {
+          const float* l = stat + (z >> 4) * 64 + (z & 15);
+          // (a stream that saw none of the row's keys has zeros, or sums of NaN)
+          sum = fmaf(l[0] + l[16] + (l[32] + l[48]),
+                     top == -INFINITY ? 1.f : exp2_approx(-refs[z] - top), sum);
+        }
+        float by = top == -INFINITY ? 1.f : exp2_approx(-refs[i] - top);
+        if (pt.whole) by *= inverse(sum);
+        if (!pt.whole && i < pt.rows) {
+          part[kRows * kDim + i] = top;
+          part[kRows * kDim + kRows + i] = sum;
+        }
+        asm volatile("bar.sync 7, 64;" ::: "memory");
+        refs[i] = by;
+      }
+      all_sync();
       // a thread has column d of V, and its group a quarter of the rows (of one
       // stream: the group's own)
       const int d = kDim == 128 ? kt : quarter * 16 + (lane & 15);
       const bool valid = kDim == 128 || lane < 16;
-      const int take = streams == 1 ? 16 : streams == 2 ? 8 : 4, from = g * take;
+      const int take = width / 4, from = g * take;
       const uint32_t o_from = lanes + Z::kColO + from;
-      float* part = p.part + (size_t)(2 * blockIdx.x + (pt.ends ? 0 : 1)) * slot_floats(kDim);
       int tok = from / a.group, head = from - tok * a.group;
 #pragma unroll 1
       for (int i = 0; ok && i < take && from + i < pt.rows; i += 4) {
-        float o[4], top[4], sum[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          o[c] = sum[c] = 0.f;
-          top[c] = -INFINITY;
-        }
-        const int at = (from + i) & 15, first = (from + i) >> 4;
-#pragma unroll 1
-        for (int z = 0; z < streams; ++z)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], -refs[(z * per + first) * 16 + at + c]);
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int z = 0; z < streams && z < n; ++z) {
           uint32_t w[kNum][4];
 #pragma unroll
           for (int e = 0; e < kNum; ++e) umma::ld_x4(o_from + z * pitch + e * pt.wide + i, w[e]);
+          const float4 by = *reinterpret_cast<const float4*>(refs + z * width + from + i);
+          const float f[4] = {by.x, by.y, by.z, by.w};
           umma::wait_ld();
-          const int gz = z * per + first;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float l = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) l += stat[gz * 64 + e * 16 + at + c];
-            const float was = -refs[gz * 16 + at + c];
-            // (a stream that saw none of the row's keys has zeros, or sums of NaN)
-            const float by = top[c] == -INFINITY ? 1.f : exp2_approx(was - top[c]);
             float v = __uint_as_float(w[0][c]);
 #pragma unroll
             for (int e = 1; e < kNum; ++e)
               v = fmaf(__uint_as_float(w[e][c]), number_unit(e), v);
-            o[c] = fmaf(v, by, o[c]);
-            sum[c] = fmaf(l, by, sum[c]);
+            o[c] = fmaf(v, f[c], o[c]);
           }
         }
 #pragma unroll
@@ -974,17 +1022,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           const int r = from + i + c;
           if (r < pt.rows && valid) {
             if (spoils && (__ldcg(p.spoiled + blockIdx.x * 128 + d) >> r & 1ull)) o[c] = NAN;
-            if (pt.whole) {
-              const uint32_t v = round16<kF16>(o[c] * inverse(sum[c]), 0.f);
+            if (pt.whole)
               (static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
-               (int64_t)(walk.h * a.group + head) * a.out_head_stride)[d] = (uint16_t)v;
-            } else {
+               (int64_t)(walk.h * a.group + head) * a.out_head_stride)[d] =
+                  (uint16_t)round16<kF16>(o[c], 0.f);
+            else
               part[r * kDim + d] = o[c];
-              if (d == 0) {
-                part[kRows * kDim + r] = top[c];
-                part[kRows * kDim + kRows + r] = sum[c];
-              }
-            }
           }
           if (++head == a.group) {
             head = 0;
@@ -994,18 +1037,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       }
       open = !pt.ends;
       umma::fence_before_sync();
-      // O, references and sums have been read before any stream goes on
+      // O and the factors have been read before any stream goes on
       all_sync();
-      if (threadIdx.x == 128) mbar_arrive(&m.q_empty[slot]);
       if (spoils) {
         if (threadIdx.x < 256) p.spoiled[blockIdx.x * 128 + threadIdx.x - 128] = 0;
         if (threadIdx.x == 128) m.spoils = 0;
         all_sync();
       }
-      counts = add_counts(counts, pt);
       ring = (ring + 2 * n) % (2 * kStages);
-      if (slot) q_parity ^= 1u;
-      slot ^= 1;
       const unsigned upto = (unsigned)(sc_first + n);
       sc_first = (int)(upto % kScaleSlots);
       sc_parity ^= upto / kScaleSlots & 1u;

@@ -60,22 +60,24 @@ MOE_DEV void mma_e4m3(uint32_t tmem_d, uint32_t alo, uint32_t blo, uint32_t ides
   }
 }
 
-// 4 consecutive columns of the thread's lane (16: tcgen05.cuh), and the reverse
-// for 16.
+// 4 consecutive columns of the thread's lane (16: tcgen05.cuh), and one, and the
+// reverse for that.
 MOE_DEV void ld_x4(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(taddr)
                : "memory");
 }
-MOE_DEV void st_x16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(taddr)
-      : "memory");
+MOE_DEV uint32_t ld_x1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+               : "=r"(r)
+               : "r"(taddr)
+               : "memory");
+  return r;
+}
+MOE_DEV void st_x1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"r"(v), "r"(taddr) : "memory");
 }
 
 }  // namespace umma
