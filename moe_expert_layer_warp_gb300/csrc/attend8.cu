@@ -126,6 +126,7 @@ struct Part {
   Item it;
   int t0, n;          // n 0: its rows see nothing
   bool whole, ends;   // all of the item; its last tile
+  bool once;          // no other item has its keys
   int rows, wide;     // query rows, and those rounded up: 16, 32, 48 or 64
   int streams, shift; // 4, 2 or 1, and its logarithm
   MOE_DEV int tile(int j) const { return tile_of(it, t0 + j); }
@@ -156,6 +157,7 @@ struct Walker {
       out->n = it.hi > 0 ? n : 0;
       out->whole = n == it.n;
       out->ends = t1 == it.n;
+      out->once = r.q <= p.block;
       out->rows = it.ntok * p.a.group;
       out->wide = (out->rows + 15) & ~15;
       out->shift = out->wide == 16 ? 2 : out->wide == 32 ? 1 : 0;
@@ -436,7 +438,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
-    const uint64_t policy = l2_evict_normal_policy();
+    // keys and values that one item reads alone are not kept in L2: the rows of
+    // the other heads beside them are (single tokens 258 -> 243 us)
+    const uint64_t stay = l2_evict_normal_policy(), go = l2_evict_first_policy();
     const CUtensorMap* map = keys ? &p.kmap : &p.vmap;
     const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
     int slot = 0;
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           const int row = page > kTile ? pt.tile(j) * kTile & (page - 1) : 0;
           if (pg0 >= 0)
             tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, walk.h, row, pg0, &m.full[stage],
-                           policy);
+                           pt.once ? go : stay);
           __syncwarp();
         }
         pg0 = pg1;
@@ -1120,7 +1124,7 @@ cudaError_t launch_attend8(const Attend8Args& a, int num_sms, cudaStream_t strea
       return encode(to, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(at), dims, strides, box,
                     steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     return map(&p.kmap, c.k) && map(&p.vmap, c.v);
