@@ -43,7 +43,8 @@
 //   0      TMA: key tiles into a ring, a box per page; the tiles' scales
 //   1      MMA issue
 //   2      TMA: value tiles into the same ring
-//   3      query rows into shared memory, the next item's ahead
+//   3      the parts of the CTA's range, for the others to read; and the next
+//          part's query rows into shared memory
 //   4-19   softmax, four groups of four warps: 16 columns of a tile each, or the
 //          tiles of a stream; and the next item's queries into e4m3 numbers
 //
@@ -84,15 +85,16 @@ struct Sizes {
   static constexpr int kQBytes = kRows * kNum * kDim;  // an item's queries as numbers
   static constexpr int kRawBytes = kRows * kDim * 2;   // and the next one's as they come
   static constexpr int kPBytes = kTile * kRows * kWide;  // in 128-byte columns, kTile rows each
-  static constexpr int kStages = kDim == 64 ? 16 : kNum == 2 ? 11 : 9;
+  static constexpr int kStages = kDim == 64 ? 16 : kNum == 2 ? 10 : 9;
   static constexpr int kOffRaw = kQBytes;
   static constexpr int kOffP = kOffRaw + kRawBytes;
   static constexpr int kOffRing = kOffP + kPBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
-  static constexpr int kMiscBytes = 3072;
+  static constexpr int kMiscBytes = 4608;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kTileBytes % 1024 == 0, "tiles");
+  static_assert(kPBytes >= kRows * kDim * 2, "results pass through P");
   static constexpr uint32_t kCols = kNum == 2 ? 256 : 512;  // tensor memory: S, then O
   static constexpr uint32_t kColO = kRows * kWide;
 };
@@ -121,73 +123,88 @@ MOE_DEV Units units_of(const Params&, const Item& it) {
   return u;
 }
 
-// The CTA's part of an item: tiles [t0, t0 + n).
+// The CTA's part of an item, in shared memory: one warp walks the range, and the
+// others read what they need of a part when they need it. (With a copy of the walk
+// and of the part in registers of every warp, a tile took a third more
+// instructions: what did not fit was worked out again at every tile.)
 struct Part {
-  Item it;
-  int t0, n;          // n 0: its rows see nothing
-  bool whole, ends;   // all of the item; its last tile
-  bool once;          // no other item has its keys
+  int n;              // tiles; 0: its rows see nothing; −1: there are no more parts
   int rows, wide;     // query rows, and those rounded up: 16, 32, 48 or 64
-  int streams, shift; // 4, 2 or 1, and its logarithm
-  MOE_DEV int tile(int j) const { return tile_of(it, t0 + j); }
-  // places in the ring behind the part's first: K_0 .. K_{streams-1}, then
-  // K_{j + streams} and V_j for j = 0, 1, ..
-  MOE_DEV int place_k(int j) const { return j < streams ? j : 2 * j - streams; }
-  MOE_DEV int place_v(int j) const { return j + streams < n ? 2 * j + streams + 1 : n + j; }
+  int shift;          // log2 of the streams: 2, 1 or 0
+  int whole, ends;    // all of the item; its last tile
+  int once;           // no other item has its keys
+  int b, h;           // request, key head
+  int row0, ntok;     // packed rows of the item
+  int pos0;           // position of its first token
+  int hi, lo, sk;     // see Item
+  int first, ns, gap; // tile j of the part is tile t = first + j, beyond ns of them t + gap
+  // tiles that not all rows see whole: from edge_hi on, and [edge_sk, edge_lo)
+  int edge_hi, edge_lo, edge_sk;
+  MOE_DEV int tile(int j) const { return first + j + (first + j < ns ? 0 : gap); }
 };
+constexpr int kParts = 8;
 
-// The next part of the walk; every role walks it by itself.
-struct Walker {
-  const Params& p;
-  Walk w;
-  Request r;
-  int b, h;  // of the present part
+// Places in the ring behind the part's first: K_0 .. K_{streams-1}, then
+// K_{j + streams} and V_j for j = 0, 1, ..
+MOE_DEV int place_k(int j, int streams) { return j < streams ? j : 2 * j - streams; }
+MOE_DEV int place_v(int j, int streams, int n) {
+  return j + streams < n ? 2 * j + streams + 1 : n + j;
+}
 
-  MOE_DEV Walker(const Params& prm, const Start& s) : p(prm), w(s.w), r(s.r), b(s.w.b), h(s.w.h) {}
-
-  MOE_DEV bool next(Part* out) {
+// The next part of the walk with tiles in it; false when there is none.
+MOE_DEV bool next_part(const Params& p, Walk& w, Request& r, Part* out) {
+  const Attend8Args& a = p.a;
 #pragma unroll 1
-    while (w.left > 0) {
-      const Item it = make_item(p.a, r, w.block, p.block);
-      const Units units = units_of(p, it);
-      const int u1 = min(w.u0 + w.left, units.all);
-      out->it = it;
-      out->t0 = units.tiles(w.u0);
-      const int t1 = units.tiles(u1), n = t1 - out->t0;
-      out->n = it.hi > 0 ? n : 0;
-      out->whole = n == it.n;
-      out->ends = t1 == it.n;
-      out->once = r.q <= p.block;
-      out->rows = it.ntok * p.a.group;
-      out->wide = (out->rows + 15) & ~15;
-      out->shift = out->wide == 16 ? 2 : out->wide == 32 ? 1 : 0;
-      out->streams = 1 << out->shift;
-      b = w.b;
-      h = w.h;
-      w.left -= u1 - w.u0;
-      w.u0 = 0;
-      if (w.left > 0 && ++w.block * p.block >= r.q) {
-        w.block = 0;
-        if (++w.h == p.a.cache.n_kv_heads) {
-          w.h = 0;
-          bool bad;
-          do {
-            r = request(p.a, p.page_shift, ++w.b, &bad);
-          } while (r.q == 0 && w.b + 1 < p.a.n_requests);
-        }
+  while (w.left > 0) {
+    const Item it = make_item(a, r, w.block, p.block);
+    const Units units = units_of(p, it);
+    const int u1 = min(w.u0 + w.left, units.all);
+    const int t0 = units.tiles(w.u0), t1 = units.tiles(u1), n = t1 - t0;
+    out->n = it.hi > 0 ? n : 0;
+    out->rows = it.ntok * a.group;
+    out->wide = (out->rows + 15) & ~15;
+    out->shift = out->wide == 16 ? 2 : out->wide == 32 ? 1 : 0;
+    out->whole = n == it.n;
+    out->ends = t1 == it.n;
+    out->once = r.q <= p.block;
+    out->b = w.b;
+    out->h = w.h;
+    out->row0 = it.row0;
+    out->ntok = it.ntok;
+    out->pos0 = it.pos0;
+    out->hi = it.hi;
+    out->lo = it.lo;
+    out->sk = it.sk;
+    out->first = t0;
+    out->ns = it.ns;
+    out->gap = it.lo_tile - it.ns;
+    // key0 + 127 > pos0; key0 below the last row's window and not all of it sinks
+    out->edge_hi = (it.pos0 + 1) >> 7;
+    out->edge_lo = a.window > 0 ? (max(0, window_from(it.hi - 1, a.window)) + kTile - 1) / kTile : 0;
+    out->edge_sk = it.sk / kTile;
+    w.left -= u1 - w.u0;
+    w.u0 = 0;
+    if (w.left > 0 && ++w.block * p.block >= r.q) {
+      w.block = 0;
+      if (++w.h == a.cache.n_kv_heads) {
+        w.h = 0;
+        bool bad;
+        do {
+          r = request(a, p.page_shift, ++w.b, &bad);
+        } while (r.q == 0 && w.b + 1 < a.n_requests);
       }
-      if (n > 0) return true;
     }
-    return false;
+    if (n > 0) return true;
   }
-};
+  return false;
+}
 
 // A place in the ring, counted modulo twice its stages: the stage, and the parity
 // of its filling.
 template <int kStages>
 struct Place {
   int at;
-  MOE_DEV explicit Place(unsigned from) : at((int)from) {}
+  MOE_DEV explicit Place(unsigned from) : at((int)(from % (2u * kStages))) {}
   MOE_DEV int stage() const { return at >= kStages ? at - kStages : at; }
   MOE_DEV uint32_t parity() const { return at >= kStages; }
 };
@@ -195,11 +212,11 @@ struct Place {
 // How many tiles each of the four streams has had, modulo 256, a byte each: all
 // roles count alike, and a barrier's parity follows from its stream's count.
 MOE_DEV uint32_t count_of(uint32_t counts, int s) { return counts >> (8 * s) & 255u; }
-MOE_DEV uint32_t add_counts(uint32_t counts, const Part& pt) {
+MOE_DEV uint32_t add_counts(uint32_t counts, int n, int shift) {
   uint32_t r = 0;
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const int more = s < pt.streams && pt.n > s ? ((pt.n - 1 - s) >> pt.shift) + 1 : 0;
+    const int more = s >> shift == 0 && n > s ? ((n - 1 - s) >> shift) + 1 : 0;
     r |= (count_of(counts, s) + (uint32_t)more & 255u) << (8 * s);
   }
   return r;
@@ -209,6 +226,7 @@ MOE_DEV uint32_t add_counts(uint32_t counts, const Part& pt) {
 template <int kStages>
 struct Misc {
   uint64_t full[kStages], empty[kStages];
+  uint64_t part_full[kParts], part_empty[kParts];
   uint64_t raw_full, raw_empty;  // queries as they come
   uint64_t q_full;               // and as numbers
   uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
@@ -218,15 +236,16 @@ struct Misc {
   long long part[8];
   uint32_t tmem;
   int lost;
-  int raw_rows, raw_wide;  // of the queries as they come; no rows: there are no more
   // NaN has been noted in the CTA's `spoiled` for the present item
   int spoils;
 };
-constexpr int kOffRef = 704;                    // [4 groups][16] −m of a column
-constexpr int kOffQScale = kOffRef + 256;       // [2][64] a row's factor
-constexpr int kOffStat = kOffQScale + 512;      // [4 groups][4 warps][16]
-constexpr int kOffScale = kOffStat + 1024;      // [slots][2][8 blocks]: ks, log2 vs + kBase
-static_assert(kOffScale + kScaleSlots * 2 * kScaleBlocks * 4 <= 3072, "misc words");
+constexpr int kScaleWords = 2 * kScaleBlocks + 4;  // of a slot: ks, log2 vs + kBase; key0, edge
+constexpr int kOffRef = 896;                       // [4 groups][16] −m of a column
+constexpr int kOffQScale = kOffRef + 256;          // [2][64] a row's factor
+constexpr int kOffStat = kOffQScale + 512;         // [4 groups][4 warps][16]
+constexpr int kOffScale = kOffStat + 1024;
+constexpr int kOffParts = kOffScale + kScaleSlots * kScaleWords * 4;
+static_assert(kOffParts + kParts * (int)sizeof(Part) <= 4608, "misc words");
 
 // ln 2's reciprocal: scores are kept in powers of two.
 constexpr float kLog2e = 1.4426950408889634f;
@@ -270,6 +289,51 @@ MOE_DEV float warp_max(float v) {
 
 // Bytes of w that are NaN, 0x80 each.
 MOE_DEV uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Query rows [n0, n1) of the part are those that see `key`.
+MOE_DEV void visible(const Attend8Args& a, const Part& pt, int key, int* n0, int* n1) {
+  const long long back = (long long)key - pt.pos0;     // of the first token that sees it
+  *n0 = (int)min(max(back, 0ll), (long long)pt.ntok) * a.group;
+  *n1 = pt.rows;
+  if (a.window > 0 && key >= a.sinks)
+    *n1 = (int)min(max(back + a.window, 0ll), (long long)pt.ntok) * a.group;
+}
+
+// In a tile of V that not all rows see whole: rows that no row of the item sees
+// become zeros; NaN in rows that some see and others do not is taken out, and
+// noted in `spoiled`. A thread takes the row of its key, the `per` groups of a
+// stream every per-th piece of it.
+template <int kDim>
+__device__ __noinline__ void clean_values(const Attend8Args& a, const Part& pt,
+                                          unsigned char* tile, int key0, int gl, int per,
+                                          unsigned long long* spoiled, int* spoils) {
+  const int kt = threadIdx.x & 127, key = key0 + kt;
+  const bool none = key >= pt.hi || (key < pt.lo && key >= pt.sk);
+  if (!none && !some_see(a, pt.pos0, pt.hi, key)) return;
+  int n0, n1;
+  visible(a, pt, key, &n0, &n1);
+#pragma unroll 1
+  for (int c = gl; c < kDim / 16; c += per) {
+    uint4* at = reinterpret_cast<uint4*>(tile + kt * kDim + c * 16);
+    if (none) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const uint4 x = *at;
+    if (!(nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w))) continue;
+    const int d0 = (int)(swizzled<kDim>(kt, c * 16) - kt * kDim);  // its first column
+    const unsigned long long rows =
+        (n1 >= 64 ? ~0ull : (1ull << n1) - 1) & ~(n0 >= 64 ? ~0ull : (1ull << n0) - 1);
+    unsigned char* bytes = reinterpret_cast<unsigned char*>(at);
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i) {
+      if ((bytes[i] & 0x7f) != 0x7f) continue;
+      bytes[i] = 0;
+      atomicOr(spoiled + d0 + i, rows);
+      *static_cast<volatile int*>(spoils) = 1;
+    }
+  }
+}
 
 template <int kDim>
 MOE_DEV const float* part_of(const Params& p, int cta, bool ends) {
@@ -376,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   float* qscale = reinterpret_cast<float*>(misc + kOffQScale);
   float* stat = reinterpret_cast<float*>(misc + kOffStat);
   float* scale_slots = reinterpret_cast<float*>(misc + kOffScale);
+  Part* parts = reinterpret_cast<Part*>(misc + kOffParts);
   // the same value in every lane, and known to be
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) - 4;
   const int lane = threadIdx.x & 31;
@@ -385,7 +450,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 1);
     }
-    mbar_init(&m.raw_full, 33);                // its lanes, with their copies, and its rows' number
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&m.part_full[i], 1);
+      mbar_init(&m.part_empty[i], 19);         // both loaders, the MMA warp, 16 of the softmax
+    }
+    mbar_init(&m.raw_full, 32);                // the lanes that copy, with their copies
     mbar_init(&m.raw_empty, 16);
     mbar_init(&m.q_full, 16);
     for (int i = 0; i < kScaleSlots; ++i) {
@@ -426,8 +495,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
       ok = wait_longer(bar, parity, lost, site) && ok;
   };
-  Part pt;
-  Walker walk(p, m.start);
+  // The parts, one after the other. A lost wait ends a role's walk: what a part
+  // says may then be another's.
+  int part_no = 0;
+  auto next = [&]() -> const Part* {
+    const int slot = part_no & (kParts - 1);
+    wait(&m.part_full[slot], part_no >> 3 & 1u, 0xB32);
+    return ok && parts[slot].n >= 0 ? parts + slot : nullptr;
+  };
+  auto done_with_part = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.part_empty[part_no & (kParts - 1)]);
+    ++part_no;
+  };
   uint32_t counts = 0;
   int ring = 0;     // place of the part's first tile, modulo twice the stages
 
@@ -445,16 +525,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
     int slot = 0;
     uint32_t slot_parity = 1;
-    while (walk.next(&pt)) {
-      const Item& it = pt.it;
-      const int n = pt.n;
-      const int32_t* table = a.block_table + (size_t)walk.b * a.max_blocks;
+    for (const Part* pt; (pt = next()); done_with_part()) {
+      const int n = pt->n, streams = 1 << pt->shift, head = pt->h;
+      const int32_t* table = a.block_table + (size_t)pt->b * a.max_blocks;
       // this lane's page of tile j (−1: it has none, or no row of it is seen)
       auto page_of = [&](int j) {
         int pg = -1;
         if (j < n && lane < n_pages) {
-          const int r0 = pt.tile(j) * kTile + lane * rows;
-          if (r0 < it.hi && (r0 + rows > it.lo || r0 < it.sk)) {
+          const int r0 = pt->tile(j) * kTile + lane * rows;
+          if (r0 < pt->hi && (r0 + rows > pt->lo || r0 < pt->sk)) {
             pg = table[r0 >> p.page_shift];
             if (pg < 0 || pg >= a.cache.n_pages) {
               report_error(a.err, ERR_CHECK, 0xB21);
@@ -471,12 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         const int mine = __shfl_sync(0xffffffffu, pg, e * 16 / rows);
         float s = 1.f;
         if (lane < 16 && mine >= 0 && mine < a.cache.n_pages) {
-          const int key = pt.tile(j) * kTile + e * 16;
-          if (key < it.hi && (key + 16 > it.lo || key < it.sk)) {
+          const int key = pt->tile(j) * kTile + e * 16;
+          if (key < pt->hi && (key + 16 > pt->lo || key < pt->sk)) {
             const int at = (key & (page - 1)) >> (p.page_shift - p.blocks_shift);
             const float* from = lane < 8 ? a.cache.k_scale : a.cache.v_scale;
-            s = __ldg(from + ((((int64_t)mine * a.cache.n_kv_heads) + walk.h) << p.blocks_shift) +
-                      at);
+            s = __ldg(from + ((((int64_t)mine * a.cache.n_kv_heads) + head) << p.blocks_shift) + at);
           }
         }
         return s;
@@ -490,11 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       }
 #pragma unroll 1
       for (int j = 0; ok && j < n; ++j) {
-        const int pg4 = page_of(j + 4);
+        const int pg4 = page_of(j + 4), tile = pt->tile(j);
         float s2 = 1.f;
         if (keys) s2 = scale_of(j + 2, pg2);
-        const Place<kStages> at((unsigned)(ring + (keys ? pt.place_k(j) : pt.place_v(j))) %
-                                (2u * kStages));
+        const Place<kStages> at(ring + (keys ? place_k(j, streams) : place_v(j, streams, n)));
         const int stage = at.stage();
         if (keys) {
           wait(&m.sc_empty[slot], slot_parity, 0xB31);
@@ -507,7 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             const uint32_t bits = __float_as_uint(s0);
             s0 = (bits & 0x7fffffu ? log2f(s0) : (float)((int)(bits >> 23) - 127)) + kBase;
           }
-          if (lane < 16) scale_slots[slot * 2 * kScaleBlocks + lane] = s0;
+          const bool edge = tile >= pt->edge_hi || (tile < pt->edge_lo && tile >= pt->edge_sk);
+          if (lane == 16) s0 = __int_as_float(tile * kTile);
+          if (lane == 17) s0 = __int_as_float(edge);
+          if (lane < 18) scale_slots[slot * kScaleWords + lane] = s0;
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(&m.sc_full[slot]);
           if (++slot == kScaleSlots) {
@@ -520,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           const uint32_t wanted = __ballot_sync(0xffffffffu, pg0 >= 0);
           if (lane == 0) mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim);
           __syncwarp();
-          const int row = page > kTile ? pt.tile(j) * kTile & (page - 1) : 0;
+          const int row = page > kTile ? tile * kTile & (page - 1) : 0;
           if (pg0 >= 0)
-            tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, walk.h, row, pg0, &m.full[stage],
-                           pt.once ? go : stay);
+            tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, head, row, pg0, &m.full[stage],
+                           pt->once ? go : stay);
           __syncwarp();
         }
         pg0 = pg1;
@@ -551,27 +631,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const uint32_t p_at = (smem_addr(smem) + Z::kOffP) >> 4;
     constexpr uint32_t kNextP = (kTile * 128u >> 4) << 16;  // the next 128 columns of P
     int sc_slot = 0;
-    uint32_t q_parity = 0;
     auto commit = [&](uint64_t* bar) {                 // arrives when the MMAs so far are done
       if (ok) umma::commit_elect(bar);
     };
-    while (walk.next(&pt)) {
-      const int n = pt.n, streams = pt.streams, cols = pt.wide * kNum;
-      const int pitch = pt.wide * Z::kWide;            // columns between streams
+    for (const Part* pt; (pt = next()); done_with_part()) {
+      const int n = pt->n, shift = pt->shift, streams = 1 << shift, cols = pt->wide * kNum;
+      const int pitch = pt->wide * Z::kWide;           // columns between streams
       const uint32_t id_s = umma::idesc_e4m3(kTile, cols, false);
       const uint32_t id_o = umma::idesc_e4m3(kDim, cols, true);
       // S may be laid out anew once the last scores of every stream are read
 #pragma unroll 1
       for (int s = 0; s < 4; ++s) wait(&m.s_empty[s], count_of(counts, s) & 1u ^ 1u, 0xB41);
-      wait(&m.q_full, q_parity, 0xB42);
-      q_parity ^= 1u;
+      wait(&m.q_full, part_no & 1u, 0xB42);
 #pragma unroll 1
-      for (int j = -streams; j < n; ++j) {
+      for (int j = -streams; ok && j < n; ++j) {
         const int s = (j + streams) & (streams - 1);
+        const uint32_t count = count_of(counts, s);
         if (j + streams < n) {                         // the scores of tile j + streams
           const int i = j + streams;
-          const uint32_t k = count_of(counts, s) + (uint32_t)(i >> pt.shift);
-          const Place<kStages> at((unsigned)(ring + pt.place_k(i)) % (2u * kStages));
+          const uint32_t k = count + (uint32_t)(i >> shift);
+          const Place<kStages> at(ring + place_k(i, streams));
           wait(&m.full[at.stage()], at.parity(), 0xB43);
           wait(&m.s_empty[s], k & 1u ^ 1u, 0xB44);
           umma::fence_after_sync();
@@ -583,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           commit(&m.empty[at.stage()]);
         }
         if (j >= 0) {                                  // Oᵀ (+)= Vᵀ · Pᵀ of tile j
-          const uint32_t k = count_of(counts, s) + (uint32_t)(j >> pt.shift);
-          const Place<kStages> at((unsigned)(ring + pt.place_v(j)) % (2u * kStages));
+          const uint32_t k = count + (uint32_t)(j >> shift);
+          const Place<kStages> at(ring + place_v(j, streams, n));
           wait(&m.full[at.stage()], at.parity(), 0xB45);
           wait(&m.p_full[s], k & 1u, 0xB46);
           umma::fence_after_sync();
@@ -602,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           if (++sc_slot == kScaleSlots) sc_slot = 0;
         }
       }
-      counts = add_counts(counts, pt);
+      counts = add_counts(counts, n, shift);
       ring = (ring + 2 * n) % (2 * kStages);
     }
     // Every MMA, and every arrival that hangs on one, is done before tensor
@@ -613,38 +692,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp == -1) {
-    // ------------------------------------------------------------ queries --
+    // -------------------------------------------------- parts and queries --
     constexpr int kPieces = kDim / 8;                  // of a row, 16 bytes each
-    uint32_t parity = 1;
+    Walk w = m.start.w;
+    Request r = m.start.r;
     bool more = true;
-    while (more) {
-      more = walk.next(&pt);
+    int published = 0;
+    uint32_t parity = 1;
+    for (bool last = false; !last;) {
+      // parts are there three ahead of their queries, for the loaders
+      while (more && ok && published < part_no + 4) {
+        const int slot = published & (kParts - 1);
+        wait(&m.part_empty[slot], published >> 3 & 1u ^ 1u, 0xB61);
+        Part next_one;
+        more = next_part(p, w, r, &next_one);
+        if (!more) next_one.n = -1;
+        if (lane == 0) {
+          parts[slot] = next_one;
+          mbar_arrive(&m.part_full[slot]);
+        }
+        __syncwarp();
+        ++published;
+      }
+      const Part* pt = parts + (part_no & (kParts - 1));
       wait(&m.raw_empty, parity, 0xB60);
       parity ^= 1u;
-      const int rows = more && ok ? pt.rows : 0;
+      last = !ok || pt->n < 0;
+      const int rows = last ? 0 : pt->rows;
       const uint32_t to = smem_addr(smem) + Z::kOffRaw;
       const uint16_t* from = static_cast<const uint16_t*>(a.q) +
-                             (int64_t)pt.it.row0 * a.q_token_stride +
-                             (int64_t)walk.h * a.group * a.q_head_stride;
+                             (int64_t)pt->row0 * a.q_token_stride +
+                             (int64_t)pt->h * a.group * a.q_head_stride;
 #pragma unroll 1
       for (int i = lane; i < rows * kPieces; i += 32) {
-        const int r = i / kPieces, t = r / a.group;
-        const uint16_t* at = from + t * a.q_token_stride + (r - t * a.group) * a.q_head_stride +
+        const int row = i / kPieces, t = row / a.group;
+        const uint16_t* at = from + t * a.q_token_stride + (row - t * a.group) * a.q_head_stride +
                              i % kPieces * 8;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(at)
                      : "memory");
       }
-      if (lane == 0) {
-        m.raw_rows = rows;
-        m.raw_wide = pt.wide;
-        mbar_arrive(&m.raw_full);
-      }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                        smem_addr(&m.raw_full))
                    : "memory");
+      ++part_no;
     }
-    // the copies have landed when the last softmax warp has seen their barrier; a
-    // lost wait leaves that to this one
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ softmax --
@@ -659,131 +750,232 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       asm volatile("bar.sync %0, 128;" ::"r"(3 + g) : "memory");
     };
     auto all_sync = [&]() { asm volatile("bar.sync 2, 512;" ::: "memory"); };
-    int sc_first = 0, slot = 0;                        // slots of the part's first scales, factors
-    uint32_t sc_parity = 0, raw_parity = 0;
+    int sc_at = 0;                                     // slot of the part's first scales
+    uint32_t sc_parity = 0;
     bool open = false;                                 // the last part does not end its item
-    // The next item's queries into numbers: a warp takes every 16th row, divides it
-    // by the power of two that makes its largest size 224 to 448, and leaves that
-    // power with the scale as the row's factor.
-    auto next_queries = [&]() {
-      constexpr int kMine = kDim / 32;                 // columns of a lane
-      wait(&m.raw_full, raw_parity, 0xB58);
-      raw_parity ^= 1u;
-      const int rows = ok ? m.raw_rows : 0, wide = m.raw_wide;
-      const float to_log2 = a.scale * kLog2e;
+    const Part* pt = nullptr;                          // the present part
+    int gone = 0;                                      // some warp has lost a wait: all of them stop
 #pragma unroll 1
-      for (int r = warp; r < rows; r += 16) {
-        const unsigned char* at = smem + Z::kOffRaw + r * (kDim * 2) + lane * (kMine * 2);
-        uint32_t x[kMine / 2];
-        if constexpr (kMine == 4) {
-          const uint2 w = *reinterpret_cast<const uint2*>(at);
-          x[0] = w.x;
-          x[1] = w.y;
-        } else {
-          x[0] = *reinterpret_cast<const uint32_t*>(at);
-        }
-        float v[kMine];
-        float top = 0.f;
+    for (;;) {
+      // The next part's queries into numbers: a warp takes every 16th row, divides
+      // it by the power of two that makes its largest size 224 to 448, and leaves
+      // that power with the scale as the row's factor. (For all but the first, the
+      // products with the present part's are done, and the tensor cores begin with
+      // the next one's while the present one's results go out.)
+      const int no = pt ? part_no + 1 : part_no;
+      const Part* then = parts + (no & (kParts - 1));
+      wait(&m.part_full[no & (kParts - 1)], no >> 3 & 1u, 0xB32);
+      wait(&m.raw_full, no & 1u, 0xB58);
+      if (!ok || then->n < 0) then = nullptr;
+      if (then) {
+        constexpr int kMine = kDim / 32;               // columns of a lane
+        const int rows = then->rows, wide = then->wide;
+        const float to_log2 = a.scale * kLog2e;
+#pragma unroll 1
+        for (int r = warp; r < rows; r += 16) {
+          const unsigned char* at = smem + Z::kOffRaw + r * (kDim * 2) + lane * (kMine * 2);
+          uint32_t x[kMine / 2];
+          if constexpr (kMine == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(at);
+            x[0] = w.x;
+            x[1] = w.y;
+          } else {
+            x[0] = *reinterpret_cast<const uint32_t*>(at);
+          }
+          float v[kMine];
+          float top = 0.f;
 #pragma unroll
-        for (int c = 0; c < kMine; ++c) {
-          const uint32_t w = x[c / 2] >> (16 * (c & 1));
-          v[c] = kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
-                      : __uint_as_float(w << 16);
-          top = fmaxf(top, fabsf(v[c]));
-          if (v[c] != v[c]) top = INFINITY;
-        }
-        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-        const uint32_t bits = __float_as_uint(top);
-        int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = min(max(e, -120), 120);
-        const float inv = pow2(-e);
-        uint16_t num[kMine / 2][kNum];
+          for (int c = 0; c < kMine; ++c) {
+            const uint32_t w = x[c / 2] >> (16 * (c & 1));
+            v[c] = kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
+                        : __uint_as_float(w << 16);
+            top = fmaxf(top, fabsf(v[c]));
+            if (v[c] != v[c]) top = INFINITY;
+          }
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          const uint32_t bits = __float_as_uint(top);
+          int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+          e = min(max(e, -120), 120);
+          const float inv = pow2(-e);
+          uint16_t num[kMine / 2][kNum];
 #pragma unroll
-        for (int c = 0; c < kMine; c += 2) numbers_of<kNum>(v[c] * inv, v[c + 1] * inv, num[c / 2]);
+          for (int c = 0; c < kMine; c += 2)
+            numbers_of<kNum>(v[c] * inv, v[c + 1] * inv, num[c / 2]);
 #pragma unroll
-        for (int k = 0; k < kNum; ++k) {
-          unsigned char* to = smem + swizzled<kDim>(k * wide + r, lane * kMine);
-          if constexpr (kMine == 4)
-            *reinterpret_cast<uint32_t*>(to) = num[0][k] | (uint32_t)num[1][k] << 16;
-          else
-            *reinterpret_cast<uint16_t*>(to) = num[0][k];
+          for (int k = 0; k < kNum; ++k) {
+            unsigned char* to = smem + swizzled<kDim>(k * wide + r, lane * kMine);
+            if constexpr (kMine == 4)
+              *reinterpret_cast<uint32_t*>(to) = num[0][k] | (uint32_t)num[1][k] << 16;
+            else
+              *reinterpret_cast<uint16_t*>(to) = num[0][k];
+          }
+          // (a row with NaN or an infinity has NaN for its factor)
+          if (lane == 0)
+            qscale[(no & 1) * kRows + r] = top <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
         }
-        // (a row with NaN or an infinity has NaN for its factor)
-        if (lane == 0)
-          qscale[slot * kRows + r] = top <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&m.raw_empty);
+          mbar_arrive(&m.q_full);
+        }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&m.raw_empty);
-        mbar_arrive(&m.q_full);
+      // the last products of every stream
+#pragma unroll 1
+      for (int z = 0; z < 4; ++z) wait(&m.p_done[z], count_of(counts, z) & 1u ^ 1u, 0xB57);
+      gone = !ok;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.s32 p, %0, 0;\n\t"
+          "bar.red.or.pred q, 2, 512, p;\n\t"
+          "selp.s32 %0, 1, 0, q;\n\t}"
+          : "+r"(gone)::"memory");
+      if (gone) break;
+      if (pt) {
+        // ---- the present part's results out
+        const int n = pt->n, shift = pt->shift, streams = 1 << shift;
+        umma::fence_after_sync();
+        const bool spoils = *static_cast<volatile int*>(&m.spoils);
+        float* slot = p.part + (size_t)(2 * blockIdx.x + (pt->ends ? 0 : 1)) * slot_floats(kDim);
+        // What each column of each stream counts: its sums join those of the row's
+        // other streams, and are divided by Σ where the item is whole. The factors
+        // take the references' place; column i is that of row i % width of its
+        // stream.
+        const int width = kRows >> shift;
+        if (warp < 2) {
+          const int i = threadIdx.x - 128, row = i & (width - 1);
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+          for (int z = row; z < kRows; z += width) top = fmaxf(top, -refs[z]);
+#pragma unroll 1
+          for (int z = row; z < kRows; z += width) {
+            const float* l = stat + (z >> 4) * 64 + (z & 15);
+            // (a stream that saw none of the row's keys has zeros, or sums of NaN)
+            sum = fmaf(l[0] + l[16] + (l[32] + l[48]),
+                       top == -INFINITY ? 1.f : exp2_approx(-refs[z] - top), sum);
+          }
+          float by = top == -INFINITY ? 1.f : exp2_approx(-refs[i] - top);
+          if (pt->whole) {
+            by *= inverse(sum);
+          } else if (i < pt->rows) {
+            slot[kRows * kDim + i] = top;
+            slot[kRows * kDim + kRows + i] = sum;
+          }
+          asm volatile("bar.sync 7, 64;" ::: "memory");
+          refs[i] = by;
+        }
+        all_sync();
+        // A thread has column d of V, and its group a quarter of the rows (of one
+        // stream: the group's own).
+        const int d = kDim == 128 ? kt : quarter * 16 + (lane & 15);
+        const bool valid = kDim == 128 || lane < 16;
+        const int take = width / 4, from = g * take, rows = pt->rows, wide = pt->wide;
+        const uint32_t o_from = lanes + Z::kColO + from;
+        const unsigned long long spoilt =
+            spoils ? __ldcg(p.spoiled + blockIdx.x * 128 + d) : 0ull;
+        uint16_t* through = reinterpret_cast<uint16_t*>(smem + Z::kOffP);
+#pragma unroll 1
+        for (int i = 0; i < take && from + i < rows; i += 4) {
+          float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int z = 0; z < streams && z < n; ++z) {
+            uint32_t w[kNum][4];
+#pragma unroll
+            for (int e = 0; e < kNum; ++e)
+              umma::ld_x4(o_from + z * wide * Z::kWide + e * wide + i, w[e]);
+            const float4 by = *reinterpret_cast<const float4*>(refs + z * width + from + i);
+            const float f[4] = {by.x, by.y, by.z, by.w};
+            umma::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float v = __uint_as_float(w[0][c]);
+#pragma unroll
+              for (int e = 1; e < kNum; ++e)
+                v = fmaf(__uint_as_float(w[e][c]), number_unit(e), v);
+              o[c] = fmaf(v, f[c], o[c]);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int r = from + i + c;
+            if (spoilt >> r & 1ull) o[c] = NAN;
+            if (!valid) continue;
+            if (pt->whole)
+              through[r * kDim + d] = (uint16_t)round16<kF16>(o[c], 0.f);
+            else
+              slot[r * kDim + d] = o[c];
+          }
+        }
+        open = !pt->ends;
+        umma::fence_before_sync();
+        // O and the factors have been read before any stream goes on
+        all_sync();
+        if (pt->whole) {
+          // rows of results pass through P, 16 bytes a thread
+          constexpr int kPieces = kDim / 8;
+          uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)pt->row0 * a.out_token_stride +
+                          (int64_t)pt->h * a.group * a.out_head_stride;
+#pragma unroll 1
+          for (int i = threadIdx.x - 128; i < rows * kPieces; i += 512) {
+            const int r = i / kPieces, t = r / a.group;
+            *reinterpret_cast<uint4*>(out + t * a.out_token_stride +
+                                      (r - t * a.group) * a.out_head_stride + i % kPieces * 8) =
+                *reinterpret_cast<const uint4*>(through + i * 8);
+          }
+        }
+        if (spoils) {
+          if (threadIdx.x < 256) p.spoiled[blockIdx.x * 128 + threadIdx.x - 128] = 0;
+          if (threadIdx.x == 128) m.spoils = 0;
+        }
+        if (pt->whole || spoils) all_sync();
+        done_with_part();
       }
-    };
-    next_queries();
-    while (walk.next(&pt)) {
-      const Item& it = pt.it;
-      const int n = pt.n, streams = pt.streams, per = 4 / streams;  // groups of a stream
-      const int s = g / per, gl = g - s * per;
+      pt = then;
+      if (!pt) break;
+
+      // ---- a part's tiles
+      const int n = pt->n, shift = pt->shift, streams = 1 << shift, wide = pt->wide;
+      const int s = g >> (2 - shift), gl = g & (3 >> shift);  // stream, and group of it
       const int c0 = 16 * gl;                          // the group's first query row
-      const bool active = c0 < pt.wide;
-      const int pitch = pt.wide * Z::kWide;
-      const uint32_t s_addr = lanes + s * pitch + c0;
-      const uint32_t o_addr = lanes + Z::kColO + s * pitch + c0;
-      // a stream's barriers count 16: each of its 4·per warps arrives for 4 / per
-      const uint32_t weight = streams;
+      const bool active = c0 < wide;
+      const uint32_t column = s * wide * Z::kWide + c0;
+      const uint32_t s_addr = lanes + column, o_addr = s_addr + Z::kColO;
+      // a stream's barriers count 16: each of its 16 / streams warps arrives for as many
       auto arrive = [&](uint64_t* bar) {
         __syncwarp();
         if (lane == 0)
           asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
                            smem_addr(bar)),
-                       "r"(weight)
+                       "r"(streams)
                        : "memory");
       };
       // rows that do not exist stay out of every vote; the others' references are 0
       // until they have seen a key
-      if (quarter == 0 && lane < 16) ref[lane] = c0 + lane < pt.rows ? 0.f : -INFINITY;
-      uint32_t fresh = low_bits(pt.rows - c0) & 0xffffu;
+      if (quarter == 0 && lane < 16) ref[lane] = c0 + lane < pt->rows ? 0.f : -INFINITY;
+      uint32_t fresh = low_bits(pt->rows - c0) & 0xffffu;
       group_sync();
-      const float* factor = qscale + slot * kRows + c0;
+      const float* factor = qscale + (part_no & 1) * kRows + c0;
       uint64_t sums[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) sums[c] = 0;
       uint32_t k = count_of(counts, s);
-      int sc_at = sc_first + s;                        // the next tile's scales
+      int sc_j = sc_at + s;                            // the next tile's scales
       uint32_t sc_p = sc_parity;
-      if (sc_at >= kScaleSlots) sc_at -= kScaleSlots, sc_p ^= 1u;
+      if (sc_j >= kScaleSlots) sc_j -= kScaleSlots, sc_p ^= 1u;
 #pragma unroll 1
       for (int j = s; j < n; j += streams, ++k) {
-        const int key0 = pt.tile(j) * kTile, key = key0 + kt;
         wait(&m.s_full[s], k & 1u, 0xB51);
         // (a lost wait leaves the sums wrong, and the barriers in step)
-        if (!active) {
-          arrive(&m.s_empty[s]);
-          wait(&m.p_done[s], k & 1u ^ 1u, 0xB52);
-        }
-        const bool edge = tile_some_see(a, it, key0) || key0 + kTile > it.hi ||
-                          (key0 < it.lo && key0 + kTile > it.sk);
-        // rows of the item that see the key: [n0, n1)
-        int n0 = 0, n1 = kRows;
-        if (edge) {
-          asm volatile("" ::: "memory");               // (a branch, and not selections for every tile)
-          const long long g0 = (long long)key - it.pos0;
-          n0 = (int)min(max(g0, 0ll), (long long)it.ntok) * a.group;
-          n1 = it.ntok * a.group;
-          if (a.window > 0 && key >= a.sinks)
-            n1 = (int)min(max(g0 + a.window, 0ll), (long long)it.ntok) * a.group;
-        }
+        wait(&m.sc_full[sc_j], sc_p, 0xB53);
+        const float* sc = scale_slots + sc_j * kScaleWords;
+        const bool edge = __float_as_int(sc[2 * kScaleBlocks + 1]);
         if (active) {
           umma::fence_after_sync();
           uint32_t x[16], y[kNum - 1][16];
           umma::ld_x16(s_addr, x);
 #pragma unroll
-          for (int i = 1; i < kNum; ++i) umma::ld_x16(s_addr + i * pt.wide, y[i - 1]);
-          wait(&m.sc_full[sc_at], sc_p, 0xB53);
-          const float* sc = scale_slots + sc_at * 2 * kScaleBlocks + (kt >> 4);
-          sc_at += streams;
-          if (sc_at >= kScaleSlots) sc_at -= kScaleSlots, sc_p ^= 1u;
-          const float ks = sc[0], lv = sc[kScaleBlocks];
+          for (int i = 1; i < kNum; ++i) umma::ld_x16(s_addr + i * wide, y[i - 1]);
+          const float ks = sc[kt >> 4], lv = sc[kScaleBlocks + (kt >> 4)];
           const float iv = exp2_approx(kBase - lv);    // 1 / vs
           umma::wait_ld();
           umma::fence_before_sync();
@@ -813,7 +1005,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
                        add2(lv2, pair_f(r.z, r.w))), &t[c + 2], &t[c + 3]);
           }
           if (edge) {
-            asm volatile("" ::: "memory");
+            int n0, n1;
+            visible(a, *pt, __float_as_int(sc[2 * kScaleBlocks]) + kt, &n0, &n1);
             const uint32_t seen = low_bits(n1 - c0) & ~low_bits(n0 - c0);
 #pragma unroll
             for (int c = 0; c < 16; ++c) t[c] = seen >> c & 1u ? t[c] : -INFINITY;
@@ -885,58 +1078,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
               const float by = __shfl_sync(0xffffffffu, keep, c);
               uint32_t o[kNum];
 #pragma unroll
-              for (int i = 0; i < kNum; ++i) o[i] = umma::ld_x1(o_addr + i * pt.wide + c);
+              for (int i = 0; i < kNum; ++i) o[i] = umma::ld_x1(o_addr + i * wide + c);
               umma::wait_ld();
 #pragma unroll
               for (int i = 0; i < kNum; ++i)
-                umma::st_x1(o_addr + i * pt.wide + c, __float_as_uint(__uint_as_float(o[i]) * by));
+                umma::st_x1(o_addr + i * wide + c, __float_as_uint(__uint_as_float(o[i]) * by));
             }
             umma::wait_st();
             umma::fence_before_sync();
           }
 #pragma unroll
           for (int i = 0; i < kNum; ++i) {
-            const uint32_t col = s * pitch + i * pt.wide + c0;
-            *reinterpret_cast<uint4*>(smem + Z::kOffP + (col >> 7) * (kTile * 128) +
-                                      swizzled<128>(kt, col & 127u)) =
+            const uint32_t at = column + i * wide;
+            *reinterpret_cast<uint4*>(smem + Z::kOffP + (at >> 7) * (kTile * 128) +
+                                      swizzled<128>(kt, at & 127u)) =
                 make_uint4(num[i][0], num[i][1], num[i][2], num[i][3]);
           }
+        } else {
+          arrive(&m.s_empty[s]);
+          wait(&m.p_done[s], k & 1u ^ 1u, 0xB52);
         }
         if (edge) {
-          // the stream's groups share the tile's rows of V: what no row of the item
-          // sees becomes zeros, NaN that some see and others do not is taken out
-          const Place<kStages> at((unsigned)(ring + pt.place_v(j)) % (2u * kStages));
+          const Place<kStages> at(ring + place_v(j, streams, n));
           wait(&m.full[at.stage()], at.parity(), 0xB56);
-          const bool none = key >= it.hi || (key < it.lo && key >= it.sk);
-          if (ok && (none || some_see(a, it.pos0, it.hi, key))) {
-            unsigned char* v = smem + Z::kOffRing + at.stage() * Z::kTileBytes + kt * kDim;
-#pragma unroll 1
-            for (int c = gl; c < kDim / 16; c += per) {
-              uint4* to = reinterpret_cast<uint4*>(v + c * 16);
-              if (none) {
-                *to = make_uint4(0, 0, 0, 0);
-                continue;
-              }
-              uint32_t w[4] = {to->x, to->y, to->z, to->w};
-              if (!(nan_bytes(w[0]) | nan_bytes(w[1]) | nan_bytes(w[2]) | nan_bytes(w[3]))) continue;
-              const int d0 = (int)(swizzled<kDim>(kt, c * 16) - kt * kDim);  // its first column
-#pragma unroll 1
-              for (int i = 0; i < 16; ++i) {
-                if (!(nan_bytes(w[i >> 2]) >> (8 * (i & 3)) & 0x80u)) continue;
-                w[i >> 2] &= ~(0xffu << (8 * (i & 3)));
-                const unsigned long long rows =
-                    (n1 >= 64 ? ~0ull : (1ull << n1) - 1) & ~(n0 >= 64 ? ~0ull : (1ull << n0) - 1);
-                atomicOr(p.spoiled + blockIdx.x * 128 + d0 + i, n0 < n1 ? rows : 0ull);
-                *static_cast<volatile int*>(&m.spoils) = 1;
-              }
-              *to = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
+          if (ok)
+            clean_values<kDim>(a, *pt, smem + Z::kOffRing + at.stage() * Z::kTileBytes,
+                               __float_as_int(sc[2 * kScaleBlocks]), gl, 4 >> shift,
+                               p.spoiled + blockIdx.x * 128, &m.spoils);
         }
         fence_proxy_async_smem();
         arrive(&m.p_full[s]);
+        sc_j += streams;
+        if (sc_j >= kScaleSlots) sc_j -= kScaleSlots, sc_p ^= 1u;
       }
-      // ---- results out
       // the sums over keys: 16 columns of 32 lanes, by halves
       {
         float v[16];
@@ -947,115 +1121,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           const bool up = lane & (2 * half);
 #pragma unroll
           for (int i = 0; i < half; ++i) {
-            const float give = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * half);
+            const float give = up ? v[i] : v[i + half], stays = up ? v[i + half] : v[i];
+            v[i] = stays + __shfl_xor_sync(0xffffffffu, give, 2 * half);
           }
         }
         v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
         if (!(lane & 1)) mine[lane >> 1] = v[0];
       }
-      counts = add_counts(counts, pt);
-      // the next item's queries, once the last products with these are done (the
-      // tensor cores begin with them while this item's results go out)
-#pragma unroll 1
-      for (int z = 0; z < 4; ++z) wait(&m.s_full[z], count_of(counts, z) & 1u ^ 1u, 0xB59);
-      slot ^= 1;
-      next_queries();
       // (a column that saw no key has no reference)
       if (quarter == 0 && lane < 16 && (fresh >> lane & 1u)) ref[lane] = INFINITY;
-      if (n > s) wait(&m.p_done[s], k & 1u ^ 1u, 0xB57);  // the stream's last product
-      all_sync();
-      umma::fence_after_sync();
-      const bool spoils = *static_cast<volatile int*>(&m.spoils);
-      float* part = p.part + (size_t)(2 * blockIdx.x + (pt.ends ? 0 : 1)) * slot_floats(kDim);
-      // what each column of each stream counts: its sums join those of the row's
-      // other streams, and are divided by Σ where the item is whole. The factors
-      // take the references' place; column i is that of row i % width of its stream.
-      const int width = kRows >> pt.shift;
-      if (warp < 2) {
-        const int i = threadIdx.x - 128, row = i & (width - 1);
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll 1
-        for (int z = row; z < kRows; z += width) top = fmaxf(top, -refs[z]);
-#pragma unroll 1
-        for (int z = row; z < kRows; z += width) {
-          const float* l = stat + (z >> 4) * 64 + (z & 15);
-          // (a stream that saw none of the row's keys has zeros, or sums of NaN)
-          sum = fmaf(l[0] + l[16] + (l[32] + l[48]),
-                     top == -INFINITY ? 1.f : exp2_approx(-refs[z] - top), sum);
-        }
-        float by = top == -INFINITY ? 1.f : exp2_approx(-refs[i] - top);
-        if (pt.whole) by *= inverse(sum);
-        if (!pt.whole && i < pt.rows) {
-          part[kRows * kDim + i] = top;
-          part[kRows * kDim + kRows + i] = sum;
-        }
-        asm volatile("bar.sync 7, 64;" ::: "memory");
-        refs[i] = by;
-      }
-      all_sync();
-      // a thread has column d of V, and its group a quarter of the rows (of one
-      // stream: the group's own)
-      const int d = kDim == 128 ? kt : quarter * 16 + (lane & 15);
-      const bool valid = kDim == 128 || lane < 16;
-      const int take = width / 4, from = g * take;
-      const uint32_t o_from = lanes + Z::kColO + from;
-      int tok = from / a.group, head = from - tok * a.group;
-#pragma unroll 1
-      for (int i = 0; ok && i < take && from + i < pt.rows; i += 4) {
-        float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-        for (int z = 0; z < streams && z < n; ++z) {
-          uint32_t w[kNum][4];
-#pragma unroll
-          for (int e = 0; e < kNum; ++e) umma::ld_x4(o_from + z * pitch + e * pt.wide + i, w[e]);
-          const float4 by = *reinterpret_cast<const float4*>(refs + z * width + from + i);
-          const float f[4] = {by.x, by.y, by.z, by.w};
-          umma::wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float v = __uint_as_float(w[0][c]);
-#pragma unroll
-            for (int e = 1; e < kNum; ++e)
-              v = fmaf(__uint_as_float(w[e][c]), number_unit(e), v);
-            o[c] = fmaf(v, f[c], o[c]);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int r = from + i + c;
-          if (r < pt.rows && valid) {
-            if (spoils && (__ldcg(p.spoiled + blockIdx.x * 128 + d) >> r & 1ull)) o[c] = NAN;
-            if (pt.whole)
-              (static_cast<uint16_t*>(a.out) + (int64_t)(it.row0 + tok) * a.out_token_stride +
-               (int64_t)(walk.h * a.group + head) * a.out_head_stride)[d] =
-                  (uint16_t)round16<kF16>(o[c], 0.f);
-            else
-              part[r * kDim + d] = o[c];
-          }
-          if (++head == a.group) {
-            head = 0;
-            ++tok;
-          }
-        }
-      }
-      open = !pt.ends;
-      umma::fence_before_sync();
-      // O and the factors have been read before any stream goes on
-      all_sync();
-      if (spoils) {
-        if (threadIdx.x < 256) p.spoiled[blockIdx.x * 128 + threadIdx.x - 128] = 0;
-        if (threadIdx.x == 128) m.spoils = 0;
-        all_sync();
-      }
+      counts = add_counts(counts, n, shift);
       ring = (ring + 2 * n) % (2 * kStages);
-      const unsigned upto = (unsigned)(sc_first + n);
-      sc_first = (int)(upto % kScaleSlots);
+      const unsigned upto = (unsigned)(sc_at + n);
+      sc_at = (int)(upto % kScaleSlots);
       sc_parity ^= upto / kScaleSlots & 1u;
+      // all scores with these queries are there
+#pragma unroll 1
+      for (int z = 0; z < 4; ++z) wait(&m.s_full[z], count_of(counts, z) & 1u ^ 1u, 0xB59);
     }
     // The last part is left to the CTA that ends its item, and an item that began
     // in earlier ranges joined, when all of the range's results are there.
-    if (open || m.start.joins) {
+    if (!gone && (open || m.start.joins)) {
       all_sync();
       unsigned long long before = 0;                   // (used at the end: it takes a while)
       if (open && threadIdx.x == 128) before = exchange(p.left + blockIdx.x, p.call);
