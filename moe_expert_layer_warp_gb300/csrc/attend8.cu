@@ -40,11 +40,11 @@
 // own sums, joined at the end.
 //
 // Warps (one CTA per SM):
-//   0      TMA: key tiles into a ring, a box per page; the tiles' scales
+//   0      TMA: key tiles into a ring, a box per page
 //   1      MMA issue
 //   2      TMA: value tiles into the same ring
-//   3      the parts of the CTA's range, for the others to read; and the next
-//          part's query rows into shared memory
+//   3      ahead of the others: the parts of the CTA's range, their tiles' pages
+//          and scales, the next part's query rows into shared memory
 //   4-19   softmax, four groups of four warps: 16 columns of a tile each, or the
 //          tiles of a stream; and the next item's queries into e4m3 numbers
 //
@@ -52,6 +52,7 @@
 // NaN is NaN: rows of V that no row of the item sees are cleared, and NaN in rows
 // that some see and others do not is taken out of the tile and noted for the rows
 // that do see it (in `spoiled`, a bit per column of V and row).
+#include <stddef.h>
 #include <string.h>
 
 #include "attend8_mma.cuh"
@@ -74,29 +75,30 @@ constexpr float kGrow = 4.5f;     // m follows growth beyond this (powers of two
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
 // the 4 others leave 64 (4·104 + 64 = 5·96).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-constexpr int kScaleSlots = 8;    // tiles whose scales are there
+constexpr int kSlots = 16;        // tiles whose pages and scales are there
 constexpr int kScaleBlocks = kTile / 16;
 
 // kDim: columns of a head; kNum: e4m3 numbers of a query's element or a weight.
 template <int kDim, int kNum>
 struct Sizes {
-  static constexpr int kWide = kNum == 2 ? 2 : 4;  // columns set aside for a row's numbers
   static constexpr int kTileBytes = kTile * kDim;
   static constexpr int kQBytes = kRows * kNum * kDim;  // an item's queries as numbers
   static constexpr int kRawBytes = kRows * kDim * 2;   // and the next one's as they come
-  static constexpr int kPBytes = kTile * kRows * kWide;  // in 128-byte columns, kTile rows each
+  // Columns of S, of O and of P (a byte each): a quarter, half or all of them are a
+  // stream's. (A stream's P lies within 128 columns, or begins with them.)
+  static constexpr int kColumns = kNum == 2 ? 128 : 256;
+  static constexpr int kPBytes = kTile * kColumns;
   static constexpr int kStages = kDim == 64 ? 16 : kNum == 2 ? 10 : 9;
   static constexpr int kOffRaw = kQBytes;
   static constexpr int kOffP = kOffRaw + kRawBytes;
   static constexpr int kOffRing = kOffP + kPBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
-  static constexpr int kMiscBytes = 4608;
+  static constexpr int kMiscBytes = 6656;
   static constexpr int kSmem = kOffMisc + kMiscBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kTileBytes % 1024 == 0, "tiles");
   static_assert(kPBytes >= kRows * kDim * 2, "results pass through P");
-  static constexpr uint32_t kCols = kNum == 2 ? 256 : 512;  // tensor memory: S, then O
-  static constexpr uint32_t kColO = kRows * kWide;
+  static constexpr uint32_t kCols = 2 * kColumns, kColO = kColumns;  // tensor memory: S, O
 };
 // one slot of the workspace: O as [64 rows][dim] floats, then m and Σ
 constexpr size_t slot_floats(int dim) { return size_t(kRows) * (dim + 2); }
@@ -229,7 +231,7 @@ struct Misc {
   uint64_t part_full[kParts], part_empty[kParts];
   uint64_t raw_full, raw_empty;  // queries as they come
   uint64_t q_full;               // and as numbers
-  uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots];
+  uint64_t pg_full[kSlots], sc_full[kSlots], tile_done[kSlots];  // of a tile's slot
   uint64_t s_full[4], s_empty[4], p_full[4], p_done[4];  // of a stream
   uint64_t drain;
   Start start;
@@ -239,13 +241,18 @@ struct Misc {
   // NaN has been noted in the CTA's `spoiled` for the present item
   int spoils;
 };
-constexpr int kScaleWords = 2 * kScaleBlocks + 4;  // of a slot: ks, log2 vs + kBase; key0, edge
-constexpr int kOffRef = 896;                       // [4 groups][16] −m of a column
-constexpr int kOffQScale = kOffRef + 256;          // [2][64] a row's factor
-constexpr int kOffStat = kOffQScale + 512;         // [4 groups][4 warps][16]
-constexpr int kOffScale = kOffStat + 1024;
-constexpr int kOffParts = kOffScale + kScaleSlots * kScaleWords * 4;
-static_assert(kOffParts + kParts * (int)sizeof(Part) <= 4608, "misc words");
+// A tile's slot: ks, log2 vs + kBase and pages of its 16-key blocks; key0, edge
+struct Slot {
+  float ks[kScaleBlocks], lv[kScaleBlocks];
+  int page[kScaleBlocks];
+  int key0, edge;
+};
+constexpr int kOffRef = 1152;                      // [4 groups][rows] −m of a column
+constexpr int kOffQScale = kOffRef + 512;          // [2][64] a row's factor
+constexpr int kOffStat = kOffQScale + 512;         // [4 groups][4 warps][rows]
+constexpr int kOffSlots = kOffStat + 2048;
+constexpr int kOffParts = kOffSlots + kSlots * (int)sizeof(Slot);
+static_assert(kOffParts + kParts * (int)sizeof(Part) <= 6656, "misc words");
 
 // ln 2's reciprocal: scores are kept in powers of two.
 constexpr float kLog2e = 1.4426950408889634f;
@@ -257,24 +264,67 @@ MOE_DEV uint32_t swizzled(uint32_t row, uint32_t at) {
   return o ^ (o >> 3 & (kRow == 128 ? 0x70u : 0x30u));
 }
 
-// A wait that does not end at once (see wait_or_abort), kept out of the places
-// where it stands.
-MOE_DEV bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* lost,
-                                         int site) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, lost, site));
+// Barriers and words by their address in shared memory.
+MOE_DEV bool try_at(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+MOE_DEV bool try_at_longer(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return done != 0;
+}
+MOE_DEV int ld_shared(uint32_t at) {
+  int v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+MOE_DEV void ld_shared2(uint32_t at, uint64_t* a, uint64_t* b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(*a), "=l"(*b) : "r"(at) : "memory");
+}
+MOE_DEV void st_shared4(uint32_t at, const uint32_t* v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
-// Two values' e4m3 numbers: each is 16 times what the ones before it left. (In
+// A wait that does not end at once (see wait_or_abort).
+MOE_DEV bool wait_longer(uint32_t bar, uint32_t parity, volatile int* lost, int site) {
+  bool done = false;
+#pragma unroll 1
+  for (int i = 0; !done && i < kTries && *lost == 0; ++i)
+    done = __all_sync(0xffffffffu, try_at_longer(bar, parity));
+  if (!done && *lost == 0) *lost = site;
+  return __all_sync(0xffffffffu, done);
+}
+
+// Four values' e4m3 numbers: each is 16 times what the ones before it left. (In
 // fp16: the differences of numbers and their multiples by 16 are exact.)
 template <int kNum>
-MOE_DEV void numbers_of(float lo, float hi, uint16_t (&out)[kNum]) {
-  __half2 rest = __floats2half2_rn(lo, hi);
+MOE_DEV void numbers_of(float a, float b, float c, float d, uint32_t (&out)[kNum]) {
+  __half2 lo = __floats2half2_rn(a, b), hi = __floats2half2_rn(c, d);
 #pragma unroll
   for (int i = 0; i < kNum; ++i) {
-    out[i] = e4m3_of(rest);
-    if (i + 1 < kNum)
-      rest = __hfma2(half2_of(out[i]), __float2half2_rn(-16.f),
-                     __hmul2(rest, __float2half2_rn(16.f)));
+    out[i] = e4m3_of(lo, hi);
+    if (i + 1 < kNum) {
+      __half2 x, y;
+      halves_of(out[i], &x, &y);
+      lo = __hfma2(x, __float2half2_rn(-16.f), __hmul2(lo, __float2half2_rn(16.f)));
+      hi = __hfma2(y, __float2half2_rn(-16.f), __hmul2(hi, __float2half2_rn(16.f)));
+    }
   }
 }
 // What a number counts.
@@ -439,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   float* refs = reinterpret_cast<float*>(misc + kOffRef);
   float* qscale = reinterpret_cast<float*>(misc + kOffQScale);
   float* stat = reinterpret_cast<float*>(misc + kOffStat);
-  float* scale_slots = reinterpret_cast<float*>(misc + kOffScale);
+  Slot* slots = reinterpret_cast<Slot*>(misc + kOffSlots);
   Part* parts = reinterpret_cast<Part*>(misc + kOffParts);
   // the same value in every lane, and known to be
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0) - 4;
@@ -457,9 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     mbar_init(&m.raw_full, 32);                // the lanes that copy, with their copies
     mbar_init(&m.raw_empty, 16);
     mbar_init(&m.q_full, 16);
-    for (int i = 0; i < kScaleSlots; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&m.pg_full[i], 1);
       mbar_init(&m.sc_full[i], 1);
-      mbar_init(&m.sc_empty[i], 1);
+      mbar_init(&m.tile_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&m.s_full[i], 1);
@@ -491,10 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
 
   volatile int* lost = &m.lost;
   bool ok = true;  // no wait of this role has been lost
-  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
-      ok = wait_longer(bar, parity, lost, site) && ok;
+  auto wait_at = [&](uint32_t bar, uint32_t parity, int site) {
+    if (!__all_sync(0xffffffffu, try_at(bar, parity))) ok = wait_longer(bar, parity, lost, site) && ok;
   };
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) { wait_at(smem_addr(bar), parity, site); };
   // The parts, one after the other. A lost wait ends a role's walk: what a part
   // says may then be another's.
   int part_no = 0;
@@ -517,101 +568,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const bool keys = warp == -4;
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
-    const int n_pages = kTile / rows;           // pages of a tile (1 if a page spans tiles)
     // keys and values that one item reads alone are not kept in L2: the rows of
     // the other heads beside them are (single tokens 258 -> 243 us)
     const uint64_t stay = l2_evict_normal_policy(), go = l2_evict_first_policy();
     const CUtensorMap* map = keys ? &p.kmap : &p.vmap;
     const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
-    int slot = 0;
-    uint32_t slot_parity = 1;
+    const int block = min(lane * rows / 16, kScaleBlocks - 1);  // first of the lane's box
+    int tile_no = 0;
     for (const Part* pt; (pt = next()); done_with_part()) {
       const int n = pt->n, streams = 1 << pt->shift, head = pt->h;
-      const int32_t* table = a.block_table + (size_t)pt->b * a.max_blocks;
-      // this lane's page of tile j (−1: it has none, or no row of it is seen)
-      auto page_of = [&](int j) {
-        int pg = -1;
-        if (j < n && lane < n_pages) {
-          const int r0 = pt->tile(j) * kTile + lane * rows;
-          if (r0 < pt->hi && (r0 + rows > pt->lo || r0 < pt->sk)) {
-            pg = table[r0 >> p.page_shift];
-            if (pg < 0 || pg >= a.cache.n_pages) {
-              report_error(a.err, ERR_CHECK, 0xB21);
-              pg = (int)a.cache.n_pages;        // out of the map: the box reads zeros
-            }
-          }
-        }
-        return pg;
-      };
-      // this lane's scale of tile j: lanes 0-7 those of its keys, by 16, 8-15 of
-      // its values (1 where there is none, or none is wanted)
-      auto scale_of = [&](int j, int pg) {
-        const int e = lane & 7;
-        const int mine = __shfl_sync(0xffffffffu, pg, e * 16 / rows);
-        float s = 1.f;
-        if (lane < 16 && mine >= 0 && mine < a.cache.n_pages) {
-          const int key = pt->tile(j) * kTile + e * 16;
-          if (key < pt->hi && (key + 16 > pt->lo || key < pt->sk)) {
-            const int at = (key & (page - 1)) >> (p.page_shift - p.blocks_shift);
-            const float* from = lane < 8 ? a.cache.k_scale : a.cache.v_scale;
-            s = __ldg(from + ((((int64_t)mine * a.cache.n_kv_heads) + head) << p.blocks_shift) + at);
-          }
-        }
-        return s;
-      };
-      // pages are asked for four tiles ahead, scales two
-      int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2), pg3 = page_of(3);
-      float s0 = 1.f, s1 = 1.f;
-      if (keys) {
-        s0 = scale_of(0, pg0);
-        s1 = scale_of(1, pg1);
-      }
+      const uint64_t policy = pt->once ? go : stay;
 #pragma unroll 1
-      for (int j = 0; ok && j < n; ++j) {
-        const int pg4 = page_of(j + 4), tile = pt->tile(j);
-        float s2 = 1.f;
-        if (keys) s2 = scale_of(j + 2, pg2);
+      for (int j = 0; ok && j < n; ++j, ++tile_no) {
+        const int slot = tile_no & (kSlots - 1);
+        wait(&m.pg_full[slot], tile_no / kSlots & 1u, 0xB31);
+        const int pg = lane * rows < kTile ? slots[slot].page[block] : -1;
+        const int row = page > kTile ? slots[slot].key0 & (page - 1) : 0;
         const Place<kStages> at(ring + (keys ? place_k(j, streams) : place_v(j, streams, n)));
         const int stage = at.stage();
-        if (keys) {
-          wait(&m.sc_empty[slot], slot_parity, 0xB31);
-          const float least = pow2(MOE_KV8_MIN_EXP), most = pow2(MOE_KV8_MAX_EXP);
-          if (!(s0 >= least && s0 <= most)) {
-            report_error(a.err, ERR_CHECK, 0xB33);
-            s0 = s0 > most ? most : least;
-          }
-          if (lane >= 8) {                             // (a power of two's is exact)
-            const uint32_t bits = __float_as_uint(s0);
-            s0 = (bits & 0x7fffffu ? log2f(s0) : (float)((int)(bits >> 23) - 127)) + kBase;
-          }
-          const bool edge = tile >= pt->edge_hi || (tile < pt->edge_lo && tile >= pt->edge_sk);
-          if (lane == 16) s0 = __int_as_float(tile * kTile);
-          if (lane == 17) s0 = __int_as_float(edge);
-          if (lane < 18) scale_slots[slot * kScaleWords + lane] = s0;
-          __syncwarp();
-          if (ok && lane == 0) mbar_arrive(&m.sc_full[slot]);
-          if (++slot == kScaleSlots) {
-            slot = 0;
-            slot_parity ^= 1u;
-          }
-        }
         wait(&m.empty[stage], at.parity() ^ 1u, 0xB30);
         if (ok) {
-          const uint32_t wanted = __ballot_sync(0xffffffffu, pg0 >= 0);
+          const uint32_t wanted = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane == 0) mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim);
           __syncwarp();
-          const int row = page > kTile ? tile * kTile & (page - 1) : 0;
-          if (pg0 >= 0)
-            tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, head, row, pg0, &m.full[stage],
-                           pt->once ? go : stay);
+          if (pg >= 0)
+            tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, head, row, pg, &m.full[stage],
+                           policy);
           __syncwarp();
         }
-        pg0 = pg1;
-        pg1 = pg2;
-        pg2 = pg3;
-        pg3 = pg4;
-        s0 = s1;
-        s1 = s2;
       }
       ring = (ring + 2 * n) % (2 * kStages);
     }
@@ -630,13 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const uint32_t q_at = smem_addr(smem) >> 4;
     const uint32_t p_at = (smem_addr(smem) + Z::kOffP) >> 4;
     constexpr uint32_t kNextP = (kTile * 128u >> 4) << 16;  // the next 128 columns of P
-    int sc_slot = 0;
+    int tile_no = 0;
     auto commit = [&](uint64_t* bar) {                 // arrives when the MMAs so far are done
       if (ok) umma::commit_elect(bar);
     };
     for (const Part* pt; (pt = next()); done_with_part()) {
       const int n = pt->n, shift = pt->shift, streams = 1 << shift, cols = pt->wide * kNum;
-      const int pitch = pt->wide * Z::kWide;           // columns between streams
+      const int pitch = Z::kColumns >> shift;             // columns between streams
       const uint32_t id_s = umma::idesc_e4m3(kTile, cols, false);
       const uint32_t id_o = umma::idesc_e4m3(kDim, cols, true);
       // S may be laid out anew once the last scores of every stream are read
@@ -653,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           const Place<kStages> at(ring + place_k(i, streams));
           wait(&m.full[at.stage()], at.parity(), 0xB43);
           wait(&m.s_empty[s], k & 1u ^ 1u, 0xB44);
+          // (who waits for the scores then has the scales too)
+          wait(&m.sc_full[(tile_no + i) & (kSlots - 1)], (tile_no + i) / kSlots & 1u, 0xB47);
           umma::fence_after_sync();
           if (ok)
             umma::mma_e4m3<kSteps, kRowHi, kRowHi, 2, 2>(
@@ -677,10 +663,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
                 id_o, j >= streams ? 1u : 0u);
           commit(&m.p_done[s]);
           commit(&m.empty[at.stage()]);
-          commit(&m.sc_empty[sc_slot]);
-          if (++sc_slot == kScaleSlots) sc_slot = 0;
+          commit(&m.tile_done[(tile_no + j) & (kSlots - 1)]);
         }
       }
+      tile_no += n;
       counts = add_counts(counts, n, shift);
       ring = (ring + 2 * n) % (2 * kStages);
     }
@@ -692,49 +678,159 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp == -1) {
-    // -------------------------------------------------- parts and queries --
-    constexpr int kPieces = kDim / 8;                  // of a row, 16 bytes each
+    // ------------------------------------------------------------- ahead --
+    // Three things, each as soon as there is room for it: the parts; the pages and
+    // scales of four tiles at a time, 8 lanes a tile, a lane its 16 keys (the pages
+    // of the next four are asked for while the scales of these are on their way);
+    // a part's queries, 16 bytes a lane.
+    constexpr int kPieces = kDim / 8;                  // of a query row
     Walk w = m.start.w;
     Request r = m.start.r;
-    bool more = true;
-    int published = 0;
-    uint32_t parity = 1;
-    for (bool last = false; !last;) {
-      // parts are there three ahead of their queries, for the loaders
-      while (more && ok && published < part_no + 4) {
-        const int slot = published & (kParts - 1);
-        wait(&m.part_empty[slot], published >> 3 & 1u ^ 1u, 0xB61);
-        Part next_one;
-        more = next_part(p, w, r, &next_one);
-        if (!more) next_one.n = -1;
-        if (lane == 0) {
-          parts[slot] = next_one;
-          mbar_arrive(&m.part_full[slot]);
-        }
-        __syncwarp();
-        ++published;
-      }
-      const Part* pt = parts + (part_no & (kParts - 1));
-      wait(&m.raw_empty, parity, 0xB60);
-      parity ^= 1u;
-      last = !ok || pt->n < 0;
-      const int rows = last ? 0 : pt->rows;
-      const uint32_t to = smem_addr(smem) + Z::kOffRaw;
-      const uint16_t* from = static_cast<const uint16_t*>(a.q) +
-                             (int64_t)pt->row0 * a.q_token_stride +
-                             (int64_t)pt->h * a.group * a.q_head_stride;
+    bool more = true;                                  // parts to come
+    int published = 0, queries = 0;                    // parts
+    int tiles = 0, t_part = 0, t_next = 0;             // tiles written; the next one's part, and place in it
+    bool q_done = false;
+    const int q = lane >> 3, block = lane & 7;
+    const int page_mask = (1 << p.page_shift) - 1, block_shift = p.page_shift - p.blocks_shift;
+    const int box = min(page_mask + 1, kTile) / 16;    // blocks of a box
+    // the next four tiles: how many there are, and this lane's (tile < 0: none)
+    int count = 0, tile = -1, edge = 0, page = -1, head = 0;
+    bool wants = false;
+    auto ask = [&]() {
+      count = 0;
+      tile = page = -1;
+      wants = false;
 #pragma unroll 1
-      for (int i = lane; i < rows * kPieces; i += 32) {
-        const int row = i / kPieces, t = row / a.group;
-        const uint16_t* at = from + t * a.q_token_stride + (row - t * a.group) * a.q_head_stride +
-                             i % kPieces * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(at)
-                     : "memory");
+      for (int i = 0; i < 4; ++i) {
+        while (t_part < published && parts[t_part & (kParts - 1)].n >= 0 &&
+               t_next >= parts[t_part & (kParts - 1)].n) {
+          ++t_part;
+          t_next = 0;
+        }
+        const Part& pt = parts[t_part & (kParts - 1)];
+        if (t_part >= published || pt.n < 0) break;
+        if (q == i) {
+          tile = pt.tile(t_next);
+          head = pt.h;
+          edge = tile >= pt.edge_hi || (tile < pt.edge_lo && tile >= pt.edge_sk);
+          const int key = tile * kTile + block * 16;
+          wants = key < pt.hi && (key + 16 > pt.lo || key < pt.sk);  // some row sees of the block
+          if (wants) page = a.block_table[(size_t)pt.b * a.max_blocks + (key >> p.page_shift)];
+        }
+        ++t_next;
+        ++count;
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                       smem_addr(&m.raw_full))
-                   : "memory");
-      ++part_no;
+    };
+    int idle = 0;
+    while (ok && (more || !q_done || count || t_part < published - 1)) {
+      bool did = false;
+      // parts
+      if (more && published < min(queries, t_part) + kParts - 1) {
+        const int slot = published & (kParts - 1);
+        if (__all_sync(0xffffffffu, try_now(&m.part_empty[slot], published >> 3 & 1u ^ 1u))) {
+          Part next_one;
+          more = next_part(p, w, r, &next_one);
+          if (!more) next_one.n = -1;
+          if (lane == 0) {
+            parts[slot] = next_one;
+            mbar_arrive(&m.part_full[slot]);
+          }
+          __syncwarp();
+          ++published;
+          did = true;
+        }
+      }
+      if (count == 0 && t_part < published) ask();
+      // queries
+      if (!q_done && queries < published &&
+          __all_sync(0xffffffffu, try_now(&m.raw_empty, queries & 1u ^ 1u))) {
+        const Part& pt = parts[queries & (kParts - 1)];
+        const int rows = pt.n >= 0 ? pt.rows : 0;
+        q_done = pt.n < 0;
+        const uint32_t to = smem_addr(smem) + Z::kOffRaw;
+        const uint16_t* from = static_cast<const uint16_t*>(a.q) +
+                               (int64_t)pt.row0 * a.q_token_stride +
+                               (int64_t)pt.h * a.group * a.q_head_stride;
+#pragma unroll 1
+        for (int i = lane; i < rows * kPieces; i += 32) {
+          const int row = i / kPieces, t = row / a.group;
+          const uint16_t* at = from + t * a.q_token_stride + (row - t * a.group) * a.q_head_stride +
+                               i % kPieces * 8;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 16), "l"(at)
+                       : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_addr(&m.raw_full))
+                     : "memory");
+        ++queries;
+        did = true;
+      }
+      // tiles
+      if (count > 0) {
+        const int last = tiles + count - 1;            // (slots are given back in order)
+        if (__all_sync(0xffffffffu, try_now(&m.tile_done[last & (kSlots - 1)],
+                                            last / kSlots & 1u ^ 1u))) {
+          const int now = count, first = tiles, mine = tile, is_edge = edge;
+          int pg = page;
+          const bool there = wants && pg >= 0 && pg < a.cache.n_pages;
+          if (wants && !there) {
+            report_error(a.err, ERR_CHECK, 0xB21);
+            pg = (int)a.cache.n_pages;                 // out of the map: the box reads zeros
+          }
+          float ks = 1.f, vs = 1.f;
+          if (there) {
+            const int64_t at =
+                ((((int64_t)pg * a.cache.n_kv_heads) + head) << p.blocks_shift) +
+                ((mine * kTile + block * 16 & page_mask) >> block_shift);
+            ks = __ldg(a.cache.k_scale + at);
+            vs = __ldg(a.cache.v_scale + at);
+          }
+          // a box's page: that of any of its blocks that is wanted
+#pragma unroll
+          for (int o = 1; o < kScaleBlocks; o <<= 1) {
+            const int other = __shfl_xor_sync(0xffffffffu, pg, o);
+            if (o < box) pg = max(pg, other);
+          }
+          Slot& slot = slots[(first + q) & (kSlots - 1)];
+          if (mine >= 0) {
+            slot.page[block] = pg;
+            if (block == 0) {
+              slot.key0 = mine * kTile;
+              slot.edge = is_edge;
+            }
+          }
+          __syncwarp();
+          if (lane < now) mbar_arrive(&m.pg_full[(first + lane) & (kSlots - 1)]);
+          tiles += now;
+          ask();
+          const float least = pow2(MOE_KV8_MIN_EXP), most = pow2(MOE_KV8_MAX_EXP);
+          if (!(ks >= least && ks <= most && vs >= least && vs <= most)) {
+            report_error(a.err, ERR_CHECK, 0xB33);
+            ks = ks > most ? most : ks >= least ? ks : least;
+            vs = vs > most ? most : vs >= least ? vs : least;
+          }
+          const uint32_t bits = __float_as_uint(vs);   // (a power of two's is exact)
+          const float l = bits & 0x7fffffu ? log2f(vs) : (float)((int)(bits >> 23) - 127);
+          if (mine >= 0) {
+            slot.ks[block] = ks;
+            slot.lv[block] = l + kBase;
+          }
+          __syncwarp();
+          if (lane < now) mbar_arrive(&m.sc_full[(first + lane) & (kSlots - 1)]);
+          did = true;
+        }
+      }
+      if (did) {
+        idle = 0;
+      } else {
+        // (a limit of about half a second; see wait_or_abort)
+        __nanosleep(100);
+        if ((++idle & 255) == 255 && (*lost || idle > (1 << 22))) {
+          if (*lost == 0) *lost = 0xB60;
+          ok = false;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
@@ -744,14 +840,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const int g = warp >> 2, quarter = warp & 3;       // group, and the warp's quarter of a tile
     const int kt = threadIdx.x & 127;                  // key of the tile, TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);  // 32 · quarter in the upper half
-    float* ref = refs + g * 16;                        // −m of the group's columns
-    float* mine = stat + g * 64 + quarter * 16;
+    float* ref = refs + g * 16;                // −m of the group's columns
+    float* group_stat = stat + g * 4 * 16;     // [4 warps][rows]
     auto group_sync = [&]() {
       asm volatile("bar.sync %0, 128;" ::"r"(3 + g) : "memory");
     };
     auto all_sync = [&]() { asm volatile("bar.sync 2, 512;" ::: "memory"); };
-    int sc_at = 0;                                     // slot of the part's first scales
-    uint32_t sc_parity = 0;
+    int tile_no = 0;                                   // of the part's first tile
     bool open = false;                                 // the last part does not end its item
     const Part* pt = nullptr;                          // the present part
     int gone = 0;                                      // some warp has lost a wait: all of them stop
@@ -782,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           } else {
             x[0] = *reinterpret_cast<const uint32_t*>(at);
           }
-          float v[kMine];
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
           float top = 0.f;
 #pragma unroll
           for (int c = 0; c < kMine; ++c) {
@@ -797,17 +892,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
           e = min(max(e, -120), 120);
           const float inv = pow2(-e);
-          uint16_t num[kMine / 2][kNum];
-#pragma unroll
-          for (int c = 0; c < kMine; c += 2)
-            numbers_of<kNum>(v[c] * inv, v[c + 1] * inv, num[c / 2]);
+          uint32_t num[kNum];
+          numbers_of<kNum>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv, num);
 #pragma unroll
           for (int k = 0; k < kNum; ++k) {
             unsigned char* to = smem + swizzled<kDim>(k * wide + r, lane * kMine);
             if constexpr (kMine == 4)
-              *reinterpret_cast<uint32_t*>(to) = num[0][k] | (uint32_t)num[1][k] << 16;
+              *reinterpret_cast<uint32_t*>(to) = num[k];
             else
-              *reinterpret_cast<uint16_t*>(to) = num[0][k];
+              *reinterpret_cast<uint16_t*>(to) = (uint16_t)num[k];
           }
           // (a row with NaN or an infinity has NaN for its factor)
           if (lane == 0)
@@ -842,16 +935,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         // take the references' place; column i is that of row i % width of its
         // stream.
         const int width = kRows >> shift;
-        if (warp < 2) {
+        if (warp < kRows / 32) {
           const int i = threadIdx.x - 128, row = i & (width - 1);
           float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
           for (int z = row; z < kRows; z += width) top = fmaxf(top, -refs[z]);
 #pragma unroll 1
           for (int z = row; z < kRows; z += width) {
-            const float* l = stat + (z >> 4) * 64 + (z & 15);
+            const float* l = stat + z / 16 * (4 * 16) + z % 16;
             // (a stream that saw none of the row's keys has zeros, or sums of NaN)
-            sum = fmaf(l[0] + l[16] + (l[32] + l[48]),
+            sum = fmaf(l[0] + l[16] + (l[2 * 16] + l[3 * 16]),
                        top == -INFINITY ? 1.f : exp2_approx(-refs[z] - top), sum);
           }
           float by = top == -INFINITY ? 1.f : exp2_approx(-refs[i] - top);
@@ -861,28 +954,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             slot[kRows * kDim + i] = top;
             slot[kRows * kDim + kRows + i] = sum;
           }
-          asm volatile("bar.sync 7, 64;" ::: "memory");
+          asm volatile("bar.sync 7, %0;" ::"n"(kRows) : "memory");
           refs[i] = by;
         }
         all_sync();
-        // A thread has column d of V, and its group a quarter of the rows (of one
-        // stream: the group's own).
+        // A thread has column d of V, and its group a quarter of the rows.
         const int d = kDim == 128 ? kt : quarter * 16 + (lane & 15);
         const bool valid = kDim == 128 || lane < 16;
-        const int take = width / 4, from = g * take, rows = pt->rows, wide = pt->wide;
+        const int rows = pt->rows, wide = pt->wide, take = wide / 4, from = g * take;
         const uint32_t o_from = lanes + Z::kColO + from;
         const unsigned long long spoilt =
             spoils ? __ldcg(p.spoiled + blockIdx.x * 128 + d) : 0ull;
         uint16_t* through = reinterpret_cast<uint16_t*>(smem + Z::kOffP);
 #pragma unroll 1
-        for (int i = 0; i < take && from + i < rows; i += 4) {
+        for (int i = 0; i < take && from + i < rows; i += 4) {  // (take: a multiple of 4)
           float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int z = 0; z < streams && z < n; ++z) {
             uint32_t w[kNum][4];
 #pragma unroll
             for (int e = 0; e < kNum; ++e)
-              umma::ld_x4(o_from + z * wide * Z::kWide + e * wide + i, w[e]);
+              umma::ld_x4(o_from + z * (Z::kColumns >> shift) + e * wide + i, w[e]);
             const float4 by = *reinterpret_cast<const float4*>(refs + z * width + from + i);
             const float f[4] = {by.x, by.y, by.z, by.w};
             umma::wait_ld();
@@ -936,50 +1028,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       // ---- a part's tiles
       const int n = pt->n, shift = pt->shift, streams = 1 << shift, wide = pt->wide;
       const int s = g >> (2 - shift), gl = g & (3 >> shift);  // stream, and group of it
-      const int c0 = 16 * gl;                          // the group's first query row
+      const int c0 = 16 * gl;                  // the group's first query row
       const bool active = c0 < wide;
-      const uint32_t column = s * wide * Z::kWide + c0;
+      const uint32_t column = s * (Z::kColumns >> shift) + c0;
       const uint32_t s_addr = lanes + column, o_addr = s_addr + Z::kColO;
       // a stream's barriers count 16: each of its 16 / streams warps arrives for as many
-      auto arrive = [&](uint64_t* bar) {
+      auto arrive = [&](uint32_t bar) {
         __syncwarp();
-        if (lane == 0)
-          asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(
-                           smem_addr(bar)),
-                       "r"(streams)
-                       : "memory");
+        asm volatile(
+            "{\n\t.reg .pred e;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+            "r"(streams)
+            : "memory");
       };
       // rows that do not exist stay out of every vote; the others' references are 0
       // until they have seen a key
-      if (quarter == 0 && lane < 16) ref[lane] = c0 + lane < pt->rows ? 0.f : -INFINITY;
-      uint32_t fresh = low_bits(pt->rows - c0) & 0xffffu;
+      if (quarter == 0 && lane < 16)
+        ref[lane] = c0 + lane < pt->rows ? 0.f : -INFINITY;
+      uint32_t fresh = low_bits(min(pt->rows - c0, 16));
       group_sync();
       const float* factor = qscale + (part_no & 1) * kRows + c0;
       uint64_t sums[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) sums[c] = 0;
       uint32_t k = count_of(counts, s);
-      int sc_j = sc_at + s;                            // the next tile's scales
-      uint32_t sc_p = sc_parity;
-      if (sc_j >= kScaleSlots) sc_j -= kScaleSlots, sc_p ^= 1u;
+      // what a tile needs, as shared-memory addresses
+      const uint32_t bars = smem_addr(&m.s_full[s]), factors = smem_addr(factor), refs_at = smem_addr(ref);
+      constexpr uint32_t kEmpty = 32, kPFull = 64, kPDone = 96;  // of the stream's, behind s_full
+      const uint32_t first_slot = smem_addr(slots) + (kt >> 4) * 4;
+      uint32_t p_at[kNum];                             // of the thread's weights
+#pragma unroll
+      for (int i = 0; i < kNum; ++i) {
+        const uint32_t at = column + i * wide;
+        p_at[i] = smem_addr(smem) + Z::kOffP + (at >> 7) * (kTile * 128) + swizzled<128>(kt, at & 127u);
+      }
 #pragma unroll 1
       for (int j = s; j < n; j += streams, ++k) {
-        wait(&m.s_full[s], k & 1u, 0xB51);
+        wait_at(bars, k & 1u, 0xB51);
         // (a lost wait leaves the sums wrong, and the barriers in step)
-        wait(&m.sc_full[sc_j], sc_p, 0xB53);
-        const float* sc = scale_slots + sc_j * kScaleWords;
-        const bool edge = __float_as_int(sc[2 * kScaleBlocks + 1]);
+        const uint32_t slot = first_slot + (uint32_t)((tile_no + j) & (kSlots - 1)) * sizeof(Slot);
+        const int edge = ld_shared(slot + offsetof(Slot, edge) - (kt >> 4) * 4);
         if (active) {
           umma::fence_after_sync();
           uint32_t x[16], y[kNum - 1][16];
           umma::ld_x16(s_addr, x);
 #pragma unroll
           for (int i = 1; i < kNum; ++i) umma::ld_x16(s_addr + i * wide, y[i - 1]);
-          const float ks = sc[kt >> 4], lv = sc[kScaleBlocks + (kt >> 4)];
+          const float ks = __int_as_float(ld_shared(slot)),
+                      lv = __int_as_float(ld_shared(slot + offsetof(Slot, lv)));
           const float iv = exp2_approx(kBase - lv);    // 1 / vs
           umma::wait_ld();
           umma::fence_before_sync();
-          arrive(&m.s_empty[s]);
+          arrive(bars + kEmpty);
           // q · K
 #pragma unroll
           for (int i = 1; i < kNum; ++i) {
@@ -997,17 +1098,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           float t[16];
 #pragma unroll
           for (int c = 0; c < 16; c += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(factor + c);
-            const float4 r = *reinterpret_cast<const float4*>(ref + c);
-            split(fma2(mul2(pair(x[c], x[c + 1]), pair_f(f.x, f.y)), ks2,
-                       add2(lv2, pair_f(r.x, r.y))), &t[c], &t[c + 1]);
-            split(fma2(mul2(pair(x[c + 2], x[c + 3]), pair_f(f.z, f.w)), ks2,
-                       add2(lv2, pair_f(r.z, r.w))), &t[c + 2], &t[c + 3]);
+            uint64_t f0, f1, r0, r1;
+            ld_shared2(factors + c * 4, &f0, &f1);
+            ld_shared2(refs_at + c * 4, &r0, &r1);
+            split(fma2(mul2(pair(x[c], x[c + 1]), f0), ks2, add2(lv2, r0)), &t[c], &t[c + 1]);
+            split(fma2(mul2(pair(x[c + 2], x[c + 3]), f1), ks2, add2(lv2, r1)), &t[c + 2],
+                  &t[c + 3]);
           }
           if (edge) {
             int n0, n1;
-            visible(a, *pt, __float_as_int(sc[2 * kScaleBlocks]) + kt, &n0, &n1);
+            visible(a, *pt, slots[(tile_no + j) & (kSlots - 1)].key0 + kt, &n0, &n1);
             const uint32_t seen = low_bits(n1 - c0) & ~low_bits(n0 - c0);
+            asm volatile("" ::: "memory");             // (a branch, not selections at every tile)
 #pragma unroll
             for (int c = 0; c < 16; ++c) t[c] = seen >> c & 1u ? t[c] : -INFINITY;
           }
@@ -1033,16 +1135,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
               const float v = warp_max(t[c]);
-              if (lane == c) mine[c] = v;
+              if (lane == c) group_stat[quarter * 16 + c] = v;
             }
             group_sync();
-            float best = stat[g * 64 + col];
+            float best = group_stat[col];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) best = fmaxf(best, stat[g * 64 + w * 16 + col]);
+            for (int w = 1; w < 4; ++w) best = fmaxf(best, group_stat[w * 16 + col]);
             const bool first = fresh >> col & 1u;
             const bool follows = best > (first ? -INFINITY : kBase + kGrow);
             const float by = follows ? best - kBase : 0.f;
-            if (quarter == 0 && lane < 16 && follows) ref[lane] = ref_was - by;
+            if (quarter == 0 && lane < 16 && follows) ref[col] = ref_was - by;
             if (!first) keep = exp2_approx(-by);
             cols = __ballot_sync(0xffffffffu, follows) & 0xffffu;
             fresh &= ~cols;
@@ -1059,17 +1161,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           // weights, their sum, and their numbers
           uint32_t num[kNum][4];
 #pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float p0 = exp2_approx(t[c]), p1 = exp2_approx(t[c + 1]);
-            sums[c / 2] = fma2(pair_f(p0, p1), iv2, sums[c / 2]);
-            uint16_t v[kNum];
-            numbers_of<kNum>(p0, p1, v);
+          for (int c = 0; c < 16; c += 4) {
+            float w[4];
 #pragma unroll
-            for (int i = 0; i < kNum; ++i)
-              num[i][c / 4] = c & 2 ? num[i][c / 4] | (uint32_t)v[i] << 16 : v[i];
+            for (int e = 0; e < 4; ++e) w[e] = exp2_approx(t[c + e]);
+            sums[c / 2] = fma2(pair_f(w[0], w[1]), iv2, sums[c / 2]);
+            sums[c / 2 + 1] = fma2(pair_f(w[2], w[3]), iv2, sums[c / 2 + 1]);
+            uint32_t v[kNum];
+            numbers_of<kNum>(w[0], w[1], w[2], w[3], v);
+#pragma unroll
+            for (int i = 0; i < kNum; ++i) num[i][c / 4] = v[i];
           }
           // the product with the weights before them has read those, and added to O
-          wait(&m.p_done[s], k & 1u ^ 1u, 0xB55);
+          wait_at(bars + kPDone, k & 1u ^ 1u, 0xB55);
           if (cols && j >= streams) {
             umma::fence_after_sync();
 #pragma unroll 1
@@ -1088,28 +1192,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             umma::fence_before_sync();
           }
 #pragma unroll
-          for (int i = 0; i < kNum; ++i) {
-            const uint32_t at = column + i * wide;
-            *reinterpret_cast<uint4*>(smem + Z::kOffP + (at >> 7) * (kTile * 128) +
-                                      swizzled<128>(kt, at & 127u)) =
-                make_uint4(num[i][0], num[i][1], num[i][2], num[i][3]);
-          }
+          for (int i = 0; i < kNum; ++i) st_shared4(p_at[i], num[i]);
         } else {
-          arrive(&m.s_empty[s]);
-          wait(&m.p_done[s], k & 1u ^ 1u, 0xB52);
+          arrive(bars + kEmpty);
+          wait_at(bars + kPDone, k & 1u ^ 1u, 0xB52);
         }
         if (edge) {
           const Place<kStages> at(ring + place_v(j, streams, n));
           wait(&m.full[at.stage()], at.parity(), 0xB56);
           if (ok)
             clean_values<kDim>(a, *pt, smem + Z::kOffRing + at.stage() * Z::kTileBytes,
-                               __float_as_int(sc[2 * kScaleBlocks]), gl, 4 >> shift,
+                               slots[(tile_no + j) & (kSlots - 1)].key0, gl, 4 >> shift,
                                p.spoiled + blockIdx.x * 128, &m.spoils);
         }
         fence_proxy_async_smem();
-        arrive(&m.p_full[s]);
-        sc_j += streams;
-        if (sc_j >= kScaleSlots) sc_j -= kScaleSlots, sc_p ^= 1u;
+        arrive(bars + kPFull);
       }
       // the sums over keys: 16 columns of 32 lanes, by halves
       {
@@ -1126,15 +1223,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           }
         }
         v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-        if (!(lane & 1)) mine[lane >> 1] = v[0];
+        if (!(lane & 1)) group_stat[quarter * 16 + (lane >> 1)] = v[0];
       }
       // (a column that saw no key has no reference)
       if (quarter == 0 && lane < 16 && (fresh >> lane & 1u)) ref[lane] = INFINITY;
       counts = add_counts(counts, n, shift);
       ring = (ring + 2 * n) % (2 * kStages);
-      const unsigned upto = (unsigned)(sc_at + n);
-      sc_at = (int)(upto % kScaleSlots);
-      sc_parity ^= upto / kScaleSlots & 1u;
+      tile_no += n;
       // all scores with these queries are there
 #pragma unroll 1
       for (int z = 0; z < 4; ++z) wait(&m.s_full[z], count_of(counts, z) & 1u ^ 1u, 0xB59);

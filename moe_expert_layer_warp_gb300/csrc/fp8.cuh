@@ -16,17 +16,35 @@ MOE_DEV uint16_t e4m3_of(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-MOE_DEV uint16_t e4m3_of(__half2 v) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&v)));
-  return r;
-}
 
 // Two codes' values; fp16 holds every one.
 MOE_DEV __half2 half2_of(uint16_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
   return *reinterpret_cast<__half2*>(&r);
+}
+
+// Four values, a and b in the lower half; and four codes' values likewise.
+MOE_DEV uint32_t e4m3_of(__half2 a, __half2 b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 y, %2;\n\t"
+      "mov.b32 %0, {x, y};\n\t}"
+      : "=r"(r)
+      : "r"(*reinterpret_cast<uint32_t*>(&a)), "r"(*reinterpret_cast<uint32_t*>(&b)));
+  return r;
+}
+MOE_DEV void halves_of(uint32_t codes, __half2* a, __half2* b) {
+  uint32_t x, y;
+  asm("{\n\t.reg .b16 u, v;\n\t"
+      "mov.b32 {u, v}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, u;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, v;\n\t}"
+      : "=r"(x), "=r"(y)
+      : "r"(codes));
+  *a = *reinterpret_cast<__half2*>(&x);
+  *b = *reinterpret_cast<__half2*>(&y);
 }
 
 // Four codes' values.
