@@ -40,9 +40,10 @@
 // own sums, joined at the end.
 //
 // Warps (one CTA per SM):
-//   0      TMA: key tiles into a ring, a box per page
-//   1      MMA issue
-//   2      TMA: value tiles into the same ring
+//   0      TMA: key and value tiles into a ring, a box per page
+//   1, 2   MMA issue: scores, and results. (An MMA holds the warp that issues it for
+//          the 64 cycles that it takes, a wait that ends at once takes 100, a commit
+//          50: with both products in one warp that warp was what a tile took.)
 //   3      ahead of the others: the parts of the CTA's range, their tiles' pages
 //          and scales, the next part's query rows into shared memory
 //   4-19   softmax, four groups of four warps: 16 columns of a tile each, or the
@@ -209,6 +210,7 @@ struct Place {
   MOE_DEV explicit Place(unsigned from) : at((int)(from % (2u * kStages))) {}
   MOE_DEV int stage() const { return at >= kStages ? at - kStages : at; }
   MOE_DEV uint32_t parity() const { return at >= kStages; }
+  MOE_DEV void next() { at = at + 1 == 2 * kStages ? 0 : at + 1; }
 };
 
 // How many tiles each of the four streams has had, modulo 256, a byte each: all
@@ -233,7 +235,7 @@ struct Misc {
   uint64_t q_full;               // and as numbers
   uint64_t pg_full[kSlots], sc_full[kSlots], tile_done[kSlots];  // of a tile's slot
   uint64_t s_full[4], s_empty[4], p_full[4], p_done[4];  // of a stream
-  uint64_t drain;
+  uint64_t drain[2];
   Start start;
   long long part[8];
   uint32_t tmem;
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&m.part_full[i], 1);
-      mbar_init(&m.part_empty[i], 19);         // both loaders, the MMA warp, 16 of the softmax
+      mbar_init(&m.part_empty[i], 19);         // the loader, both MMA warps, 16 of the softmax
     }
     mbar_init(&m.raw_full, 32);                // the lanes that copy, with their copies
     mbar_init(&m.raw_empty, 16);
@@ -518,7 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       mbar_init(&m.p_full[i], 16);
       mbar_init(&m.p_done[i], 1);
     }
-    mbar_init(&m.drain, 1);
+    mbar_init(&m.drain[0], 1);
+    mbar_init(&m.drain[1], 1);
     fence_mbar_init();
     m.lost = m.spoils = 0;
     m.start.joins = 0;
@@ -546,6 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     if (!__all_sync(0xffffffffu, try_at(bar, parity))) ok = wait_longer(bar, parity, lost, site) && ok;
   };
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) { wait_at(smem_addr(bar), parity, site); };
+  auto wait_both = [&](uint64_t* a, uint32_t a_parity, uint64_t* b, uint32_t b_parity, int site) {
+    const bool first = try_at(smem_addr(a), a_parity), second = try_at(smem_addr(b), b_parity);
+    if (!__all_sync(0xffffffffu, first && second)) {
+      wait(a, a_parity, site);
+      wait(b, b_parity, site + 0x80);
+    }
+  };
   // The parts, one after the other. A lost wait ends a role's walk: what a part
   // says may then be another's.
   int part_no = 0;
@@ -563,31 +573,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   int ring = 0;     // place of the part's first tile, modulo twice the stages
 
   if (warp < 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-  if (warp == -4 || warp == -2) {
-    // ------------------------------------------------------------ loaders --
-    const bool keys = warp == -4;
+  if (warp == -4) {
+    // ------------------------------------------------------------- loader --
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     // keys and values that one item reads alone are not kept in L2: the rows of
     // the other heads beside them are (single tokens 258 -> 243 us)
     const uint64_t stay = l2_evict_normal_policy(), go = l2_evict_first_policy();
-    const CUtensorMap* map = keys ? &p.kmap : &p.vmap;
     const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
     const int block = min(lane * rows / 16, kScaleBlocks - 1);  // first of the lane's box
     int tile_no = 0;
+    Place<kStages> at(0);                       // the next place in the ring
     for (const Part* pt; (pt = next()); done_with_part()) {
       const int n = pt->n, streams = 1 << pt->shift, head = pt->h;
       const uint64_t policy = pt->once ? go : stay;
-#pragma unroll 1
-      for (int j = 0; ok && j < n; ++j, ++tile_no) {
-        const int slot = tile_no & (kSlots - 1);
-        wait(&m.pg_full[slot], tile_no / kSlots & 1u, 0xB31);
-        const int pg = lane * rows < kTile ? slots[slot].page[block] : -1;
-        const int row = page > kTile ? slots[slot].key0 & (page - 1) : 0;
-        const Place<kStages> at(ring + (keys ? place_k(j, streams) : place_v(j, streams, n)));
-        const int stage = at.stage();
-        wait(&m.empty[stage], at.parity() ^ 1u, 0xB30);
+      auto load = [&](const CUtensorMap* map, int j) {
+        const int slot = (tile_no + j) & (kSlots - 1), stage = at.stage();
+        wait_both(&m.pg_full[slot], (tile_no + j) / kSlots & 1u, &m.empty[stage],
+                  at.parity() ^ 1u, 0xB30);
         if (ok) {
+          const int pg = lane * rows < kTile ? slots[slot].page[block] : -1;
+          const int row = page > kTile ? slots[slot].key0 & (page - 1) : 0;
           const uint32_t wanted = __ballot_sync(0xffffffffu, pg >= 0);
           if (lane == 0) mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim);
           __syncwarp();
@@ -596,8 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
                            policy);
           __syncwarp();
         }
+        at.next();
+      };
+      // K_0 .. K_{streams-1}, then K_{j + streams} and V_j
+#pragma unroll 1
+      for (int j = -streams; ok && j < n; ++j) {
+        if (j + streams < n) load(&p.kmap, j + streams);
+        if (j >= 0) load(&p.vmap, j);
       }
-      ring = (ring + 2 * n) % (2 * kStages);
+      tile_no += n;
     }
     // After a lost wait the tiles still in flight must land before the CTA
     // ends; without one, every tile has been waited for by the MMA warp.
@@ -605,8 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
 #pragma unroll 1
       for (int i = 0; i < 2 * 500 * kStages; ++i) try_longer(&m.full[i / 1000], i & 1);
     }
-  } else if (warp == -3) {
+  } else if (warp == -3 || warp == -2) {
     // ---------------------------------------------------------------- MMA --
+    const bool scores = warp == -3;
     constexpr int kSteps = kDim / 32;
     constexpr uint32_t kRowHi = umma::kDescHi8<kDim>, kPHi = umma::kDescHi8<128>;
     constexpr uint32_t kOne = 1u << 16;                // (a K-major tile has no other distance)
@@ -620,47 +634,47 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     };
     for (const Part* pt; (pt = next()); done_with_part()) {
       const int n = pt->n, shift = pt->shift, streams = 1 << shift, cols = pt->wide * kNum;
-      const int pitch = Z::kColumns >> shift;             // columns between streams
-      const uint32_t id_s = umma::idesc_e4m3(kTile, cols, false);
-      const uint32_t id_o = umma::idesc_e4m3(kDim, cols, true);
-      // S may be laid out anew once the last scores of every stream are read
+      const int pitch = Z::kColumns >> shift;          // columns between streams
+      if (scores) {                                    // S = K · Qᵀ
+        const uint32_t id = umma::idesc_e4m3(kTile, cols, false);
+        // S may be laid out anew once the last scores of every stream are read
 #pragma unroll 1
-      for (int s = 0; s < 4; ++s) wait(&m.s_empty[s], count_of(counts, s) & 1u ^ 1u, 0xB41);
-      wait(&m.q_full, part_no & 1u, 0xB42);
+        for (int s = 0; s < 4; ++s) wait(&m.s_empty[s], count_of(counts, s) & 1u ^ 1u, 0xB41);
+        wait(&m.q_full, part_no & 1u, 0xB42);
 #pragma unroll 1
-      for (int j = -streams; ok && j < n; ++j) {
-        const int s = (j + streams) & (streams - 1);
-        const uint32_t count = count_of(counts, s);
-        if (j + streams < n) {                         // the scores of tile j + streams
-          const int i = j + streams;
-          const uint32_t k = count + (uint32_t)(i >> shift);
-          const Place<kStages> at(ring + place_k(i, streams));
-          wait(&m.full[at.stage()], at.parity(), 0xB43);
-          wait(&m.s_empty[s], k & 1u ^ 1u, 0xB44);
+        for (int j = 0; ok && j < n; ++j) {
+          const int s = j & (streams - 1);
+          const uint32_t k = count_of(counts, s) + (uint32_t)(j >> shift);
+          const Place<kStages> at(ring + place_k(j, streams));
           // (who waits for the scores then has the scales too)
-          wait(&m.sc_full[(tile_no + i) & (kSlots - 1)], (tile_no + i) / kSlots & 1u, 0xB47);
+          wait_both(&m.full[at.stage()], at.parity(), &m.sc_full[(tile_no + j) & (kSlots - 1)],
+                    (tile_no + j) / kSlots & 1u, 0xB43);
+          wait(&m.s_empty[s], k & 1u ^ 1u, 0xB44);
           umma::fence_after_sync();
           if (ok)
             umma::mma_e4m3<kSteps, kRowHi, kRowHi, 2, 2>(
                 tmem + s * pitch, (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
-                q_at & 0x3fffu | kOne, id_s, 0u);
+                q_at & 0x3fffu | kOne, id, 0u);
           commit(&m.s_full[s]);
           commit(&m.empty[at.stage()]);
         }
-        if (j >= 0) {                                  // Oᵀ (+)= Vᵀ · Pᵀ of tile j
-          const uint32_t k = count + (uint32_t)(j >> shift);
+      } else {                                         // Oᵀ (+)= Vᵀ · Pᵀ
+        const uint32_t id = umma::idesc_e4m3(kDim, cols, true);
+#pragma unroll 1
+        for (int j = 0; ok && j < n; ++j) {
+          const int s = j & (streams - 1);
+          const uint32_t k = count_of(counts, s) + (uint32_t)(j >> shift);
           const Place<kStages> at(ring + place_v(j, streams, n));
-          wait(&m.full[at.stage()], at.parity(), 0xB45);
-          wait(&m.p_full[s], k & 1u, 0xB46);
-          umma::fence_after_sync();
           const uint32_t first = s * pitch;            // column of P
+          wait_both(&m.p_full[s], k & 1u, &m.full[at.stage()], at.parity(), 0xB45);
+          umma::fence_after_sync();
           if (ok)
             umma::mma_e4m3<4, kRowHi, kPHi, (32 * kDim >> 4), (32 * 128 >> 4)>(
                 tmem + Z::kColO + s * pitch,
                 (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
                 (p_at + (first >> 7) * (kTile * 128 >> 4) + ((first & 127u) >> 4)) & 0x3fffu |
                     kNextP,
-                id_o, j >= streams ? 1u : 0u);
+                id, j >= streams ? 1u : 0u);
           commit(&m.p_done[s]);
           commit(&m.empty[at.stage()]);
           commit(&m.tile_done[(tile_no + j) & (kSlots - 1)]);
@@ -672,9 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     }
     // Every MMA, and every arrival that hangs on one, is done before tensor
     // memory is released.
-    umma::commit_elect(&m.drain);
+    umma::commit_elect(&m.drain[scores]);
 #pragma unroll 1
-    for (int i = 0; i < kTries && !try_longer(&m.drain, 0); ++i) {
+    for (int i = 0; i < kTries && !try_longer(&m.drain[scores], 0); ++i) {
     }
     __syncwarp();
   } else if (warp == -1) {
