@@ -126,6 +126,15 @@ struct Params {
   unsigned long long call;
 };
 
+// An item's units: first `cost`, then one for every key tile of a block of one
+// query tile, two for one of a block of two. A tile belongs to the CTA whose
+// range has its first unit.
+struct Units {
+  int cost, each, all;
+  MOE_DEV int tiles(int u) const {  // that begin before unit u
+    return (max(0, u - cost) + each - 1) >> (each - 1);
+  }
+};
 MOE_DEV Units units_of(const Params& p, const Item& it) {
   Units u;
   u.cost = it.hi > 0 ? kItemUnits : 0;  // (rows that see nothing are only cleared)
@@ -133,6 +142,12 @@ MOE_DEV Units units_of(const Params& p, const Item& it) {
   u.all = u.cost + it.n * u.each;
   return u;
 }
+
+// Units of a range, at least: 2 where a request has more rows than a query
+// tile. In blocks of two every range inside an item then begins a tile; in
+// blocks of one, ranges of one tile would save less than their joins cost
+// (three short prompts among three passes, 13.5 us for 11.7).
+MOE_DEV long long most_ranges(const Params&, long long total, int two) { return total >> two; }
 
 // The CTA's part of an item: tiles [t0, t1). Or two whole items of one request
 // that differ in their key head only (`pair`), a stream for each: the ring's

@@ -69,8 +69,9 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kRows = 64;         // query rows of an item, at most
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
-// What an item costs beside its tiles when the work is cut, in tiles.
-constexpr int kItemUnits = 3;
+// What an item costs beside its tiles when the work is cut, and 2 for every 16 rows
+// of it (see Units).
+constexpr int kItemUnits = 8;
 constexpr float kBase = 4.f;      // weights are held 2^4 larger
 constexpr float kGrow = 4.5f;     // m follows growth beyond this (powers of two)
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
@@ -118,13 +119,25 @@ struct Params {
   unsigned long long call;
 };
 
-MOE_DEV Units units_of(const Params&, const Item& it) {
+// An item's units, a quarter of what a tile of 64 query rows takes: first `cost`,
+// then `each` for every key tile. A tile belongs to the CTA whose range has its
+// first unit.
+struct Units {
+  int cost, each, all;
+  MOE_DEV int tiles(int u) const {  // that begin before unit u
+    return (int)((uint32_t)(max(0, u - cost) + each - 1) / (uint32_t)each);
+  }
+};
+MOE_DEV Units units_of(const Params& p, const Item& it) {
+  const int wide = (it.ntok * p.a.group + 15) >> 4;  // query rows, by 16
   Units u;
-  u.cost = it.hi > 0 ? kItemUnits : 0;  // (rows that see nothing are only cleared)
-  u.each = 1;
-  u.all = u.cost + it.n;
+  u.cost = it.hi > 0 ? kItemUnits + 2 * wide : 0;    // (rows that see nothing are only cleared)
+  u.each = it.hi <= 0 ? 2 : wide == 1 ? 2 : wide == 2 ? 3 : 4;
+  u.all = u.cost + it.n * u.each;
   return u;
 }
+// (A range of less than a tile would only add a part to be joined.)
+MOE_DEV long long most_ranges(const Params&, long long total, int) { return total >> 2; }
 
 // The CTA's part of an item, in shared memory: one warp walks the range, and the
 // others read what they need of a part when they need it. (With a copy of the walk
@@ -759,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (!q_done && queries < published &&
           __all_sync(0xffffffffu, try_now(&m.raw_empty, queries & 1u ^ 1u))) {
         const Part& pt = parts[queries & (kParts - 1)];
-        const int rows = pt.n >= 0 ? pt.rows : 0;
+        const int rows = pt.n > 0 ? pt.rows : 0;
         q_done = pt.n < 0;
         const uint32_t to = smem_addr(smem) + Z::kOffRaw;
         const uint16_t* from = static_cast<const uint16_t*>(a.q) +
@@ -878,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (!ok || then->n < 0) then = nullptr;
       if (then) {
         constexpr int kMine = kDim / 32;               // columns of a lane
-        const int rows = then->rows, wide = then->wide;
+        const int rows = then->n > 0 ? then->rows : 0, wide = then->wide;
         const float to_log2 = a.scale * kLog2e;
 #pragma unroll 1
         for (int r = warp; r < rows; r += 16) {
@@ -938,7 +951,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           "selp.s32 %0, 1, 0, q;\n\t}"
           : "+r"(gone)::"memory");
       if (gone) break;
-      if (pt) {
+      if (pt && pt->n == 0) {
+        // rows that see nothing
+        constexpr int kPieces = kDim / 8;
+        uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)pt->row0 * a.out_token_stride +
+                        (int64_t)pt->h * a.group * a.out_head_stride;
+        for (int i = threadIdx.x - 128; i < pt->rows * kPieces; i += 512) {
+          const int r = i / kPieces, t = r / a.group;
+          *reinterpret_cast<uint4*>(out + t * a.out_token_stride +
+                                    (r - t * a.group) * a.out_head_stride + i % kPieces * 8) =
+              make_uint4(0, 0, 0, 0);
+        }
+        open = false;
+        done_with_part();
+      } else if (pt) {
         // ---- the present part's results out
         const int n = pt->n, shift = pt->shift, streams = 1 << shift;
         umma::fence_after_sync();
@@ -1038,6 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       }
       pt = then;
       if (!pt) break;
+      if (pt->n == 0) continue;
 
       // ---- a part's tiles
       const int n = pt->n, shift = pt->shift, streams = 1 << shift, wide = pt->wide;

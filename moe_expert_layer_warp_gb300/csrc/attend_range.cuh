@@ -85,15 +85,6 @@ MOE_DEV bool tile_some_see(const Args& a, const Item& it, int key0) {
          (a.window > 0 && key0 + kTile > a.sinks && key0 < window_from(it.hi - 1, a.window));
 }
 
-// An item's units: first `cost`, then one for every key tile of a block of one
-// query tile, two for one of a block of two. A tile belongs to the CTA whose
-// range has its first unit.
-struct Units {
-  int cost, each, all;
-  MOE_DEV int tiles(int u) const {  // that begin before unit u
-    return (max(0, u - cost) + each - 1) >> (each - 1);
-  }
-};
 // Where a CTA is in its range; every role walks it by itself.
 struct Walk {
   int b, h, block, u0, left;
@@ -126,8 +117,10 @@ MOE_DEV long long divide(long long a, long long b) {
   return q;
 }
 
-// The CTA's range: prefix sums over the requests' units, then the place of
-// its first one. The first kPlanThreads threads call it, warps converged;
+// The CTA's range: prefix sums over the requests' units (units_of(p, item): how
+// many there are, and which tiles begin before one), then the place of its first
+// one. most_ranges(p, total, two): how many ranges that many units are cut into at
+// most, `two` when a request has more rows than a query tile. The first kPlanThreads threads call it, warps converged;
 // `count` [MOE_MAX_REQUESTS] and `part` [8] are shared memory. (Every loop
 // stays a loop: unrolled, this took a quarter of the kernel's instructions,
 // which are fetched anew by every launch.)
@@ -187,17 +180,14 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
     if (lane >= o) incl += t;
   }
   if (lane == min(B, 32) - 1) part[warp] = incl;
-  // Units of a range, at least: 2 where a request has more rows than a query
-  // tile. In blocks of two every range inside an item then begins a tile; in
-  // blocks of one, ranges of one tile would save less than their joins cost
-  // (three short prompts among three passes, 13.5 us for 11.7).
-  int least = any_two;
+  // whether a request has more rows than a query tile
+  int two = any_two;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.s32 p, %0, 0;\n\t"
       "bar.red.or.pred q, 1, 256, p;\n\t"
-      "selp.s32 %0, 2, 1, q;\n\t}"
-      : "+r"(least)::"memory");
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "+r"(two)::"memory");
   long long before = incl - sum, total = 0;
 #pragma unroll 1
   for (int w = 0; w < kPlanThreads / 32 && w * 32 * per < B; ++w) {
@@ -208,7 +198,7 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
   before *= H;
   sum *= H;
   // the first `more` ranges are one unit longer than the others
-  const long long C = min((long long)gridDim.x, total >> (least - 1)), c = blockIdx.x;
+  const long long C = min((long long)gridDim.x, most_ranges(p, total, two)), c = blockIdx.x;
   const long long each = C > 0 ? divide(total, C) : 0, more = total - each * C;
   const long long w0 = c * each + min(c, more), w1 = c < C ? w0 + each + (c < more ? 1 : 0) : w0;
   if (tid == 0) {
@@ -233,7 +223,7 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
   for (int q0 = 0; q0 * fixed < r.q; q0 += 32) {
     const int q = q0 + lane;
     Item it;
-    Units units;
+    decltype(units_of(p, it)) units;
     long long n = 0, upto;
     if (q * fixed < r.q) {
       it = make_item(a, r, q, fixed);
