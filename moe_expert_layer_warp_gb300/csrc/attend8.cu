@@ -69,9 +69,9 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kRows = 64;         // query rows of an item, at most
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
-// What an item costs beside its tiles when the work is cut, and 2 for every 16 rows
-// of it (see Units).
-constexpr int kItemUnits = 8;
+// What an item costs beside its tiles when the work is cut, and what every 16 rows of
+// it add (see Units).
+constexpr int kItemUnits = 32, kItemRowUnits = 7;
 constexpr float kBase = 4.f;      // weights are held 2^4 larger
 constexpr float kGrow = 4.5f;     // m follows growth beyond this (powers of two)
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
@@ -119,9 +119,11 @@ struct Params {
   unsigned long long call;
 };
 
-// An item's units, a quarter of what a tile of 64 query rows takes: first `cost`,
+// An item's units, an eighth of what a tile of 64 query rows takes: first `cost`,
 // then `each` for every key tile. A tile belongs to the CTA whose range has its
-// first unit.
+// first unit. (Fitted to the times of 8 batches' ranges: tiles of 16, 32, 48 and 64
+// rows took 0.9, 1.1, 1.4 and 1.6 thousand cycles, a part of an item 7.9, 8.5, 10.8 and
+// 12.1 besides.)
 struct Units {
   int cost, each, all;
   MOE_DEV int tiles(int u) const {  // that begin before unit u
@@ -131,20 +133,20 @@ struct Units {
 MOE_DEV Units units_of(const Params& p, const Item& it) {
   const int wide = (it.ntok * p.a.group + 15) >> 4;  // query rows, by 16
   Units u;
-  u.cost = it.hi > 0 ? kItemUnits + 2 * wide : 0;    // (rows that see nothing are only cleared)
-  u.each = it.hi <= 0 ? 2 : wide == 1 ? 2 : wide == 2 ? 3 : 4;
-  u.all = u.cost + it.n * u.each;
+  u.cost = kItemUnits + kItemRowUnits * wide;
+  u.each = wide == 1 ? 4 : wide == 2 ? 5 : wide == 3 ? 7 : 8;
+  u.all = it.hi > 0 ? u.cost + it.n * u.each : 0;    // (see clear_blind)
   return u;
 }
 // (A range of less than a tile would only add a part to be joined.)
-MOE_DEV long long most_ranges(const Params&, long long total, int) { return total >> 2; }
+MOE_DEV long long most_ranges(const Params&, long long total, int) { return total >> 3; }
 
 // The CTA's part of an item, in shared memory: one warp walks the range, and the
 // others read what they need of a part when they need it. (With a copy of the walk
 // and of the part in registers of every warp, a tile took a third more
 // instructions: what did not fit was worked out again at every tile.)
 struct Part {
-  int n;              // tiles; 0: its rows see nothing; −1: there are no more parts
+  int n;              // tiles; −1: there are no more parts
   int rows, wide;     // query rows, and those rounded up: 16, 32, 48 or 64
   int shift;          // log2 of the streams: 2, 1 or 0
   int whole, ends;    // all of the item; its last tile
@@ -176,7 +178,7 @@ MOE_DEV bool next_part(const Params& p, Walk& w, Request& r, Part* out) {
     const Units units = units_of(p, it);
     const int u1 = min(w.u0 + w.left, units.all);
     const int t0 = units.tiles(w.u0), t1 = units.tiles(u1), n = t1 - t0;
-    out->n = it.hi > 0 ? n : 0;
+    out->n = n;
     out->rows = it.ntok * a.group;
     out->wide = (out->rows + 15) & ~15;
     out->shift = out->wide == 16 ? 2 : out->wide == 32 ? 1 : 0;
@@ -369,7 +371,7 @@ MOE_DEV void visible(const Attend8Args& a, const Part& pt, int key, int* n0, int
 // noted in `spoiled`. A thread takes the row of its key, the `per` groups of a
 // stream every per-th piece of it.
 template <int kDim>
-__device__ __noinline__ void clean_values(const Attend8Args& a, const Part& pt,
+MOE_DEV void clean_values(const Attend8Args& a, const Part& pt,
                                           unsigned char* tile, int key0, int gl, int per,
                                           unsigned long long* spoiled, int* spoils) {
   const int kt = threadIdx.x & 127, key = key0 + kt;
@@ -403,6 +405,34 @@ __device__ __noinline__ void clean_values(const Attend8Args& a, const Part& pt,
 template <int kDim>
 MOE_DEV const float* part_of(const Params& p, int cta, bool ends) {
   return p.part + (size_t)(2 * cta + (ends ? 0 : 1)) * slot_floats(kDim);
+}
+
+// Tokens that see nothing, at positions below 0 (a refused request's, whose cache
+// length is 0, or those of a cache shorter than the pass), have no part in the work
+// that is cut: the softmax threads of all CTAs share their rows, and clear them.
+template <int kDim>
+__device__ __noinline__ void clear_blind(const Attend8Args& a, int page_shift) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.n_requests; b0 += 32) {
+    Request mine = {0, 0, 0};
+    bool bad;
+    if (b0 + lane < a.n_requests) mine = request(a, page_shift, b0 + lane, &bad);
+#pragma unroll 1
+    for (uint32_t todo = __ballot_sync(0xffffffffu, mine.q > mine.len); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1, q = __shfl_sync(0xffffffffu, mine.q, from);
+      const int len = __shfl_sync(0xffffffffu, mine.len, from);
+      const int first = __shfl_sync(0xffffffffu, mine.first, from);
+      const int64_t n = (int64_t)(q - len) * a.n_heads * (kDim / 8);
+      for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x - 128; i < n; i += gridDim.x * 512) {
+        const int64_t row = i / (kDim / 8), t = row / a.n_heads;
+        uint16_t* to = static_cast<uint16_t*>(a.out) + (first + t) * a.out_token_stride +
+                       (row - t * a.n_heads) * a.out_head_stride;
+        reinterpret_cast<uint4*>(to)[i % (kDim / 8)] = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+    }
+  }
 }
 
 // The parts of an item joined in key order, those of CTAs `first` to this one: a
@@ -548,11 +578,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   pdl_trigger();
   if (threadIdx.x < 128) p.spoiled[blockIdx.x * 128 + threadIdx.x] = 0;
   // (the ring holds the plan's counts until the first tiles are on their way)
-  if (threadIdx.x < kPlanThreads)
+  int blind = 0;                               // some tokens see nothing
+  if (threadIdx.x < kPlanThreads) {
     find_start(p, reinterpret_cast<long long*>(smem + Z::kOffRing), m.part, &m.start);
+  } else {
+    for (int b = threadIdx.x - kPlanThreads; b < a.n_requests; b += kThreads - kPlanThreads) {
+      bool bad;
+      const Request r = request(a, p.page_shift, b, &bad);
+      blind |= r.q > r.len;
+    }
+  }
   fence_proxy_async_smem();
   umma::fence_before_sync();
-  __syncthreads();
+  blind = __syncthreads_or(blind);
   umma::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, m.tmem, 0);
 
@@ -772,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (!q_done && queries < published &&
           __all_sync(0xffffffffu, try_now(&m.raw_empty, queries & 1u ^ 1u))) {
         const Part& pt = parts[queries & (kParts - 1)];
-        const int rows = pt.n > 0 ? pt.rows : 0;
+        const int rows = pt.n >= 0 ? pt.rows : 0;
         q_done = pt.n < 0;
         const uint32_t to = smem_addr(smem) + Z::kOffRaw;
         const uint16_t* from = static_cast<const uint16_t*>(a.q) +
@@ -864,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     // ------------------------------------------------------------ softmax --
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     if (a.clear) clear_rows<kDim>(a);                  // while the first tiles are on their way
+    if (blind) clear_blind<kDim>(a, p.page_shift);
     const int g = warp >> 2, quarter = warp & 3;       // group, and the warp's quarter of a tile
     const int kt = threadIdx.x & 127;                  // key of the tile, TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)quarter << 21);  // 32 · quarter in the upper half
@@ -891,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (!ok || then->n < 0) then = nullptr;
       if (then) {
         constexpr int kMine = kDim / 32;               // columns of a lane
-        const int rows = then->n > 0 ? then->rows : 0, wide = then->wide;
+        const int rows = then->rows, wide = then->wide;
         const float to_log2 = a.scale * kLog2e;
 #pragma unroll 1
         for (int r = warp; r < rows; r += 16) {
@@ -951,20 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           "selp.s32 %0, 1, 0, q;\n\t}"
           : "+r"(gone)::"memory");
       if (gone) break;
-      if (pt && pt->n == 0) {
-        // rows that see nothing
-        constexpr int kPieces = kDim / 8;
-        uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)pt->row0 * a.out_token_stride +
-                        (int64_t)pt->h * a.group * a.out_head_stride;
-        for (int i = threadIdx.x - 128; i < pt->rows * kPieces; i += 512) {
-          const int r = i / kPieces, t = r / a.group;
-          *reinterpret_cast<uint4*>(out + t * a.out_token_stride +
-                                    (r - t * a.group) * a.out_head_stride + i % kPieces * 8) =
-              make_uint4(0, 0, 0, 0);
-        }
-        open = false;
-        done_with_part();
-      } else if (pt) {
+      if (pt) {
         // ---- the present part's results out
         const int n = pt->n, shift = pt->shift, streams = 1 << shift;
         umma::fence_after_sync();
@@ -1064,7 +1090,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       }
       pt = then;
       if (!pt) break;
-      if (pt->n == 0) continue;
 
       // ---- a part's tiles
       const int n = pt->n, shift = pt->shift, streams = 1 << shift, wide = pt->wide;

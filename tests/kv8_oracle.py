@@ -136,9 +136,10 @@ def attend(q, k, v, vs, q_start, kv_len, table, scale, window, sinks):
     number above 2^-6 is off by at most 2^-4 of itself, one below by 2^-10.
     Queries are scaled so that their row's largest is above 224: 8 (11) bits are
     exact, but for what is below 2^-10 · 16^-1 (16^-2), 2^-21.8 (2^-25.8) of the largest.
-    Weights are scaled so that the largest w · vs is 2^7 or more, and rounded to
+    Weights are scaled so that the largest w · vs is 2^4 or more, and rounded to
     fp16 before (2^-11 of themselves): off by 2^-8 + 2^-11 (2^-11 + 2^-12) of themselves
-    and 2^-14 · 2^-7 (2^-18 · 2^-7) of the largest.
+    and, where they are below 2^-6, by 2^-10 · 16^-1 = 2^-14 (2^-10 · 16^-2 = 2^-18), which is
+    2^-14 · 2^-4 (2^-18 · 2^-4) of the largest.
     The result is rounded to the type of q. Sums are fp32 (a score is off by at most
     (D + 8)·2^-22·scale·Σ|q k|: the tensor cores add e4m3 products with 2^-22 of
     the sum of their sizes, which was measured; that moves a weight by as much,
@@ -147,9 +148,9 @@ def attend(q, k, v, vs, q_start, kv_len, table, scale, window, sinks):
     page, H = k.shape[1], k.shape[2]
     per = Hq // H
     f16 = q.dtype == torch.float16
-    eps, w_rel, w_abs, q_abs = half_step(q.dtype), 2.0 ** -8 + 2.0 ** -11, 2.0 ** -21, 2.0 ** -21.8
+    eps, w_rel, w_abs, q_abs = half_step(q.dtype), 2.0 ** -8 + 2.0 ** -11, 2.0 ** -18, 2.0 ** -21.8
     if f16:
-        w_rel, w_abs, q_abs = 2.0 ** -11 + 2.0 ** -12, 2.0 ** -25, 2.0 ** -25.8
+        w_rel, w_abs, q_abs = 2.0 ** -11 + 2.0 ** -12, 2.0 ** -22, 2.0 ** -25.8
     tiny = 2.0 ** -25 if f16 else 2.0 ** -134
     out = torch.zeros((T, Hq, D), dtype=torch.float64, device=q.device)
     bound = torch.zeros((T, Hq, D), dtype=torch.float64, device=q.device)
