@@ -17,9 +17,11 @@
 // is hi + lo/16 (+ lolo/256), each number the rounding of 16 times what the ones
 // before it left; e4m3 has 4 significant bits, so two numbers hold the 8 of bf16
 // exactly, three the 11 of fp16, as long as they are within 2^-14 of the row's
-// largest. Weights are split likewise, times 2^7: m follows growth beyond 2^1.5
-// only, so they stay below 2^8.5, and 448 is e4m3's largest. The numbers are
-// columns of one operand beside each other, so a product takes them at once.
+// largest. Weights are split likewise, times 2^4: m follows growth beyond 2^4.5
+// only, so they stay below 2^8.5, and 448 is e4m3's largest; a weight is off by
+// 2^-8 (2^-12) of itself, or 2^-18 (2^-22) of the largest where that is more. The
+// numbers are columns of one operand beside each other, so a product takes them at
+// once.
 //
 // Tiles. Keys are the rows of both products, query rows their columns:
 //   Sᵀ = K · Qᵀ   128 keys × (16 to 64 query rows, times 2 or 3), and
@@ -48,6 +50,18 @@
 //          and scales, the next part's query rows into shared memory
 //   4-19   softmax, four groups of four warps: 16 columns of a tile each, or the
 //          tiles of a stream; and the next item's queries into e4m3 numbers
+//
+// What bounds it, beside the rates measured for a copy and a dense product (6.65
+// TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 228
+// us, 5.7 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 100 us for 456 MB
+// that a copy moves in 69, and 110 for 61 within a window: a CTA has few tiles, and
+// its start, its joins and its parts of items (8 to 12 thousand cycles each; a tile 0.9
+// to 1.6) are half of its time. Long prompts' chunks: 560 us, 471 TFLOP/s: a tile of 64
+// rows takes 2500 cycles, half of them the softmax warps' instructions, most of those
+// for splitting weights into numbers, and half of them waits, of four warps of a
+// sub-partition for each other and for what they load (an instruction every other
+// cycle, tensor cores a sixth of the time). One pass of 5 tokens over 777 keys: 9 us
+// beyond an empty launch, the chain from the plan to a part's end.
 //
 // Values that are not finite (NaN; e4m3 has no infinities). A weight of 0 times
 // NaN is NaN: rows of V that no row of the item sees are cleared, and NaN in rows
@@ -198,7 +212,8 @@ MOE_DEV bool next_part(const Params& p, Walk& w, Request& r, Part* out) {
     out->gap = it.lo_tile - it.ns;
     // key0 + 127 > pos0; key0 below the last row's window and not all of it sinks
     out->edge_hi = (it.pos0 + 1) >> 7;
-    out->edge_lo = a.window > 0 ? (max(0, window_from(it.hi - 1, a.window)) + kTile - 1) / kTile : 0;
+    const int seen = a.window > 0 ? max(0, window_from(it.hi - 1, a.window)) : 0;
+    out->edge_lo = (seen + kTile - 1) / kTile;
     out->edge_sk = it.sk / kTile;
     w.left -= u1 - w.u0;
     w.u0 = 0;
@@ -371,9 +386,8 @@ MOE_DEV void visible(const Attend8Args& a, const Part& pt, int key, int* n0, int
 // noted in `spoiled`. A thread takes the row of its key, the `per` groups of a
 // stream every per-th piece of it.
 template <int kDim>
-MOE_DEV void clean_values(const Attend8Args& a, const Part& pt,
-                                          unsigned char* tile, int key0, int gl, int per,
-                                          unsigned long long* spoiled, int* spoils) {
+MOE_DEV void clean_values(const Attend8Args& a, const Part& pt, unsigned char* tile, int key0,
+                          int gl, int per, unsigned long long* spoiled, int* spoils) {
   const int kt = threadIdx.x & 127, key = key0 + kt;
   const bool none = key >= pt.hi || (key < pt.lo && key >= pt.sk);
   if (!none && !some_see(a, pt.pos0, pt.hi, key)) return;
@@ -597,9 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   volatile int* lost = &m.lost;
   bool ok = true;  // no wait of this role has been lost
   auto wait_at = [&](uint32_t bar, uint32_t parity, int site) {
-    if (!__all_sync(0xffffffffu, try_at(bar, parity))) ok = wait_longer(bar, parity, lost, site) && ok;
+    if (!__all_sync(0xffffffffu, try_at(bar, parity)))
+      ok = wait_longer(bar, parity, lost, site) && ok;
   };
-  auto wait = [&](uint64_t* bar, uint32_t parity, int site) { wait_at(smem_addr(bar), parity, site); };
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+    wait_at(smem_addr(bar), parity, site);
+  };
   auto wait_both = [&](uint64_t* a, uint32_t a_parity, uint64_t* b, uint32_t b_parity, int site) {
     const bool first = try_at(smem_addr(a), a_parity), second = try_at(smem_addr(b), b_parity);
     if (!__all_sync(0xffffffffu, first && second)) {
@@ -753,7 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     Request r = m.start.r;
     bool more = true;                                  // parts to come
     int published = 0, queries = 0;                    // parts
-    int tiles = 0, t_part = 0, t_next = 0;             // tiles written; the next one's part, and place in it
+    // tiles written; the next one's part, and place in it
+    int tiles = 0, t_part = 0, t_next = 0;
     bool q_done = false;
     const int q = lane >> 3, block = lane & 7;
     const int page_mask = (1 << p.page_shift) - 1, block_shift = p.page_shift - p.blocks_shift;
@@ -1120,14 +1138,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       for (int c = 0; c < 8; ++c) sums[c] = 0;
       uint32_t k = count_of(counts, s);
       // what a tile needs, as shared-memory addresses
-      const uint32_t bars = smem_addr(&m.s_full[s]), factors = smem_addr(factor), refs_at = smem_addr(ref);
+      const uint32_t bars = smem_addr(&m.s_full[s]);
+      const uint32_t factors = smem_addr(factor), refs_at = smem_addr(ref);
       constexpr uint32_t kEmpty = 32, kPFull = 64, kPDone = 96;  // of the stream's, behind s_full
       const uint32_t first_slot = smem_addr(slots) + (kt >> 4) * 4;
       uint32_t p_at[kNum];                             // of the thread's weights
 #pragma unroll
       for (int i = 0; i < kNum; ++i) {
         const uint32_t at = column + i * wide;
-        p_at[i] = smem_addr(smem) + Z::kOffP + (at >> 7) * (kTile * 128) + swizzled<128>(kt, at & 127u);
+        p_at[i] = smem_addr(smem) + Z::kOffP + (at >> 7) * (kTile * 128) +
+                  swizzled<128>(kt, at & 127u);
       }
 #pragma unroll 1
       for (int j = s; j < n; j += streams, ++k) {

@@ -120,10 +120,10 @@ MOE_DEV long long divide(long long a, long long b) {
 // The CTA's range: prefix sums over the requests' units (units_of(p, item): how
 // many there are, and which tiles begin before one), then the place of its first
 // one. most_ranges(p, total, two): how many ranges that many units are cut into at
-// most, `two` when a request has more rows than a query tile. The first kPlanThreads threads call it, warps converged;
-// `count` [MOE_MAX_REQUESTS] and `part` [8] are shared memory. (Every loop
-// stays a loop: unrolled, this took a quarter of the kernel's instructions,
-// which are fetched anew by every launch.)
+// most, `two` when a request has more rows than a query tile. The first
+// kPlanThreads threads call it, warps converged; `count` [MOE_MAX_REQUESTS] and
+// `part` [8] are shared memory. (Every loop stays a loop: unrolled, this took a
+// quarter of the kernel's instructions, which are fetched anew by every launch.)
 template <class Params>
 MOE_DEV void find_start(const Params& p, long long* count, long long* part, Start* out) {
   const auto& a = p.a;
@@ -323,7 +323,9 @@ MOE_DEV uint64_t pair(uint32_t lo, uint32_t hi) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
   return r;
 }
-MOE_DEV uint64_t pair_f(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+MOE_DEV uint64_t pair_f(float lo, float hi) {
+  return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
 MOE_DEV void split(uint64_t v, float* lo, float* hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
 }

@@ -39,7 +39,8 @@ const char* cache_fault(const moe_kv8_cache* c, moe_status* st) {
   if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
     return "cache scales null or misaligned";
   if (c->n_pages < 1 || c->n_pages > 0x7fffffff) return "n_pages out of range";
-  if (c->n_kv_heads < 1 || c->head_dim < 1 || c->page_size < 1) return "cache sizes out of range";
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 0x7fff || c->head_dim < 1 || c->page_size < 1)
+    return "cache sizes out of range";
   if (c->page_stride < 1 || c->token_stride < 1 || c->head_stride < 1 ||
       c->page_stride % 16 != 0 || c->token_stride % 16 != 0 || c->head_stride % 16 != 0)
     return "cache strides must be positive multiples of 16";
@@ -175,7 +176,8 @@ moe_status moe_rotary(const moe_rotary_desc* d, int32_t dtype, const moe_rotary_
   if (n_tokens < 0) return bad("n_tokens out of range");
   if (d->head_dim % 16 != 0 || d->head_dim > 1024 || d->n_rotated % 16 != 0 || d->first % 8 != 0)
     return moe::refuse(MOE_EUNSUPPORTED, fn,
-                       "head_dim and n_rotated must be multiples of 16, at most 1024, first one of 8");
+                       "head_dim and n_rotated must be multiples of 16, at most 1024, first one "
+                       "of 8");
   moe::RotaryArgs a = {*d, {{}, {}}, positions, n_tokens};
   const moe_rotary_rows* rows[2] = {q, k};
   int64_t heads = 0;

@@ -8,7 +8,13 @@
 // element; where the scale grows, the other codes are divided by the growth,
 // which rounds only those that fall below 2^-6.
 //
-// Both are bound by memory, or by a launch and a chain of loads for a few tokens.
+// Bound by memory, or by a launch and a chain of loads for a few tokens. 4747 rows
+// of 8 heads of 128 fp32 columns, keys and values, in blocks of 32 (49 MB): 13 us
+// beyond an empty launch, 3.7 TB/s: the chain from slots to rows to a block's
+// largest size to its codes, which is what 36 rows' 2 us are too. Read back, 32001
+// rows of 8 heads of 128 columns in bf16 (196 MB, 131 of them written): 44 us, 4.5
+// TB/s; filling those 131 MB alone takes 35. (More rows a thread, their loads ahead,
+// were slower: 2 rows 51 us, 8 rows 65, against 49 on the same card.)
 #include "batch_launch.h"
 #include "common.cuh"
 #include "fp8.cuh"
@@ -61,9 +67,10 @@ MOE_DEV int exponent_for(float a) {
 constexpr int kAppendThreads = 128;
 constexpr int kHold = 4;  // pieces of 8 elements that a thread keeps from the first pass
 
-// A CTA takes the blocks whose first token in the call is one of `per` tokens,
-// for one head, of keys or of values: a pass over the block's new rows for their
-// largest size, then one that writes codes.
+// A CTA takes the blocks whose first token in the call is one of `per` tokens (16 at
+// most), for one head, of keys or of values: a pass over the block's new rows for
+// their largest size, then one that writes codes. What both need of the slots is
+// loaded once, a token a lane.
 template <int kType>
 __global__ void __launch_bounds__(kAppendThreads)
     kv8_append_kernel(const __grid_constant__ Append8Args a, int page_shift, int block_shift,
@@ -81,30 +88,36 @@ __global__ void __launch_bounds__(kAppendThreads)
   uint8_t* codes = static_cast<uint8_t*>(blockIdx.z ? c.v : c.k) + h * c.head_stride;
   float* scales = blockIdx.z ? c.v_scale : c.k_scale;
   const int pieces = 1 << row_shift;               // of a row, 8 elements each
-  auto block_of = [&](int t) -> int64_t {          // -1: none
-    const int64_t s = a.slots[t];
+  const int c0 = blockIdx.x * per, c1 = min(c0 + per, a.n_tokens);
+  // lane l: the slot of token c0 − 1 + l (-1: none), and its block
+  auto slot_of = [&](int t) -> int64_t { return t >= 0 && t < a.n_tokens ? a.slots[t] : -1; };
+  auto block_of = [&](int64_t s) -> int64_t {
     return s >= 0 && s < n_slots ? s >> block_shift : -1;
   };
-  const int t_end = min((int)(blockIdx.x + 1) * per, a.n_tokens);
-  for (int t0 = blockIdx.x * per; t0 < t_end; ++t0) {
-    const int64_t slot0 = a.slots[t0];
-    if (slot0 < 0 || slot0 >= n_slots) {
-      if (slot0 != -1 && tid == 0) report_error(a.err, ERR_CHECK, 0xB10);
-      continue;
+  const int64_t slot_l = slot_of(c0 - 1 + lane), block_l = block_of(slot_l);
+  if (tid < 32 && lane > 0 && c0 - 1 + lane < c1 && block_l < 0 && slot_l != -1)
+    report_error(a.err, ERR_CHECK, 0xB10);
+  // tokens that are the first of their block in the call
+  const int64_t before = __shfl_up_sync(0xffffffffu, block_l, 1);
+  uint32_t leaders = __ballot_sync(0xffffffffu, lane > 0 && c0 - 1 + lane < c1 && block_l >= 0 &&
+                                                    block_l != before);
+  for (; leaders; leaders &= leaders - 1) {
+    const int l0 = __ffs(leaders) - 1, t0 = c0 - 1 + l0;
+    const int64_t b = __shfl_sync(0xffffffffu, block_l, l0);
+    // its tokens: those that follow with the same block
+    uint32_t other = __ballot_sync(0xffffffffu, block_l != b) & (0xffffffffu << l0);
+    int n = (other ? __ffs(other) - 1 : 32) - l0;
+    for (bool more = other == 0; more;) {
+      other = __ballot_sync(0xffffffffu, block_of(slot_of(t0 + n + lane)) != b);
+      n += other ? __ffs(other) - 1 : 32;
+      more = other == 0;
     }
-    const int64_t b = slot0 >> block_shift;
-    if (t0 > 0 && block_of(t0 - 1) == b) continue;  // an earlier token's
-    int n = 0;                                      // tokens of the block
-    for (bool more = true; more;) {
-      const int t = t0 + n + lane;
-      const uint32_t same = __ballot_sync(0xffffffffu, t < a.n_tokens && block_of(t) == b);
-      n += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-      more = same == 0xffffffffu;
-    }
+    // the scale that the block has (one that this library did not write counts by
+    // its exponent)
+    const int64_t page = b / blocks;
+    float* scale = scales + (page * c.n_kv_heads + h) * blocks + (b - page * blocks);
+    const uint32_t was_bits = __float_as_uint(*scale);
     // the new rows' largest finite size, and which rows they are
-    __syncthreads();
-    if (tid < 8) written[tid] = 0;
-    __syncthreads();
     const int all = n << row_shift;
     Eight held[kHold];
     float top = 0.f;
@@ -120,28 +133,26 @@ __global__ void __launch_bounds__(kAppendThreads)
       }
     };
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-      const int i = tid + k * kAppendThreads;
-      if (i < all) {
-        held[k] = piece(i);
-        size_of(held[k]);
-      }
-    }
-    for (int i = tid + kHold * kAppendThreads; i < all; i += kAppendThreads) size_of(piece(i));
+    for (int k = 0; k < kHold; ++k)
+      if (tid + k * kAppendThreads < all) held[k] = piece(tid + k * kAppendThreads);
+    __syncthreads();                               // (the block before is done with these)
+    if (tid < 8) written[tid] = 0;
+    __syncthreads();
     for (int i = tid; i < n; i += kAppendThreads) {
       const int row = (int)(a.slots[t0 + i] & (block - 1));
       atomicOr(&written[row >> 5], 1u << (row & 31));
     }
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+      if (tid + k * kAppendThreads < all) size_of(held[k]);
+    for (int i = tid + kHold * kAppendThreads; i < all; i += kAppendThreads) size_of(piece(i));
     // (sizes are not negative: their bits order as they do)
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     if (lane == 0) warp_max[tid >> 5] = top;
-    const int64_t page = b / blocks;
-    float* scale = scales + (page * c.n_kv_heads + h) * blocks + (b - page * blocks);
-    // (a scale that this library did not write counts by its exponent)
-    const int was = min(max((int)(__float_as_uint(*scale) >> 23 & 0xffu) - 127, MOE_KV8_MIN_EXP),
-                        MOE_KV8_MAX_EXP);
     __syncthreads();
     for (int w = 0; w < kAppendThreads / 32; ++w) top = fmaxf(top, warp_max[w]);
+    const int was =
+        min(max((int)(was_bits >> 23 & 0xffu) - 127, MOE_KV8_MIN_EXP), MOE_KV8_MAX_EXP);
     const bool anew = written[0] & 1u;
     const int needs = exponent_for(top), e = anew ? needs : max(was, needs);
     if (tid == 0) *scale = pow2(e);
@@ -177,17 +188,15 @@ __global__ void __launch_bounds__(kAppendThreads)
           make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
     };
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-      const int i = tid + k * kAppendThreads;
-      if (i < all) write(held[k], i);
-    }
+    for (int k = 0; k < kHold; ++k)
+      if (tid + k * kAppendThreads < all) write(held[k], tid + k * kAppendThreads);
     for (int i = tid + kHold * kAppendThreads; i < all; i += kAppendThreads) write(piece(i), i);
   }
 }
 
 constexpr int kReadThreads = 256;
 
-// A thread takes 8 codes.
+// A thread takes 8 codes of a row's keys and the same 8 of its values.
 template <int kType>
 __global__ void __launch_bounds__(kReadThreads)
     kv8_read_kernel(const __grid_constant__ Read8Args a, int page_shift, int block_shift,
@@ -198,40 +207,46 @@ __global__ void __launch_bounds__(kReadThreads)
   const int64_t n_slots = c.n_pages << page_shift;
   const int blocks = c.page_size >> block_shift;
   const int per_row = c.n_kv_heads << row_shift;
-  const int64_t n = (int64_t)a.n * per_row;
-  const uint8_t* codes = static_cast<const uint8_t*>(blockIdx.y ? c.v : c.k);
-  const float* scales = blockIdx.y ? c.v_scale : c.k_scale;
-  void* out = blockIdx.y ? a.v : a.k;
-  for (int64_t i = (int64_t)blockIdx.x * kReadThreads + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * kReadThreads) {
-    const int t = (int)(i / per_row);
-    const int j = (int)(i - (int64_t)t * per_row);
+  // a row takes `of` threads, and a CTA that many rows
+  const int of = min(per_row, kReadThreads), rows = kReadThreads / of;
+  const int group = threadIdx.x / of;
+  const int64_t t = (int64_t)blockIdx.x * rows + group;
+  if (group >= rows || t >= a.n) return;
+  const int64_t slot = a.slots[t];
+  const bool there = slot >= 0 && slot < n_slots;
+  if (!there && slot != -1) report_error(a.err, ERR_CHECK, 0xB20);
+  const int64_t page = slot >> page_shift;
+  const int row = (int)slot & (c.page_size - 1);
+  for (int j = threadIdx.x - group * of; j < per_row; j += of) {
     const int h = j >> row_shift, e = (j & ((1 << row_shift) - 1)) * 8;
-    const int64_t slot = a.slots[t];
-    float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-    if (slot >= 0 && slot < n_slots) {
-      const int64_t page = slot >> page_shift;
-      const int row = (int)(slot & (c.page_size - 1));
-      const float s = __ldg(scales + (page * c.n_kv_heads + h) * blocks + (row >> block_shift));
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(
-          codes + page * c.page_stride + row * c.token_stride + h * c.head_stride + e));
-      lo = floats_of(x.x);
-      hi = floats_of(x.y);
-      lo = make_float4(lo.x * s, lo.y * s, lo.z * s, lo.w * s);
-      hi = make_float4(hi.x * s, hi.y * s, hi.z * s, hi.w * s);
-    } else if (slot != -1) {
-      report_error(a.err, ERR_CHECK, 0xB20);
-    }
     const int64_t to = t * a.token_stride + h * a.head_stride + e;
-    if constexpr (kType == kF32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
-      p[0] = lo;
-      p[1] = hi;
-    } else {
-      constexpr bool f16 = kType == kFp16;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to) =
-          make_uint4(round16<f16>(lo.x, lo.y), round16<f16>(lo.z, lo.w), round16<f16>(hi.x, hi.y),
-                     round16<f16>(hi.z, hi.w));
+    uint2 x[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+    float s[2] = {0.f, 0.f};
+    if (there) {
+      const int64_t at = (page * c.n_kv_heads + h) * blocks + (row >> block_shift);
+      const int64_t from = page * c.page_stride + row * c.token_stride + h * c.head_stride + e;
+      x[0] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.k) + from));
+      x[1] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(c.v) + from));
+      s[0] = __ldg(c.k_scale + at);
+      s[1] = __ldg(c.v_scale + at);
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      void* out = which ? a.v : a.k;
+      const float by = s[which];
+      float4 lo = floats_of(x[which].x), hi = floats_of(x[which].y);
+      lo = make_float4(lo.x * by, lo.y * by, lo.z * by, lo.w * by);
+      hi = make_float4(hi.x * by, hi.y * by, hi.z * by, hi.w * by);
+      if constexpr (kType == kF32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + to);
+        p[0] = lo;
+        p[1] = hi;
+      } else {
+        constexpr bool f16 = kType == kFp16;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + to) =
+            make_uint4(round16<f16>(lo.x, lo.y), round16<f16>(lo.z, lo.w),
+                       round16<f16>(hi.x, hi.y), round16<f16>(hi.z, hi.w));
+      }
     }
   }
 }
@@ -243,7 +258,9 @@ int log2i(int v) { return 31 - __builtin_clz(v); }
 cudaError_t launch_kv8_append(const Append8Args& a, int src_dtype, int num_sms,
                               cudaStream_t stream) {
   const moe_kv8_cache& c = a.cache;
-  // tokens whose blocks a CTA takes: one, while the GPU has room for a CTA each
+  // Tokens whose blocks a CTA takes: one, while the GPU has room for a CTA each.
+  // (With the replay that measures it, 7 us: 36 tokens of 8 heads take 9.3 us one to
+  // a CTA and 11.4 sixteen, 4747 tokens 83 us one, 46 two, 28 four, 21 sixteen.)
   int per = 1;
   while (per < 16 && (int64_t)a.n_tokens * c.n_kv_heads * 2 > (int64_t)per * num_sms * 16) per *= 2;
   const dim3 grid((a.n_tokens - 1) / per + 1, c.n_kv_heads, 2);
@@ -256,10 +273,9 @@ cudaError_t launch_kv8_append(const Append8Args& a, int src_dtype, int num_sms,
 
 cudaError_t launch_kv8_read(const Read8Args& a, int dtype, int num_sms, cudaStream_t stream) {
   const moe_kv8_cache& c = a.cache;
-  const int row_shift = log2i(c.head_dim / 8);
-  const int64_t n = ((int64_t)a.n * c.n_kv_heads) << row_shift;
-  const int64_t ctas = (n + kReadThreads - 1) / kReadThreads, most = (int64_t)num_sms * 32;
-  const dim3 grid((unsigned)(ctas < most ? ctas : most), 2);
+  const int row_shift = log2i(c.head_dim / 8), per_row = c.n_kv_heads << row_shift;
+  const int rows = per_row < kReadThreads ? kReadThreads / per_row : 1;
+  const dim3 grid((unsigned)((a.n - 1) / rows + 1));
   auto* kernel = dtype == MOE_F32    ? kv8_read_kernel<kF32>
                  : dtype == MOE_BF16 ? kv8_read_kernel<kBf16>
                                      : kv8_read_kernel<kFp16>;

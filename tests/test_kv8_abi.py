@@ -166,6 +166,7 @@ CACHE_FAULTS = [
     (dict(n_pages=0), api.MOE_EINVAL, "n_pages"),
     (dict(n_pages=1 << 31), api.MOE_EINVAL, "n_pages"),
     (dict(n_kv_heads=0), api.MOE_EINVAL, "sizes"),
+    (dict(n_kv_heads=1 << 15), api.MOE_EINVAL, "sizes"),
     (dict(token_stride=120), api.MOE_EINVAL, "strides"),
     (dict(head_stride=0), api.MOE_EINVAL, "strides"),
     (dict(page_stride=1 << 40), api.MOE_EINVAL, "stride out of range"),
