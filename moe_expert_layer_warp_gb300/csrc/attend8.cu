@@ -218,14 +218,15 @@ MOE_DEV bool next_part(const Params& p, Walk& w, Request& r, Part* out) {
     w.left -= u1 - w.u0;
     w.u0 = 0;
     if (w.left > 0 && ++w.block * p.block >= r.q) {
-      w.block = 0;
       if (++w.h == a.cache.n_kv_heads) {
         w.h = 0;
         bool bad;
         do {
-          r = request(a, p.page_shift, ++w.b, &bad);
-        } while (r.q == 0 && w.b + 1 < a.n_requests);
+          if (++w.b >= a.n_requests) return false;
+          r = request(a, p.page_shift, w.b, &bad);
+        } while (r.q == 0 || r.len == 0);
       }
+      w.block = max(0, r.q - r.len) / p.block;   // (those before it see nothing)
     }
     if (n > 0) return true;
   }
@@ -624,6 +625,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       wait(b, b_parity, site + 0x80);
     }
   };
+  // a barrier of each stream, from that of stream 0 on: phase counts − 1 has ended
+  auto wait_four = [&](uint64_t* bars, uint32_t counts, int site) {
+    bool done = true;
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      done = try_at(smem_addr(bars + s), count_of(counts, s) & 1u ^ 1u) && done;
+    if (!__all_sync(0xffffffffu, done)) {
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) wait(bars + s, count_of(counts, s) & 1u ^ 1u, site);
+    }
+  };
   // The parts, one after the other. A lost wait ends a role's walk: what a part
   // says may then be another's.
   int part_no = 0;
@@ -648,35 +660,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     // keys and values that one item reads alone are not kept in L2: the rows of
     // the other heads beside them are (single tokens 258 -> 243 us)
     const uint64_t stay = l2_evict_normal_policy(), go = l2_evict_first_policy();
-    const uint32_t to = smem_addr(smem) + Z::kOffRing + lane * rows * kDim;
-    const int block = min(lane * rows / 16, kScaleBlocks - 1);  // first of the lane's box
+    // Lanes 0-15 load K_{j + streams}, a box each, lanes 16-31 V_j: with one after the
+    // other the loader was what a tile of 16 rows took.
+    const int half = lane >> 4, piece = lane & 15;
+    const CUtensorMap* map = half ? &p.vmap : &p.kmap;
+    const uint32_t to = smem_addr(smem) + Z::kOffRing + piece * rows * kDim;
+    const int block = min(piece * rows / 16, kScaleBlocks - 1);  // first of the lane's box
     int tile_no = 0;
     Place<kStages> at(0);                       // the next place in the ring
     for (const Part* pt; (pt = next()); done_with_part()) {
       const int n = pt->n, streams = 1 << pt->shift, head = pt->h;
       const uint64_t policy = pt->once ? go : stay;
-      auto load = [&](const CUtensorMap* map, int j) {
-        const int slot = (tile_no + j) & (kSlots - 1), stage = at.stage();
-        wait_both(&m.pg_full[slot], (tile_no + j) / kSlots & 1u, &m.empty[stage],
-                  at.parity() ^ 1u, 0xB30);
+#pragma unroll 1
+      for (int j = -streams; ok && j < n; ++j) {
+        const bool keys = j + streams < n, values = j >= 0;
+        Place<kStages> mine = at;
+        if (half && keys) mine.next();
+        const bool has = half ? values : keys;
+        const int no = tile_no + (half ? j : j + streams), slot = no & (kSlots - 1);
+        const int stage = mine.stage();
+        // (a tile's pages are there for V when they were for K)
+        const uint32_t empty = smem_addr(&m.empty[stage]), pages = smem_addr(&m.pg_full[slot]);
+        const bool there = !has || (try_at(empty, mine.parity() ^ 1u) &&
+                                    (half || try_at(pages, no / kSlots & 1u)));
+        if (!__all_sync(0xffffffffu, there)) {
+          const int first = tile_no + j + streams;
+          if (keys) wait(&m.pg_full[first & (kSlots - 1)], first / kSlots & 1u, 0xB30);
+          Place<kStages> next_at = at;
+          wait(&m.empty[next_at.stage()], next_at.parity() ^ 1u, 0xB31);
+          next_at.next();
+          if (keys && values) wait(&m.empty[next_at.stage()], next_at.parity() ^ 1u, 0xB31);
+        }
         if (ok) {
-          const int pg = lane * rows < kTile ? slots[slot].page[block] : -1;
-          const int row = page > kTile ? slots[slot].key0 & (page - 1) : 0;
+          const int pg = has && piece * rows < kTile ? slots[slot].page[block] : -1;
+          const int row = page > kTile && has ? slots[slot].key0 & (page - 1) : 0;
           const uint32_t wanted = __ballot_sync(0xffffffffu, pg >= 0);
-          if (lane == 0) mbar_arrive_expect_tx(&m.full[stage], __popc(wanted) * rows * kDim);
+          if (piece == 0 && has)
+            mbar_arrive_expect_tx(&m.full[stage],
+                                  __popc(wanted >> (16 * half) & 0xffffu) * rows * kDim);
           __syncwarp();
           if (pg >= 0)
             tma_load_4d_at(to + stage * Z::kTileBytes, map, 0, head, row, pg, &m.full[stage],
                            policy);
           __syncwarp();
         }
-        at.next();
-      };
-      // K_0 .. K_{streams-1}, then K_{j + streams} and V_j
-#pragma unroll 1
-      for (int j = -streams; ok && j < n; ++j) {
-        if (j + streams < n) load(&p.kmap, j + streams);
-        if (j >= 0) load(&p.vmap, j);
+        if (keys) at.next();
+        if (values) at.next();
       }
       tile_no += n;
     }
@@ -706,8 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (scores) {                                    // S = K · Qᵀ
         const uint32_t id = umma::idesc_e4m3(kTile, cols, false);
         // S may be laid out anew once the last scores of every stream are read
-#pragma unroll 1
-        for (int s = 0; s < 4; ++s) wait(&m.s_empty[s], count_of(counts, s) & 1u ^ 1u, 0xB41);
+        wait_four(m.s_empty, counts, 0xB41);
         wait(&m.q_full, part_no & 1u, 0xB42);
 #pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
@@ -783,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       count = 0;
       tile = page = -1;
       wants = false;
+      size_t entry = 0;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         while (t_part < published && parts[t_part & (kParts - 1)].n >= 0 &&
@@ -798,11 +827,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           edge = tile >= pt.edge_hi || (tile < pt.edge_lo && tile >= pt.edge_sk);
           const int key = tile * kTile + block * 16;
           wants = key < pt.hi && (key + 16 > pt.lo || key < pt.sk);  // some row sees of the block
-          if (wants) page = a.block_table[(size_t)pt.b * a.max_blocks + (key >> p.page_shift)];
+          entry = (size_t)pt.b * a.max_blocks + (key >> p.page_shift);
         }
         ++t_next;
         ++count;
       }
+      // (one load of all lanes: in the loop, each waited for the one before it)
+      if (wants) page = a.block_table[entry];
     };
     int idle = 0;
     while (ok && (more || !q_done || count || t_part < published - 1)) {
@@ -950,32 +981,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         constexpr int kMine = kDim / 32;               // columns of a lane
         const int rows = then->rows, wide = then->wide;
         const float to_log2 = a.scale * kLog2e;
-#pragma unroll 1
-        for (int r = warp; r < rows; r += 16) {
+        // (the chains of its four rows side by side)
+        uint32_t x[4][kMine / 2];
+        float top[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = min(warp + 16 * i, rows - 1);
           const unsigned char* at = smem + Z::kOffRaw + r * (kDim * 2) + lane * (kMine * 2);
-          uint32_t x[kMine / 2];
           if constexpr (kMine == 4) {
             const uint2 w = *reinterpret_cast<const uint2*>(at);
-            x[0] = w.x;
-            x[1] = w.y;
+            x[i][0] = w.x;
+            x[i][1] = w.y;
           } else {
-            x[0] = *reinterpret_cast<const uint32_t*>(at);
+            x[i][0] = *reinterpret_cast<const uint32_t*>(at);
           }
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          float top = 0.f;
+        }
+        auto element = [&](int i, int c) {
+          const uint32_t w = x[i][c / 2] >> (16 * (c & 1));
+          return kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
+                      : __uint_as_float(w << 16);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          top[i] = 0.f;
 #pragma unroll
           for (int c = 0; c < kMine; ++c) {
-            const uint32_t w = x[c / 2] >> (16 * (c & 1));
-            v[c] = kF16 ? __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)))
-                        : __uint_as_float(w << 16);
-            top = fmaxf(top, fabsf(v[c]));
-            if (v[c] != v[c]) top = INFINITY;
+            const float v = element(i, c);
+            top[i] = fmaxf(top[i], fabsf(v));
+            if (v != v) top[i] = INFINITY;
           }
-          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          const uint32_t bits = __float_as_uint(top);
+          top[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top[i])));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = warp + 16 * i;
+          if (r >= rows) break;
+          const uint32_t bits = __float_as_uint(top[i]);
           int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
           e = min(max(e, -120), 120);
           const float inv = pow2(-e);
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) v[c] = element(i, c);
           uint32_t num[kNum];
           numbers_of<kNum>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv, num);
 #pragma unroll
@@ -988,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           }
           // (a row with NaN or an infinity has NaN for its factor)
           if (lane == 0)
-            qscale[(no & 1) * kRows + r] = top <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
+            qscale[(no & 1) * kRows + r] = top[i] <= 3.402823466e38f ? to_log2 * pow2(e) : NAN;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -998,8 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         }
       }
       // the last products of every stream
-#pragma unroll 1
-      for (int z = 0; z < 4; ++z) wait(&m.p_done[z], count_of(counts, z) & 1u ^ 1u, 0xB57);
+      wait_four(m.p_done, counts, 0xB57);
       gone = !ok;
       asm volatile(
           "{\n\t.reg .pred p, q;\n\t"
@@ -1103,7 +1149,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           if (threadIdx.x < 256) p.spoiled[blockIdx.x * 128 + threadIdx.x - 128] = 0;
           if (threadIdx.x == 128) m.spoils = 0;
         }
-        if (pt->whole || spoils) all_sync();
         done_with_part();
       }
       pt = then;
@@ -1131,7 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (quarter == 0 && lane < 16)
         ref[lane] = c0 + lane < pt->rows ? 0.f : -INFINITY;
       uint32_t fresh = low_bits(min(pt->rows - c0, 16));
-      group_sync();
+      all_sync();
       const float* factor = qscale + (part_no & 1) * kRows + c0;
       uint64_t sums[8];
 #pragma unroll
@@ -1317,8 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       ring = (ring + 2 * n) % (2 * kStages);
       tile_no += n;
       // all scores with these queries are there
-#pragma unroll 1
-      for (int z = 0; z < 4; ++z) wait(&m.s_full[z], count_of(counts, z) & 1u ^ 1u, 0xB59);
+      wait_four(m.s_full, counts, 0xB59);
     }
     // The last part is left to the CTA that ends its item, and an item that began
     // in earlier ranges joined, when all of the range's results are there.

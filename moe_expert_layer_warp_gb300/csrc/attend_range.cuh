@@ -131,11 +131,11 @@ MOE_DEV void find_start(const Params& p, long long* count, long long* part, Star
   const int fixed = p.block, H = a.cache.n_kv_heads, B = a.n_requests;
   constexpr uint32_t kAll = 0xffffffffu;
   // units of every request for one key head: a request of one block by its
-  // own thread, longer ones by the warp
+  // own thread, longer ones by the warp (every eighth its, so that a few are shared)
   int any_two = 0;
 #pragma unroll 1
-  for (int b0 = warp * 32; b0 < B; b0 += kPlanThreads) {
-    const int b = b0 + lane;
+  for (int b0 = warp; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + lane * (kPlanThreads / 32);
     Request mine = {0, 0, 0};
     bool bad = false;
     if (b < B) mine = request(a, p.page_shift, b, &bad);
