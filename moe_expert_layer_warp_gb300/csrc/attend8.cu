@@ -85,7 +85,7 @@ constexpr int kRows = 64;         // query rows of an item, at most
 constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 // What an item costs beside its tiles when the work is cut, and what every 16 rows of
 // it add (see Units).
-constexpr int kItemUnits = 32, kItemRowUnits = 7;
+constexpr int kItemUnits = 26, kItemRowUnits = 5;
 constexpr float kBase = 4.f;      // weights are held 2^4 larger
 constexpr float kGrow = 4.5f;     // m follows growth beyond this (powers of two)
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
@@ -133,11 +133,13 @@ struct Params {
   unsigned long long call;
 };
 
-// An item's units, an eighth of what a tile of 64 query rows takes: first `cost`,
-// then `each` for every key tile. A tile belongs to the CTA whose range has its
-// first unit. (Fitted to the times of 8 batches' ranges: tiles of 16, 32, 48 and 64
-// rows took 0.9, 1.1, 1.4 and 1.6 thousand cycles, a part of an item 7.9, 8.5, 10.8 and
-// 12.1 besides.)
+// An item's units, an eighth of what a tile of 64 query rows takes (1.15 us): first
+// `cost`, then `each` for every key tile. A tile belongs to the CTA whose range has
+// its first unit. Measured for parts of items alone: 64 rows and one tile 6.2 us, 34
+// tiles 43.7; 48 rows, 22 and 26 tiles, 26.3 and 29.5; 16 rows, 2, 8 and 34 tiles, 5.2,
+// 6.5 and 18.3; and 33 of those, in pages of 16, 28 (their boxes bound them: five units
+// a tile). A batch of chunks and passes took 85 us with 32 + 7 for 16 rows, 79 with
+// these and 77 with 16 + 2, long chunks 543, 554 and 580.
 struct Units {
   int cost, each, all;
   MOE_DEV int tiles(int u) const {  // that begin before unit u
@@ -148,7 +150,7 @@ MOE_DEV Units units_of(const Params& p, const Item& it) {
   const int wide = (it.ntok * p.a.group + 15) >> 4;  // query rows, by 16
   Units u;
   u.cost = kItemUnits + kItemRowUnits * wide;
-  u.each = wide == 1 ? 4 : wide == 2 ? 5 : wide == 3 ? 7 : 8;
+  u.each = max(wide == 1 ? 4 : wide == 2 ? 5 : wide == 3 ? 7 : 8, 80 >> p.page_shift);
   u.all = it.hi > 0 ? u.cost + it.n * u.each : 0;    // (see clear_blind)
   return u;
 }
@@ -661,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     // the other heads beside them are (single tokens 258 -> 243 us)
     const uint64_t stay = l2_evict_normal_policy(), go = l2_evict_first_policy();
     // Lanes 0-15 load K_{j + streams}, a box each, lanes 16-31 V_j: with one after the
-    // other the loader was what a tile of 16 rows took.
+    // other the loader was what a tile of 16 rows took. (A box takes its 80 cycles to
+    // issue: a lane each, or one lane of the warp for all, which took longer.)
     const int half = lane >> 4, piece = lane & 15;
     const CUtensorMap* map = half ? &p.vmap : &p.kmap;
     const uint32_t to = smem_addr(smem) + Z::kOffRing + piece * rows * kDim;
@@ -808,32 +811,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     int count = 0, tile = -1, edge = 0, page = -1, head = 0;
     bool wants = false;
     auto ask = [&]() {
-      count = 0;
+      // the 8 lanes of a tile look for it from the part of the first of the four on
+      int at = t_part, j = t_next + q;
       tile = page = -1;
       wants = false;
-      size_t entry = 0;
-#pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        while (t_part < published && parts[t_part & (kParts - 1)].n >= 0 &&
-               t_next >= parts[t_part & (kParts - 1)].n) {
-          ++t_part;
-          t_next = 0;
-        }
-        const Part& pt = parts[t_part & (kParts - 1)];
-        if (t_part >= published || pt.n < 0) break;
-        if (q == i) {
-          tile = pt.tile(t_next);
-          head = pt.h;
-          edge = tile >= pt.edge_hi || (tile < pt.edge_lo && tile >= pt.edge_sk);
-          const int key = tile * kTile + block * 16;
-          wants = key < pt.hi && (key + 16 > pt.lo || key < pt.sk);  // some row sees of the block
-          entry = (size_t)pt.b * a.max_blocks + (key >> p.page_shift);
-        }
-        ++t_next;
-        ++count;
+      while (at < published) {
+        const int n = parts[at & (kParts - 1)].n;
+        if (n < 0) at = published;
+        if (j < n || n < 0) break;
+        j -= n;
+        ++at;
       }
-      // (one load of all lanes: in the loop, each waited for the one before it)
-      if (wants) page = a.block_table[entry];
+      if (at < published) {
+        const Part& pt = parts[at & (kParts - 1)];
+        tile = pt.tile(j);
+        head = pt.h;
+        edge = tile >= pt.edge_hi || (tile < pt.edge_lo && tile >= pt.edge_sk);
+        const int key = tile * kTile + block * 16;
+        wants = key < pt.hi && (key + 16 > pt.lo || key < pt.sk);  // some row sees of the block
+        if (wants) page = a.block_table[(size_t)pt.b * a.max_blocks + (key >> p.page_shift)];
+      }
+      __syncwarp();
+      count = __popc(__ballot_sync(0xffffffffu, tile >= 0)) >> 3;
+      t_next += count;
+      while (t_part < published) {
+        const int n = parts[t_part & (kParts - 1)].n;
+        if (n < 0 || t_next < n) break;
+        t_next -= n;
+        ++t_part;
+      }
     };
     int idle = 0;
     while (ok && (more || !q_done || count || t_part < published - 1)) {
