@@ -38,7 +38,8 @@ typedef struct {
 
 /* Rows [n_tokens][n_heads][head_dim] of queries or keys. in and out: 16-byte
  * aligned, strides (in elements) multiples of 16 bytes; out may be in, with the
- * same strides, and must not overlap it otherwise. Rows of out must not overlap. */
+ * same strides, and must not overlap it otherwise. Rows of out must not overlap,
+ * nor the other call argument's rows. */
 typedef struct {
   const void* in;
   void* out;
@@ -104,8 +105,9 @@ typedef struct {
  *              MOE_F16.
  *   slots      [n_tokens] int64, −1 skips a token. The tokens of one block are
  *              consecutive rows of the call, as moe_plan_batch orders them, and
- *              no two share a slot. Rows of a block are first written from its
- *              first row on.                                                 */
+ *              no two share a slot (where one does, codes of either may stay).
+ *              Rows of a block are first written from its first row on. Keys and
+ *              values of the cache do not share memory.                      */
 moe_status moe_kv8_append(const moe_kv8_cache* cache, const void* k, const void* v,
                           int32_t src_dtype, int64_t token_stride, int64_t head_stride,
                           int32_t n_tokens, const int64_t* slots, void* stream);
@@ -134,8 +136,10 @@ size_t moe_attend8_workspace_bytes(const moe_kv8_cache* cache, const moe_attn_de
  * reported, and read as the nearer end.
  * The codes go to the tensor cores as they are; queries and softmax weights go
  * as sums of two e4m3 numbers (bf16) or three (fp16), which hold all bits of a
- * bf16 or fp16 query whose size is within 2^-14 of its row's largest, and of a
- * weight as many as its type has. Sums and statistics are fp32.              */
+ * bf16 or fp16 query whose size is within 2^-14 of its row's largest; a softmax
+ * weight is off by 2^-8 (bf16) or 2^-12 (fp16) of itself, or by 2^-18 or 2^-22 of
+ * the row's largest where that is more. Sums and statistics are fp32. A query row
+ * with NaN or an infinity gives NaN (or zeros, where it sees nothing).         */
 moe_status moe_attend8(const moe_kv8_cache* cache, const moe_attn_desc* attn, int32_t dtype,
                        const void* q, int64_t q_token_stride, int64_t q_head_stride,
                        int32_t n_tokens, const int32_t* q_start, const int32_t* kv_len,

@@ -321,13 +321,13 @@ class Rotary:
         self.desc = api.RotaryDesc(head_dim, n, first, 1 if interleaved else 0, amplitude,
                                    self._turns.data_ptr())
         self._lib, self._index, self._dref = api.load(), self.device.index, ctypes.byref(self.desc)
-        self._q, self._k = api.RotaryRows(), api.RotaryRows()
-        self._qref, self._kref = ctypes.byref(self._q), ctypes.byref(self._k)
         # the descriptor's own checks, before the first step
         api._check(self._lib.moe_rotary(self._dref, api.MOE_F32, None, None, None, 0, None),
                    "Rotary")
 
-    def _rows(self, c, name, x, out, n):
+    def _rows(self, name, x, out, n):
+        """The C rows of q or k (a struct of its own for each call: host threads may
+        share the object), and the tensor that they are written to."""
         D = self.head_dim
         s = x.stride()
         if x.dim() != 3 or x.shape[0] != n or x.shape[2] != D or x.get_device() != self._index or (
@@ -335,19 +335,17 @@ class Rotary:
             raise ValueError("%s must be a [%d][heads][%d] tensor on %s with contiguous rows"
                              % (name, n, D, self.device))
         H = x.shape[1]
-        c.n_heads = H
-        c.in_ = x.data_ptr()
-        c.in_token_stride, c.in_head_stride = s[0] if n > 1 else D, s[1] if H > 1 else D
         if out is None:
-            out = x
+            out, t = x, s
         elif out.shape != x.shape or out.dtype is not x.dtype or (
                 out.get_device() != self._index or out.stride(2) != 1):
             raise ValueError("%s_out must be a %s %s tensor on %s with contiguous rows"
                              % (name, str(x.dtype)[6:], list(x.shape), self.device))
-        s = out.stride()
-        c.out = out.data_ptr()
-        c.out_token_stride, c.out_head_stride = s[0] if n > 1 else D, s[1] if H > 1 else D
-        return out
+        else:
+            t = out.stride()
+        return api.RotaryRows(
+            x.data_ptr(), out.data_ptr(), H, s[0] if n > 1 else D, s[1] if H > 1 else D,
+            t[0] if n > 1 else D, t[1] if H > 1 else D), out
 
     def rotate(self, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
                positions: torch.Tensor, q_out: Optional[torch.Tensor] = None,
@@ -359,13 +357,13 @@ class Rotary:
         if x is None or (q is not None and k is not None and q.dtype is not k.dtype) or (
                 x.dtype not in api.DTYPES):
             raise ValueError("give q or k, of one type: float32, bfloat16 or float16")
+        q_rows = k_rows = None
         if q is not None:
-            q = self._rows(self._q, "q", q, q_out, n)
+            q_rows, q = self._rows("q", q, q_out, n)
         if k is not None:
-            k = self._rows(self._k, "k", k, k_out, n)
+            k_rows, k = self._rows("k", k, k_out, n)
         st = self._lib.moe_rotary(
-            self._dref, api.DTYPES[x.dtype], None if q is None else self._qref,
-            None if k is None else self._kref,
+            self._dref, api.DTYPES[x.dtype], q_rows, k_rows,
             _need(positions, "positions", torch.int32, (n,), self._index), n,
             _handle(stream, self._index))
         if st:

@@ -190,6 +190,10 @@ moe_status moe_rotary(const moe_rotary_desc* d, int32_t dtype, const moe_rotary_
   if (heads > 0x7fff) return bad("n_heads out of range");
   if (n_tokens == 0 || heads == 0) return MOE_OK;
   if (!positions || !aligned(positions, 4)) return bad("positions null or misaligned");
+  const moe_rotary_rows &x = a.rows[0], &y = a.rows[1];
+  if (x.n_heads > 0 && y.n_heads > 0 &&
+      (x.out == y.out || (x.out == y.in && x.out != x.in) || (y.out == x.in && y.out != y.in)))
+    return bad("rows of q and k must not share memory that is written");
   int sms;
   unsigned int* err;
   const moe_status st = moe::call_device(&sms, &err);
@@ -214,6 +218,8 @@ moe_status moe_kv8_append(const moe_kv8_cache* cache, const void* k, const void*
   if (n_tokens == 0) return MOE_OK;
   if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))
     return bad("k, v or slots null or misaligned");
+  if (cache->k == cache->v || cache->k_scale == cache->v_scale)
+    return bad("the cache's keys and values share memory");
   int sms;
   moe::Append8Args a = {*cache, k, v, token_stride, head_stride, n_tokens, slots, nullptr};
   st = moe::call_device(&sms, &a.err);

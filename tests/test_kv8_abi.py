@@ -108,6 +108,12 @@ def test_rotary_other_refusals(lib):
     assert f(d, api.MOE_BF16, r, r, ONE, -1, None) == api.MOE_EINVAL and "n_tokens" in _why()
     assert f(d, api.MOE_BF16, r, r, None, 3, None) == api.MOE_EINVAL and "positions" in _why()
     assert f(d, api.MOE_BF16, r, r, ONE + 2, 3, None) == api.MOE_EINVAL and "positions" in _why()
+    # memory that one writes and the other has
+    for over in (dict(), dict(in_=ONE + 8192), dict(in_=ONE + 4096, out=ONE + 8192),
+                 dict(in_=ONE + 8192, out=ONE)):
+        other = ctypes.byref(_rows(**over))
+        assert f(d, api.MOE_BF16, r, other, ONE, 3, None) == api.MOE_EINVAL
+        assert "share memory" in _why()
     # nothing to do: no token, no rows
     assert f(d, api.MOE_BF16, r, r, None, 0, None) == api.MOE_OK
     assert f(d, api.MOE_BF16, None, None, ONE, 3, None) == api.MOE_OK
@@ -202,6 +208,15 @@ def test_append_refusals(lib, at, value, reason):
     args[at] = value
     assert lib.moe_kv8_append(ctypes.byref(_cache()), *args, None) == api.MOE_EINVAL
     assert reason in _why()
+
+
+@pytest.mark.parametrize("over", [dict(v=ONE, v_scale=ONE + 4096),
+                                  dict(v=ONE + 4096, v_scale=ONE)])
+def test_append_refuses_keys_and_values_in_one_place(lib, over):
+    c = _cache(k=ONE, k_scale=ONE, **over)
+    assert lib.moe_kv8_append(ctypes.byref(c), ONE, ONE, api.MOE_BF16, 128, 64, 3, ONE,
+                              None) == api.MOE_EINVAL
+    assert "share memory" in _why()
 
 
 @pytest.mark.parametrize("at,value,reason", [

@@ -56,6 +56,11 @@ ROTARIES = {
     "amplified": dict(n=9, H=2, K=1, D=64, r=32, far=5000, amplitude=1.25),
     "turned back": dict(n=9, H=2, K=1, D=64, r=64, far=5000, sign=-1.0),
     "many tokens": dict(n=3001, H=3, K=1, D=64, r=64, far=3000),
+    # several tokens a CTA: one piece a head, and counts that are no powers of two
+    "many tokens, one piece a head": dict(n=8003, H=3, K=1, D=16, r=16, far=9000),
+    "many tokens, one head": dict(n=6001, H=1, K=0, D=16, r=16, far=9000),
+    "many tokens, odd heads": dict(n=5003, H=7, K=3, D=80, r=48, first=8, far=9000),
+    "many heads": dict(n=1300, H=70, K=5, D=192, r=96, first=96, far=9000),
 }
 
 
@@ -423,6 +428,16 @@ ATTENDS = {
                                    for i in range(200)], 9, 3, 64, F16, 32, heads_first=True),
     "short items, windows": spec([i % 6 for i in range(150)], [40 + 11 * i for i in range(150)], 28,
                                  4, 64, B16, 256, block=32, window=200, sinks=2),
+    "many tokens that see nothing": spec([3, 400, 5, 0, 260, 2, 333], [300, 0, 90, 50, 30, 700, 0],
+                                         14, 2, 64, F16, 16),
+    "nothing but the last sees": spec([40, 300, 1], [0, 0, 1], 8, 2, 128, B16, 64),
+    "nothing behind the first sees": spec([1, 300, 40], [200, 0, 0], 8, 2, 64, B16, 16),
+    "chunks longer than their caches": spec([700, 300, 65, 9], [1, 120, 64, 8], 28, 4, 128, B16,
+                                            32),
+    "widest window and sinks": spec([9, 200, 1], [700, 300, 129], 8, 2, 64, B16, 16,
+                                    window=2 ** 31 - 1, sinks=2 ** 31 - 1),
+    "window and widest sinks": spec([9, 200, 1], [700, 300, 129], 8, 2, 64, B16, 16, window=20,
+                                    sinks=2 ** 31 - 1),
     "requests of different widths": spec([1, 16, 4, 1, 8, 200, 1, 2, 31], [900, 800, 700, 600, 500,
                                          400, 300, 200, 100], 8, 2, 128, B16, 32, block=32),
 }
@@ -507,6 +522,114 @@ def test_attend_other_stream_and_graph(lib):
         g.replay()
         torch.cuda.synchronize()
         a.check(out)
+
+
+def test_attend_two_at_once(lib):
+    """Two calls in flight at a time, each with its workspace: the bits of one
+    after the other."""
+    problems = [problem("many passes"), problem("mixed batch")]
+    runs = [(a.runner(), a.args(), torch.cuda.Stream()) for a in problems]
+    want = [r.attend(*args).clone() for r, args, _ in runs]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (r, args, stream), out in zip(runs, outs):
+            r.attend(*args, out=out, stream=stream)
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out.view(torch.int16), w.view(torch.int16))
+            out.zero_()
+        torch.cuda.synchronize()
+    assert lib.moe_last_device_error() == lib.MOE_OK
+
+
+def test_graph_of_steps_while_requests_grow(lib):
+    """One captured step of rotate, append, attend and read, replayed with other
+    tokens, positions, slots and lengths: the bits of steps without a graph."""
+    from moe_expert_layer_warp_gb300 import batch
+    B, H, K, D, page, n = 3, 8, 2, 64, 16, 10
+    g = torch.Generator().manual_seed(3)
+    rotary = batch.Rotary(D)
+    sides = []
+    for _ in range(2):
+        cache = batch.PagedCache8.allocate(60, page, K, D)
+        cache.k.view(torch.uint8).zero_()
+        cache.v.view(torch.uint8).zero_()
+        cache.k_scale.fill_(1.0)
+        cache.v_scale.fill_(1.0)
+        sides.append((cache, batch.PagedAttention8(cache, H, n)))
+    table = torch.randperm(60, generator=g).int().view(B, 20)
+    x, pos = torch.zeros(n, H + 2 * K, D, dtype=B16, device="cuda"), i32([-1] * n)
+    slots, q_start, kv_len = i64([-1] * n), i32([0] * (B + 1)), i32([0] * B)
+    dev_table, out = table.cuda(), torch.zeros(n, H, D, dtype=B16, device="cuda")
+    back = [torch.zeros(n, K, D, dtype=B16, device="cuda") for _ in range(2)]
+
+    def step(side, x, out, back):
+        cache, attention = side
+        q, k, v = x[:, :H], x[:, H:H + K], x[:, H + K:]
+        rotary.rotate(q, k, pos)
+        cache.append(k, v, slots)
+        attention.attend(q, q_start, kv_len, dev_table, out=out)
+        cache.read(slots, k=back[0], v=back[1])
+
+    step(sides[0], x, out, back)                   # (nothing: every row is padding)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(sides[0], x, out, back)
+    lens = [0, 0, 0]
+    for i in range(12):
+        q_len = [[3, 5, 2], [1, 0, 7], [4, 4, 1], [0, 1, 0]][i % 4]
+        at, p, s, starts = 0, [], [], [0]
+        for b, m in enumerate(q_len):
+            for j in range(lens[b], lens[b] + m):
+                p.append(j)
+                s.append(int(table[b, j // page]) * page + j % page)
+            lens[b] += m
+            at += m
+            starts.append(at)
+        pos.copy_(i32(p + [-1] * (n - at)))
+        slots.copy_(i64(s + [-1] * (n - at)))
+        q_start.copy_(i32(starts))
+        kv_len.copy_(i32(lens))
+        new = torch.randn(x.shape, generator=g).to(B16).cuda() * 2.0 ** (i % 5)
+        x.copy_(new)
+        out.fill_(7.0)
+        graph.replay()
+        plain = new.clone()
+        out2, back2 = torch.full_like(out, 7.0), [torch.zeros_like(y) for y in back]
+        step(sides[1], plain, out2, back2)
+        torch.cuda.synchronize()
+        for y, z in ((x, plain), (out, out2), (back[0], back2[0]), (back[1], back2[1])):
+            assert torch.equal(y.view(torch.int16), z.view(torch.int16))
+        assert (out[at:] == 7.0).all() and torch.isfinite(out[:at]).all()
+    assert lib.moe_last_device_error() == lib.MOE_OK
+
+
+def test_rotary_of_several_host_threads(lib):
+    """One object, four threads with tensors and streams of their own."""
+    from concurrent.futures import ThreadPoolExecutor
+    from moe_expert_layer_warp_gb300 import batch
+    r = batch.Rotary(64)
+
+    def work(i):
+        n, H = 5 + i, 3 + 2 * i
+        x = torch.randn(n, H, 64, generator=torch.Generator().manual_seed(i)).cuda()
+        pos = torch.arange(100 * i, 100 * i + n).int().cuda()
+        y, bound = oracle.rotate(x, pos.cpu(), r.frequencies, 0, False, 1.0)
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for _ in range(200):
+            out = torch.zeros_like(x)
+            torch.cuda.current_stream().synchronize()
+            r.rotate(x, None, pos, q_out=out, stream=stream)
+            stream.synchronize()
+            if not ((out.double() - y).abs() <= bound).all():
+                return False
+        return True
+
+    with ThreadPoolExecutor(4) as pool:
+        assert all(pool.map(work, range(4)))
 
 
 def test_attend_reports_bad_pages_lengths_and_scales(lib):
@@ -601,6 +724,24 @@ def test_attend_values_that_are_not_finite(lib):
         assert torch.equal(torch.isnan(got).cpu(), nan)
         fine = ~nan.cuda()
         assert ((got.double() - want).abs() <= bound)[fine].all()
+
+
+@pytest.mark.parametrize("name", ["ragged passes", "chunk over a cache", "window and sinks"])
+def test_attend_queries_that_are_not_finite(lib, name):
+    """NaN or an infinity in a query row: NaN in its result, and the others' bits
+    as without."""
+    a = problem(name)
+    r, (q, *rest) = a.runner(), a.args()
+    want = r.attend(q, *rest).clone()
+    q = q.clone()
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool)
+    for i, bad in enumerate((math.nan, math.inf, -math.inf)):
+        t, h = i * (q.shape[0] - 1) // 2, i % q.shape[1]
+        q[t, h, (17 * i + 3) % q.shape[2]] = bad
+        hit[t, h] = True
+    got = r.attend(q, *rest)
+    assert torch.equal(torch.isnan(got).all(-1).cpu(), hit)
+    assert torch.equal(got[~hit].view(torch.int16), want[~hit].view(torch.int16))
 
 
 def test_beyond_32_bit_offsets(lib):
