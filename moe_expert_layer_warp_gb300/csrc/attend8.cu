@@ -53,15 +53,15 @@
 //
 // What bounds it, beside the rates measured for a copy and a dense product (6.65
 // TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 228
-// us, 5.7 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 100 us for 456 MB
-// that a copy moves in 69, and 110 for 61 within a window: a CTA has few tiles, and
-// its start, its joins and its parts of items (8 to 12 thousand cycles each; a tile 0.9
-// to 1.6) are half of its time. Long prompts' chunks: 560 us, 471 TFLOP/s: a tile of 64
-// rows takes 2500 cycles, half of them the softmax warps' instructions, most of those
-// for splitting weights into numbers, and half of them waits, of four warps of a
-// sub-partition for each other and for what they load (an instruction every other
-// cycle, tensor cores a sixth of the time). One pass of 5 tokens over 777 keys: 9 us
-// beyond an empty launch, the chain from the plan to a part's end.
+// us, 5.7 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 98 us for 456 MB
+// that a copy moves in 69, and 104 for 61 within a window: a CTA has few tiles, and
+// its start (6 us), its joins (4) and its parts of items (3 to 5 us each beside 0.5 to
+// 1.15 a tile) are half of its time. Long prompts' chunks: 553 us, 477 TFLOP/s: a
+// tile of 64 rows takes 2200 cycles, half of them the softmax warps' instructions,
+// most of those for splitting weights into numbers, and half of them waits, of four
+// warps of a sub-partition for each other and for what they load (an instruction
+// every other cycle, tensor cores a fifth of the time). One pass of 5 tokens over 777
+// keys: 10 us beyond an empty launch, the chain from the plan to a part's end.
 //
 // Values that are not finite (NaN; e4m3 has no infinities). A weight of 0 times
 // NaN is NaN: rows of V that no row of the item sees are cleared, and NaN in rows
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const int page = 1 << p.page_shift;
     const int rows = min(page, kTile);          // rows of a box
     // keys and values that one item reads alone are not kept in L2: the rows of
-    // the other heads beside them are (single tokens 258 -> 243 us)
+    // the other heads beside them are (single tokens 258 us otherwise, 243)
     const uint64_t stay = l2_evict_normal_policy(), go = l2_evict_first_policy();
     // Lanes 0-15 load K_{j + streams}, a box each, lanes 16-31 V_j: with one after the
     // other the loader was what a tile of 16 rows took. (A box takes its 80 cycles to
