@@ -56,7 +56,7 @@
 // us, 5.7 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 98 us for 456 MB
 // that a copy moves in 69, and 104 for 61 within a window: a CTA has few tiles, and
 // its start (6 us), its joins (4) and its parts of items (3 to 5 us each beside 0.5 to
-// 1.15 a tile) are half of its time. Long prompts' chunks: 553 us, 477 TFLOP/s: a
+// 1.15 a tile) are half of its time. Long prompts' chunks: 543 us, 486 TFLOP/s: a
 // tile of 64 rows takes 2200 cycles, half of them the softmax warps' instructions,
 // most of those for splitting weights into numbers, and half of them waits, of four
 // warps of a sub-partition for each other and for what they load (an instruction
@@ -1102,6 +1102,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         const unsigned long long spoilt =
             spoils ? __ldcg(p.spoiled + blockIdx.x * 128 + d) : 0ull;
         uint16_t* through = reinterpret_cast<uint16_t*>(smem + Z::kOffP);
+        const bool whole = pt->whole;
 #pragma unroll 1
         for (int i = 0; i < take && from + i < rows; i += 4) {  // (take: a multiple of 4)
           float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1123,15 +1124,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
               o[c] = fmaf(v, f[c], o[c]);
             }
           }
+          if (spoilt >> (from + i) & 15ull) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int r = from + i + c;
-            if (spoilt >> r & 1ull) o[c] = NAN;
-            if (!valid) continue;
-            if (pt->whole)
-              through[r * kDim + d] = (uint16_t)round16<kF16>(o[c], 0.f);
-            else
-              slot[r * kDim + d] = o[c];
+            for (int c = 0; c < 4; ++c)
+              if (spoilt >> (from + i + c) & 1ull) o[c] = NAN;
+          }
+          if (whole) {
+            const uint32_t w0 = round16<kF16>(o[0], o[1]), w1 = round16<kF16>(o[2], o[3]);
+            uint16_t* to = through + (from + i) * kDim + d;
+            if (valid) {
+              to[0] = (uint16_t)w0;
+              to[kDim] = (uint16_t)(w0 >> 16);
+              to[2 * kDim] = (uint16_t)w1;
+              to[3 * kDim] = (uint16_t)(w1 >> 16);
+            }
+          } else if (valid) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) slot[(from + i + c) * kDim + d] = o[c];
           }
         }
         open = !pt->ends;
