@@ -5,8 +5,10 @@ ones (the first step: its prompt). One step runs, on one stream and without
 reading anything back:
 
   plan    pages, slots and positions of the new tokens (BatchPlanner)
-  append  their keys and values into the paged cache (PagedCache)
-  attend  their attention over every request's cache (PagedAttention)
+  rotate  rotary positions of their queries and keys (Rotary; with --cache8)
+  append  their keys and values into the paged cache (PagedCache, PagedCache8)
+  attend  their attention over every request's cache (PagedAttention,
+          PagedAttention8)
   route   gate, then grouped routing with sigmoid scores and a balance bias
           (GroupedRouter) into the expert layer's buffers
   experts the deduplicating engine and the combine (PassRunner)
@@ -15,7 +17,7 @@ The projections around the attention are plain matrix products. Weights are
 random; a "verifier" accepts a random number of drafted tokens. Rejected
 tokens leave their pages to the request: the next plan writes over them.
 
-    python examples/verify_step.py [--requests 12] [--steps 20]
+    python examples/verify_step.py [--requests 12] [--steps 20] [--cache8]
 """
 from __future__ import annotations
 
@@ -30,7 +32,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from moe_expert_layer_warp_gb300 import api, synth                      # noqa: E402
 from moe_expert_layer_warp_gb300.batch import (BatchPlanner, GroupedRouter,  # noqa: E402
-                                               PagedAttention, PagedCache)
+                                               PagedAttention, PagedAttention8, PagedCache,
+                                               PagedCache8, Rotary)
 from moe_expert_layer_warp_gb300.configs import LayerShape, W_BF16      # noqa: E402
 from moe_expert_layer_warp_gb300.layer import DEDUP, PassRunner         # noqa: E402
 
@@ -39,9 +42,11 @@ SHAPE = LayerShape(512, 32, 4, 256, 1, W_BF16)      # 32 routed experts top-4, 1
 
 
 class Block:
-    """One decoder block's weights, cache and step."""
+    """One decoder block's weights, cache and step. cache8: with rotary positions,
+    and the cache in 8 bits."""
 
-    def __init__(self, requests: int, max_tokens: int, max_blocks: int, seed: int = 0):
+    def __init__(self, requests: int, max_tokens: int, max_blocks: int, seed: int = 0,
+                 cache8: bool = False):
         g = torch.Generator(device="cuda").manual_seed(seed)
         d = SHAPE.d
 
@@ -51,9 +56,15 @@ class Block:
         self.w_qkv = weight(d, (HEADS + 2 * KV_HEADS) * DIM)
         self.w_out = weight(HEADS * DIM, d)
         pages = requests * max_blocks
-        self.cache = PagedCache.allocate(pages, PAGE, KV_HEADS, DIM)
         self.planner = BatchPlanner(PAGE, requests, max_tokens)
-        self.attention = PagedAttention(self.cache, HEADS, max_tokens)
+        if cache8:
+            self.rotary = Rotary(DIM)
+            self.cache = PagedCache8.allocate(pages, PAGE, KV_HEADS, DIM)
+            self.attention = PagedAttention8(self.cache, HEADS, max_tokens)
+        else:
+            self.rotary = None
+            self.cache = PagedCache.allocate(pages, PAGE, KV_HEADS, DIM)
+            self.attention = PagedAttention(self.cache, HEADS, max_tokens)
         self.moe = PassRunner(synth.make_layer(SHAPE, seed + 1, "cuda"), max_tokens)
         bias = torch.randn(SHAPE.n_experts, generator=g, device="cuda") * 0.1
         self.router = GroupedRouter(SHAPE.n_experts, SHAPE.top_k, max_tokens, n_groups=4,
@@ -75,8 +86,10 @@ class Block:
         self.held.copy_(plan.held)
         self.free_range[:1].copy_(plan.free_head)
         qkv = (x @ self.w_qkv).view(T, HEADS + 2 * KV_HEADS, DIM)
-        q = qkv[:, :HEADS].to(self.cache.dtype)
-        k, v = qkv[:, HEADS:HEADS + KV_HEADS], qkv[:, HEADS + KV_HEADS:]
+        q, k, v = qkv.split((HEADS, KV_HEADS, KV_HEADS), dim=1)
+        if self.rotary is not None:
+            self.rotary.rotate(q, k, plan.positions)  # in place, in fp32
+        q = q.to(torch.bfloat16)
         self.cache.append(k, v, plan.slots)           # rounded from fp32 on the way
         y = self.attention.attend(q, plan.q_start, plan.kv_len, self.table)
         h = x + y.view(T, -1).float() @ self.w_out
@@ -96,6 +109,8 @@ def main(argv=None):
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     p.add_argument("--requests", type=int, default=12)
     p.add_argument("--steps", type=int, default=20)
+    p.add_argument("--cache8", action="store_true",
+                   help="rotary positions, and keys and values in 8 bits")
     a = p.parse_args(argv)
     # an expert pass takes 128 tokens at most: every request brings one at least
     if not 1 <= a.requests <= 128 or a.steps < 1:
@@ -104,7 +119,7 @@ def main(argv=None):
     prompt, draft = min(10, 128 // a.requests), min(5, 128 // a.requests)
     # pages for the longest request: every draft kept
     block = Block(a.requests, max_tokens=min(128, a.requests * 10),
-                  max_blocks=(prompt + a.steps * draft - 1) // PAGE + 1)
+                  max_blocks=(prompt + a.steps * draft - 1) // PAGE + 1, cache8=a.cache8)
     total, timed_from = 0, min(2, a.steps - 1)            # the first steps warm up
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     for step in range(a.steps):

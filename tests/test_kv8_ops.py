@@ -817,3 +817,38 @@ def test_steps_together(lib):
                                     table, D ** -0.5, 90, 2)
         assert ((got.double() - want).abs() <= bound).all()
         cached += i32([n if step == 0 else n - n // 3 for n in q_len])
+
+
+def test_example_with_a_cache_in_8_bits(lib):
+    """The example's block with rotary positions and this cache: attention against
+    its definition on what the cache holds, over several steps; and the command."""
+    from examples import verify_step as ex
+    B, g = 5, torch.Generator().manual_seed(2)
+    block = ex.Block(B, max_tokens=50, max_blocks=6, seed=7, cache8=True)
+    block.cache.k.view(torch.uint8).zero_()
+    block.cache.v.view(torch.uint8).zero_()
+    block.cache.k_scale.fill_(1.0)
+    block.cache.v_scale.fill_(1.0)
+    for step in range(4):
+        q_len = torch.randint(1 if step == 0 else 0, 11 if step == 0 else 7, (B,), generator=g)
+        n = int(q_len.sum())
+        x = torch.randn((n, ex.SHAPE.d), generator=g).cuda()
+        _, got = block.step(x, q_len.int().cuda())
+        assert lib.moe_last_device_error() == lib.MOE_OK
+        plan, c = got["plan"], block.cache
+        plain = (x @ block.w_qkv).view(n, -1, ex.DIM)
+        for y, was, step_of in ((got["q"], plain[:, :ex.HEADS], 2.0 ** -8),
+                                (got["k"], plain[:, ex.HEADS:ex.HEADS + ex.KV_HEADS], 0.0)):
+            want, bound = oracle.rotate(was, plan.positions, block.rotary.frequencies, 0, False,
+                                        1.0)
+            # (queries are rounded once more, to bf16)
+            over = (y.double() - want).abs() - bound * (1 + step_of) - step_of * want.abs()
+            assert (over <= 0).all()
+        pools = [oracle.Pool.of(c.k, c.k_scale, 16), oracle.Pool.of(c.v, c.v_scale, 16)]
+        kk, vv = (p.all_values().cuda() for p in pools)
+        vs = torch.exp2(pools[1].exp.double()).permute(0, 2, 1).repeat_interleave(16, dim=1).cuda()
+        want, bound = oracle.attend(got["q"], kk, vv, vs, plan.q_start.tolist(),
+                                    plan.kv_len.tolist(), block.table, ex.DIM ** -0.5, 0, 0)
+        assert ((got["attention"].double() - want).abs() <= bound).all()
+        block.accept((q_len - q_len // 3).int().cuda())
+    ex.main(["--requests", "4", "--steps", "3", "--cache8"])
