@@ -42,7 +42,7 @@
 // own sums, joined at the end.
 //
 // Warps (one CTA per SM):
-//   0      TMA: key and value tiles into a ring, a box per page
+//   0      TMA: key and value tiles into a ring each, a box per page
 //   1, 2   MMA issue: scores, and results. (An MMA holds the warp that issues it for
 //          the 64 cycles that it takes, a wait that ends at once takes 100, a commit
 //          50: with both products in one warp that warp was what a tile took.)
@@ -104,7 +104,15 @@ struct Sizes {
   // stream's. (A stream's P lies within 128 columns, or begins with them.)
   static constexpr int kColumns = kNum == 2 ? 128 : 256;
   static constexpr int kPBytes = kTile * kColumns;
-  static constexpr int kStages = kDim == 64 ? 16 : kNum == 2 ? 10 : 9;
+  // A ring for keys and one for values, each waited on in order by the one warp that
+  // issues its products: with both in one ring, the warp that waits for keys came to
+  // a stage whose last tile, values, had not landed yet, and a parity tells only
+  // neighbouring fills apart. (tests/test_kv8_rings.py has the roles as a model.)
+  static constexpr int kKeyStages = kDim == 64 ? 8 : kNum == 2 ? 5 : 4;
+  static constexpr int kValueStages = kDim == 64 ? 8 : 5;
+  static constexpr int kStages = kKeyStages + kValueStages;
+  // (a value tile that a softmax warp waits for is not further behind; see there)
+  static_assert(kValueStages >= 4, "a stage for every stream");
   static constexpr int kOffRaw = kQBytes;
   static constexpr int kOffP = kOffRaw + kRawBytes;
   static constexpr int kOffRing = kOffP + kPBytes;
@@ -178,13 +186,6 @@ struct Part {
 };
 constexpr int kParts = 8;
 
-// Places in the ring behind the part's first: K_0 .. K_{streams-1}, then
-// K_{j + streams} and V_j for j = 0, 1, ..
-MOE_DEV int place_k(int j, int streams) { return j < streams ? j : 2 * j - streams; }
-MOE_DEV int place_v(int j, int streams, int n) {
-  return j + streams < n ? 2 * j + streams + 1 : n + j;
-}
-
 // The next part of the walk with tiles in it; false when there is none.
 MOE_DEV bool next_part(const Params& p, Walk& w, Request& r, Part* out) {
   const Attend8Args& a = p.a;
@@ -235,8 +236,8 @@ MOE_DEV bool next_part(const Params& p, Walk& w, Request& r, Part* out) {
   return false;
 }
 
-// A place in the ring, counted modulo twice its stages: the stage, and the parity
-// of its filling.
+// A place in a ring (a tile's number in the CTA's range), counted modulo twice its
+// stages: the stage, and the parity of its filling.
 template <int kStages>
 struct Place {
   int at;
@@ -262,7 +263,7 @@ MOE_DEV uint32_t add_counts(uint32_t counts, int n, int shift) {
 // Barriers and words behind the ring.
 template <int kStages>
 struct Misc {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kStages], empty[kStages];        // keys' stages, then values'
   uint64_t part_full[kParts], part_empty[kParts];
   uint64_t raw_full, raw_empty;  // queries as they come
   uint64_t q_full;               // and as numbers
@@ -537,7 +538,9 @@ template <int kDim, int kNum>
 __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_constant__ Params p) {
   using Z = Sizes<kDim, kNum>;
   constexpr bool kF16 = kNum == 3;
-  constexpr int kStages = Z::kStages;
+  constexpr int kStages = Z::kStages, kKeyStages = Z::kKeyStages;
+  using KeyPlace = Place<kKeyStages>;
+  using ValuePlace = Place<Z::kValueStages>;
   using M = Misc<kStages>;
   static_assert(sizeof(M) <= kOffRef, "misc words");
   const Attend8Args& a = p.a;
@@ -652,7 +655,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     ++part_no;
   };
   uint32_t counts = 0;
-  int ring = 0;     // place of the part's first tile, modulo twice the stages
 
   if (warp < 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == -4) {
@@ -670,29 +672,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
     const uint32_t to = smem_addr(smem) + Z::kOffRing + piece * rows * kDim;
     const int block = min(piece * rows / 16, kScaleBlocks - 1);  // first of the lane's box
     int tile_no = 0;
-    Place<kStages> at(0);                       // the next place in the ring
+    KeyPlace k_at(0);                           // the next places in the rings
+    ValuePlace v_at(0);
     for (const Part* pt; (pt = next()); done_with_part()) {
       const int n = pt->n, streams = 1 << pt->shift, head = pt->h;
       const uint64_t policy = pt->once ? go : stay;
 #pragma unroll 1
       for (int j = -streams; ok && j < n; ++j) {
         const bool keys = j + streams < n, values = j >= 0;
-        Place<kStages> mine = at;
-        if (half && keys) mine.next();
         const bool has = half ? values : keys;
         const int no = tile_no + (half ? j : j + streams), slot = no & (kSlots - 1);
-        const int stage = mine.stage();
+        const int k_stage = k_at.stage(), v_stage = kKeyStages + v_at.stage();
+        const int stage = half ? v_stage : k_stage;
         // (a tile's pages are there for V when they were for K)
         const uint32_t empty = smem_addr(&m.empty[stage]), pages = smem_addr(&m.pg_full[slot]);
-        const bool there = !has || (try_at(empty, mine.parity() ^ 1u) &&
+        const bool there = !has || (try_at(empty, (half ? v_at.parity() : k_at.parity()) ^ 1u) &&
                                     (half || try_at(pages, no / kSlots & 1u)));
         if (!__all_sync(0xffffffffu, there)) {
-          const int first = tile_no + j + streams;
-          if (keys) wait(&m.pg_full[first & (kSlots - 1)], first / kSlots & 1u, 0xB30);
-          Place<kStages> next_at = at;
-          wait(&m.empty[next_at.stage()], next_at.parity() ^ 1u, 0xB31);
-          next_at.next();
-          if (keys && values) wait(&m.empty[next_at.stage()], next_at.parity() ^ 1u, 0xB31);
+          if (keys) {
+            const int first = tile_no + j + streams;
+            wait(&m.pg_full[first & (kSlots - 1)], first / kSlots & 1u, 0xB30);
+            wait(&m.empty[k_stage], k_at.parity() ^ 1u, 0xB31);
+          }
+          if (values) wait(&m.empty[v_stage], v_at.parity() ^ 1u, 0xB31);
         }
         if (ok) {
           const int pg = has && piece * rows < kTile ? slots[slot].page[block] : -1;
@@ -707,8 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
                            policy);
           __syncwarp();
         }
-        if (keys) at.next();
-        if (values) at.next();
+        if (keys) k_at.next();
+        if (values) v_at.next();
       }
       tile_no += n;
     }
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         for (int j = 0; ok && j < n; ++j) {
           const int s = j & (streams - 1);
           const uint32_t k = count_of(counts, s) + (uint32_t)(j >> shift);
-          const Place<kStages> at(ring + place_k(j, streams));
+          const KeyPlace at(tile_no + j);
           // (who waits for the scores then has the scales too)
           wait_both(&m.full[at.stage()], at.parity(), &m.sc_full[(tile_no + j) & (kSlots - 1)],
                     (tile_no + j) / kSlots & 1u, 0xB43);
@@ -763,25 +765,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
         for (int j = 0; ok && j < n; ++j) {
           const int s = j & (streams - 1);
           const uint32_t k = count_of(counts, s) + (uint32_t)(j >> shift);
-          const Place<kStages> at(ring + place_v(j, streams, n));
+          const ValuePlace at(tile_no + j);
+          const int stage = kKeyStages + at.stage();
           const uint32_t first = s * pitch;            // column of P
-          wait_both(&m.p_full[s], k & 1u, &m.full[at.stage()], at.parity(), 0xB45);
+          wait_both(&m.p_full[s], k & 1u, &m.full[stage], at.parity(), 0xB45);
           umma::fence_after_sync();
           if (ok)
             umma::mma_e4m3<4, kRowHi, kPHi, (32 * kDim >> 4), (32 * 128 >> 4)>(
                 tmem + Z::kColO + s * pitch,
-                (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
+                (ring_at + stage * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
                 (p_at + (first >> 7) * (kTile * 128 >> 4) + ((first & 127u) >> 4)) & 0x3fffu |
                     kNextP,
                 id, j >= streams ? 1u : 0u);
           commit(&m.p_done[s]);
-          commit(&m.empty[at.stage()]);
+          commit(&m.empty[stage]);
           commit(&m.tile_done[(tile_no + j) & (kSlots - 1)]);
         }
       }
       tile_no += n;
       counts = add_counts(counts, n, shift);
-      ring = (ring + 2 * n) % (2 * kStages);
     }
     // Every MMA, and every arrival that hangs on one, is done before tensor
     // memory is released.
@@ -1344,10 +1346,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           wait_at(bars + kPDone, k & 1u ^ 1u, 0xB52);
         }
         if (edge) {
-          const Place<kStages> at(ring + place_v(j, streams, n));
-          wait(&m.full[at.stage()], at.parity(), 0xB56);
+          // (the stage's last tile has landed: the products up to the stream's tile
+          // before this one are done, and that is less than the ring behind)
+          const ValuePlace at(tile_no + j);
+          const int stage = kKeyStages + at.stage();
+          wait(&m.full[stage], at.parity(), 0xB56);
           if (ok)
-            clean_values<kDim>(a, *pt, smem + Z::kOffRing + at.stage() * Z::kTileBytes,
+            clean_values<kDim>(a, *pt, smem + Z::kOffRing + stage * Z::kTileBytes,
                                slots[(tile_no + j) & (kSlots - 1)].key0, gl, 4 >> shift,
                                p.spoiled + blockIdx.x * 128, &m.spoils);
         }
@@ -1374,7 +1379,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       // (a column that saw no key has no reference)
       if (quarter == 0 && lane < 16 && (fresh >> lane & 1u)) ref[lane] = INFINITY;
       counts = add_counts(counts, n, shift);
-      ring = (ring + 2 * n) % (2 * kStages);
       tile_no += n;
       // all scores with these queries are there
       wait_four(m.s_full, counts, 0xB59);
