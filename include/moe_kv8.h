@@ -134,11 +134,19 @@ size_t moe_attend8_workspace_bytes(const moe_kv8_cache* cache, const moe_attn_de
  *   n_heads    at most 64 for each key head.
  * Scales of blocks with a visible key lie within [2^-50, 2^50]: others are
  * reported, and read as the nearer end.
- * The codes go to the tensor cores as they are; queries and softmax weights go
- * as sums of two e4m3 numbers (bf16) or three (fp16), which hold all bits of a
- * bf16 or fp16 query whose size is within 2^-14 of its row's largest; a softmax
- * weight is off by 2^-8 (bf16) or 2^-12 (fp16) of itself, or by 2^-18 or 2^-22 of
- * the row's largest where that is more. Sums and statistics are fp32. A query row
+ * The codes go to the tensor cores as they are; queries go as sums of two e4m3
+ * numbers (bf16) or three (fp16), which hold all bits of a bf16 or fp16 query whose
+ * size is within 2^-14 of its row's largest. The products of a softmax weight p_j
+ * and its block's value scale vs_j are rounded, to either side alike: off by 2^-8
+ * (bf16) or 2^-11 (fp16) of themselves, or by 2^-27 or 2^-30 of the row's largest
+ * product where that is more. Sums and statistics are fp32; over n keys the tensor
+ * cores' sums are cut by n/32 · 2^-23 of their terms' sizes, as moe_attend's are
+ * by n/16. A result is then off by
+ *   (2^-8 + n · 2^-28) Σ p_j |v_j| + 2^-27 max_j(p_j vs_j) Σ |code_j|    (bf16)
+ *   (2^-11 + n · 2^-28) Σ p_j |v_j| + 2^-30 max_j(p_j vs_j) Σ |code_j|   (fp16)
+ * at most, the codes those of the keys that the row sees, beside its scores' errors
+ * in fp32 and its own rounding. What the sum's last term says: a block whose scale is
+ * far above the others' takes their bits, though its codes be zeros. A query row
  * with NaN or an infinity gives NaN (or zeros, where it sees nothing).         */
 moe_status moe_attend8(const moe_kv8_cache* cache, const moe_attn_desc* attn, int32_t dtype,
                        const void* q, int64_t q_token_stride, int64_t q_head_stride,

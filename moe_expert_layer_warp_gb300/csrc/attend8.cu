@@ -13,26 +13,33 @@
 //
 // Codes go to the tensor cores as they lie in the cache (tcgen05 kind::f8f6f4):
 // nothing is widened, and half the bytes of a 16-bit cache are read. Their other
-// operands are sums of e4m3 numbers: a query row, divided by a power of two,
-// is hi + lo/16 (+ lolo/256), each number the rounding of 16 times what the ones
-// before it left; e4m3 has 4 significant bits, so two numbers hold the 8 of bf16
+// operands are sums of numbers in 8 bits, columns of one operand beside each other,
+// so that a product takes them at once. A query row, divided by a power of two,
+// is hi + lo/16 (+ lolo/256), each an e4m3 number, the rounding of 16 times what the
+// ones before it left; e4m3 has 4 significant bits, so two numbers hold the 8 of bf16
 // exactly, three the 11 of fp16, as long as they are within 2^-14 of the row's
-// largest. Weights are split likewise, times 2^4: m follows growth beyond 2^4.5
-// only, so they stay below 2^8.5, and 448 is e4m3's largest; a weight is off by
-// 2^-8 (2^-12) of itself, or 2^-18 (2^-22) of the largest where that is more. The
-// numbers are columns of one operand beside each other, so a product takes them at
-// once.
+// largest. Weights need range before bits: where one key takes most of a row, what
+// the others bring is a sum of many weights that are each far below it. They are
+// rounded to fp16, and that is cut into three (bf16) or four (fp16) e5m2 numbers, 3
+// bits each and 8 times what the ones before it left. m follows growth beyond 2^9.5
+// only and weights are held 2^5 larger, so they stay below 2^14.5 and a row's largest
+// is 2^5 at least: a weight is off by 2^-9 and fp16's 2^-11 of itself (fp16: by the
+// latter), or by 2^-28 (2^-30) of the row's largest where that is more, to either
+// side alike. (Two e4m3 numbers, which end at 2^-18, left rows of 16384 keys whose
+// first took 0.9 of the weight off by 0.05 of their norm. Weights 2^4, 2^6 or 2^10 larger, with what
+// that leaves for growth, keep 2^-27, 2^-29 or 2^-33: prompt chunks 531, 546 and 576 us
+// for 540, verification 94, 96 and 101 for 96.)
 //
 // Tiles. Keys are the rows of both products, query rows their columns:
-//   Sᵀ = K · Qᵀ   128 keys × (16 to 64 query rows, times 2 or 3), and
-//   Oᵀ += Vᵀ · Pᵀ  head_dim × the same columns,
+//   Sᵀ = K · Qᵀ    128 keys × (16 to 64 query rows, times 2 or 3), and
+//   Oᵀ += Vᵀ · Pᵀ  head_dim × (the same rows, times 3 or 4),
 // so that a pass of a few tokens pays for its 16 columns and not for 128 rows
-// (an instruction takes 64 cycles for any width up to 128 columns), K and V are
-// read in the order in which they lie, and a key's scales are one thread's. A
-// softmax thread has one key and 16 query rows. Its rows' references are those of
-// its group of four warps, which hold the tile's 128 keys: they change only when
-// some weight passes 2^8.5 (asked by one barrier's vote), and then by the exact
-// maximum over the tile.
+// (an instruction takes 64 cycles for any width up to 128 columns; the second
+// product of 64 rows has 192 or 256), K and V are read in the order in which they
+// lie, and a key's scales are one thread's. A softmax thread has one key and 16 query
+// rows. Its rows' references are those of its group of four warps, which hold the
+// tile's 128 keys: they change only when some weight passes 2^14.5 (asked by one
+// barrier's vote), and then by the exact maximum over the tile.
 //
 // Work is cut into equal ranges as in attend.cu (attend_range.cuh): an item is
 // (request, key head, block of tokens with at most 64 rows), a CTA whose range
@@ -52,11 +59,11 @@
 //          tiles of a stream; and the next item's queries into e4m3 numbers
 //
 // What bounds it, beside the rates measured for a copy and a dense product (6.65
-// TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 228
-// us, 5.7 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 98 us for 456 MB
+// TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 225
+// us, 5.8 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 96 us for 456 MB
 // that a copy moves in 69, and 104 for 61 within a window: a CTA has few tiles, and
 // its start (6 us), its joins (4) and its parts of items (3 to 5 us each beside 0.5 to
-// 1.15 a tile) are half of its time. Long prompts' chunks: 543 us, 486 TFLOP/s: a
+// 1.15 a tile) are half of its time. Long prompts' chunks: 540 us, 489 TFLOP/s: a
 // tile of 64 rows takes 2200 cycles, half of them the softmax warps' instructions,
 // most of those for splitting weights into numbers, and half of them waits, of four
 // warps of a sub-partition for each other and for what they load (an instruction
@@ -86,29 +93,31 @@ constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 // What an item costs beside its tiles when the work is cut, and what every 16 rows of
 // it add (see Units).
 constexpr int kItemUnits = 26, kItemRowUnits = 5;
-constexpr float kBase = 4.f;      // weights are held 2^4 larger
-constexpr float kGrow = 4.5f;     // m follows growth beyond this (powers of two)
+constexpr float kBase = 5.f;      // weights are held 2^5 larger
+constexpr float kGrow = 9.5f;     // m follows growth beyond this (powers of two)
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
 // the 4 others leave 64 (4·104 + 64 = 5·96).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kSlots = 16;        // tiles whose pages and scales are there
 constexpr int kScaleBlocks = kTile / 16;
 
-// kDim: columns of a head; kNum: e4m3 numbers of a query's element or a weight.
+// kDim: columns of a head; kNum: e4m3 numbers of a query's element, one fewer than
+// a weight's e5m2 numbers.
 template <int kDim, int kNum>
 struct Sizes {
+  static constexpr int kWeightNum = kNum + 1;
   static constexpr int kTileBytes = kTile * kDim;
   static constexpr int kQBytes = kRows * kNum * kDim;  // an item's queries as numbers
   static constexpr int kRawBytes = kRows * kDim * 2;   // and the next one's as they come
-  // Columns of S, of O and of P (a byte each): a quarter, half or all of them are a
+  // Columns of S, and of O and P (a byte each): a quarter, half or all of them are a
   // stream's. (A stream's P lies within 128 columns, or begins with them.)
-  static constexpr int kColumns = kNum == 2 ? 128 : 256;
+  static constexpr int kScoreColumns = kNum == 2 ? 128 : 256, kColumns = 256;
   static constexpr int kPBytes = kTile * kColumns;
   // A ring for keys and one for values, each waited on in order by the one warp that
   // issues its products: with both in one ring, the warp that waits for keys came to
   // a stage whose last tile, values, had not landed yet, and a parity tells only
   // neighbouring fills apart. (tests/test_kv8_rings.py has the roles as a model.)
-  static constexpr int kKeyStages = kDim == 64 ? 8 : kNum == 2 ? 5 : 4;
+  static constexpr int kKeyStages = kDim == 64 ? 8 : 4;
   static constexpr int kValueStages = kDim == 64 ? 8 : 5;
   static constexpr int kStages = kKeyStages + kValueStages;
   // (a value tile that a softmax warp waits for is not further behind; see there)
@@ -122,7 +131,8 @@ struct Sizes {
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kQBytes % 1024 == 0 && kPBytes % 1024 == 0 && kTileBytes % 1024 == 0, "tiles");
   static_assert(kPBytes >= kRows * kDim * 2, "results pass through P");
-  static constexpr uint32_t kCols = 2 * kColumns, kColO = kColumns;  // tensor memory: S, O
+  // tensor memory: S, then O (a power of two is allocated)
+  static constexpr uint32_t kCols = 512, kColO = kScoreColumns;
 };
 // one slot of the workspace: O as [64 rows][dim] floats, then m and Σ
 constexpr size_t slot_floats(int dim) { return size_t(kRows) * (dim + 2); }
@@ -366,6 +376,36 @@ MOE_DEV void numbers_of(float a, float b, float c, float d, uint32_t (&out)[kNum
 // What a number counts.
 MOE_DEV constexpr float number_unit(int i) { return i == 0 ? 1.f : i == 1 ? 0x1p-4f : 0x1p-8f; }
 
+// Four weights' e5m2 numbers, from their roundings to fp16: an e5m2 number is the
+// upper byte of an fp16 number, so each is the upper byte of 8 times what the ones
+// before it left, which is exact, and four hold all 11 bits. The last of three is
+// rounded to nearest by what is added to its lower byte: half a step, or a bit less, so
+// that ties, one of four roundings, go up for every second key and down for the
+// others. (All of them up, a row's weights would be 2^-12 too large.)
+template <int kNum>
+MOE_DEV void weight_numbers(float a, float b, float c, float d, uint32_t ties,
+                            uint32_t (&out)[kNum]) {
+  __half2 w[2] = {__floats2half2_rn(a, b), __floats2half2_rn(c, d)};
+#pragma unroll
+  for (int i = 0; i < kNum; ++i) {
+    uint32_t x[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x[k] = *reinterpret_cast<const uint32_t*>(&w[k]);
+      if (i == 2 && kNum == 3) x[k] += ties;
+      if (i + 1 < kNum) {
+        const uint32_t upper = x[k] & 0xff00ff00u;
+        w[k] = __hmul2(__hsub2(w[k], *reinterpret_cast<const __half2*>(&upper)),
+                       __float2half2_rn(8.f));
+      }
+    }
+    out[i] = __byte_perm(x[0], x[1], 0x7531);
+  }
+}
+MOE_DEV constexpr float weight_unit(int i) {
+  return i == 0 ? 1.f : i == 1 ? 0x1p-3f : i == 2 ? 0x1p-6f : 0x1p-9f;
+}
+
 // The largest of the warp's values; NaN are passed over.
 MOE_DEV float warp_max(float v) {
   float r;
@@ -539,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   using Z = Sizes<kDim, kNum>;
   constexpr bool kF16 = kNum == 3;
   constexpr int kStages = Z::kStages, kKeyStages = Z::kKeyStages;
+  constexpr int kWeightNum = Z::kWeightNum;
   using KeyPlace = Place<kKeyStages>;
   using ValuePlace = Place<Z::kValueStages>;
   using M = Misc<kStages>;
@@ -735,10 +776,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       if (ok) umma::commit_elect(bar);
     };
     for (const Part* pt; (pt = next()); done_with_part()) {
-      const int n = pt->n, shift = pt->shift, streams = 1 << shift, cols = pt->wide * kNum;
-      const int pitch = Z::kColumns >> shift;          // columns between streams
+      const int n = pt->n, shift = pt->shift, streams = 1 << shift;
       if (scores) {                                    // S = K · Qᵀ
-        const uint32_t id = umma::idesc_e4m3(kTile, cols, false);
+        const int cols = pt->wide * kNum;
+        const int pitch = Z::kScoreColumns >> shift;   // columns between streams
+        const uint32_t id = umma::idesc_f8(kTile, cols, false, false);
         // S may be laid out anew once the last scores of every stream are read
         wait_four(m.s_empty, counts, 0xB41);
         wait(&m.q_full, part_no & 1u, 0xB42);
@@ -753,14 +795,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           wait(&m.s_empty[s], k & 1u ^ 1u, 0xB44);
           umma::fence_after_sync();
           if (ok)
-            umma::mma_e4m3<kSteps, kRowHi, kRowHi, 2, 2>(
+            umma::mma_f8<kSteps, kRowHi, kRowHi, 2, 2>(
                 tmem + s * pitch, (ring_at + at.stage() * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
                 q_at & 0x3fffu | kOne, id, 0u);
           commit(&m.s_full[s]);
           commit(&m.empty[at.stage()]);
         }
       } else {                                         // Oᵀ (+)= Vᵀ · Pᵀ
-        const uint32_t id = umma::idesc_e4m3(kDim, cols, true);
+        const int cols = pt->wide * kWeightNum;
+        const int pitch = Z::kColumns >> shift;
+        const uint32_t id = umma::idesc_f8(kDim, cols, true, true);
 #pragma unroll 1
         for (int j = 0; ok && j < n; ++j) {
           const int s = j & (streams - 1);
@@ -771,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           wait_both(&m.p_full[s], k & 1u, &m.full[stage], at.parity(), 0xB45);
           umma::fence_after_sync();
           if (ok)
-            umma::mma_e4m3<4, kRowHi, kPHi, (32 * kDim >> 4), (32 * 128 >> 4)>(
+            umma::mma_f8<4, kRowHi, kPHi, (32 * kDim >> 4), (32 * 128 >> 4)>(
                 tmem + Z::kColO + s * pitch,
                 (ring_at + stage * (Z::kTileBytes >> 4)) & 0x3fffu | kOne,
                 (p_at + (first >> 7) * (kTile * 128 >> 4) + ((first & 127u) >> 4)) & 0x3fffu |
@@ -1110,9 +1154,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
           float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int z = 0; z < streams && z < n; ++z) {
-            uint32_t w[kNum][4];
+            uint32_t w[kWeightNum][4];
 #pragma unroll
-            for (int e = 0; e < kNum; ++e)
+            for (int e = 0; e < kWeightNum; ++e)
               umma::ld_x4(o_from + z * (Z::kColumns >> shift) + e * wide + i, w[e]);
             const float4 by = *reinterpret_cast<const float4*>(refs + z * width + from + i);
             const float f[4] = {by.x, by.y, by.z, by.w};
@@ -1121,8 +1165,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             for (int c = 0; c < 4; ++c) {
               float v = __uint_as_float(w[0][c]);
 #pragma unroll
-              for (int e = 1; e < kNum; ++e)
-                v = fmaf(__uint_as_float(w[e][c]), number_unit(e), v);
+              for (int e = 1; e < kWeightNum; ++e)
+                v = fmaf(__uint_as_float(w[e][c]), weight_unit(e), v);
               o[c] = fmaf(v, f[c], o[c]);
             }
           }
@@ -1176,8 +1220,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       const int s = g >> (2 - shift), gl = g & (3 >> shift);  // stream, and group of it
       const int c0 = 16 * gl;                  // the group's first query row
       const bool active = c0 < wide;
-      const uint32_t column = s * (Z::kColumns >> shift) + c0;
-      const uint32_t s_addr = lanes + column, o_addr = s_addr + Z::kColO;
+      const uint32_t column = s * (Z::kColumns >> shift) + c0;  // of O and P
+      const uint32_t s_addr = lanes + s * (Z::kScoreColumns >> shift) + c0;
+      const uint32_t o_addr = lanes + Z::kColO + column;
       // a stream's barriers count 16: each of its 16 / streams warps arrives for as many
       auto arrive = [&](uint32_t bar) {
         __syncwarp();
@@ -1204,9 +1249,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
       const uint32_t factors = smem_addr(factor), refs_at = smem_addr(ref);
       constexpr uint32_t kEmpty = 32, kPFull = 64, kPDone = 96;  // of the stream's, behind s_full
       const uint32_t first_slot = smem_addr(slots) + (kt >> 4) * 4;
-      uint32_t p_at[kNum];                             // of the thread's weights
+      const uint32_t ties = kt & 1 ? 0x00800080u : 0x007f007fu;  // see weight_numbers
+      uint32_t p_at[kWeightNum];                       // of the thread's weights
 #pragma unroll
-      for (int i = 0; i < kNum; ++i) {
+      for (int i = 0; i < kWeightNum; ++i) {
         const uint32_t at = column + i * wide;
         p_at[i] = smem_addr(smem) + Z::kOffP + (at >> 7) * (kTile * 128) +
                   swizzled<128>(kt, at & 127u);
@@ -1307,7 +1353,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             group_sync();
           }
           // weights, their sum, and their numbers
-          uint32_t num[kNum][4];
+          uint32_t num[kWeightNum][4];
 #pragma unroll
           for (int c = 0; c < 16; c += 4) {
             float w[4];
@@ -1315,10 +1361,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             for (int e = 0; e < 4; ++e) w[e] = exp2_approx(t[c + e]);
             sums[c / 2] = fma2(pair_f(w[0], w[1]), iv2, sums[c / 2]);
             sums[c / 2 + 1] = fma2(pair_f(w[2], w[3]), iv2, sums[c / 2 + 1]);
-            uint32_t v[kNum];
-            numbers_of<kNum>(w[0], w[1], w[2], w[3], v);
+            uint32_t v[kWeightNum];
+            weight_numbers<kWeightNum>(w[0], w[1], w[2], w[3], ties, v);
 #pragma unroll
-            for (int i = 0; i < kNum; ++i) num[i][c / 4] = v[i];
+            for (int i = 0; i < kWeightNum; ++i) num[i][c / 4] = v[i];
           }
           // the product with the weights before them has read those, and added to O
           wait_at(bars + kPDone, k & 1u ^ 1u, 0xB55);
@@ -1328,19 +1374,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             for (uint32_t todo = cols; todo; todo &= todo - 1) {
               const int c = __ffs(todo) - 1;
               const float by = __shfl_sync(0xffffffffu, keep, c);
-              uint32_t o[kNum];
+              uint32_t o[kWeightNum];
 #pragma unroll
-              for (int i = 0; i < kNum; ++i) o[i] = umma::ld_x1(o_addr + i * wide + c);
+              for (int i = 0; i < kWeightNum; ++i) o[i] = umma::ld_x1(o_addr + i * wide + c);
               umma::wait_ld();
 #pragma unroll
-              for (int i = 0; i < kNum; ++i)
+              for (int i = 0; i < kWeightNum; ++i)
                 umma::st_x1(o_addr + i * wide + c, __float_as_uint(__uint_as_float(o[i]) * by));
             }
             umma::wait_st();
             umma::fence_before_sync();
           }
 #pragma unroll
-          for (int i = 0; i < kNum; ++i) st_shared4(p_at[i], num[i]);
+          for (int i = 0; i < kWeightNum; ++i) st_shared4(p_at[i], num[i]);
         } else {
           arrive(bars + kEmpty);
           wait_at(bars + kPDone, k & 1u ^ 1u, 0xB52);

@@ -1,5 +1,5 @@
 // attend8_mma.cuh — what attention over a cache in 8 bits needs of tcgen05
-// beyond attend_mma.cuh: products of e4m3 operands, whose rows may run along K
+// beyond attend_mma.cuh: products of 8-bit operands, whose rows may run along K
 // or across it, and short loads and stores of tensor memory.
 #pragma once
 
@@ -8,11 +8,12 @@
 namespace moe {
 namespace umma {
 
-// Instruction descriptor of kind::f8f6f4: A and B e4m3, fp32 accumulators; mn:
-// both with rows that run along K (else both K-major). M 64 or 128, N a multiple
-// of 16.
-MOE_DEV uint32_t idesc_e4m3(int M, int N, bool mn) {
-  return (1u << 4) | (mn ? 3u << 15 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4 (whose operands' types are independent):
+// A e4m3, B e4m3 or e5m2, fp32 accumulators; mn: both with rows that run along K
+// (else both K-major). M 64 or 128, N a multiple of 16.
+MOE_DEV uint32_t idesc_f8(int M, int N, bool b_e5m2, bool mn) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | (mn ? 3u << 15 : 0u) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // The high word of a shared-memory descriptor: tiles of rows of 128 or 64 bytes,
@@ -25,7 +26,7 @@ constexpr uint32_t kDescHi8 =
 // (see mma4_ss). alo, blo: low words of the operands' descriptors at the first
 // step; kA, kB: what a step adds to them, in 16-byte units.
 template <int kSteps, uint32_t kAHi, uint32_t kBHi, int kA, int kB>
-MOE_DEV void mma_e4m3(uint32_t tmem_d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc) {
+MOE_DEV void mma_f8(uint32_t tmem_d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t acc) {
   static_assert(kSteps == 2 || kSteps == 4, "steps");
   if constexpr (kSteps == 4) {
     asm volatile(
