@@ -256,10 +256,11 @@ class PagedAttention:
 
 
 def rotary_frequencies(n_rotated: int, base: float = 10000.0, scaling: str = "none",
-                       factor: float = 1.0, original: int = 4096, fast: float = 32.0,
+                       factor: float = 1.0, original: int = 4096, fast: Optional[float] = None,
                        slow: float = 1.0) -> list:
     """Angles per position in radians of n_rotated / 2 pairs, base^(-2i/n_rotated),
-    stretched for contexts `factor` times as long as `original` positions:
+    stretched for contexts `factor` times as long as the `original` positions that
+    the unstretched angles were made for (these and the others are a checkpoint's):
 
       "linear"  every angle divided by factor;
       "base"    the base times factor^(n/(n-2)): the slowest pair is stretched by
@@ -267,10 +268,12 @@ def rotary_frequencies(n_rotated: int, base: float = 10000.0, scaling: str = "no
       "ramp"    pairs that turn less than `slow` times within `original` positions
                 divided, those that turn more than `fast` times kept, the pairs
                 between by their index (usual with an amplitude of
-                0.1 ln(factor) + 1);
-      "bands"   the same by the number of turns itself.
+                0.1 ln(factor) + 1); fast is 32 if not given;
+      "bands"   the same by the number of turns itself; fast is 4 if not given.
     """
     n = n_rotated
+    if fast is None:
+        fast = 4.0 if scaling == "bands" else 32.0
     if n < 2 or n % 2 or not base > 0 or not factor > 0 or original < 1 or not 0 < slow < fast:
         raise ValueError("n_rotated must be even and positive, base, factor and original positive, "
                          "and slow below fast")
