@@ -460,6 +460,9 @@ def moe_rotary(rotary: RotaryDesc, q, k, positions, q_out=None, k_out=None, stre
     _shaped("positions", positions, torch.int32, (None,))
     if not given:
         raise ValueError("give q or k")
+    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
+        if x is None and out is not None:
+            raise ValueError("%s_out without %s" % (name, name))
     dtype = given[0].dtype
     if dtype not in DTYPES or any(x.dtype is not dtype for x in given):
         raise ValueError("q and k must be of one type: float32, bfloat16 or float16")

@@ -360,6 +360,8 @@ class Rotary:
         if x is None or (q is not None and k is not None and q.dtype is not k.dtype) or (
                 x.dtype not in api.DTYPES):
             raise ValueError("give q or k, of one type: float32, bfloat16 or float16")
+        if (q is None and q_out is not None) or (k is None and k_out is not None):
+            raise ValueError("q_out and k_out take what q and k give: one is there without the other")
         q_rows = k_rows = None
         if q is not None:
             q_rows, q = self._rows("q", q, q_out, n)
