@@ -11,13 +11,12 @@ weights (1.14 GB) are far larger than L2 and consecutive layers read different
 weights, so every layer reads its expert weights cold from HBM. The step is
 captured once in a CUDA graph and replayed.
 
-Besides the headline the line carries the per-call breakdown of the layers'
-passes (the step-time model's inputs), the stack check (the model fitted on
-one layer run alone against the measured stack, at four hidden-state
-correlations), and per-pass-size tables of the Mixtral- and DeepSeek-V3-shaped
-layers.
-
-Prints one JSON line (rank 0). ``--impl reference`` times the float64 CPU
+Prints one JSON line on stdout (rank 0), short enough for a log that keeps a few
+thousand characters. What goes with it, a line on stderr: the per-call breakdown of
+the layers' passes (the step-time model's inputs), the stack check (the model fitted
+on one layer run alone against the measured stack, at four hidden-state correlations),
+and per-pass-size tables of the Mixtral- and DeepSeek-V3-shaped layers.
+``--impl reference`` times the float64 CPU
 oracle on the same workload instead (a bounded sample per step).
 """
 from __future__ import annotations
@@ -51,6 +50,9 @@ N_PASSES_PER_N = 2        # distinct hidden-state passes per n, alternated acros
 EXPERT_BYTES = 3 * 2048 * 1408 * 2
 BREAKDOWN_PASSES = 8      # passes per (pass size, engine) in the per-call breakdown
 BREAKDOWN_ROUNDS = 9      # replays of each breakdown graph (median taken)
+# What does not go into the line on stdout: tables, and notes on its numbers
+EXTRAS = ("layer_breakdown", "stack_check", "best_engine", "tables", "roofline.bytes",
+          "roofline.traffic_source", "e2e.path", "e2e_eager.note", "cpu_baseline.single_thread")
 SPIN_CYCLES = 2_000_000   # ~1 ms of device spin before a timed pass: the host queues the whole
                           # pass meanwhile, so no launch waits on the host inside the timed span
 
@@ -1118,7 +1120,22 @@ def run_ours(args):
         "best_engine": best_engine_rate(stack),
         "tables": tables,
     }
+    line, extras = split_line(line)
+    print(json.dumps({"extras": extras}), file=sys.stderr, flush=True)
     print(json.dumps(line), flush=True)
+
+
+def split_line(line):
+    """The line for stdout, and what EXTRAS names of it."""
+    line, extras = dict(line), {}
+    for name in EXTRAS:
+        key, _, part = name.partition(".")
+        if not part:
+            extras[key] = line.pop(key, None)
+        elif line.get(key):
+            line[key] = dict(line[key])
+            extras[name] = line[key].pop(part, None)
+    return line, extras
 
 
 def run_reference(args):
