@@ -104,8 +104,10 @@ typedef struct {
  *   k, v       as for moe_kv_append, of type src_dtype: MOE_F32, MOE_BF16 or
  *              MOE_F16.
  *   slots      [n_tokens] int64, −1 skips a token. The tokens of one block are
- *              consecutive rows of the call, as moe_plan_batch orders them, and
- *              no two share a slot (where one does, codes of either may stay).
+ *              consecutive rows of the call with none between them, skipped ones
+ *              neither, as moe_plan_batch orders them (else what the block holds
+ *              is not defined), and no two share a slot (where one does, codes
+ *              of either may stay).
  *              Rows of a block are first written from its first row on. Keys and
  *              values of the cache do not share memory.                      */
 moe_status moe_kv8_append(const moe_kv8_cache* cache, const void* k, const void* v,
@@ -137,13 +139,13 @@ size_t moe_attend8_workspace_bytes(const moe_kv8_cache* cache, const moe_attn_de
  * The codes go to the tensor cores as they are; queries go as sums of two e4m3
  * numbers (bf16) or three (fp16), which hold all bits of a bf16 or fp16 query whose
  * size is within 2^-14 of its row's largest. The products of a softmax weight p_j
- * and its block's value scale vs_j are rounded, to either side alike: off by 2^-8
- * (bf16) or 2^-11 (fp16) of themselves, or by 2^-27 or 2^-30 of the row's largest
+ * and its block's value scale vs_j are rounded, to either side alike: off by 2^-9
+ * (bf16) or 2^-11 (fp16) of themselves, or by 2^-26 or 2^-32 of the row's largest
  * product where that is more. Sums and statistics are fp32; over n keys the tensor
  * cores' sums are cut by n/32 · 2^-23 of their terms' sizes, as moe_attend's are
  * by n/16. A result is then off by
- *   (2^-8 + n · 2^-28) Σ p_j |v_j| + 2^-27 max_j(p_j vs_j) Σ |code_j|    (bf16)
- *   (2^-11 + n · 2^-28) Σ p_j |v_j| + 2^-30 max_j(p_j vs_j) Σ |code_j|   (fp16)
+ *   (2^-9 + n · 2^-28) Σ p_j |v_j| + 2^-26 max_j(p_j vs_j) Σ |code_j|    (bf16)
+ *   (2^-11 + n · 2^-28) Σ p_j |v_j| + 2^-32 max_j(p_j vs_j) Σ |code_j|   (fp16)
  * at most, the codes those of the keys that the row sees, beside its scores' errors
  * in fp32 and its own rounding. What the sum's last term says: a block whose scale is
  * far above the others' takes their bits, though its codes be zeros. A query row

@@ -20,22 +20,23 @@
 // exactly, three the 11 of fp16, as long as they are within 2^-14 of the row's
 // largest. Weights need range before bits: where one key takes most of a row, what
 // the others bring is a sum of many weights that are each far below it. They are
-// rounded to fp16, and that is cut into three (bf16) or four (fp16) e5m2 numbers, 3
-// bits each and 8 times what the ones before it left. m follows growth beyond 2^9.5
-// only and weights are held 2^5 larger, so they stay below 2^14.5 and a row's largest
-// is 2^5 at least: a weight is off by 2^-9 and fp16's 2^-11 of itself (fp16: by the
-// latter), or by 2^-28 (2^-30) of the row's largest where that is more, to either
-// side alike. (Two e4m3 numbers, which end at 2^-18, left rows of 16384 keys whose
-// first took 0.9 of the weight off by 0.05 of their norm. Weights 2^4, 2^6 or 2^10 larger, with what
-// that leaves for growth, keep 2^-27, 2^-29 or 2^-33: prompt chunks 531, 546 and 576 us
-// for 540, verification 94, 96 and 101 for 96.)
+// rounded to fp16, and that becomes three e5m2 numbers, 3 bits each and 8 times what
+// the ones before it left (weight_numbers). Weights stay below 2^14.5, and a row's
+// largest is 2^4 (bf16) or 2^10 (fp16) at least: m follows growth beyond 2^10.5 (2^4.5)
+// only. A weight is then off by 2^-9 (2^-11) of itself, or by 2^-26 (2^-32) of the row's
+// largest where that is more, to either side alike. (Two e4m3 numbers, which end at
+// 2^-18, left rows of 16384 keys whose first took 0.9 of the weight off by 0.05 of their
+// norm. The margin for growth is speed: with 2^9.5 and 2^8.5 prompt chunks in bf16 took 540
+// and 548 us for 532. In fp16 it is 2^4.5, 2^6.5 or 2^9.5 for 144, 140 and 136 us, but a
+// row's largest weight is exact only where m is its own, and with wider margins
+// errors grew from 2.2e-4 to 2.3e-4 and 2.4e-4.)
 //
 // Tiles. Keys are the rows of both products, query rows their columns:
 //   Sᵀ = K · Qᵀ    128 keys × (16 to 64 query rows, times 2 or 3), and
-//   Oᵀ += Vᵀ · Pᵀ  head_dim × (the same rows, times 3 or 4),
+//   Oᵀ += Vᵀ · Pᵀ  head_dim × (the same rows, times 3),
 // so that a pass of a few tokens pays for its 16 columns and not for 128 rows
 // (an instruction takes 64 cycles for any width up to 128 columns; the second
-// product of 64 rows has 192 or 256), K and V are read in the order in which they
+// product of 64 rows has 192), K and V are read in the order in which they
 // lie, and a key's scales are one thread's. A softmax thread has one key and 16 query
 // rows. Its rows' references are those of its group of four warps, which hold the
 // tile's 128 keys: they change only when some weight passes 2^14.5 (asked by one
@@ -62,12 +63,12 @@
 // TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 225
 // us, 5.8 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 96 us for 456 MB
 // that a copy moves in 69, and 104 for 61 within a window: a CTA has few tiles, and
-// its start (6 us), its joins (4) and its parts of items (3 to 5 us each beside 0.5 to
-// 1.15 a tile) are half of its time. Long prompts' chunks: 540 us, 489 TFLOP/s: a
-// tile of 64 rows takes 2200 cycles, half of them the softmax warps' instructions,
-// most of those for splitting weights into numbers, and half of them waits, of four
+// its start (6 us), its joins (4) and its parts of items (4 to 6 us each beside 0.4 to
+// 0.8 a tile) are half of its time. Long prompts' chunks: 532 us, 496 TFLOP/s: a
+// tile of 64 rows takes 2200 cycles there, half of them the softmax warps' instructions,
+// many of those for cutting weights into numbers, and half of them waits, of four
 // warps of a sub-partition for each other and for what they load (an instruction
-// every other cycle, tensor cores a fifth of the time). One pass of 5 tokens over 777
+// every other cycle, tensor cores a quarter of the time). One pass of 5 tokens over 777
 // keys: 10 us beyond an empty launch, the chain from the plan to a part's end.
 //
 // Values that are not finite (NaN; e4m3 has no infinities). A weight of 0 times
@@ -93,19 +94,21 @@ constexpr int kMaxCtas = 160;     // workspace slots are sized for this many
 // What an item costs beside its tiles when the work is cut, and what every 16 rows of
 // it add (see Units).
 constexpr int kItemUnits = 26, kItemRowUnits = 5;
-constexpr float kBase = 5.f;      // weights are held 2^5 larger
-constexpr float kGrow = 9.5f;     // m follows growth beyond this (powers of two)
+// Weights are held 2^kBase larger, and m follows growth beyond 2^kGrow (see above).
+template <bool kF16>
+constexpr float kBase = kF16 ? 10.f : 4.f;
+template <bool kF16>
+constexpr float kGrow = 14.5f - kBase<kF16>;
+constexpr int kWeightNum = 3;     // e5m2 numbers of a weight
 // Registers per thread: launched with 96, the 16 softmax warps take 104 and
 // the 4 others leave 64 (4·104 + 64 = 5·96).
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr int kSlots = 16;        // tiles whose pages and scales are there
 constexpr int kScaleBlocks = kTile / 16;
 
-// kDim: columns of a head; kNum: e4m3 numbers of a query's element, one fewer than
-// a weight's e5m2 numbers.
+// kDim: columns of a head; kNum: e4m3 numbers of a query's element.
 template <int kDim, int kNum>
 struct Sizes {
-  static constexpr int kWeightNum = kNum + 1;
   static constexpr int kTileBytes = kTile * kDim;
   static constexpr int kQBytes = kRows * kNum * kDim;  // an item's queries as numbers
   static constexpr int kRawBytes = kRows * kDim * 2;   // and the next one's as they come
@@ -151,13 +154,15 @@ struct Params {
   unsigned long long call;
 };
 
-// An item's units, an eighth of what a tile of 64 query rows takes (1.15 us): first
+// An item's units, an eighth of what a tile of 64 query rows takes (0.83 us): first
 // `cost`, then `each` for every key tile. A tile belongs to the CTA whose range has
-// its first unit. Measured for parts of items alone: 64 rows and one tile 6.2 us, 34
-// tiles 43.7; 48 rows, 22 and 26 tiles, 26.3 and 29.5; 16 rows, 2, 8 and 34 tiles, 5.2,
-// 6.5 and 18.3; and 33 of those, in pages of 16, 28 (their boxes bound them: five units
-// a tile). A batch of chunks and passes took 85 us with 32 + 7 for 16 rows, 79 with
-// these and 77 with 16 + 2, long chunks 543, 554 and 580.
+// its first unit. Measured with one CTA alone (bf16, pages of 64): tiles of 16, 32, 48
+// and 64 rows 0.42, 0.51, 0.74 and 0.83 us, and a part of one tile behind another 4.7,
+// 4.9, 5.8 and 6.8. With tiles of 3, 4, 6 and 8 units single tokens took 226 us for 224,
+// prompts beside passes 82 for 79 and windows 100 for 103.6; with 4, 5, 6 and 8
+// verification passes 102 for 95, windows 107. In pages of 16 a tile of 16 rows takes 0.79
+// us (its boxes bound it), in pages of 32 0.53: as 5 units at least where the page is
+// of 16, prompts beside passes took 78 us, as 4 81, as 8 79.6.
 struct Units {
   int cost, each, all;
   MOE_DEV int tiles(int u) const {  // that begin before unit u
@@ -377,23 +382,27 @@ MOE_DEV void numbers_of(float a, float b, float c, float d, uint32_t (&out)[kNum
 MOE_DEV constexpr float number_unit(int i) { return i == 0 ? 1.f : i == 1 ? 0x1p-4f : 0x1p-8f; }
 
 // Four weights' e5m2 numbers, from their roundings to fp16: an e5m2 number is the
-// upper byte of an fp16 number, so each is the upper byte of 8 times what the ones
-// before it left, which is exact, and four hold all 11 bits. The last of three is
-// rounded to nearest by what is added to its lower byte: half a step, or a bit less, so
-// that ties, one of four roundings, go up for every second key and down for the
-// others. (All of them up, a row's weights would be 2^-12 too large.)
-template <int kNum>
+// upper byte of an fp16 number, and half a step of it added to the lower byte rounds
+// to nearest. Each is 8 times what the ones before it left, which is exact, rounded. Of
+// 11 bits the first leaves multiples of 2^-10 up to 2^-3, the second up to 2^-7, and that
+// the third holds, so fp16's results see their weights' roundings to fp16 alone. For bf16
+// the first is cut, an instruction less for two weights (prompt chunks 549 us
+// otherwise): it leaves up to 2^-2, the second up to 2^-6, and the third is off by 2^-10
+// at most. Weights below 2^-12 are off by half a step of the third, 2^-23; its ties go up
+// for every second key and down for the others.
+template <bool kF16>
 MOE_DEV void weight_numbers(float a, float b, float c, float d, uint32_t ties,
-                            uint32_t (&out)[kNum]) {
+                            uint32_t (&out)[kWeightNum]) {
   __half2 w[2] = {__floats2half2_rn(a, b), __floats2half2_rn(c, d)};
 #pragma unroll
-  for (int i = 0; i < kNum; ++i) {
+  for (int i = 0; i < kWeightNum; ++i) {
     uint32_t x[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       x[k] = *reinterpret_cast<const uint32_t*>(&w[k]);
-      if (i == 2 && kNum == 3) x[k] += ties;
-      if (i + 1 < kNum) {
+      if (i == 2) x[k] += ties;
+      else if (i == 1 || kF16) x[k] += 0x00800080u;
+      if (i + 1 < kWeightNum) {
         const uint32_t upper = x[k] & 0xff00ff00u;
         w[k] = __hmul2(__hsub2(w[k], *reinterpret_cast<const __half2*>(&upper)),
                        __float2half2_rn(8.f));
@@ -403,7 +412,7 @@ MOE_DEV void weight_numbers(float a, float b, float c, float d, uint32_t ties,
   }
 }
 MOE_DEV constexpr float weight_unit(int i) {
-  return i == 0 ? 1.f : i == 1 ? 0x1p-3f : i == 2 ? 0x1p-6f : 0x1p-9f;
+  return i == 0 ? 1.f : i == 1 ? 0x1p-3f : 0x1p-6f;
 }
 
 // The largest of the warp's values; NaN are passed over.
@@ -579,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
   using Z = Sizes<kDim, kNum>;
   constexpr bool kF16 = kNum == 3;
   constexpr int kStages = Z::kStages, kKeyStages = Z::kKeyStages;
-  constexpr int kWeightNum = Z::kWeightNum;
+  constexpr float kBase = moe::kBase<kF16>, kGrow = moe::kGrow<kF16>;
   using KeyPlace = Place<kKeyStages>;
   using ValuePlace = Place<Z::kValueStages>;
   using M = Misc<kStages>;
@@ -1362,7 +1371,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const __grid_const
             sums[c / 2] = fma2(pair_f(w[0], w[1]), iv2, sums[c / 2]);
             sums[c / 2 + 1] = fma2(pair_f(w[2], w[3]), iv2, sums[c / 2 + 1]);
             uint32_t v[kWeightNum];
-            weight_numbers<kWeightNum>(w[0], w[1], w[2], w[3], ties, v);
+            weight_numbers<kF16>(w[0], w[1], w[2], w[3], ties, v);
 #pragma unroll
             for (int i = 0; i < kWeightNum; ++i) num[i][c / 4] = v[i];
           }

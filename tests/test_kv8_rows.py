@@ -3,16 +3,16 @@ values whose scales differ widely: what the other keys bring must stay.
 
 A row's error is held against that of its result with weights rounded to 16 bits
 (and nothing else), and every element against a bound in which no term grows with
-the number of keys to a size that matters. Weights are held as three (bf16) or
-four (fp16) e5m2 numbers of a rounding to fp16, 2^5 or more times larger than
-they are relative to the row's largest product of a weight and its block's scale.
-Numbers are truncated to 3 bits, each 8 times what the ones before left, so three
-rounded ones hold 9 bits: off by 2^-9 of the weight and 2^-11 for the rounding to
-fp16, four by the latter alone; and, where they are small, by half a step of the last
-number, 2^-16 · 8^-2 / 2 = 2^-23, and of fp16, 2^-25: 2^-28 + 2^-30 of the largest one,
-or 2^-30. A product takes 32 keys at a time, and the tensor cores cut each sum to the
-24 bits of its fp32 accumulator: off by 2^-23 of the sum, so that n keys add n/32 ·
-2^-23 of the sum of their sizes at most (2^-11 of it for 131072)."""
+the number of keys to a size that matters. Weights are rounded to fp16, 2^4 (bf16) or
+2^10 (fp16) times larger or more than they are relative to the row's largest product
+of a weight and its block's scale, and held as three e5m2 numbers of 3 bits, each the
+rounding of 8 times what the ones before left: 11 bits for fp16, off by 2^-11 for the
+rounding to fp16, and for bf16, whose first number is cut and not rounded, by 2^-10
+more. Where they are small they are off by half a step of the last number, 2^-16 · 8^-2
+/ 2 = 2^-23, and of fp16, 2^-25: 2^-27 + 2^-29 of the largest one, or 2^-33 + 2^-35. A
+product takes 32 keys at a time, and the tensor cores cut each sum to the 24 bits of
+its fp32 accumulator: off by 2^-23 of the sum, so that n keys add n/32 · 2^-23 of the
+sum of their sizes at most (2^-11 of it for 131072)."""
 import math
 
 import pytest
@@ -119,8 +119,8 @@ class Rows:
             k.abs().sum(-1).t()[None, :, None]) * self.scale
         ds = torch.where(see, size * (self.D + 8) * 2.0 ** -22 + lost, 0.0).amax(-1)[..., None]
         total = w.sum(-1, keepdim=True)
-        rel, far = (2.0 ** -11, 2.0 ** -30) if f16 else (2.0 ** -9 + 2.0 ** -11,
-                                                         2.0 ** -28 + 2.0 ** -30)
+        rel, far = (2.0 ** -11, 2.0 ** -33 + 2.0 ** -35) if f16 else (
+            2.0 ** -10 + 2.0 ** -11, 2.0 ** -27 + 2.0 ** -29)
         y = torch.einsum("thgn,nhd->thgd", w, v) / total
         a = torch.einsum("thgn,nhd->thgd", w, v.abs()) / total
         most = (w * unit.t()[None, :, None]).amax(-1, keepdim=True) / total
@@ -128,7 +128,8 @@ class Rows:
                              v.abs() / unit[..., None])
         eps = half_step(self.dtype)
         lost = far * most * codes + see.sum(-1)[..., None] / 32 * 2.0 ** -23 * a
-        # a row's reference need not be the large key's (it follows growth beyond 2^9.5),
+        # a row's reference need not be the large key's (it follows growth beyond 2^10.5
+        # or 2^4.5),
         # and then its weight is rounded as any other, where that in 16 bits is exactly 1
         lost += rel * (w[..., self.at] / total[..., 0])[..., None] * v[self.at].abs()[:, None]
         bound = (eps * y.abs() + (rel * (1 + eps) + 2 * ds + 2.0 ** -19) * a + lost) * (
