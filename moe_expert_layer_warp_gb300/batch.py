@@ -65,6 +65,19 @@ def _handle(stream, index):
     return api._stream(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor that a call on `stream` writes: of that stream's memory. (Memory of
+    torch's current stream may be in use by what that one still has to do.)"""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = api._stream(stream).value
+        stream = (torch.cuda.ExternalStream(handle, device) if handle else
+                  torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _cuda(device) -> torch.device:
     device = torch.device(device)
     if device.type != "cuda":
@@ -415,8 +428,8 @@ class PagedCache8:
         """New keys and values [n][n_kv_heads][head_dim] (float32, bfloat16 or
         float16) to their slots, rounded to codes (moe_kv8_append). A block's
         scale grows with what comes into it, and starts anew when its first row
-        is written; the tokens of a block are consecutive rows of the call. Rows
-        must be contiguous; token and head strides may be any multiple of 16
+        is written; the tokens of a block are consecutive rows of the call, with no
+        skipped one (slot -1) between them. Rows must be contiguous; token and head strides may be any multiple of 16
         bytes."""
         n, dt, at = k.shape[0], k.dtype, self._index
         sk, sv = k.stride(), v.stride()
@@ -438,11 +451,11 @@ class PagedCache8:
              v: Optional[torch.Tensor] = None, stream=None):
         """(keys, values) [n][n_kv_heads][head_dim] that the rows of slots [n] int64
         stand for (moe_kv8_read), zeros for slot -1, written to k and v if given
-        (of one type and strides), else to new tensors of `dtype`."""
+        (of one type and strides), else to new tensors of `dtype`, which are
+        `stream`'s as torch counts them."""
         n, at = slots.shape[0], self._index
         if k is None and v is None:
-            k, v = (torch.empty((n, *self._row), dtype=dtype, device=self.device)
-                    for _ in range(2))
+            k, v = (_empty((n, *self._row), dtype, self.device, stream) for _ in range(2))
         elif k is None or v is None:
             raise ValueError("give both k and v, or neither")
         sk, sv = k.stride(), v.stride()
