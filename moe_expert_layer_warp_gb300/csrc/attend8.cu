@@ -60,11 +60,11 @@
 //          tiles of a stream; and the next item's queries into e4m3 numbers
 //
 // What bounds it, beside the rates measured for a copy and a dense product (6.65
-// TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 225
+// TB/s, 1894 TFLOP/s). Single tokens of 126 requests, 1.3 GB of keys and values: 224
 // us, 5.8 TB/s: reading them. 64 requests' passes of 1 to 9 tokens: 96 us for 456 MB
 // that a copy moves in 69, and 104 for 61 within a window: a CTA has few tiles, and
 // its start (6 us), its joins (4) and its parts of items (4 to 6 us each beside 0.4 to
-// 0.8 a tile) are half of its time. Long prompts' chunks: 532 us, 496 TFLOP/s: a
+// 0.8 a tile) are half of its time. Long prompts' chunks: 532 us, 497 TFLOP/s: a
 // tile of 64 rows takes 2200 cycles there, half of them the softmax warps' instructions,
 // many of those for cutting weights into numbers, and half of them waits, of four
 // warps of a sub-partition for each other and for what they load (an instruction
